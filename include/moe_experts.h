@@ -2,7 +2,9 @@
  * moe_experts.h — C ABI of the MI355X (gfx950) MoE experts library.
  *
  * The library runs the experts step of a mixture-of-experts layer on one GPU
- * (and, optionally, the router step before it, moe_route):
+ * (and, optionally, the router step before it, moe_route, and the operators
+ * around it in a layer: row norm, microscaled quantization, a dense product
+ * with MXFP4 weights and general routing, at the end of this file):
  * group the router's top-k slots by expert (histogram, prefix sum to segment
  * end offsets, stable permutation), a grouped GEMM for the gate and up
  * projections with the activation and route weight applied in its epilogue,
@@ -447,6 +449,136 @@ int moe_device_error(const void* workspace, int32_t* n_bad);
  */
 int moe_check_expert_params(const moe_problem* p, const float* alpha_e, const float* beta_e,
                             const float* limit_e, const float* fc1_alpha, const float* fc2_alpha);
+
+/* ------------------------------------------------------------------------
+ * Operators around the experts step. Each enqueues one kernel on `stream`,
+ * needs no workspace and allocates nothing, so it may be captured into a HIP
+ * graph and calls may overlap as long as their outputs are distinct. A leading
+ * dimension of 0 means contiguous rows. Unless said otherwise, value pointers
+ * and codes are 16-byte aligned (else MOE_EINVAL) and the byte distance of
+ * their rows is a multiple of 16 (else MOE_ENOTSUP); outputs do not overlap
+ * inputs. Zero rows (T, M or rows 0) are accepted and enqueue nothing.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of values. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
+
+/* Microscaled rows (OCP Microscaling v1.0 reading; trtllm_mxfp4_moe page,
+ * TrtLlmMxfp4ExpertsBase._supports_quant_scheme: MXFP4 weights, MXFP8
+ * activations). Each 32 consecutive values share an e8m0 scale code c, worth
+ * 2^(c - 127); codes are e2m1 (MOE_MX_FP4: two to a byte, value 2i in the low
+ * half of byte i) or e4m3 (MOE_MX_FP8: one to a byte). For a block whose largest
+ * magnitude lies in [2^e, 2^(e+1)) the scale is 2^(e - 2) (FP4) or 2^(e - 8)
+ * (FP8), c clamped to [0, 254], and each element is value / scale rounded to
+ * nearest, ties to even, saturated at 6 or 448: the rule of moe_problem.a_fmt.
+ * A block that holds an infinity or NaN gets c = 255 (NaN) and codes 0, so that
+ * it reads as NaN everywhere. */
+typedef enum { MOE_MX_NONE = 0, MOE_MX_FP4 = 1, MOE_MX_FP8 = 2 } moe_mxfmt;
+
+typedef struct {
+  int32_t rows, K;    /* K a multiple of 32 (else MOE_ENOTSUP); rows * K at most 2^34 */
+  int32_t type;       /* moe_dtype of the values */
+  int32_t fmt;        /* MOE_MX_FP4 or MOE_MX_FP8 */
+  int64_t ld;         /* values: elements between rows */
+  int64_t ld_codes;   /* bytes between rows of codes, a multiple of 16 */
+  int64_t ld_scales;  /* bytes between rows of scales */
+} moe_mx_rows;
+
+/* Values to microscaled rows (the MXFP4 weights of moe_problem and of
+ * moe_mx_linear, or their activations).
+ *   x      (device) values [rows, K]
+ *   codes  (device) [rows, K/2] (FP4) or [rows, K] bytes (FP8), overwritten
+ *   scales (device) [rows, K/32], overwritten, any alignment */
+int moe_mx_quantize(const moe_mx_rows* p, const void* x, void* codes, uint8_t* scales, moe_stream_t stream);
+
+/* Microscaled rows to values: code * 2^(c - 127) rounded to the type (exact in
+ * bf16 and float32 down to their smallest numbers); c = 255 gives NaN. */
+int moe_mx_dequantize(const moe_mx_rows* p, const void* codes, const uint8_t* scales, void* out,
+                      moe_stream_t stream);
+
+typedef struct {
+  int32_t T, H;       /* H <= 16384, a multiple of 8, or of 32 with mx_fmt (else MOE_ENOTSUP) */
+  int32_t type;       /* moe_dtype of x, residual, residual_out and y */
+  int32_t w_type;     /* moe_dtype of weight */
+  int32_t mx_fmt;     /* moe_mxfmt: MOE_MX_NONE = no microscaled output */
+  float eps;          /* finite, >= 0 */
+  int64_t ldx, ld_res, ld_res_out, ldy;  /* elements between rows */
+  int64_t ld_codes, ld_scales;           /* bytes between rows */
+} moe_norm_problem;
+
+/* Residual addition and root-mean-square norm of the rows that enter the
+ * router and the experts:
+ *   h = x + residual rounded to the type (h = x without a residual)
+ *   y = h * weight / sqrt(mean(h^2) + eps), in float32
+ *   x            (device) [T, H]
+ *   residual     (device) [T, H] or NULL
+ *   weight       (device) [H]
+ *   residual_out (device) [T, H]: h; given exactly when residual is; may be
+ *                residual itself, or x
+ *   y            (device) [T, H], y rounded to the type, or NULL; may be x
+ *   codes, scales (device) with mx_fmt: float32 y as microscaled rows, else ignored
+ * At least one of y and the microscaled output is asked for. */
+int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight,
+                    void* residual_out, void* y, void* codes, uint8_t* scales, moe_stream_t stream);
+
+typedef struct {
+  int32_t M, N, K;    /* K a multiple of 32, at most 2^20 (else MOE_ENOTSUP) */
+  int32_t a_fmt;      /* moe_mxfmt of a: MOE_MX_FP8 or MOE_MX_FP4 */
+  int32_t out_type;   /* moe_dtype of out and add */
+  float alpha;        /* finite; 1 = none */
+  int64_t lda;        /* bytes between rows of a, a multiple of 16, at most 2^22 */
+  int64_t ld_as;      /* bytes between rows of a_scales, at most 2^22 */
+  int64_t ldo, ld_add; /* elements between rows */
+} moe_mx_linear_problem;
+
+/* Dense product with MXFP4 weights (a shared expert's or any other projection
+ * beside the routed experts):
+ *   out = alpha * a w^T + bias + add, accumulated in float32, rounded once
+ *   a, a_scales (device) microscaled rows [M, K]
+ *   w           (device) e2m1 codes [N, K/2], contiguous
+ *   w_scales    (device) e8m0 [N, K/32], contiguous
+ *   bias        (device) float32 [N] or NULL
+ *   add         (device) [M, N] or NULL; may be out itself (with ld_add == ldo)
+ *   out         (device) [M, N], overwritten
+ * out and add need their type's alignment only; N is free. A row of a with a NaN
+ * scale gives a NaN row of out. */
+int moe_mx_linear(const moe_mx_linear_problem* p, const void* a, const uint8_t* a_scales, const void* w,
+                  const uint8_t* w_scales, const float* bias, const void* add, void* out, moe_stream_t stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+typedef struct {
+  int32_t T, E, k;    /* E <= 1024, k <= 32 (else MOE_ENOTSUP) */
+  int32_t type;       /* moe_dtype of the logits */
+  int32_t score;      /* moe_score */
+  int32_t n_group;    /* 0 or 1 = no group limit; at most 64 (else MOE_ENOTSUP) */
+  int32_t topk_group;
+  int32_t group_score; /* moe_group_score: a group's largest selection score, or the sum of its two largest */
+  int32_t renormalize; /* 1: divide the weights by their sum over the picks */
+  float routed_scaling_factor;
+  int64_t ld;         /* elements between rows of logits */
+} moe_route_topk_problem;
+
+/* Routing with the choices moe_route fixes left open (trtllm_mxfp4_moe page,
+ * TrtLlmMxfp4ExpertsMonolithic.apply: correction bias, expert groups, groups
+ * kept, routed scaling factor; the formulas are readings, as for moe_route):
+ * scores s are a softmax over all E logits or sigmoids, evaluated in double
+ * and rounded to float32; selection scores are s + bias (float32 additions);
+ * with n_group > 1 only the topk_group best of n_group contiguous groups stay
+ * eligible; the k largest selection scores are picked, ties to the lower
+ * index, in descending order; weights are the picked s, divided by their sum
+ * with renormalize (0 if that sum is 0), times routed_scaling_factor.
+ * Logits are clamped to the finite float32 range first (NaN = most negative).
+ *   logits       (device) [T, E], aligned to their type
+ *   bias         (device) float32 [E], finite or -infinity, or NULL
+ *   topk_ids     (device) int32 [T, k], overwritten
+ *   topk_weights (device) float32 [T, k], overwritten
+ * n_group > 1 needs E % n_group == 0, 1 <= topk_group <= n_group,
+ * k <= topk_group * E / n_group and, for MOE_GROUP_TOP2, E / n_group >= 2
+ * (MOE_EINVAL otherwise). */
+int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const float* bias, int32_t* topk_ids,
+                   float* topk_weights, moe_stream_t stream);
 
 /* Static description of a status code. */
 const char* moe_strerror(int status);

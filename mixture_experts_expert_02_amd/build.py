@@ -7,14 +7,14 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "moe_experts.hip")
+SRCS = [os.path.join(HERE, "csrc", n) for n in ("moe_experts.hip", "layer_ops.hip")]
 LIB = os.path.join(HERE, "libmoe_experts.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     # packed fp32 (v_pk_*_f32) instructions stay off in device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-Wno-unused-result",
+    "-Wno-unused-result", "-parallel-jobs=2",
 ]
 
 
@@ -28,7 +28,7 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     """Always recompiles; returns the library path."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), SRC, "-o", tmp]
+    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *SRCS, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

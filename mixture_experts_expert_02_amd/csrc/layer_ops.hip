@@ -1,0 +1,324 @@
+// Host side of the operators around the experts step: row norm, microscaled
+// quantization, the dense MXFP4 product, general routing. Argument checks and
+// launches; one kernel per call, no workspace, no host synchronisation.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_experts.h"
+#include "mx_linear.hpp"
+#include "mx_quant.hpp"
+#include "norm.hpp"
+#include "route_topk.hpp"
+
+namespace {
+
+int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool type_ok(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP16 || t == MOE_T_FP32; }
+int64_t or_default(int64_t ld, int64_t d) { return ld ? ld : d; }
+
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+
+// rows of n values of the type, ld elements apart: 16-byte accesses at every multiple of 8
+int check_rows(const void* p, int64_t ld, int64_t n, int32_t type) {
+  if (!p || !aligned(p, 16) || ld < n) return MOE_EINVAL;
+  if ((ld * moe::elem_size(type)) % 16 || ld > kMaxLd) return MOE_ENOTSUP;
+  return MOE_OK;
+}
+// rows of codes and scales, byte strides
+int check_codes(const void* codes, int64_t ld, const void* scales, int64_t lds, int64_t K, int32_t fmt) {
+  if (!codes || !scales || !aligned(codes, 16)) return MOE_EINVAL;
+  if (ld < moe::mxf::code_bytes(fmt, K) || lds < K / 32) return MOE_EINVAL;
+  if (ld % 16 || ld > kMaxLd || lds > kMaxLd) return MOE_ENOTSUP;
+  return MOE_OK;
+}
+
+// Calls f with the element type (and the block format) as compile-time constants.
+template <class F>
+void with_type(int32_t type, F f) {
+  if (type == MOE_T_BF16) f(std::integral_constant<int, moe::T_BF16>{});
+  else if (type == MOE_T_FP16) f(std::integral_constant<int, moe::T_FP16>{});
+  else f(std::integral_constant<int, moe::T_FP32>{});
+}
+
+// ------------------------------------------------------------- quantization
+int rows_params(const moe_mx_rows* p, moe::mxf::RowsParams& q, bool& flat) {
+  if (!p || p->rows < 0 || p->K <= 0 || !type_ok(p->type)) return MOE_EINVAL;
+  if (p->fmt != MOE_MX_FP4 && p->fmt != MOE_MX_FP8) return MOE_EINVAL;
+  if (p->K % 32) return MOE_ENOTSUP;
+  if ((int64_t)p->rows * p->K > (int64_t)1 << 34) return MOE_ENOTSUP;
+  const int64_t cb = moe::mxf::code_bytes(p->fmt, p->K);
+  q.ld = or_default(p->ld, p->K);
+  q.ld_codes = or_default(p->ld_codes, cb);
+  q.ld_scales = or_default(p->ld_scales, p->K / 32);
+  q.per_row = (uint32_t)p->K / 8;
+  q.n = (uint32_t)((int64_t)p->rows * p->K / 8);
+  flat = q.ld == p->K && q.ld_codes == cb && q.ld_scales == p->K / 32;
+  return MOE_OK;
+}
+
+int check_mx_rows(const moe_mx_rows* p, const moe::mxf::RowsParams& q, const void* values) {
+  int rc = check_rows(values, q.ld, p->K, p->type);
+  if (rc) return rc;
+  return check_codes(q.codes, q.ld_codes, q.scales, q.ld_scales, p->K, p->fmt);
+}
+
+// ------------------------------------------------------------------- norm
+template <int DT, int FMT>
+void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
+  const int n8 = q.H / 8;
+  const dim3 g((unsigned)T);
+#define MOE_NORM(NT, C) hipLaunchKernelGGL((moe::k_add_rmsnorm<DT, FMT, NT, C>), g, dim3(NT), 0, s, q)
+  if (n8 <= 64) MOE_NORM(64, 1);
+  else if (n8 <= 128) MOE_NORM(128, 1);
+  else if (n8 <= 256) MOE_NORM(256, 1);
+  else if (T <= 512) {  // too few rows to fill the card: a row's chunks side by side
+    if (n8 <= 512) MOE_NORM(512, 1);
+    else if (n8 <= 1024) MOE_NORM(1024, 1);
+    else MOE_NORM(1024, 2);
+  } else if (n8 <= 512) MOE_NORM(256, 2);
+  else if (n8 <= 1024) MOE_NORM(256, 4);
+  else MOE_NORM(256, 8);
+#undef MOE_NORM
+}
+
+// ------------------------------------------------------------------ linear
+int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
+  if (!p || p->M < 0 || p->N <= 0 || p->K <= 0 || !type_ok(p->out_type) || !std::isfinite(p->alpha)) return MOE_EINVAL;
+  if (p->a_fmt != MOE_MX_FP4 && p->a_fmt != MOE_MX_FP8) return MOE_EINVAL;
+  if (p->K % 32 || p->K > 1 << 20) return MOE_ENOTSUP;
+  const int64_t cb = moe::mxf::code_bytes(p->a_fmt, p->K);
+  q.lda = or_default(p->lda, cb);
+  q.ld_as = or_default(p->ld_as, p->K / 32);
+  q.ldo = or_default(p->ldo, p->N);
+  q.ld_add = or_default(p->ld_add, p->N);
+  if (q.lda < cb || q.ld_as < p->K / 32 || q.ldo < p->N || q.ld_add < p->N) return MOE_EINVAL;
+  if (q.lda % 16 || q.lda > 1 << 22 || q.ld_as > 1 << 22 || q.ldo > kMaxLd || q.ld_add > kMaxLd) return MOE_ENOTSUP;
+  q.M = p->M;
+  q.N = p->N;
+  q.K = p->K;
+  q.out_type = p->out_type;
+  q.alpha = p->alpha;
+  return MOE_OK;
+}
+
+template <int AF, int BM, int BN>
+int launch_tile(moe::mxl::Params& q, hipStream_t s) {
+  q.mt = (q.M + BM - 1) / BM;
+  q.nt = (q.N + BN - 1) / BN;
+  const int64_t n = (int64_t)q.mt * q.nt;
+  if (n > 0x7ffffff0) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
+  return launch_status();
+}
+
+template <int AF, int S, int MT>
+int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
+  q.nt = (q.N + 15) / 16;
+  q.mt = (q.M + 16 * MT - 1) / (16 * MT);
+  const int64_t n = (int64_t)q.mt * q.nt;
+  if (n > 0x7ffffff0) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, MT>), dim3((unsigned)n), dim3(64 * S), 0, s, q);
+  return launch_status();
+}
+
+template <int AF, int MT>
+int launch_skinny_split(moe::mxl::Params& q, hipStream_t s) {
+  const int nt = (q.N + 15) / 16, kt = (q.K + 127) / 128;
+  if (nt >= 512 || kt <= 8) return launch_skinny<AF, 4, MT>(q, s);
+  if (nt >= 256 || kt <= 32) return launch_skinny<AF, 8, MT>(q, s);
+  return launch_skinny<AF, 16, MT>(q, s);
+}
+
+template <int AF>
+int launch_linear(moe::mxl::Params& q, hipStream_t s) {
+  if (q.M <= 16) return launch_skinny_split<AF, 1>(q, s);
+  if (q.M <= 32) return launch_skinny_split<AF, 2>(q, s);
+  constexpr int BM = AF == moe::mxf::MXFP8 ? 128 : 256;
+  const int64_t big = (int64_t)((q.M + BM - 1) / BM) * ((q.N + 255) / 256);
+  const int64_t mid = (int64_t)((q.M + 127) / 128) * ((q.N + 127) / 128);
+  if (big >= 192) return launch_tile<AF, BM, 256>(q, s);
+  if (mid >= 192) return launch_tile<AF, 128, 128>(q, s);
+  return launch_tile<AF, 64, 64>(q, s);
+}
+
+// ----------------------------------------------------------------- routing
+template <int DT>
+void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
+#define MOE_ROUTE_TOPK(L, PER)                                                                                 \
+  hipLaunchKernelGGL((moe::k_route_topk<DT, L, PER>), dim3((unsigned)((q.T + 256 / L - 1) / (256 / L))), dim3(256), 0, \
+                     s, q)
+  if (q.E <= 64) MOE_ROUTE_TOPK(16, 4);
+  else if (q.E <= 128) MOE_ROUTE_TOPK(16, 8);
+  else if (q.E <= 256) MOE_ROUTE_TOPK(16, 16);
+  else if (q.E <= 512) MOE_ROUTE_TOPK(64, 8);
+  else MOE_ROUTE_TOPK(64, 16);
+#undef MOE_ROUTE_TOPK
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_mx_quantize(const moe_mx_rows* p, const void* x, void* codes, uint8_t* scales, moe_stream_t stream) {
+  moe::mxf::RowsParams q{};
+  bool flat = false;
+  int rc = rows_params(p, q, flat);
+  if (rc) return rc;
+  if (p->rows == 0) return MOE_OK;
+  q.x = x;
+  q.codes = (uint8_t*)codes;
+  q.scales = scales;
+  if ((rc = check_mx_rows(p, q, x))) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  const dim3 g((q.n + 256 * moe::mxf::kUnroll - 1) / (256 * moe::mxf::kUnroll)), b(256);
+  with_type(p->type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    using namespace moe::mxf;
+    if (p->fmt == MOE_MX_FP4) {
+      if (flat) hipLaunchKernelGGL((k_quantize<DT, MXFP4, true>), g, b, 0, s, q);
+      else hipLaunchKernelGGL((k_quantize<DT, MXFP4, false>), g, b, 0, s, q);
+    } else {
+      if (flat) hipLaunchKernelGGL((k_quantize<DT, MXFP8, true>), g, b, 0, s, q);
+      else hipLaunchKernelGGL((k_quantize<DT, MXFP8, false>), g, b, 0, s, q);
+    }
+  });
+  return launch_status();
+}
+
+int moe_mx_dequantize(const moe_mx_rows* p, const void* codes, const uint8_t* scales, void* out, moe_stream_t stream) {
+  moe::mxf::RowsParams q{};
+  bool flat = false;
+  int rc = rows_params(p, q, flat);
+  if (rc) return rc;
+  if (p->rows == 0) return MOE_OK;
+  q.out = out;
+  q.codes = (uint8_t*)const_cast<void*>(codes);
+  q.scales = const_cast<uint8_t*>(scales);
+  if ((rc = check_mx_rows(p, q, out))) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  const dim3 g((q.n + 256 * moe::mxf::kUnroll - 1) / (256 * moe::mxf::kUnroll)), b(256);
+  with_type(p->type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    using namespace moe::mxf;
+    if (p->fmt == MOE_MX_FP4) {
+      if (flat) hipLaunchKernelGGL((k_dequantize<DT, MXFP4, true>), g, b, 0, s, q);
+      else hipLaunchKernelGGL((k_dequantize<DT, MXFP4, false>), g, b, 0, s, q);
+    } else {
+      if (flat) hipLaunchKernelGGL((k_dequantize<DT, MXFP8, true>), g, b, 0, s, q);
+      else hipLaunchKernelGGL((k_dequantize<DT, MXFP8, false>), g, b, 0, s, q);
+    }
+  });
+  return launch_status();
+}
+
+int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight,
+                    void* residual_out, void* y, void* codes, uint8_t* scales, moe_stream_t stream) {
+  if (!p || p->T < 0 || p->H <= 0 || !type_ok(p->type) || !type_ok(p->w_type)) return MOE_EINVAL;
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return MOE_EINVAL;
+  if (p->mx_fmt != MOE_MX_NONE && p->mx_fmt != MOE_MX_FP4 && p->mx_fmt != MOE_MX_FP8) return MOE_EINVAL;
+  const bool mx = p->mx_fmt != MOE_MX_NONE;
+  if (p->H > 16384 || p->H % (mx ? 32 : 8)) return MOE_ENOTSUP;
+  if (p->T == 0) return MOE_OK;
+  if (!x || !weight || !aligned(weight, 16) || !residual != !residual_out || (!y && !mx)) return MOE_EINVAL;
+  moe::NormParams q{};
+  q.x = x;
+  q.res = residual;
+  q.w = weight;
+  q.res_out = residual_out;
+  q.y = y;
+  q.codes = mx ? (uint8_t*)codes : nullptr;
+  q.scales = mx ? scales : nullptr;
+  q.ldx = or_default(p->ldx, p->H);
+  q.ld_res = or_default(p->ld_res, p->H);
+  q.ld_res_out = or_default(p->ld_res_out, p->H);
+  q.ldy = or_default(p->ldy, p->H);
+  q.ld_codes = or_default(p->ld_codes, moe::mxf::code_bytes(p->mx_fmt, p->H));
+  q.ld_scales = or_default(p->ld_scales, p->H / 32);
+  q.H = p->H;
+  q.w_type = p->w_type;
+  q.eps = p->eps;
+  int rc = check_rows(x, q.ldx, p->H, p->type);
+  if (!rc && residual) rc = check_rows(residual, q.ld_res, p->H, p->type);
+  if (!rc && residual) rc = check_rows(residual_out, q.ld_res_out, p->H, p->type);
+  if (!rc && y) rc = check_rows(y, q.ldy, p->H, p->type);
+  if (!rc && mx) rc = check_codes(codes, q.ld_codes, scales, q.ld_scales, p->H, p->mx_fmt);
+  if (rc) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  with_type(p->type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (p->mx_fmt == MOE_MX_FP4) launch_norm<DT, moe::mxf::MXFP4>(q, p->T, s);
+    else if (p->mx_fmt == MOE_MX_FP8) launch_norm<DT, moe::mxf::MXFP8>(q, p->T, s);
+    else launch_norm<DT, 0>(q, p->T, s);
+  });
+  return launch_status();
+}
+
+int moe_mx_linear(const moe_mx_linear_problem* p, const void* a, const uint8_t* a_scales, const void* w,
+                  const uint8_t* w_scales, const float* bias, const void* add, void* out, moe_stream_t stream) {
+  moe::mxl::Params q{};
+  int rc = mx_linear_params(p, q);
+  if (rc) return rc;
+  if (p->M == 0) return MOE_OK;
+  if (!a || !a_scales || !w || !w_scales || !out) return MOE_EINVAL;
+  const size_t size = (size_t)moe::elem_size(p->out_type);
+  if (!aligned(bias, 4) || !aligned(out, size) || !aligned(add, size) || !aligned(a, 16) || !aligned(w, 16))
+    return MOE_EINVAL;
+  q.a = (const uint8_t*)a;
+  q.a_sc = a_scales;
+  q.w = (const uint8_t*)w;
+  q.w_sc = w_scales;
+  q.bias = bias;
+  q.add = add;
+  q.out = out;
+  q.vec = q.ldo % 4 == 0 && aligned(out, 4 * size) && (!add || (q.ld_add % 4 == 0 && aligned(add, 4 * size)));
+  hipStream_t s = (hipStream_t)stream;
+  return p->a_fmt == MOE_MX_FP8 ? launch_linear<moe::mxf::MXFP8>(q, s) : launch_linear<moe::mxf::MXFP4>(q, s);
+}
+
+int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const float* bias, int32_t* topk_ids,
+                   float* topk_weights, moe_stream_t stream) {
+  if (!p || p->T < 0 || p->E <= 0 || p->k <= 0 || p->k > p->E || !type_ok(p->type)) return MOE_EINVAL;
+  if (p->score != MOE_SCORE_SOFTMAX && p->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if (p->group_score != MOE_GROUP_MAX && p->group_score != MOE_GROUP_TOP2) return MOE_EINVAL;
+  if (p->renormalize != 0 && p->renormalize != 1) return MOE_EINVAL;
+  if (p->n_group < 0 || !std::isfinite(p->routed_scaling_factor)) return MOE_EINVAL;
+  if (p->E > moe::kRouteMaxE || p->k > moe::kRouteMaxK || p->n_group > moe::kTopkGroups) return MOE_ENOTSUP;
+  const bool grouped = p->n_group > 1;
+  if (grouped && (p->E % p->n_group || p->topk_group < 1 || p->topk_group > p->n_group ||
+                  (p->group_score == MOE_GROUP_TOP2 && p->E / p->n_group < 2) ||
+                  (int64_t)p->k > (int64_t)p->topk_group * (p->E / p->n_group)))
+    return MOE_EINVAL;
+  const int64_t ld = or_default(p->ld, p->E);
+  if (ld < p->E) return MOE_EINVAL;
+  if (ld > kMaxLd) return MOE_ENOTSUP;
+  if (p->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights) return MOE_EINVAL;
+  if (!aligned(logits, (size_t)moe::elem_size(p->type)) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(bias, 4))
+    return MOE_EINVAL;
+  moe::RouteTopkParams q;
+  q.logits = logits;
+  q.bias = bias;
+  q.ids = topk_ids;
+  q.w = topk_weights;
+  q.ld = ld;
+  q.T = p->T;
+  q.E = p->E;
+  q.k = p->k;
+  q.sigmoid = p->score == MOE_SCORE_SIGMOID;
+  q.n_group = grouped ? p->n_group : 0;
+  q.topk_group = p->topk_group;
+  q.top2 = p->group_score == MOE_GROUP_TOP2;
+  q.renorm = p->renormalize;
+  q.scale = p->routed_scaling_factor;
+  hipStream_t s = (hipStream_t)stream;
+  with_type(p->type, [&](auto dt) { launch_route<decltype(dt)::value>(q, s); });
+  return launch_status();
+}
+
+}  // extern "C"

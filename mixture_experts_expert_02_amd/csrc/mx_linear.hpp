@@ -1,0 +1,541 @@
+// Dense product with MXFP4 weights: out = alpha a W^T + bias + add, a in
+// MXFP8 or MXFP4 rows, on the block-scaled MFMA (moe_mx_linear).
+//
+// trtllm_mxfp4_moe page, TrtLlmMxfp4ExpertsBase._supports_quant_scheme (MXFP4
+// weights, MXFP8 activations; OCP Microscaling v1.0 reading).
+#pragma once
+
+#include "elem.hpp"
+#include "mx_format.hpp"
+
+namespace moe {
+namespace mxl {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+struct Params {
+  const uint8_t* a;        // codes, rows of lda bytes
+  const uint8_t* a_sc;     // e8m0, rows of ld_as bytes
+  const uint8_t* w;        // e2m1 codes [N, K/2]
+  const uint8_t* w_sc;     // e8m0 [N, K/32]
+  const float* bias;       // [N] or nullptr
+  const void* add;         // [M, ld_add] of the output type or nullptr
+  void* out;               // [M, ldo]
+  int64_t lda, ld_as, ldo, ld_add;
+  int32_t M, N, K;
+  int32_t out_type;
+  int32_t vec;             // out and add rows take 4-element accesses at columns that are multiples of 4
+  float alpha;
+  int32_t mt, nt;          // row and column tiles
+};
+
+constexpr uint32_t kNoLoad = 0x80000000u;  // buffer offset past any operand: reads 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// 16 consecutive scale bytes at base + off.
+__device__ __forceinline__ u32x4 load_sc16(const uint8_t* base, uint32_t off) {
+  u32x4 v;
+  __builtin_memcpy(&v, base + off, 16);
+  return v;
+}
+
+// The same where only `valid` (<= 16) of them belong to the row and the array
+// ends at base + total: bytes past the row come back 0 (a zero code times any
+// finite scale is 0, but scale code 255 would make it NaN), and nothing past the
+// array is read: the load is moved back to end with it and shifted.
+__device__ __forceinline__ u32x4 load_sc_tail(const uint8_t* base, uint32_t off, uint32_t total, int valid) {
+  uint64_t lo = 0, hi = 0;
+  if (valid <= 0) return u32x4{0u, 0u, 0u, 0u};
+  if (total >= 16) {
+    const uint32_t start = min(off, total - 16);
+    uint32_t d = 8 * (off - start);
+    __builtin_memcpy(&lo, base + start, 8);
+    __builtin_memcpy(&hi, base + start + 8, 8);
+    if (d >= 64) {
+      lo = hi;
+      hi = 0;
+      d -= 64;
+    }
+    if (d) {
+      lo = (lo >> d) | (hi << (64 - d));
+      hi >>= d;
+    }
+  } else {
+#pragma unroll 1
+    for (int j = valid - 1; j >= 0; --j) {
+      hi = (hi << 8) | (lo >> 56);
+      lo = (lo << 8) | base[off + j];
+    }
+  }
+  const int nl = 8 * min(valid, 8), nh = 8 * max(valid - 8, 0);
+  lo &= nl == 64 ? ~0ull : (1ull << nl) - 1;
+  hi &= nh == 64 ? ~0ull : (1ull << nh) - 1;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// 4 results at out[row][col .. col + 3], those below N.
+__device__ __forceinline__ void store4(const Params& p, int row, int col, f32x4 v) {
+  if (col >= p.N) return;
+  const bool whole = p.vec && col + 4 <= p.N;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] *= p.alpha;
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < p.N) v[j] += p.bias[col + j];
+  }
+  const size_t o = (size_t)row * p.ldo + col;
+  const size_t oa = (size_t)row * p.ld_add + col;
+  if (p.out_type == T_FP32) {
+    float* q = (float*)p.out + o;
+    const float* ad = (const float*)p.add + oa;
+    if (whole) {
+      if (p.add) {
+        const f32x4 x = *(const f32x4*)ad;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += x[j];
+      }
+      *(f32x4*)q = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < p.N) q[j] = v[j] + (p.add ? ad[j] : 0.f);
+    }
+    return;
+  }
+  const bool h = p.out_type == T_FP16;
+  uint16_t* q = (uint16_t*)p.out + o;
+  const uint16_t* ad = (const uint16_t*)p.add + oa;
+  auto widen = [&](uint16_t b) { return h ? (float)__builtin_bit_cast(_Float16, b) : bf16_bits_to_f32(b); };
+  auto narrow = [&](float f) -> uint16_t {
+    return h ? __builtin_bit_cast(uint16_t, (_Float16)f) : __builtin_bit_cast(uint16_t, (__bf16)f);
+  };
+  typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+  if (whole) {
+    if (p.add) {
+      const u16x4 x = *(const u16x4*)ad;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += widen(x[j]);
+    }
+    *(u16x4*)q = u16x4{narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < p.N) q[j] = narrow(v[j] + (p.add ? widen(ad[j]) : 0.f));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel. A workgroup of 4 waves computes BM rows x BN columns; a stage is
+// 256 K values: BM rows of activation codes (128 or 256 bytes) and BN rows of
+// weight codes (128 bytes), loaded HBM -> LDS with buffer_load ... lds into one
+// of two buffers while the other is multiplied. Rows past M or N and K past
+// the row's end read zeros through the buffer's range check. 16-byte chunk c of
+// row r sits at slot c ^ ((r >> 1) & 7) (128-byte rows) or c ^ (r & 15)
+// (256-byte rows), so the 16 rows of one ds_read_b128 pass fall on distinct banks.
+//
+// The weights are the MFMA's A operand (row lane & 31), the activations its B
+// operand (column lane & 31), so a lane's results are 4 consecutive columns of
+// one output row. 32x32x64 operands, group q = lane >> 5: e2m1 K values
+// 32q..32q+31 (16 bytes); e4m3 16q..16q+15 and 32+16q..32+16q+15; the lane
+// gives the scale of block q.
+//
+// Scales go straight to registers, 1024 K values (four stages) at a time: lane
+// (r, q) loads bytes 16q..16q+15 of its row's 32, splits them into even and odd
+// blocks, and one v_permlane32_swap per pair hands each half the blocks of its
+// own parity: one register per stage whose byte s is the scale of step s.
+template <int AF, int BM, int BN>
+struct Tile {
+  static constexpr int AB = AF == mxf::MXFP8 ? 256 : 128;  // bytes of an activation row per stage
+  static constexpr int A_BYTES = BM * AB, W_BYTES = BN * 128;
+  static constexpr int STAGE = A_BYTES + W_BYTES;
+  static constexpr int FM = BM / 64, FN = BN / 64;         // 32 x 32 results of a wave
+  static constexpr int AL = A_BYTES / 4096, WL = W_BYTES / 4096;  // loads per wave and stage
+  static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
+  static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
+  static_assert(2 * 32 * EROW * 4 <= STAGE, "epilogue staging: two waves per buffer");
+};
+
+struct ScaleRegs {
+  uint32_t s[4];  // one per stage of the group
+};
+
+// bytes 16q .. 16q + 15 of the 32 block scales -> per-stage registers
+__device__ __forceinline__ ScaleRegs spread_scales(u32x4 v) {
+  const uint32_t e0 = __builtin_amdgcn_perm(v[1], v[0], 0x06040200u), o0 = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
+  const uint32_t e1 = __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), o1 = __builtin_amdgcn_perm(v[3], v[2], 0x07050301u);
+  const auto x = __builtin_amdgcn_permlane32_swap(e0, o0, false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(e1, o1, false, false);
+  ScaleRegs r;
+  r.s[0] = x[0];
+  r.s[2] = x[1];
+  r.s[1] = y[0];
+  r.s[3] = y[1];
+  return r;
+}
+
+template <int AF, int BM, int BN>
+__global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
+  using T = Tile<AF, BM, BN>;
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[T::STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int lr = lane & 31, lq = lane >> 5;
+
+  // Workgroup b runs on XCD b mod 8; each XCD takes a contiguous run of the
+  // tiles, ordered in groups of 4 row tiles, columns outer inside a group, so
+  // the tiles it holds at one time share operand panels in its L2.
+  const int n_tiles = p.mt * p.nt;
+  const int per = (n_tiles + 7) >> 3;
+  const int item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || item >= n_tiles) return;
+  const int g = item / (4 * p.nt), gm = min(4, p.mt - 4 * g);
+  const int in = item - g * 4 * p.nt;
+  const int m0 = (4 * g + in % gm) * BM, n0 = in / gm * BN;
+
+  const int KS = (p.K + 255) >> 8;       // stages
+  const int nblk = p.K >> 5;
+  const uint32_t a_row = AF == mxf::MXFP8 ? (uint32_t)p.K : (uint32_t)p.K / 2, w_row = (uint32_t)p.K / 2;
+  const int a_rows = min(BM, p.M - m0), w_rows = min(BN, p.N - n0);
+  const __amdgpu_buffer_rsrc_t rsA = rsrc(p.a + (size_t)m0 * p.lda, (uint32_t)((a_rows - 1) * p.lda + a_row));
+  const __amdgpu_buffer_rsrc_t rsW = rsrc(p.w + (size_t)n0 * w_row, (uint32_t)w_rows * w_row);
+
+  // load assignment: wave w fills the w-th quarter of each operand
+  uint32_t a_off[T::AL], w_off[T::WL];
+  uint32_t a_ch[T::AL], w_chunk[T::WL];  // byte of the row within a stage
+#pragma unroll
+  for (int i = 0; i < T::AL; ++i) {
+    const int at = wave * (T::A_BYTES / 4) + i * 1024 + lane * 16;
+    const int r = at / T::AB, slot = (at % T::AB) / 16;
+    a_ch[i] = 16u * (AF == mxf::MXFP8 ? slot ^ (r & 15) : slot ^ ((r >> 1) & 7));
+    a_off[i] = r < a_rows ? (uint32_t)(r * p.lda) + a_ch[i] : kNoLoad;
+  }
+#pragma unroll
+  for (int i = 0; i < T::WL; ++i) {
+    const int at = wave * (T::W_BYTES / 4) + i * 1024 + lane * 16;
+    const int r = at / 128, slot = (at % 128) / 16;
+    w_chunk[i] = 16u * (slot ^ ((r >> 1) & 7));
+    w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_chunk[i] : kNoLoad;
+  }
+  // Load instruction q of stage s into buf: first the activations', then the
+  // weights'. A piece past the row's end, or of a stage past the last, reads nothing.
+  auto load_piece = [&](uint8_t* buf, int s, int q) {
+    if (q < T::AL) {
+      const uint32_t k = (uint32_t)s * T::AB;
+      const uint32_t off = k + a_ch[q] < a_row ? a_off[q] + k : kNoLoad;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsA, (__attribute__((address_space(3))) void*)(buf + wave * (T::A_BYTES / 4) + q * 1024), 16, off, 0, 0, 0);
+    } else {
+      const int i = q - T::AL;
+      const uint32_t k = (uint32_t)s * 128u;
+      const uint32_t off = k + w_chunk[i] < w_row ? w_off[i] + k : kNoLoad;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsW, (__attribute__((address_space(3))) void*)(buf + T::A_BYTES + wave * (T::W_BYTES / 4) + i * 1024), 16,
+          off, 0, 0, 0);
+    }
+  };
+
+  // scale rows of this lane (rows past the end repeat the last: never stored)
+  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
+  const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
+  const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
+  const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
+  uint32_t a_so[T::FM], w_so[T::FN];
+#pragma unroll
+  for (int j = 0; j < T::FM; ++j)
+    a_so[j] = (uint32_t)(min(wm * (BM / 2) + j * 32 + lr, a_rows - 1) * (int)p.ld_as + 16 * lq);
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i)
+    w_so[i] = (uint32_t)(min(wn * (BN / 2) + i * 32 + lr, w_rows - 1) * nblk + 16 * lq);
+
+  f32x16 acc[T::FN][T::FM];
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // LDS byte offsets of this lane's operands, per step
+  uint32_t a_rd[4][2], w_rd[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int sw = (lr >> 1) & 7;
+    w_rd[s] = (uint32_t)(T::A_BYTES + (wn * (BN / 2) + lr) * 128 + 16 * ((2 * s + lq) ^ sw));
+    if (AF == mxf::MXFP8) {
+      a_rd[s][0] = (uint32_t)((wm * (BM / 2) + lr) * 256 + 16 * ((4 * s + lq) ^ (lr & 15)));
+      a_rd[s][1] = (uint32_t)((wm * (BM / 2) + lr) * 256 + 16 * ((4 * s + 2 + lq) ^ (lr & 15)));
+    } else {
+      a_rd[s][0] = (uint32_t)((wm * (BM / 2) + lr) * 128 + 16 * ((2 * s + lq) ^ sw));
+      a_rd[s][1] = 0;
+    }
+  }
+
+  u32x4 raw_a[T::FM] = {}, raw_w[T::FN] = {};
+  ScaleRegs sa[T::FM], sw[T::FN];
+  auto load_scales = [&](int grp) {
+    if (32 * grp + 32 <= nblk) {
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) raw_a[j] = load_sc16(a_scb, a_so[j] + 32 * grp);
+#pragma unroll
+      for (int i = 0; i < T::FN; ++i) raw_w[i] = load_sc16(w_scb, w_so[i] + 32 * grp);
+    } else {
+      const int valid = min(nblk - 32 * grp - 16 * lq, 16);
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) raw_a[j] = load_sc_tail(a_scb, a_so[j] + 32 * grp, a_tot, valid);
+#pragma unroll
+      for (int i = 0; i < T::FN; ++i) raw_w[i] = load_sc_tail(w_scb, w_so[i] + 32 * grp, w_tot, valid);
+    }
+  };
+
+  // Operands of one step, two sets: while one is multiplied the other loads.
+  i32x8 av[2][T::FM];
+  i32x4 wv[2][T::FN];
+  auto read_a = [&](const uint8_t* buf, int st, i32x8& d, int j) {
+    const i32x4 lo = *(const i32x4*)(buf + a_rd[st][0] + j * 32 * T::AB);
+    if (AF == mxf::MXFP8) {
+      const i32x4 hi = *(const i32x4*)(buf + a_rd[st][1] + j * 32 * T::AB);
+      d = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      d = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, -1, -1, -1, -1);
+    }
+  };
+  auto read_w = [&](const uint8_t* buf, int st, i32x4& d, int i) { d = *(const i32x4*)(buf + w_rd[st] + i * 4096); };
+
+  // Step S of a stage, operand set S & 1, one row of MFMAs at a time with the
+  // reads of the next step's operands (RD: their buffer, RS: their step) and,
+  // in step 3, the loads of a later stage between them; the scheduling barriers keep
+  // that order, so the matrix pipe always has work behind the reads.
+#define MOE_MXL_MFMA(S, TS, i)                                                                              \
+  {                                                                                                         \
+    const i32x8 w8 = __builtin_shufflevector(wv[(S) & 1][i], wv[(S) & 1][i], 0, 1, 2, 3, -1, -1, -1, -1);   \
+    _Pragma("unroll") for (int j = 0; j < T::FM; ++j)                                                       \
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                          \
+          w8, av[(S) & 1][j], acc[i][j], 4, AF == mxf::MXFP8 ? 0 : 4, S, (int)sw[i].s[TS], S, (int)sa[j].s[TS]); \
+  }
+#define MOE_MXL_STEP(S, TS, RD, RS, LOAD, LBUF, LST)                                         \
+  _Pragma("unroll") for (int i = 0; i < T::FN; ++i) {                                        \
+    MOE_MXL_MFMA(S, TS, i)                                                                   \
+    read_w(RD, RS, wv[((S) + 1) & 1][i], i);                                                 \
+    _Pragma("unroll") for (int j = i; j < T::FM; j += T::FN) read_a(RD, RS, av[((S) + 1) & 1][j], j); \
+    if (LOAD) {                                                                              \
+      _Pragma("unroll") for (int q = i; q < T::AL + T::WL; q += T::FN) load_piece(LBUF, LST, q); \
+    }                                                                                        \
+    __builtin_amdgcn_sched_barrier(0);                                                       \
+  }
+  // A stage: steps 0-2 read on in its own buffer. Before step 3 its last reads
+  // are in; once every wave is there (and the next stage has landed), step 3 reads
+  // the first operands from the other buffer and loads stage NEXT2 into this one.
+#define MOE_MXL_STAGE(CUR, OTHER, NEXT2, TS)                             \
+  {                                                                      \
+    MOE_MXL_STEP(0, TS, CUR, 1, false, CUR, 0)                           \
+    MOE_MXL_STEP(1, TS, CUR, 2, false, CUR, 0)                           \
+    MOE_MXL_STEP(2, TS, CUR, 3, false, CUR, 0)                           \
+    __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */        \
+    asm volatile("s_barrier" ::: "memory");                              \
+    __builtin_amdgcn_sched_barrier(0);                                   \
+    MOE_MXL_STEP(3, TS, OTHER, 0, true, CUR, NEXT2)                      \
+  }
+  // scale registers of stages 2 pr and 2 pr + 1 into s[0] and s[1]
+  auto next_scales = [&](int pr) {
+    if (pr & 1) {
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) sa[j].s[0] = sa[j].s[2], sa[j].s[1] = sa[j].s[3];
+#pragma unroll
+      for (int i = 0; i < T::FN; ++i) sw[i].s[0] = sw[i].s[2], sw[i].s[1] = sw[i].s[3];
+    } else {
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) sa[j] = spread_scales(raw_a[j]);
+#pragma unroll
+      for (int i = 0; i < T::FN; ++i) sw[i] = spread_scales(raw_w[i]);
+      if (2 * pr + 4 < KS) load_scales(pr / 2 + 1);
+    }
+  };
+
+#pragma unroll
+  for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf0, 0, q);
+  load_scales(0);
+#pragma unroll
+  for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf1, 1, q);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i) read_w(buf0, 0, wv[0][i], i);
+#pragma unroll
+  for (int j = 0; j < T::FM; ++j) read_a(buf0, 0, av[0][j], j);
+  for (int pr = 0; pr < KS / 2; ++pr) {
+    next_scales(pr);
+    MOE_MXL_STAGE(buf0, buf1, 2 * pr + 2, 0)
+    MOE_MXL_STAGE(buf1, buf0, 2 * pr + 3, 1)
+  }
+  if (KS & 1) {
+    next_scales(KS / 2);
+    MOE_MXL_STAGE(buf0, buf1, KS + 1, 0)
+  }
+#undef MOE_MXL_STAGE
+#undef MOE_MXL_STEP
+#undef MOE_MXL_MFMA
+
+  // Epilogue: each wave turns its block around through its own part of the
+  // (now idle) buffers, 32 rows x EF column fragments at a time, in fp32.
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("s_barrier" ::: "memory");
+  float* strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
+  constexpr int CPR = T::EF * 8;       // 4-column pieces per strip row
+  constexpr int RPP = 64 / CPR;        // rows per pass
+#pragma unroll
+  for (int j = 0; j < T::FM; ++j)
+#pragma unroll
+    for (int i0 = 0; i0 < T::FN; i0 += T::EF) {
+#pragma unroll
+      for (int i = 0; i < T::EF; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& c = acc[i0 + i][j];
+          *(f32x4*)(strip + lr * T::EROW + i * 32 + 8 * q + 4 * lq) =
+              f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 1
+      for (int pass = 0; pass < 32 / RPP; ++pass) {
+        const int r = pass * RPP + lane / CPR, c = 4 * (lane % CPR);
+        const int m = m0 + wm * (BM / 2) + j * 32 + r;
+        const f32x4 v = *(const f32x4*)(strip + r * T::EROW + c);
+        if (m < p.M) store4(p, m, n0 + wn * (BN / 2) + i0 * 32 + c, v);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (decode): the weights stream from HBM once. A workgroup owns 16
+// weight rows (output columns) and its S waves split K between them, each with
+// the activations of up to 16 MT rows as the other operand of
+// v_mfma_scale_f32_16x16x128_f8f6f4, both straight from global memory into
+// operand registers; the partial sums meet in LDS in wave order. Operands of a
+// 128-K step, group q = lane >> 4: e2m1 K values 32q..32q+31; e4m3 16q..16q+15 and
+// 64+16q..64+16q+15; the lane gives the scale of block q.
+//
+// A wave works on batches of 4 steps, the loads of the next batch issued
+// before the current one is multiplied; a batch's 16 scale bytes of a row are
+// one load. Loads past the row's end, the wave's K range or the last row read nothing.
+template <int AF, int S, int MT>
+__global__ __launch_bounds__(64 * S) void k_skinny(const Params p) {
+  constexpr bool F8 = AF == mxf::MXFP8;
+  __shared__ f32x4 red[S][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int n0 = (int)(blockIdx.x % p.nt) * 16, m0 = (int)(blockIdx.x / p.nt) * (16 * MT);
+  const int nblk = p.K >> 5;
+  const int KT = (p.K + 127) >> 7;
+  const int lo = wave * KT / S, hi = (wave + 1) * KT / S;
+  const uint32_t w_row = (uint32_t)p.K / 2, a_row = F8 ? (uint32_t)p.K : (uint32_t)p.K / 2;
+  const int w_rows = min(16, p.N - n0), a_rows = min(16 * MT, p.M - m0);
+  const __amdgpu_buffer_rsrc_t rsW = rsrc(p.w + (size_t)n0 * w_row, (uint32_t)w_rows * w_row);
+  const __amdgpu_buffer_rsrc_t rsA = rsrc(p.a + (size_t)m0 * p.lda, (uint32_t)((a_rows - 1) * p.lda + a_row));
+  const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
+  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
+  const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
+  const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
+  const uint32_t w_so = (uint32_t)(min(l16, w_rows - 1) * nblk);
+  uint32_t a_so[MT], a_off[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = l16 + 16 * i;
+    a_so[i] = (uint32_t)(min(r, a_rows - 1) * (int)p.ld_as);
+    a_off[i] = r < a_rows ? (uint32_t)(r * (int)p.lda) + 16 * q : kNoLoad;
+  }
+  const uint32_t w_off = l16 < w_rows ? (uint32_t)l16 * w_row + 16 * q : kNoLoad;
+  constexpr int kNt = 2;  // weights are read once: non-temporal
+
+  struct Batch {
+    i32x4 w[4];
+    i32x4 a[MT][4][F8 ? 2 : 1];
+    u32x4 ws, as[MT];
+  };
+  auto load = [&](Batch& b, int t0) {
+    const int valid = min(nblk, 4 * hi) - 4 * t0;  // blocks of the wave's range from step t0 on
+    if (valid >= 16) {
+      b.ws = load_sc16(w_scb, w_so + 4 * t0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) b.as[i] = load_sc16(a_scb, a_so[i] + 4 * t0);
+    } else {
+      b.ws = load_sc_tail(w_scb, w_so + 4 * t0, w_tot, valid);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) b.as[i] = load_sc_tail(a_scb, a_so[i] + 4 * t0, a_tot, valid);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u;
+      const bool in = t < hi;
+      const uint32_t kw = 64u * t, ka = (F8 ? 128u : 64u) * t;
+      b.w[u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          rsW, in && kw + 16 * q < w_row ? w_off + kw : kNoLoad, 0, kNt));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < (F8 ? 2 : 1); ++h)
+          b.a[i][u][h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              rsA, in && ka + 64 * h + 16 * q < a_row ? a_off[i] + ka + 64 * h : kNoLoad, 0, 0));
+    }
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Batch& b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const i32x8 w8 = __builtin_shufflevector(b.w[u], b.w[u], 0, 1, 2, 3, -1, -1, -1, -1);
+      const int sw = (int)(b.ws[u] >> (8 * q));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        i32x8 a8;
+        if constexpr (F8) a8 = __builtin_shufflevector(b.a[i][u][0], b.a[i][u][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        else a8 = __builtin_shufflevector(b.a[i][u][0], b.a[i][u][0], 0, 1, 2, 3, -1, -1, -1, -1);
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, acc[i], 4, F8 ? 0 : 4, 0, sw, 0,
+                                                                  (int)(b.as[i][u] >> (8 * q)));
+      }
+    }
+  };
+  Batch b0, b1;
+  load(b0, lo);
+  for (int t = lo; t < hi; t += 8) {
+    load(b1, t + 4);
+    multiply(b0);
+    if (t + 4 >= hi) break;
+    load(b0, t + 8);
+    multiply(b1);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+#pragma unroll
+  for (int i0 = 0; i0 < MT; i0 += S) {
+    const int i = i0 + wave;
+    if (i >= MT) break;
+    f32x4 v = red[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < S; ++w) {
+      const f32x4 x = red[w][i][lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += x[j];
+    }
+    const int m = m0 + 16 * i + l16;
+    if (m < p.M) store4(p, m, n0 + 4 * q, v);
+  }
+}
+
+}  // namespace mxl
+}  // namespace moe

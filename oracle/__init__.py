@@ -7,3 +7,4 @@ HIP library never calls it and shares no code with it.
 from .moe_oracle import *  # noqa: F401,F403
 from . import moe_router  # noqa: F401,E402
 from .moe_router import route, route_deepseek_v3, route_renormalize  # noqa: F401,E402
+from . import layer_ops  # noqa: F401,E402

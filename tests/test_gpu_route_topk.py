@@ -1,0 +1,127 @@
+"""moe_route_topk on the GPU against the float64 oracle: ids exactly, weights
+within 6 * 2^-24 (the score's rounding to fp32 may fall the other way where two
+exponentials differ in their last bit, on both sides of the division; then the
+division's and the factor's own roundings)."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_expert_02_amd as moe
+import oracle
+from oracle import layer_ops as L
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda")
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+TOL = 6 * 2.0 ** -24
+
+
+def check(l, k, bias=None, **kw):
+    ids, w = moe.route_topk(l.to(DEV), k, bias=None if bias is None else torch.from_numpy(bias).to(DEV), **kw)
+    torch.cuda.synchronize()
+    rid, rw = L.route_topk(l.double().numpy(), k, bias=bias, **kw)
+    gi, gw = ids.cpu().numpy(), w.double().cpu().numpy()
+    assert np.array_equal(gi, rid), np.argwhere(gi != rid)[:5]
+    assert (np.abs(gw - rw) <= TOL * np.abs(rw) + 1e-38).all()
+    return gi, gw
+
+
+def logits(seed, T, E, dtype):
+    return (1.5 * torch.randn(T, E, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+@pytest.mark.parametrize("score,renorm,use_bias", itertools.product(["softmax", "sigmoid"], [True, False], [True, False]))
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (33, 64, 6), (17, 65, 4), (29, 128, 8), (70, 200, 17),
+                                   (45, 256, 32), (9, 257, 3), (6, 512, 8), (5, 1000, 31), (4, 1024, 32)])
+def test_shapes(T, E, k, score, renorm, use_bias):
+    print(f"[route_topk] T={T} E={E} k={k} {score} renorm={renorm} bias={use_bias}", flush=True)
+    b = 0.1 * np.random.default_rng(E).standard_normal(E).astype(np.float32) if use_bias else None
+    check(logits(T + E, T, E, TYPES[(T + E + k) % 3]), k, b, score=score, renormalize=renorm, routed_scaling_factor=2.5)
+
+
+@pytest.mark.parametrize("score,by", itertools.product(["softmax", "sigmoid"], ["max", "top2"]))
+@pytest.mark.parametrize("T,E,k,G,keep", [(40, 256, 8, 8, 4), (21, 160, 6, 8, 3), (10, 64, 2, 32, 1), (7, 64, 9, 2, 2),
+                                          (5, 1024, 16, 64, 5), (11, 320, 8, 5, 2), (8, 512, 8, 16, 1)])
+def test_groups(T, E, k, G, keep, score, by):
+    print(f"[route_topk] T={T} E={E} k={k} groups {G}/{keep} {score} {by}", flush=True)
+    b = 0.05 * np.random.default_rng(G).standard_normal(E).astype(np.float32)
+    for bias in (b, None):
+        check(logits(T * E, T, E, torch.float32), k, bias, score=score, n_group=G, topk_group=keep, group_score=by)
+
+
+def test_single_expert_groups():
+    check(logits(2, 9, 8, torch.float32), 3, None, n_group=8, topk_group=4, group_score="max")
+
+
+def test_ties_masks_and_nonfinite_logits():
+    l = torch.zeros(7, 40)
+    l[1, [3, 7, 30]] = 2.0
+    l[2] = float("nan")
+    l[3, 0], l[3, 5] = float("inf"), -float("inf")
+    l[4] = -float("inf")
+    l[5, :30] = torch.finfo(torch.float32).min
+    l[6, [4, 9]] = float("inf")
+    for score in ("softmax", "sigmoid"):
+        for kw in ({}, dict(n_group=4, topk_group=2, group_score="top2"), dict(n_group=4, topk_group=1, group_score="max")):
+            gi, gw = check(l, 4, None, score=score, **kw)
+            assert np.isfinite(gw).all()
+    gi, gw = check(l, 4)
+    assert gi[0].tolist() == [0, 1, 2, 3] and gi[1, :3].tolist() == [3, 7, 30]
+    np.testing.assert_allclose(gw[4], 0.25)
+    np.testing.assert_allclose(gw[6], [0.5, 0.5, 0, 0])
+    _, gw = check(l[4:5], 4, score="sigmoid")                   # every score 0: nothing to divide by
+    assert (gw == 0).all()
+
+
+def test_minus_infinity_bias_masks_experts():
+    b = np.zeros(64, np.float32)
+    b[::2] = -np.inf
+    gi, _ = check(logits(5, 30, 64, torch.bfloat16), 8, b, score="sigmoid")
+    assert (gi % 2 == 1).all()
+    gi, _ = check(logits(5, 30, 64, torch.bfloat16), 8, b, n_group=8, topk_group=2)
+    assert (gi % 2 == 1).all()
+    gi, _ = check(logits(5, 3, 64, torch.float32), 32, b)       # exactly the unmasked ones
+    assert (np.sort(gi, 1) == np.arange(1, 64, 2)).all()
+    b[:] = -np.inf
+    gi, _ = check(logits(5, 3, 64, torch.float32), 5, b)        # nothing left: the lowest indices
+    assert (gi == np.arange(5)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strided_logits(dtype):
+    wide = logits(8, 50, 150, dtype)
+    ids, w = moe.route_topk(wide.to(DEV)[:, 11:11 + 96], 7)
+    ids2, w2 = moe.route_topk(wide[:, 11:11 + 96].contiguous().to(DEV), 7)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
+def test_agrees_with_route():
+    l = logits(9, 300, 128, torch.float32)
+    a = moe.route_topk(l.to(DEV), 8)
+    b = moe.route(l.to(DEV), 8)
+    assert torch.equal(a[0], b[0])
+    assert (a[1] - b[1]).abs().max().item() <= 1e-5
+    bias = (0.1 * torch.randn(128, generator=torch.Generator().manual_seed(1))).to(DEV)
+    kw = dict(bias=bias, n_group=8, topk_group=4, routed_scaling_factor=2.5)
+    a = moe.route_topk(l.to(DEV), 8, "sigmoid", **kw)
+    b = moe.route(l.to(DEV), 8, "deepseek_v3", **kw)
+    assert torch.equal(a[0], b[0]) and (a[1] - b[1]).abs().max().item() <= 2.5e-5
+    rid, _ = oracle.route_renormalize(l.numpy(), 8)
+    assert np.array_equal(moe.route_topk(l.to(DEV), 8)[0].cpu().numpy(), rid)
+
+
+def test_refusals():
+    l = torch.zeros(4, 64, device=DEV)
+    for kw in (dict(k=0), dict(k=65), dict(k=33), dict(k=2, score="relu"), dict(k=2, group_score="mean"),
+               dict(k=2, bias=torch.zeros(63, device=DEV)), dict(k=2, bias=torch.zeros(64)),
+               dict(k=2, n_group=3, topk_group=1), dict(k=2, n_group=4, topk_group=0), dict(k=17, n_group=4, topk_group=1),
+               dict(k=2, ids=torch.zeros(4, 2, device=DEV)), dict(k=2, weights=torch.zeros(4, 3, device=DEV))):
+        with pytest.raises(moe.MoeError):
+            moe.route_topk(l, **kw)
+    with pytest.raises(moe.MoeError):
+        moe.route_topk(l.double(), 2)
+    with pytest.raises(moe.MoeError):
+        moe.route_topk(l.t(), 2)
+    assert moe.route_topk(l[:0], 2)[0].shape == (0, 2)
