@@ -106,13 +106,13 @@ int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
   return MOE_OK;
 }
 
-template <int AF, int BM, int BN>
+template <int AF, int BM, int BN, int BK>
 int launch_tile(moe::mxl::Params& q, hipStream_t s) {
   q.mt = (q.M + BM - 1) / BM;
   q.nt = (q.N + BN - 1) / BN;
   const int64_t n = (int64_t)q.mt * q.nt;
   if (n > 0x7ffffff0) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
   return launch_status();
 }
 
@@ -138,12 +138,13 @@ template <int AF>
 int launch_linear(moe::mxl::Params& q, hipStream_t s) {
   if (q.M <= 16) return launch_skinny_split<AF, 1>(q, s);
   if (q.M <= 32) return launch_skinny_split<AF, 2>(q, s);
-  constexpr int BM = AF == moe::mxf::MXFP8 ? 128 : 256;
+  constexpr bool F8 = AF == moe::mxf::MXFP8;
+  constexpr int BM = F8 ? 128 : 256;
   const int64_t big = (int64_t)((q.M + BM - 1) / BM) * ((q.N + 255) / 256);
   const int64_t mid = (int64_t)((q.M + 127) / 128) * ((q.N + 127) / 128);
-  if (big >= 192) return launch_tile<AF, BM, 256>(q, s);
-  if (mid >= 192) return launch_tile<AF, 128, 128>(q, s);
-  return launch_tile<AF, 64, 64>(q, s);
+  if (big >= 192) return launch_tile<AF, BM, 256, F8 ? 128 : 256>(q, s);
+  if (mid >= 384) return launch_tile<AF, 128, 128, F8 ? 128 : 256>(q, s);
+  return launch_tile<AF, 64, 64, 256>(q, s);
 }
 
 // ----------------------------------------------------------------- routing
@@ -275,7 +276,10 @@ int moe_mx_linear(const moe_mx_linear_problem* p, const void* a, const uint8_t* 
   q.bias = bias;
   q.add = add;
   q.out = out;
-  q.vec = q.ldo % 4 == 0 && aligned(out, 4 * size) && (!add || (q.ld_add % 4 == 0 && aligned(add, 4 * size)));
+  auto wide = [&](const void* t, int64_t ld) {
+    return aligned(t, 16) && ld * (int64_t)size % 16 == 0 && ld * (int64_t)size < (int64_t)1 << 22;
+  };
+  q.vec = q.N % 8 == 0 && wide(out, q.ldo) && aligned(bias, 16) && (!add || wide(add, q.ld_add));
   hipStream_t s = (hipStream_t)stream;
   return p->a_fmt == MOE_MX_FP8 ? launch_linear<moe::mxf::MXFP8>(q, s) : launch_linear<moe::mxf::MXFP4>(q, s);
 }

@@ -26,7 +26,8 @@ struct Params {
   int64_t lda, ld_as, ldo, ld_add;
   int32_t M, N, K;
   int32_t out_type;
-  int32_t vec;             // out and add rows take 4-element accesses at columns that are multiples of 4
+  int32_t vec;             // N is a multiple of 8; out, add and bias take 16-byte accesses at such columns, and
+                           // 256 rows of out or add fit a 31-bit byte offset
   float alpha;
   int32_t mt, nt;          // row and column tiles
 };
@@ -130,14 +131,89 @@ __device__ __forceinline__ void store4(const Params& p, int row, int col, f32x4 
   }
 }
 
+// A wave's FN x FM fragments (32 columns x 32 rows each) at row mw, column nw of
+// the output, by 16-byte accesses. A lane holds columns 8g + 4 (lane / 32) + c
+// (register 4g + c) of row lane % 32: one v_permlane32_swap of registers 8h + c
+// and 8h + 4 + c leaves each half of the wave with 8 consecutive columns, so an
+// access covers 32 bytes of each of 32 rows and no LDS is needed. The accesses
+// go through buffer resources over the block's rows: one 32-bit offset per lane
+// (64-bit addresses for every row made the compiler spill), and rows past M
+// or columns past N lie outside them, read 0 and are not written.
+template <int DT, int FN, int FM>
+__device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][FM], int mw, int nw, int lane) {
+  constexpr int FG = FN < 2 ? FN : 2;  // column fragments at a time
+  constexpr uint32_t SZ = elem_size(DT);
+  const int rows = min(32 * FM, p.M - mw);
+  if (rows <= 0) return;
+  const int col0 = nw + 8 * (lane >> 5);
+  const __amdgpu_buffer_rsrc_t rsO =
+      rsrc((uint8_t*)p.out + (size_t)mw * p.ldo * SZ, (uint32_t)(((rows - 1) * p.ldo + p.N) * SZ));
+  const __amdgpu_buffer_rsrc_t rsD =
+      rsrc((const uint8_t*)p.add + (size_t)mw * p.ld_add * SZ, p.add ? (uint32_t)(((rows - 1) * p.ld_add + p.N) * SZ) : 0u);
+  const __amdgpu_buffer_rsrc_t rsB = rsrc(p.bias, p.bias ? 4u * (uint32_t)p.N : 0u);
+  uint32_t o = ((uint32_t)(lane & 31) * (uint32_t)p.ldo + (uint32_t)col0) * SZ;
+  uint32_t d = ((uint32_t)(lane & 31) * (uint32_t)p.ld_add + (uint32_t)col0) * SZ;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+#pragma unroll
+    for (int i0 = 0; i0 < FN; i0 += FG) {
+      // results stay in AGPRs until they are wanted (moved to VGPRs as a whole they would spill)
+#pragma unroll
+      for (int i = 0; i < FG; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
+      u32x4 ad[2 * FG][SZ / 2], bi[2 * FG][2];
+#pragma unroll
+      for (int q = 0; q < 2 * FG; ++q) {
+        const int c = 32 * i0 + 16 * q;  // past col0
+        const bool in = col0 + c < p.N;
+#pragma unroll
+        for (uint32_t h = 0; h < SZ / 2; ++h)
+          ad[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsD, in ? d + c * SZ + 16 * h : kNoLoad, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          bi[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsB, 4 * (uint32_t)(col0 + c) + 16 * h, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < 2 * FG; ++q) {
+        const f32x16& a = acc[i0 + q / 2][j];
+        const int h = q & 1, c = 32 * i0 + 16 * q;
+        float v[8], x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[8 * h + k]),
+                                                          __float_as_uint(a[8 * h + 4 + k]), false, false);
+          v[k] = __uint_as_float(t[0]);
+          v[4 + k] = __uint_as_float(t[1]);
+        }
+        load8<DT>(ad[q], 0, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * p.alpha + __uint_as_float(bi[q][k / 4][k % 4]) + x[k];
+        u32x4 r[SZ / 2];
+        store8<DT>(r, 0, v);
+        const bool in = col0 + c < p.N;
+#pragma unroll
+        for (uint32_t w = 0; w < SZ / 2; ++w)
+          __builtin_amdgcn_raw_buffer_store_b128(r[w], rsO, in ? o + c * SZ + 16 * w : kNoLoad, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // the registers hold no more than this much at once
+    }
+    o += 32 * (uint32_t)p.ldo * SZ;
+    d += 32 * (uint32_t)p.ld_add * SZ;
+  }
+}
+
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------
 // Tile kernel. A workgroup of 4 waves computes BM rows x BN columns; a stage is
-// 256 K values: BM rows of activation codes (128 or 256 bytes) and BN rows of
-// weight codes (128 bytes), loaded HBM -> LDS with buffer_load ... lds into one
-// of two buffers while the other is multiplied. Rows past M or N and K past
-// the row's end read zeros through the buffer's range check. 16-byte chunk c of
-// row r sits at slot c ^ ((r >> 1) & 7) (128-byte rows) or c ^ (r & 15)
-// (256-byte rows), so the 16 rows of one ds_read_b128 pass fall on distinct banks.
+// BK values of K: BM rows of activation codes and BN rows of weight codes, loaded
+// HBM -> LDS with buffer_load ... lds into one of two buffers while the other is
+// multiplied. Rows past M or N and K past the row's end read zeros through the
+// buffer's range check. The 16-byte chunks of a row are swizzled by its index so
+// that the 16 rows of one ds_read_b128 pass fall on distinct banks.
 //
 // The weights are the MFMA's A operand (row lane & 31), the activations its B
 // operand (column lane & 31), so a lane's results are 4 consecutive columns of
@@ -145,45 +221,41 @@ __device__ __forceinline__ void store4(const Params& p, int row, int col, f32x4 
 // 32q..32q+31 (16 bytes); e4m3 16q..16q+15 and 32+16q..32+16q+15; the lane
 // gives the scale of block q.
 //
-// Scales go straight to registers, 1024 K values (four stages) at a time: lane
-// (r, q) loads bytes 16q..16q+15 of its row's 32, splits them into even and odd
-// blocks, and one v_permlane32_swap per pair hands each half the blocks of its
-// own parity: one register per stage whose byte s is the scale of step s.
-template <int AF, int BM, int BN>
+// Scales: a thread loads 16 scale bytes of one row (512 K values) at a time,
+// splits them into even and odd blocks and puts them into LDS as four words
+// (even and odd blocks of the first 256 K values, then of the second); a lane
+// reads one word per fragment and 256 K values, whose byte s is the scale of its
+// block in step s.
+template <int AF, int BM, int BN, int BK>
 struct Tile {
-  static constexpr int AB = AF == mxf::MXFP8 ? 256 : 128;  // bytes of an activation row per stage
-  static constexpr int A_BYTES = BM * AB, W_BYTES = BN * 128;
+  static constexpr int AB = AF == mxf::MXFP8 ? BK : BK / 2, WB = BK / 2;  // bytes of a row per stage
+  static constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB;
   static constexpr int STAGE = A_BYTES + W_BYTES;
+  static constexpr int NS = BK / 64;                       // steps per stage
   static constexpr int FM = BM / 64, FN = BN / 64;         // 32 x 32 results of a wave
   static constexpr int AL = A_BYTES / 4096, WL = W_BYTES / 4096;  // loads per wave and stage
+  static constexpr int ROWS = BM + BN;                     // scale rows: weights, then activations
+  static constexpr int SR = (ROWS + 255) / 256;            // per thread
   static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
   static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
+  static constexpr int WGS = 2 * STAGE + 32 * ROWS <= 80 * 1024 ? 2 : 1;  // workgroups per compute unit (160 KB of LDS)
   static_assert(2 * 32 * EROW * 4 <= STAGE, "epilogue staging: two waves per buffer");
+  static_assert(BK == 128 || BK == 256, "a scale word holds 256 K values");
+  static_assert(BN % 64 == 0 && BM % 64 == 0, "whole waves load scale rows of one operand");
 };
 
-struct ScaleRegs {
-  uint32_t s[4];  // one per stage of the group
-};
-
-// bytes 16q .. 16q + 15 of the 32 block scales -> per-stage registers
-__device__ __forceinline__ ScaleRegs spread_scales(u32x4 v) {
-  const uint32_t e0 = __builtin_amdgcn_perm(v[1], v[0], 0x06040200u), o0 = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
-  const uint32_t e1 = __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), o1 = __builtin_amdgcn_perm(v[3], v[2], 0x07050301u);
-  const auto x = __builtin_amdgcn_permlane32_swap(e0, o0, false, false);
-  const auto y = __builtin_amdgcn_permlane32_swap(e1, o1, false, false);
-  ScaleRegs r;
-  r.s[0] = x[0];
-  r.s[2] = x[1];
-  r.s[1] = y[0];
-  r.s[3] = y[1];
-  return r;
+// slot of 16-byte chunk c of row r in a row of RB bytes
+template <int RB>
+__device__ __forceinline__ int slot_of(int c, int r) {
+  return RB == 256 ? c ^ (r & 15) : RB == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int AF, int BM, int BN>
-__global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
-  using T = Tile<AF, BM, BN>;
+template <int AF, int BM, int BN, int BK>
+__global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const Params p) {
+  using T = Tile<AF, BM, BN, BK>;
   __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][T::ROWS * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -200,7 +272,7 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
   const int in = item - g * 4 * p.nt;
   const int m0 = (4 * g + in % gm) * BM, n0 = in / gm * BN;
 
-  const int KS = (p.K + 255) >> 8;       // stages
+  const int KS = (p.K + BK - 1) / BK;    // stages
   const int nblk = p.K >> 5;
   const uint32_t a_row = AF == mxf::MXFP8 ? (uint32_t)p.K : (uint32_t)p.K / 2, w_row = (uint32_t)p.K / 2;
   const int a_rows = min(BM, p.M - m0), w_rows = min(BN, p.N - n0);
@@ -209,20 +281,20 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
 
   // load assignment: wave w fills the w-th quarter of each operand
   uint32_t a_off[T::AL], w_off[T::WL];
-  uint32_t a_ch[T::AL], w_chunk[T::WL];  // byte of the row within a stage
+  uint32_t a_ch[T::AL], w_ch[T::WL];     // byte of the row within a stage
 #pragma unroll
   for (int i = 0; i < T::AL; ++i) {
     const int at = wave * (T::A_BYTES / 4) + i * 1024 + lane * 16;
-    const int r = at / T::AB, slot = (at % T::AB) / 16;
-    a_ch[i] = 16u * (AF == mxf::MXFP8 ? slot ^ (r & 15) : slot ^ ((r >> 1) & 7));
+    const int r = at / T::AB;
+    a_ch[i] = 16u * slot_of<T::AB>((at % T::AB) / 16, r);
     a_off[i] = r < a_rows ? (uint32_t)(r * p.lda) + a_ch[i] : kNoLoad;
   }
 #pragma unroll
   for (int i = 0; i < T::WL; ++i) {
     const int at = wave * (T::W_BYTES / 4) + i * 1024 + lane * 16;
-    const int r = at / 128, slot = (at % 128) / 16;
-    w_chunk[i] = 16u * (slot ^ ((r >> 1) & 7));
-    w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_chunk[i] : kNoLoad;
+    const int r = at / T::WB;
+    w_ch[i] = 16u * slot_of<T::WB>((at % T::WB) / 16, r);
+    w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_ch[i] : kNoLoad;
   }
   // Load instruction q of stage s into buf: first the activations', then the
   // weights'. A piece past the row's end, or of a stage past the last, reads nothing.
@@ -234,26 +306,53 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
           rsA, (__attribute__((address_space(3))) void*)(buf + wave * (T::A_BYTES / 4) + q * 1024), 16, off, 0, 0, 0);
     } else {
       const int i = q - T::AL;
-      const uint32_t k = (uint32_t)s * 128u;
-      const uint32_t off = k + w_chunk[i] < w_row ? w_off[i] + k : kNoLoad;
+      const uint32_t k = (uint32_t)s * T::WB;
+      const uint32_t off = k + w_ch[i] < w_row ? w_off[i] + k : kNoLoad;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsW, (__attribute__((address_space(3))) void*)(buf + T::A_BYTES + wave * (T::W_BYTES / 4) + i * 1024), 16,
           off, 0, 0, 0);
     }
   };
 
-  // scale rows of this lane (rows past the end repeat the last: never stored)
+  // Scale rows of this thread: row tid + 256 i of [BN weight rows, BM activation
+  // rows]; rows past the end repeat the last (their results are never stored).
   const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
   const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
   const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
   const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
-  uint32_t a_so[T::FM], w_so[T::FN];
+  u32x4 raw[T::SR];
+  auto fetch_scales = [&](int grp) {
 #pragma unroll
-  for (int j = 0; j < T::FM; ++j)
-    a_so[j] = (uint32_t)(min(wm * (BM / 2) + j * 32 + lr, a_rows - 1) * (int)p.ld_as + 16 * lq);
+    for (int i = 0; i < T::SR; ++i) {
+      const int w = wave * 64 + 256 * i;  // uniform: the wave's first row
+      if (w >= T::ROWS) break;
+      const bool is_w = w < BN;
+      const uint8_t* base = is_w ? w_scb : a_scb;
+      const int r = is_w ? min(w + lane, w_rows - 1) : min(w - BN + lane, a_rows - 1);
+      const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as)) + 16u * grp;
+      if (16 * grp + 16 <= nblk) raw[i] = load_sc16(base, off);
+      else raw[i] = load_sc_tail(base, off, is_w ? w_tot : a_tot, nblk - 16 * grp);
+    }
+  };
+  auto publish_scales = [&](int grp) {
 #pragma unroll
-  for (int i = 0; i < T::FN; ++i)
-    w_so[i] = (uint32_t)(min(wn * (BN / 2) + i * 32 + lr, w_rows - 1) * nblk + 16 * lq);
+    for (int i = 0; i < T::SR; ++i) {
+      const int w = wave * 64 + 256 * i;
+      if (w >= T::ROWS) break;
+      const u32x4 v = raw[i];
+      *(u32x4*)(scales[grp & 1] + (w + lane) * 16) =
+          u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x06040200u), __builtin_amdgcn_perm(v[1], v[0], 0x07050301u),
+                __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), __builtin_amdgcn_perm(v[3], v[2], 0x07050301u)};
+    }
+  };
+  uint32_t sa[2][T::FM], sw[2][T::FN];  // scale words of a 256-K unit, and of the next
+  auto read_scales = [&](int unit, uint32_t (&da)[T::FM], uint32_t (&dw)[T::FN]) {
+    const uint8_t* src = scales[(unit >> 1) & 1] + (unit & 1) * 8 + 4 * lq + lr * 16;
+#pragma unroll
+    for (int i = 0; i < T::FN; ++i) dw[i] = *(const uint32_t*)(src + (wn * (BN / 2) + i * 32) * 16);
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) da[j] = *(const uint32_t*)(src + (BN + wm * (BM / 2) + j * 32) * 16);
+  };
 
   f32x16 acc[T::FN][T::FM];
 #pragma unroll
@@ -264,36 +363,14 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   // LDS byte offsets of this lane's operands, per step
-  uint32_t a_rd[4][2], w_rd[4];
+  uint32_t a_rd[T::NS][2], w_rd[T::NS];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int sw = (lr >> 1) & 7;
-    w_rd[s] = (uint32_t)(T::A_BYTES + (wn * (BN / 2) + lr) * 128 + 16 * ((2 * s + lq) ^ sw));
-    if (AF == mxf::MXFP8) {
-      a_rd[s][0] = (uint32_t)((wm * (BM / 2) + lr) * 256 + 16 * ((4 * s + lq) ^ (lr & 15)));
-      a_rd[s][1] = (uint32_t)((wm * (BM / 2) + lr) * 256 + 16 * ((4 * s + 2 + lq) ^ (lr & 15)));
-    } else {
-      a_rd[s][0] = (uint32_t)((wm * (BM / 2) + lr) * 128 + 16 * ((2 * s + lq) ^ sw));
-      a_rd[s][1] = 0;
-    }
+  for (int s = 0; s < T::NS; ++s) {
+    w_rd[s] = (uint32_t)(T::A_BYTES + (wn * (BN / 2) + lr) * T::WB + 16 * slot_of<T::WB>(2 * s + lq, lr));
+    const int c = AF == mxf::MXFP8 ? 4 * s + lq : 2 * s + lq;
+    a_rd[s][0] = (uint32_t)((wm * (BM / 2) + lr) * T::AB + 16 * slot_of<T::AB>(c, lr));
+    a_rd[s][1] = (uint32_t)((wm * (BM / 2) + lr) * T::AB + 16 * slot_of<T::AB>(c + 2, lr));
   }
-
-  u32x4 raw_a[T::FM] = {}, raw_w[T::FN] = {};
-  ScaleRegs sa[T::FM], sw[T::FN];
-  auto load_scales = [&](int grp) {
-    if (32 * grp + 32 <= nblk) {
-#pragma unroll
-      for (int j = 0; j < T::FM; ++j) raw_a[j] = load_sc16(a_scb, a_so[j] + 32 * grp);
-#pragma unroll
-      for (int i = 0; i < T::FN; ++i) raw_w[i] = load_sc16(w_scb, w_so[i] + 32 * grp);
-    } else {
-      const int valid = min(nblk - 32 * grp - 16 * lq, 16);
-#pragma unroll
-      for (int j = 0; j < T::FM; ++j) raw_a[j] = load_sc_tail(a_scb, a_so[j] + 32 * grp, a_tot, valid);
-#pragma unroll
-      for (int i = 0; i < T::FN; ++i) raw_w[i] = load_sc_tail(w_scb, w_so[i] + 32 * grp, w_tot, valid);
-    }
-  };
 
   // Operands of one step, two sets: while one is multiplied the other loads.
   i32x8 av[2][T::FM];
@@ -307,22 +384,32 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
       d = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, -1, -1, -1, -1);
     }
   };
-  auto read_w = [&](const uint8_t* buf, int st, i32x4& d, int i) { d = *(const i32x4*)(buf + w_rd[st] + i * 4096); };
+  auto read_w = [&](const uint8_t* buf, int st, i32x4& d, int i) {
+    d = *(const i32x4*)(buf + w_rd[st] + i * 32 * T::WB);
+  };
+  // keeps the MFMAs above a branch above it (nothing below needs them at once,
+  // so they would be moved down to their next use)
+  auto pin = [&]() {
+#pragma unroll
+    for (int i = 0; i < T::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
 
-  // Step S of a stage, operand set S & 1, one row of MFMAs at a time with the
-  // reads of the next step's operands (RD: their buffer, RS: their step) and,
-  // in step 3, the loads of a later stage between them; the scheduling barriers keep
-  // that order, so the matrix pipe always has work behind the reads.
-#define MOE_MXL_MFMA(S, TS, i)                                                                              \
+  // Step S of a stage, operand set S & 1, scale byte SB of set SS, one row of MFMAs at a
+  // time with the reads of the next step's operands (RD: their buffer, RS: their
+  // step) and, in the last step, the loads of a later stage between them; the
+  // scheduling barriers keep that order, so the matrix pipe always has work behind the reads.
+#define MOE_MXL_MFMA(S, SB, SS, i)                                                                          \
   {                                                                                                         \
     const i32x8 w8 = __builtin_shufflevector(wv[(S) & 1][i], wv[(S) & 1][i], 0, 1, 2, 3, -1, -1, -1, -1);   \
     _Pragma("unroll") for (int j = 0; j < T::FM; ++j)                                                       \
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                          \
-          w8, av[(S) & 1][j], acc[i][j], 4, AF == mxf::MXFP8 ? 0 : 4, S, (int)sw[i].s[TS], S, (int)sa[j].s[TS]); \
+          w8, av[(S) & 1][j], acc[i][j], 4, AF == mxf::MXFP8 ? 0 : 4, SB, (int)sw[SS][i], SB, (int)sa[SS][j]); \
   }
-#define MOE_MXL_STEP(S, TS, RD, RS, LOAD, LBUF, LST)                                         \
+#define MOE_MXL_STEP(S, SB, SS, RD, RS, LOAD, LBUF, LST)                                     \
   _Pragma("unroll") for (int i = 0; i < T::FN; ++i) {                                        \
-    MOE_MXL_MFMA(S, TS, i)                                                                   \
+    MOE_MXL_MFMA(S, SB, SS, i)                                                               \
     read_w(RD, RS, wv[((S) + 1) & 1][i], i);                                                 \
     _Pragma("unroll") for (int j = i; j < T::FM; j += T::FN) read_a(RD, RS, av[((S) + 1) & 1][j], j); \
     if (LOAD) {                                                                              \
@@ -330,63 +417,81 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
     }                                                                                        \
     __builtin_amdgcn_sched_barrier(0);                                                       \
   }
-  // A stage: steps 0-2 read on in its own buffer. Before step 3 its last reads
-  // are in; once every wave is there (and the next stage has landed), step 3 reads
-  // the first operands from the other buffer and loads stage NEXT2 into this one.
-#define MOE_MXL_STAGE(CUR, OTHER, NEXT2, TS)                             \
+  // A stage: its steps but the last read on in its own buffer. Before the last,
+  // its reads are in; once every wave is there (and the next stage has landed), the
+  // last step reads the first operands from the other buffer and loads stage NEXT2
+  // into this one. RSC: the unit whose scale words it reads too, or -1.
+#define MOE_MXL_STAGE(CUR, OTHER, NEXT2, SB0, SS, RSC, RSS)              \
   {                                                                      \
-    MOE_MXL_STEP(0, TS, CUR, 1, false, CUR, 0)                           \
-    MOE_MXL_STEP(1, TS, CUR, 2, false, CUR, 0)                           \
-    MOE_MXL_STEP(2, TS, CUR, 3, false, CUR, 0)                           \
+    MOE_MXL_STEP(0, SB0, SS, CUR, 1, false, CUR, 0)                      \
+    if constexpr (T::NS == 4) {                                          \
+      MOE_MXL_STEP(1, SB0 + 1, SS, CUR, 2, false, CUR, 0)                \
+      MOE_MXL_STEP(2, SB0 + 2, SS, CUR, 3, false, CUR, 0)                \
+    }                                                                    \
     __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */        \
     asm volatile("s_barrier" ::: "memory");                              \
     __builtin_amdgcn_sched_barrier(0);                                   \
-    MOE_MXL_STEP(3, TS, OTHER, 0, true, CUR, NEXT2)                      \
+    if ((RSC) >= 0) read_scales(RSC, sa[RSS], sw[RSS]);                  \
+    MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, true, CUR, NEXT2)     \
   }
-  // scale registers of stages 2 pr and 2 pr + 1 into s[0] and s[1]
-  auto next_scales = [&](int pr) {
-    if (pr & 1) {
-#pragma unroll
-      for (int j = 0; j < T::FM; ++j) sa[j].s[0] = sa[j].s[2], sa[j].s[1] = sa[j].s[3];
-#pragma unroll
-      for (int i = 0; i < T::FN; ++i) sw[i].s[0] = sw[i].s[2], sw[i].s[1] = sw[i].s[3];
-    } else {
-#pragma unroll
-      for (int j = 0; j < T::FM; ++j) sa[j] = spread_scales(raw_a[j]);
-#pragma unroll
-      for (int i = 0; i < T::FN; ++i) sw[i] = spread_scales(raw_w[i]);
-      if (2 * pr + 4 < KS) load_scales(pr / 2 + 1);
-    }
-  };
 
+  fetch_scales(0);
 #pragma unroll
   for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf0, 0, q);
-  load_scales(0);
 #pragma unroll
   for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf1, 1, q);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  publish_scales(0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   asm volatile("s_barrier" ::: "memory");
+  read_scales(0, sa[0], sw[0]);
 #pragma unroll
   for (int i = 0; i < T::FN; ++i) read_w(buf0, 0, wv[0][i], i);
 #pragma unroll
   for (int j = 0; j < T::FM; ++j) read_a(buf0, 0, av[0][j], j);
-  for (int pr = 0; pr < KS / 2; ++pr) {
-    next_scales(pr);
-    MOE_MXL_STAGE(buf0, buf1, 2 * pr + 2, 0)
-    MOE_MXL_STAGE(buf1, buf0, 2 * pr + 3, 1)
-  }
-  if (KS & 1) {
-    next_scales(KS / 2);
-    MOE_MXL_STAGE(buf0, buf1, KS + 1, 0)
+  if constexpr (BK == 256) {
+    // two stages = one scale group per turn
+    for (int t = 0; t < KS / 2; ++t) {
+      if (32 * (t + 1) < 2 * nblk) fetch_scales(t + 1);
+      MOE_MXL_STAGE(buf0, buf1, 2 * t + 2, 0, 0, 2 * t + 1, 1)
+      pin();
+      publish_scales(t + 1);
+      MOE_MXL_STAGE(buf1, buf0, 2 * t + 3, 0, 1, 2 * t + 2, 0)
+    }
+    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS + 1, 0, 0, -1, 0)
+  } else {
+    // two stages = one scale unit per turn, two turns per group; the last step
+    // of a turn reads the next unit's words into the other set
+    for (int t = 0; t < KS / 2; ++t) {
+      if (!(t & 1)) fetch_scales(t / 2 + 1);
+      MOE_MXL_STAGE(buf0, buf1, 2 * t + 2, 0, 0, -1, 0)
+      pin();
+      if (t & 1) publish_scales(t / 2 + 1);
+      MOE_MXL_STAGE(buf1, buf0, 2 * t + 3, 2, 0, t + 1, 1)
+#pragma unroll
+      for (int i = 0; i < T::FN; ++i) sw[0][i] = sw[1][i];
+#pragma unroll
+      for (int j = 0; j < T::FM; ++j) sa[0][j] = sa[1][j];
+    }
+    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS + 1, 0, 0, -1, 0)
   }
 #undef MOE_MXL_STAGE
 #undef MOE_MXL_STEP
 #undef MOE_MXL_MFMA
 
-  // Epilogue: each wave turns its block around through its own part of the
-  // (now idle) buffers, 32 rows x EF column fragments at a time, in fp32.
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  // The last loads (of stages past the end) have landed and every wave has read its operands.
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   asm volatile("s_barrier" ::: "memory");
+  const int mw = m0 + wm * (BM / 2), nw = n0 + wn * (BN / 2);
+  pin();
+  if (p.vec) {
+    if (p.out_type == T_BF16) store_block<T_BF16, T::FN, T::FM>(p, acc, mw, nw, lane);
+    else if (p.out_type == T_FP16) store_block<T_FP16, T::FN, T::FM>(p, acc, mw, nw, lane);
+    else store_block<T_FP32, T::FN, T::FM>(p, acc, mw, nw, lane);
+    return;
+  }
+  // Rows that take no 16-byte accesses: each wave turns its block around
+  // through its own part of the (now idle) buffers, 32 rows x EF column
+  // fragments at a time, and stores value by value.
   float* strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
   constexpr int CPR = T::EF * 8;       // 4-column pieces per strip row
   constexpr int RPP = 64 / CPR;        // rows per pass
@@ -395,6 +500,8 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
 #pragma unroll
     for (int i0 = 0; i0 < T::FN; i0 += T::EF) {
 #pragma unroll
+      for (int i = 0; i < T::EF; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
+#pragma unroll
       for (int i = 0; i < T::EF; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -402,19 +509,14 @@ __global__ __launch_bounds__(256, 1) void k_tile(const Params p) {
           *(f32x4*)(strip + lr * T::EROW + i * 32 + 8 * q + 4 * lq) =
               f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
         }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_lds_sync();
 #pragma unroll 1
       for (int pass = 0; pass < 32 / RPP; ++pass) {
         const int r = pass * RPP + lane / CPR, c = 4 * (lane % CPR);
-        const int m = m0 + wm * (BM / 2) + j * 32 + r;
         const f32x4 v = *(const f32x4*)(strip + r * T::EROW + c);
-        if (m < p.M) store4(p, m, n0 + wn * (BN / 2) + i0 * 32 + c, v);
+        if (mw + j * 32 + r < p.M) store4(p, mw + j * 32 + r, nw + i0 * 32 + c, v);
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_lds_sync();
     }
 }
 
