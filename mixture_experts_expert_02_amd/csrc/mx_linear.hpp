@@ -138,8 +138,9 @@ __device__ __forceinline__ void store4(const Params& p, int row, int col, f32x4 
 // access covers 32 bytes of each of 32 rows and no LDS is needed. The accesses
 // go through buffer resources over the block's rows: one 32-bit offset per lane
 // (64-bit addresses for every row made the compiler spill), and rows past M
-// or columns past N lie outside them, read 0 and are not written.
-template <int DT, int FN, int FM>
+// or columns past N lie outside them, read 0 and are not written. EXTRA: there is
+// a bias or an addend (one that is missing reads 0 through an empty resource).
+template <int DT, bool EXTRA, int FN, int FM>
 __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][FM], int mw, int nw, int lane) {
   constexpr int FG = FN < 2 ? FN : 2;  // column fragments at a time
   constexpr uint32_t SZ = elem_size(DT);
@@ -161,16 +162,18 @@ __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][F
 #pragma unroll
       for (int i = 0; i < FG; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
       u32x4 ad[2 * FG][SZ / 2], bi[2 * FG][2];
+      if constexpr (EXTRA) {
 #pragma unroll
-      for (int q = 0; q < 2 * FG; ++q) {
-        const int c = 32 * i0 + 16 * q;  // past col0
-        const bool in = col0 + c < p.N;
+        for (int q = 0; q < 2 * FG; ++q) {
+          const int c = 32 * i0 + 16 * q;  // past col0
+          const bool in = col0 + c < p.N;
 #pragma unroll
-        for (uint32_t h = 0; h < SZ / 2; ++h)
-          ad[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsD, in ? d + c * SZ + 16 * h : kNoLoad, 0, 0);
+          for (uint32_t h = 0; h < SZ / 2; ++h)
+            ad[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsD, in ? d + c * SZ + 16 * h : kNoLoad, 0, 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          bi[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsB, 4 * (uint32_t)(col0 + c) + 16 * h, 0, 0);
+          for (int h = 0; h < 2; ++h)
+            bi[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsB, 4 * (uint32_t)(col0 + c) + 16 * h, 0, 0);
+        }
       }
 #pragma unroll
       for (int q = 0; q < 2 * FG; ++q) {
@@ -184,9 +187,12 @@ __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][F
           v[k] = __uint_as_float(t[0]);
           v[4 + k] = __uint_as_float(t[1]);
         }
-        load8<DT>(ad[q], 0, x);
+        if constexpr (EXTRA) load8<DT>(ad[q], 0, x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * p.alpha + __uint_as_float(bi[q][k / 4][k % 4]) + x[k];
+        for (int k = 0; k < 8; ++k) {
+          v[k] *= p.alpha;
+          if constexpr (EXTRA) v[k] = v[k] + __uint_as_float(bi[q][k / 4][k % 4]) + x[k];
+        }
         u32x4 r[SZ / 2];
         store8<DT>(r, 0, v);
         const bool in = col0 + c < p.N;
@@ -297,21 +303,32 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_ch[i] : kNoLoad;
   }
   // Load instruction q of stage s into buf: first the activations', then the
-  // weights'. A piece past the row's end, or of a stage past the last, reads nothing.
+  // weights'. The stage's place in K goes into the scalar offset, which the range
+  // check does not cover: mask_loads moves the lanes that would pass the row's
+  // end in the last stage, and all of them after it, out of range.
+  // (Its arguments are plain variables: with array elements or template constants
+  // in the builtin's argument list the host pass drops the kernel's stub.)
   auto load_piece = [&](uint8_t* buf, int s, int q) {
     if (q < T::AL) {
-      const uint32_t k = (uint32_t)s * T::AB;
-      const uint32_t off = k + a_ch[q] < a_row ? a_off[q] + k : kNoLoad;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsA, (__attribute__((address_space(3))) void*)(buf + wave * (T::A_BYTES / 4) + q * 1024), 16, off, 0, 0, 0);
+      uint8_t* dst = buf + wave * (T::A_BYTES / 4) + q * 1024;
+      const uint32_t off = a_off[q];
+      const int so = s * T::AB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (__attribute__((address_space(3))) void*)dst, 16, off, so, 0, 0);
     } else {
-      const int i = q - T::AL;
-      const uint32_t k = (uint32_t)s * T::WB;
-      const uint32_t off = k + w_ch[i] < w_row ? w_off[i] + k : kNoLoad;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsW, (__attribute__((address_space(3))) void*)(buf + T::A_BYTES + wave * (T::W_BYTES / 4) + i * 1024), 16,
-          off, 0, 0, 0);
+      uint8_t* dst = buf + T::A_BYTES + wave * (T::W_BYTES / 4) + (q - T::AL) * 1024;
+      const uint32_t off = w_off[q - T::AL];
+      const int so = s * T::WB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsW, (__attribute__((address_space(3))) void*)dst, 16, off, so, 0, 0);
     }
+  };
+  auto mask_loads = [&](int s) {  // before the first load of stage s
+    if (s < KS - 1) return;
+#pragma unroll
+    for (int i = 0; i < T::AL; ++i)
+      if ((uint32_t)s * T::AB + a_ch[i] >= a_row) a_off[i] = kNoLoad;
+#pragma unroll
+    for (int i = 0; i < T::WL; ++i)
+      if ((uint32_t)s * T::WB + w_ch[i] >= w_row) w_off[i] = kNoLoad;
   };
 
   // Scale rows of this thread: row tid + 256 i of [BN weight rows, BM activation
@@ -387,6 +404,24 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
   auto read_w = [&](const uint8_t* buf, int st, i32x4& d, int i) {
     d = *(const i32x4*)(buf + w_rd[st] + i * 32 * T::WB);
   };
+  // Reads of the next step's operands beside row i of MFMAs. With registers to
+  // spare they come in the order they are wanted; else each weight fragment
+  // takes its predecessor's registers once that is used up.
+  auto read_row = [&](const uint8_t* buf, int st, i32x4 (&dw)[T::FN], i32x8 (&da)[T::FM], int i) {
+    if constexpr (T::WGS == 2) {
+      read_w(buf, st, dw[i], i);
+#pragma unroll
+      for (int j = i; j < T::FM; j += T::FN) read_a(buf, st, da[j], j);
+    } else {
+      constexpr int N = T::FN + T::FM, PER = T::FN > 1 ? (N + T::FN - 2) / (T::FN - 1) : N;
+#pragma unroll
+      for (int x = i * PER; x < (i + 1) * PER && x < N; ++x) {
+        if (x == 0) read_w(buf, st, dw[0], 0);
+        else if (x <= T::FM) read_a(buf, st, da[x - 1], x - 1);
+        else read_w(buf, st, dw[x - T::FM], x - T::FM);
+      }
+    }
+  };
   // keeps the MFMAs above a branch above it (nothing below needs them at once,
   // so they would be moved down to their next use)
   auto pin = [&]() {
@@ -407,39 +442,43 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                          \
           w8, av[(S) & 1][j], acc[i][j], 4, AF == mxf::MXFP8 ? 0 : 4, SB, (int)sw[SS][i], SB, (int)sa[SS][j]); \
   }
-#define MOE_MXL_STEP(S, SB, SS, RD, RS, LOAD, LBUF, LST)                                     \
+#define MOE_MXL_STEP(S, SB, SS, RD, RS, L0, L1, LBUF, LST)                                   \
   _Pragma("unroll") for (int i = 0; i < T::FN; ++i) {                                        \
     MOE_MXL_MFMA(S, SB, SS, i)                                                               \
-    read_w(RD, RS, wv[((S) + 1) & 1][i], i);                                                 \
-    _Pragma("unroll") for (int j = i; j < T::FM; j += T::FN) read_a(RD, RS, av[((S) + 1) & 1][j], j); \
-    if (LOAD) {                                                                              \
-      _Pragma("unroll") for (int q = i; q < T::AL + T::WL; q += T::FN) load_piece(LBUF, LST, q); \
-    }                                                                                        \
+    read_row(RD, RS, wv[((S) + 1) & 1], av[((S) + 1) & 1], i);                               \
+    _Pragma("unroll") for (int q = (L0) + i; q < (L1); q += T::FN) load_piece(LBUF, LST, q); \
     __builtin_amdgcn_sched_barrier(0);                                                       \
   }
   // A stage: its steps but the last read on in its own buffer. Before the last,
   // its reads are in; once every wave is there (and the next stage has landed), the
-  // last step reads the first operands from the other buffer and loads stage NEXT2
-  // into this one. RSC: the unit whose scale words it reads too, or -1.
-#define MOE_MXL_STAGE(CUR, OTHER, NEXT2, SB0, SS, RSC, RSS)              \
+  // last step reads the first operands from the other buffer, and the loads of
+  // the stage after the next (NEXT + 1) into this one start: half of them there,
+  // half in the next stage's first step, two instructions beside a row of MFMAs.
+  // RSC: the unit whose scale words it reads too, or -1.
+  constexpr int LT = T::AL + T::WL, LH = (LT + 1) / 2;
+#define MOE_MXL_STAGE(CUR, OTHER, NEXT, SB0, SS, RSC, RSS)               \
   {                                                                      \
-    MOE_MXL_STEP(0, SB0, SS, CUR, 1, false, CUR, 0)                      \
+    MOE_MXL_STEP(0, SB0, SS, CUR, 1, LH, LT, OTHER, NEXT)                \
     if constexpr (T::NS == 4) {                                          \
-      MOE_MXL_STEP(1, SB0 + 1, SS, CUR, 2, false, CUR, 0)                \
-      MOE_MXL_STEP(2, SB0 + 2, SS, CUR, 3, false, CUR, 0)                \
+      MOE_MXL_STEP(1, SB0 + 1, SS, CUR, 2, 0, 0, CUR, 0)                 \
+      MOE_MXL_STEP(2, SB0 + 2, SS, CUR, 3, 0, 0, CUR, 0)                 \
     }                                                                    \
+    pin();                                                               \
+    mask_loads((NEXT) + 1);                                              \
     __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */        \
     asm volatile("s_barrier" ::: "memory");                              \
     __builtin_amdgcn_sched_barrier(0);                                   \
     if ((RSC) >= 0) read_scales(RSC, sa[RSS], sw[RSS]);                  \
-    MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, true, CUR, NEXT2)     \
+    MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, 0, LH, CUR, (NEXT) + 1) \
   }
 
+  mask_loads(0);
   fetch_scales(0);
 #pragma unroll
-  for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf0, 0, q);
+  for (int q = 0; q < LT; ++q) load_piece(buf0, 0, q);
+  mask_loads(1);
 #pragma unroll
-  for (int q = 0; q < T::AL + T::WL; ++q) load_piece(buf1, 1, q);
+  for (int q = 0; q < LH; ++q) load_piece(buf1, 1, q);
   publish_scales(0);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   asm volatile("s_barrier" ::: "memory");
@@ -452,27 +491,27 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     // two stages = one scale group per turn
     for (int t = 0; t < KS / 2; ++t) {
       if (32 * (t + 1) < 2 * nblk) fetch_scales(t + 1);
-      MOE_MXL_STAGE(buf0, buf1, 2 * t + 2, 0, 0, 2 * t + 1, 1)
+      MOE_MXL_STAGE(buf0, buf1, 2 * t + 1, 0, 0, 2 * t + 1, 1)
       pin();
       publish_scales(t + 1);
-      MOE_MXL_STAGE(buf1, buf0, 2 * t + 3, 0, 1, 2 * t + 2, 0)
+      MOE_MXL_STAGE(buf1, buf0, 2 * t + 2, 0, 1, 2 * t + 2, 0)
     }
-    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS + 1, 0, 0, -1, 0)
+    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS, 0, 0, -1, 0)
   } else {
     // two stages = one scale unit per turn, two turns per group; the last step
     // of a turn reads the next unit's words into the other set
     for (int t = 0; t < KS / 2; ++t) {
       if (!(t & 1)) fetch_scales(t / 2 + 1);
-      MOE_MXL_STAGE(buf0, buf1, 2 * t + 2, 0, 0, -1, 0)
+      MOE_MXL_STAGE(buf0, buf1, 2 * t + 1, 0, 0, -1, 0)
       pin();
       if (t & 1) publish_scales(t / 2 + 1);
-      MOE_MXL_STAGE(buf1, buf0, 2 * t + 3, 2, 0, t + 1, 1)
+      MOE_MXL_STAGE(buf1, buf0, 2 * t + 2, 2, 0, t + 1, 1)
 #pragma unroll
       for (int i = 0; i < T::FN; ++i) sw[0][i] = sw[1][i];
 #pragma unroll
       for (int j = 0; j < T::FM; ++j) sa[0][j] = sa[1][j];
     }
-    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS + 1, 0, 0, -1, 0)
+    if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS, 0, 0, -1, 0)
   }
 #undef MOE_MXL_STAGE
 #undef MOE_MXL_STEP
@@ -484,9 +523,16 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
   const int mw = m0 + wm * (BM / 2), nw = n0 + wn * (BN / 2);
   pin();
   if (p.vec) {
-    if (p.out_type == T_BF16) store_block<T_BF16, T::FN, T::FM>(p, acc, mw, nw, lane);
-    else if (p.out_type == T_FP16) store_block<T_FP16, T::FN, T::FM>(p, acc, mw, nw, lane);
-    else store_block<T_FP32, T::FN, T::FM>(p, acc, mw, nw, lane);
+    const bool extra = p.bias || p.add;
+#define MOE_MXL_STORE(DT)                                                          \
+  {                                                                                \
+    if (extra) store_block<DT, true, T::FN, T::FM>(p, acc, mw, nw, lane);          \
+    else store_block<DT, false, T::FN, T::FM>(p, acc, mw, nw, lane);               \
+  }
+    if (p.out_type == T_BF16) MOE_MXL_STORE(T_BF16)
+    else if (p.out_type == T_FP16) MOE_MXL_STORE(T_FP16)
+    else MOE_MXL_STORE(T_FP32)
+#undef MOE_MXL_STORE
     return;
   }
   // Rows that take no 16-byte accesses: each wave turns its block around
