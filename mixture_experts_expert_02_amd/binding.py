@@ -452,7 +452,8 @@ def align(topk_ids, E: int, workspace=None):
 
 # ---------------------------------------------------------------- operators around the experts step
 # These check every tensor against the problem before they hand its pointer
-# over, and run on the current stream of the tensors' own device.
+# over, and run on the current stream of the tensors' own device. The checks
+# that pass are kept short: for a single token a call's host time is what counts.
 class NormOut(NamedTuple):
     """add_rmsnorm's results; what was not asked for is None."""
     y: Optional[torch.Tensor]
@@ -461,72 +462,96 @@ class NormOut(NamedTuple):
     scales: Optional[torch.Tensor]
 
 
-def _need(ok: bool, where: str, what: str, status: int = MOE_EINVAL):
-    if not ok:
-        raise MoeError(status, f"{where}: {what}")
+def _refuse(where: str, what: str, status: int = MOE_EINVAL):
+    raise MoeError(status, f"{where}: {what}")
 
 
-def _rows2d(t, where: str, name: str, shape, dtypes, device) -> None:
-    """t is a matrix of the given shape (None: any) with contiguous rows, on `device`."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == 2, where, f"{name} must be a matrix")
-    _need(t.device == device and t.is_cuda, where, f"{name} must be on the GPU of the other tensors")
-    _need(t.dtype in dtypes, where, f"{name} has type {t.dtype}")
-    _need(tuple(t.shape) == tuple(shape), where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+def _matrix(t, where: str, name: str):
+    """(rows, columns, device index) of a GPU matrix."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _refuse(where, f"{name} must be a matrix")
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(where, f"{name} must be on a GPU")
     r, c = t.shape
-    _need((c < 2 or t.stride(1) == 1) and (r < 2 or t.stride(0) >= c), where, f"{name} needs contiguous rows")
+    return r, c, dev
 
 
-def _vector(t, where: str, name: str, n: int, dtypes, device) -> None:
-    _need(isinstance(t, torch.Tensor) and tuple(t.shape) == (n,) and t.is_contiguous(), where,
-          f"{name} must be a contiguous vector of {n} values")
-    _need(t.device == device, where, f"{name} must be on the GPU of the other tensors")
-    _need(t.dtype in dtypes, where, f"{name} has type {t.dtype}")
+def _ld(t, shape, dtypes, dev: int, where: str, name: str) -> int:
+    """Elements between the rows of t (0: contiguous), a matrix of the given
+    shape and one of the types, with contiguous rows, on device dev."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.get_device() == dev:
+        if t.is_contiguous():
+            return 0
+        r, c = shape
+        if (c < 2 or t.stride(1) == 1) and (r < 2 or t.stride(0) >= c):
+            return t.stride(0) if r > 1 else 0
+        _refuse(where, f"{name} needs contiguous rows that do not overlap")
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        _refuse(where, f"{name} must have shape {tuple(shape)}, not {tuple(getattr(t, 'shape', ()))}")
+    if t.get_device() != dev:
+        _refuse(where, f"{name} must be on the GPU of the other tensors")
+    _refuse(where, f"{name} has type {t.dtype}")
 
 
-def _ld(t) -> int:
-    """Elements between the rows of a matrix (0, contiguous, where it has one row or none)."""
-    return t.stride(0) if t.shape[0] > 1 else 0
+def _vector(t, n: int, dtypes, dev: int, where: str, name: str) -> int:
+    """Address of a contiguous vector of n values."""
+    if not (isinstance(t, torch.Tensor) and t.shape == (n,) and t.is_contiguous()):
+        _refuse(where, f"{name} must be a contiguous vector of {n} values")
+    if t.get_device() != dev:
+        _refuse(where, f"{name} must be on the GPU of the other tensors")
+    if t.dtype not in dtypes:
+        _refuse(where, f"{name} has type {t.dtype}")
+    return t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+# The current stream's handle by device index, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _run(fn, where: str, device, *args) -> None:
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _run(fn, where: str, dev: int, *args) -> None:
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     if rc != MOE_OK:
         raise MoeError(rc, where)
 
 
 _U8 = (torch.uint8,)
 _F32 = (torch.float32,)
-
-
-def _code_cols(fmt: int, K: int) -> int:
-    return K // 2 if fmt == MOE_MX_FP4 else K
+_I32 = (torch.int32,)
 
 
 def _mx_fmt(fmt, where: str) -> int:
-    _need(fmt in _MX, where, f"unknown format {fmt!r}")
-    return _MX[fmt]
+    f = _MX.get(fmt) if isinstance(fmt, str) else None
+    if f is None:
+        _refuse(where, f"unknown format {fmt!r}")
+    return f
 
 
-def _mx_out(codes, scales, where: str, rows: int, K: int, fmt: int, device):
-    """The given code and scale tensors, checked, or new ones."""
-    _need(K % 32 == 0, where, "rows of a multiple of 32 values are needed", MOE_ENOTSUP)
+def _blocks(K: int, where: str) -> int:
+    if K % 32:
+        _refuse(where, "rows of a multiple of 32 values are needed", MOE_ENOTSUP)
+    return K // 32
+
+
+def _mx_out(like, codes, scales, rows: int, K: int, fmt: int, dev: int, where: str):
+    """(codes, ld, scales, ld): the given code and scale tensors, checked, or new ones."""
+    nb = _blocks(K, where)
+    cols = K // 2 if fmt == MOE_MX_FP4 else K
+    lc = ls = 0
     if codes is None:
-        codes = torch.empty(rows, _code_cols(fmt, K), dtype=torch.uint8, device=device)
+        codes = like.new_empty((rows, cols), dtype=torch.uint8)
     else:
-        _rows2d(codes, where, "codes", (rows, _code_cols(fmt, K)), _U8, device)
+        lc = _ld(codes, (rows, cols), _U8, dev, where, "codes")
     if scales is None:
-        scales = torch.empty(rows, K // 32, dtype=torch.uint8, device=device)
+        scales = like.new_empty((rows, nb), dtype=torch.uint8)
     else:
-        _rows2d(scales, where, "scales", (rows, K // 32), _U8, device)
-    return codes, scales
+        ls = _ld(scales, (rows, nb), _U8, dev, where, "scales")
+    return codes, lc, scales, ls
 
 
 def mx_quantize(x, fmt: str = "mxfp4", codes=None, scales=None):
@@ -535,12 +560,12 @@ def mx_quantize(x, fmt: str = "mxfp4", codes=None, scales=None):
     uint8 [rows, K/32]). See moe_mx_quantize."""
     where = "mx_quantize"
     f = _mx_fmt(fmt, where)
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, where, "x must be a matrix")
-    rows, K = x.shape
-    _rows2d(x, where, "x", (rows, K), _TYPE, x.device)
-    codes, scales = _mx_out(codes, scales, where, rows, K, f, x.device)
-    p = MoeMxRows(rows, K, _TYPE[x.dtype], f, _ld(x), _ld(codes), _ld(scales))
-    _run(lib().moe_mx_quantize, "moe_mx_quantize", x.device, ctypes.byref(p), _addr(x), _addr(codes), _addr(scales))
+    rows, K, dev = _matrix(x, where, "x")
+    ld = _ld(x, (rows, K), _TYPE, dev, where, "x")
+    codes, lc, scales, ls = _mx_out(x, codes, scales, rows, K, f, dev, where)
+    p = MoeMxRows(rows, K, _TYPE[x.dtype], f, ld, lc, ls)
+    _run(lib().moe_mx_quantize, "moe_mx_quantize", dev, ctypes.byref(p), x.data_ptr(), codes.data_ptr(),
+         scales.data_ptr())
     return codes, scales
 
 
@@ -548,19 +573,20 @@ def mx_dequantize(codes, scales, fmt: str = "mxfp4", dtype=torch.bfloat16, out=N
     """The values that microscaled rows stand for, [rows, K]. See moe_mx_dequantize."""
     where = "mx_dequantize"
     f = _mx_fmt(fmt, where)
-    _need(isinstance(codes, torch.Tensor) and codes.dim() == 2, where, "codes must be a matrix")
-    rows = codes.shape[0]
-    K = codes.shape[1] * (2 if f == MOE_MX_FP4 else 1)
-    dev = codes.device
-    _need(scales is not None, where, "scales are needed")
-    _mx_out(codes, scales, where, rows, K, f, dev)
+    rows, cols, dev = _matrix(codes, where, "codes")
+    K = 2 * cols if f == MOE_MX_FP4 else cols
+    lc = _ld(codes, (rows, cols), _U8, dev, where, "codes")
+    ls = _ld(scales, (rows, _blocks(K, where)), _U8, dev, where, "scales")
+    ld = 0
     if out is None:
-        _need(dtype in _TYPE, where, f"unsupported type {dtype}", MOE_ENOTSUP)
-        out = torch.empty(rows, K, dtype=dtype, device=dev)
+        if dtype not in _TYPE:
+            _refuse(where, f"unsupported type {dtype}", MOE_ENOTSUP)
+        out = codes.new_empty((rows, K), dtype=dtype)
     else:
-        _rows2d(out, where, "out", (rows, K), _TYPE, dev)
-    p = MoeMxRows(rows, K, _TYPE[out.dtype], f, _ld(out), _ld(codes), _ld(scales))
-    _run(lib().moe_mx_dequantize, "moe_mx_dequantize", dev, ctypes.byref(p), _addr(codes), _addr(scales), _addr(out))
+        ld = _ld(out, (rows, K), _TYPE, dev, where, "out")
+    p = MoeMxRows(rows, K, _TYPE[out.dtype], f, ld, lc, ls)
+    _run(lib().moe_mx_dequantize, "moe_mx_dequantize", dev, ctypes.byref(p), codes.data_ptr(), scales.data_ptr(),
+         out.data_ptr())
     return out
 
 
@@ -570,34 +596,41 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, want_y: bool = True
     x's type (unless want_y is false) and, with mx "mxfp8" or "mxfp4", as
     microscaled rows. See moe_add_rmsnorm."""
     where = "add_rmsnorm"
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, where, "x must be a matrix")
-    T, H = x.shape
-    dev = x.device
-    _rows2d(x, where, "x", (T, H), _TYPE, dev)
-    _vector(weight, where, "weight", H, _TYPE, dev)
+    T, H, dev = _matrix(x, where, "x")
+    shape = (T, H)
+    ldx = _ld(x, shape, _TYPE, dev, where, "x")
     same = (x.dtype,)
     f = MOE_MX_NONE if mx is None else _mx_fmt(mx, where)
-    _need(want_y or y is not None or f != MOE_MX_NONE, where, "no output asked for")
-    _need(f != MOE_MX_NONE or (codes is None and scales is None), where, "codes and scales need mx")
-    if residual is None:
-        _need(residual_out is None, where, "residual_out needs residual")
-    else:
-        _rows2d(residual, where, "residual", (T, H), same, dev)
+    if f == MOE_MX_NONE:
+        if codes is not None or scales is not None:
+            _refuse(where, "codes and scales need mx")
+        if not want_y and y is None:
+            _refuse(where, "no output asked for")
+    ld_res = ld_out = ldy = lc = ls = 0
+    res_ptr = out_ptr = y_ptr = c_ptr = s_ptr = None
+    if residual is not None:
+        ld_res = _ld(residual, shape, same, dev, where, "residual")
+        res_ptr = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty(T, H, dtype=x.dtype, device=dev)
+            residual_out = x.new_empty(shape)
         else:
-            _rows2d(residual_out, where, "residual_out", (T, H), same, dev)
+            ld_out = _ld(residual_out, shape, same, dev, where, "residual_out")
+        out_ptr = residual_out.data_ptr()
+    elif residual_out is not None:
+        _refuse(where, "residual_out needs residual")
     if y is not None:
-        _rows2d(y, where, "y", (T, H), same, dev)
+        ldy = _ld(y, shape, same, dev, where, "y")
+        y_ptr = y.data_ptr()
     elif want_y:
-        y = torch.empty(T, H, dtype=x.dtype, device=dev)
+        y = x.new_empty(shape)
+        y_ptr = y.data_ptr()
     if f != MOE_MX_NONE:
-        codes, scales = _mx_out(codes, scales, where, T, H, f, dev)
-    ld = lambda t: 0 if t is None else _ld(t)  # noqa: E731
-    p = MoeNormProblem(T, H, _TYPE[x.dtype], _TYPE[weight.dtype], f, eps, _ld(x), ld(residual), ld(residual_out),
-                       ld(y), ld(codes), ld(scales))
-    _run(lib().moe_add_rmsnorm, "moe_add_rmsnorm", dev, ctypes.byref(p), _addr(x), _addr(residual), _addr(weight),
-         _addr(residual_out), _addr(y), _addr(codes), _addr(scales))
+        codes, lc, scales, ls = _mx_out(x, codes, scales, T, H, f, dev, where)
+        c_ptr, s_ptr = codes.data_ptr(), scales.data_ptr()
+    w_ptr = _vector(weight, H, _TYPE, dev, where, "weight")
+    p = MoeNormProblem(T, H, _TYPE[x.dtype], _TYPE[weight.dtype], f, eps, ldx, ld_res, ld_out, ldy, lc, ls)
+    _run(lib().moe_add_rmsnorm, "moe_add_rmsnorm", dev, ctypes.byref(p), x.data_ptr(), res_ptr, w_ptr, out_ptr, y_ptr,
+         c_ptr, s_ptr)
     return NormOut(y, residual_out, codes, scales)
 
 
@@ -609,31 +642,30 @@ def mx_linear(a, a_scales, w, w_scales, a_fmt: str = "mxfp8", bias=None, add=Non
     (out may be add). See moe_mx_linear."""
     where = "mx_linear"
     f = _mx_fmt(a_fmt, where)
-    _need(isinstance(w, torch.Tensor) and w.dim() == 2, where, "w must be a matrix")
-    _need(isinstance(a, torch.Tensor) and a.dim() == 2, where, "a must be a matrix")
-    dev = a.device
-    N, K = w.shape[0], 2 * w.shape[1]
-    M = a.shape[0]
-    _need(K % 32 == 0, where, "rows of a multiple of 32 values are needed", MOE_ENOTSUP)
-    _rows2d(a, where, "a", (M, _code_cols(f, K)), _U8, dev)
-    _rows2d(a_scales, where, "a_scales", (M, K // 32), _U8, dev)
-    _rows2d(w, where, "w", (N, K // 2), _U8, dev)
-    _rows2d(w_scales, where, "w_scales", (N, K // 32), _U8, dev)
-    _need(w.is_contiguous() and w_scales.is_contiguous(), where, "w and w_scales must be contiguous")
-    if bias is not None:
-        _vector(bias, where, "bias", N, _F32, dev)
+    M, cols, dev = _matrix(a, where, "a")
+    N, half, _ = _matrix(w, where, "w")
+    K = 2 * half
+    nb = _blocks(K, where)
+    lda = _ld(a, (M, half if f == MOE_MX_FP4 else K), _U8, dev, where, "a")
+    ld_as = _ld(a_scales, (M, nb), _U8, dev, where, "a_scales")
+    if _ld(w, (N, half), _U8, dev, where, "w") or _ld(w_scales, (N, nb), _U8, dev, where, "w_scales"):
+        _refuse(where, "w and w_scales must be contiguous")
+    b_ptr = None if bias is None else _vector(bias, N, _F32, dev, where, "bias")
+    ldo = ld_add = 0
     if out is not None:
-        _rows2d(out, where, "out", (M, N), _TYPE, dev)
+        ldo = _ld(out, (M, N), _TYPE, dev, where, "out")
         dtype = out.dtype
-    _need(dtype in _TYPE, where, f"unsupported type {dtype}", MOE_ENOTSUP)
+    elif dtype not in _TYPE:
+        _refuse(where, f"unsupported type {dtype}", MOE_ENOTSUP)
+    add_ptr = None
     if add is not None:
-        _rows2d(add, where, "add", (M, N), (dtype,), dev)
+        ld_add = _ld(add, (M, N), (dtype,), dev, where, "add")
+        add_ptr = add.data_ptr()
     if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=dev)
-    p = MoeMxLinearProblem(M, N, K, f, _TYPE[dtype], alpha, _ld(a), _ld(a_scales), _ld(out),
-                           0 if add is None else _ld(add))
-    _run(lib().moe_mx_linear, "moe_mx_linear", dev, ctypes.byref(p), _addr(a), _addr(a_scales), _addr(w),
-         _addr(w_scales), _addr(bias), _addr(add), _addr(out))
+        out = a.new_empty((M, N), dtype=dtype)
+    p = MoeMxLinearProblem(M, N, K, f, _TYPE[dtype], alpha, lda, ld_as, ldo, ld_add)
+    _run(lib().moe_mx_linear, "moe_mx_linear", dev, ctypes.byref(p), a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
+         w_scales.data_ptr(), b_ptr, add_ptr, out.data_ptr())
     return out
 
 
@@ -643,27 +675,25 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
     """Top-k experts of logits [T, E] (bf16, float16 or float32; rows may be
     strided): (ids int32 [T, k], weights float32 [T, k]). See moe_route_topk."""
     where = "route_topk"
-    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2, where, "logits must be a matrix")
-    T, E = logits.shape
-    dev = logits.device
-    _rows2d(logits, where, "logits", (T, E), _TYPE, dev)
-    _need(score in _SCORE, where, f"unknown score {score!r}")
-    _need(group_score in _GROUP, where, f"unknown group score {group_score!r}")
-    if bias is not None:
-        _vector(bias, where, "bias", E, _F32, dev)
-    _need(isinstance(k, int) and k > 0, where, "k must be a positive integer")
+    T, E, dev = _matrix(logits, where, "logits")
+    ld = _ld(logits, (T, E), _TYPE, dev, where, "logits")
+    if score not in _SCORE:
+        _refuse(where, f"unknown score {score!r}")
+    if group_score not in _GROUP:
+        _refuse(where, f"unknown group score {group_score!r}")
+    if not isinstance(k, int) or k <= 0:
+        _refuse(where, "k must be a positive integer")
+    b_ptr = None if bias is None else _vector(bias, E, _F32, dev, where, "bias")
     if ids is None:
-        ids = torch.empty(T, k, dtype=torch.int32, device=dev)
-    else:
-        _rows2d(ids, where, "ids", (T, k), (torch.int32,), dev)
-        _need(ids.is_contiguous(), where, "ids must be contiguous")
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+    elif _ld(ids, (T, k), _I32, dev, where, "ids"):
+        _refuse(where, "ids must be contiguous")
     if weights is None:
-        weights = torch.empty(T, k, dtype=torch.float32, device=dev)
-    else:
-        _rows2d(weights, where, "weights", (T, k), _F32, dev)
-        _need(weights.is_contiguous(), where, "weights must be contiguous")
+        weights = logits.new_empty((T, k), dtype=torch.float32)
+    elif _ld(weights, (T, k), _F32, dev, where, "weights"):
+        _refuse(where, "weights must be contiguous")
     p = MoeRouteTopkProblem(T, E, k, _TYPE[logits.dtype], _SCORE[score], n_group, topk_group, _GROUP[group_score],
-                            int(bool(renormalize)), routed_scaling_factor, _ld(logits))
-    _run(lib().moe_route_topk, "moe_route_topk", dev, ctypes.byref(p), _addr(logits), _addr(bias), _addr(ids),
-         _addr(weights))
+                            1 if renormalize else 0, routed_scaling_factor, ld)
+    _run(lib().moe_route_topk, "moe_route_topk", dev, ctypes.byref(p), logits.data_ptr(), b_ptr, ids.data_ptr(),
+         weights.data_ptr())
     return ids, weights
