@@ -106,13 +106,13 @@ int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
   return MOE_OK;
 }
 
-template <int AF, int BM, int BN, int BK>
+template <int AF, int BM, int BN, int BK, int NBUF>
 int launch_tile(moe::mxl::Params& q, hipStream_t s) {
   q.mt = (q.M + BM - 1) / BM;
   q.nt = (q.N + BN - 1) / BN;
   const int64_t n = (int64_t)q.mt * q.nt;
   if (n > 0x7ffffff0) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
   return launch_status();
 }
 
@@ -142,9 +142,9 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
   constexpr int BM = F8 ? 128 : 256;
   const int64_t big = (int64_t)((q.M + BM - 1) / BM) * ((q.N + 255) / 256);
   const int64_t mid = (int64_t)((q.M + 127) / 128) * ((q.N + 127) / 128);
-  if (big >= 192) return launch_tile<AF, BM, 256, F8 ? 128 : 256>(q, s);
-  if (mid >= 384) return launch_tile<AF, 128, 128, F8 ? 128 : 256>(q, s);
-  return launch_tile<AF, 64, 64, 256>(q, s);
+  if (big >= 192) return launch_tile<AF, BM, 256, F8 ? 128 : 256, 2>(q, s);
+  if (mid >= 384) return launch_tile<AF, 128, 128, F8 ? 128 : 256, 2>(q, s);
+  return launch_tile<AF, 64, 64, 256, 2>(q, s);
 }
 
 // ----------------------------------------------------------------- routing

@@ -13,7 +13,14 @@ namespace mxl {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// s_waitcnt vmcnt(N) lgkmcnt(0): this wave's LDS accesses are done and all but its
+// N youngest memory operations (vmcnt in bits 3:0 and 15:14, expcnt 7 = no wait)
+template <int N>
+__device__ __forceinline__ void wait_landed() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
 
 struct Params {
   const uint8_t* a;        // codes, rows of lda bytes
@@ -232,7 +239,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // (even and odd blocks of the first 256 K values, then of the second); a lane
 // reads one word per fragment and 256 K values, whose byte s is the scale of its
 // block in step s.
-template <int AF, int BM, int BN, int BK>
+template <int AF, int BM, int BN, int BK, int NBUF>
 struct Tile {
   static constexpr int AB = AF == mxf::MXFP8 ? BK : BK / 2, WB = BK / 2;  // bytes of a row per stage
   static constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB;
@@ -241,13 +248,14 @@ struct Tile {
   static constexpr int FM = BM / 64, FN = BN / 64;         // 32 x 32 results of a wave
   static constexpr int AL = A_BYTES / 4096, WL = W_BYTES / 4096;  // loads per wave and stage
   static constexpr int ROWS = BM + BN;                     // scale rows: weights, then activations
-  static constexpr int SR = (ROWS + 255) / 256;            // per thread
+  static constexpr int SP = AF == mxf::MXFP8 && BK == 128 ? 2 : 4;  // 16-byte pieces of a scale row fetched at once
+  static constexpr int SR = ROWS * SP / 256;               // per thread
   static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
   static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
-  static constexpr int WGS = 2 * STAGE + 32 * ROWS <= 80 * 1024 ? 2 : 1;  // workgroups per compute unit (160 KB of LDS)
-  static_assert(2 * 32 * EROW * 4 <= STAGE, "epilogue staging: two waves per buffer");
-  static_assert(BK == 128 || BK == 256, "a scale word holds 256 K values");
-  static_assert(BN % 64 == 0 && BM % 64 == 0, "whole waves load scale rows of one operand");
+  static constexpr int WGS = NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 0) <= 80 * 1024 ? 2 : 1;  // workgroups per compute unit (160 KB of LDS)
+  static_assert(4 / NBUF * 32 * EROW * 4 <= STAGE, "epilogue staging: the waves share the buffers");
+  static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && BK == 128, "a scale word holds 256 K values");
+  static_assert(NBUF == 4 || BN % (256 / SP) == 0, "an instruction fetches scale rows of one operand");
 };
 
 // slot of 16-byte chunk c of row r in a row of RB bytes
@@ -256,12 +264,14 @@ __device__ __forceinline__ int slot_of(int c, int r) {
   return RB == 256 ? c ^ (r & 15) : RB == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int AF, int BM, int BN, int BK>
-__global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const Params p) {
-  using T = Tile<AF, BM, BN, BK>;
+template <int AF, int BM, int BN, int BK, int NBUF>
+__global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile(const Params p) {
+  using T = Tile<AF, BM, BN, BK, NBUF>;
   __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[T::STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2][T::ROWS * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf2[NBUF == 4 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[NBUF == 4 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][NBUF == 4 ? 16 : T::ROWS * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -276,7 +286,8 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
   if ((int)(blockIdx.x >> 3) >= per || item >= n_tiles) return;
   const int g = item / (4 * p.nt), gm = min(4, p.mt - 4 * g);
   const int in = item - g * 4 * p.nt;
-  const int m0 = (4 * g + in % gm) * BM, n0 = in / gm * BN;
+  const int m0 = __builtin_amdgcn_readfirstlane((4 * g + in % gm) * BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(in / gm * BN);
 
   const int KS = (p.K + BK - 1) / BK;    // stages
   const int nblk = p.K >> 5;
@@ -312,12 +323,12 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     if (q < T::AL) {
       uint8_t* dst = buf + wave * (T::A_BYTES / 4) + q * 1024;
       const uint32_t off = a_off[q];
-      const int so = s * T::AB;
+      const int so = __builtin_amdgcn_readfirstlane(s * T::AB);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (__attribute__((address_space(3))) void*)dst, 16, off, so, 0, 0);
     } else {
       uint8_t* dst = buf + T::A_BYTES + wave * (T::W_BYTES / 4) + (q - T::AL) * 1024;
       const uint32_t off = w_off[q - T::AL];
-      const int so = s * T::WB;
+      const int so = __builtin_amdgcn_readfirstlane(s * T::WB);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsW, (__attribute__((address_space(3))) void*)dst, 16, off, so, 0, 0);
     }
   };
@@ -331,33 +342,36 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
       if ((uint32_t)s * T::WB + w_ch[i] >= w_row) w_off[i] = kNoLoad;
   };
 
-  // Scale rows of this thread: row tid + 256 i of [BN weight rows, BM activation
-  // rows]; rows past the end repeat the last (their results are never stored).
+  // Scale rows [BN weight rows, BM activation rows]; rows past the end repeat the
+  // last (their results are never stored). SP lanes fetch SP consecutive 16-byte
+  // pieces of one row (SP * 512 K values) in one go: what bounds the loads is
+  // the number of 128-byte lines asked for, and a 16-byte piece costs a whole one.
   const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
   const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
   const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
   const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
+  constexpr int RPI = 256 / T::SP;  // rows per instruction
+  const int piece = tid % T::SP, prow = tid / T::SP;
   u32x4 raw[T::SR];
-  auto fetch_scales = [&](int grp) {
+  auto fetch_scales = [&](int super) {  // groups super * SP ..
+    const int b0 = 16 * (super * T::SP + piece);
+    const bool whole = 16 * (super + 1) * T::SP <= nblk;
 #pragma unroll
     for (int i = 0; i < T::SR; ++i) {
-      const int w = wave * 64 + 256 * i;  // uniform: the wave's first row
-      if (w >= T::ROWS) break;
-      const bool is_w = w < BN;
+      const bool is_w = i * RPI < BN;
       const uint8_t* base = is_w ? w_scb : a_scb;
-      const int r = is_w ? min(w + lane, w_rows - 1) : min(w - BN + lane, a_rows - 1);
-      const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as)) + 16u * grp;
-      if (16 * grp + 16 <= nblk) raw[i] = load_sc16(base, off);
-      else raw[i] = load_sc_tail(base, off, is_w ? w_tot : a_tot, nblk - 16 * grp);
+      const int r = is_w ? min(i * RPI + prow, w_rows - 1) : min(i * RPI - BN + prow, a_rows - 1);
+      const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
+      if (whole) raw[i] = load_sc16(base, off);
+      else raw[i] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
     }
   };
   auto publish_scales = [&](int grp) {
+    if (piece != grp % T::SP) return;
 #pragma unroll
     for (int i = 0; i < T::SR; ++i) {
-      const int w = wave * 64 + 256 * i;
-      if (w >= T::ROWS) break;
       const u32x4 v = raw[i];
-      *(u32x4*)(scales[grp & 1] + (w + lane) * 16) =
+      *(u32x4*)(scales[grp & 1] + (i * RPI + prow) * 16) =
           u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x06040200u), __builtin_amdgcn_perm(v[1], v[0], 0x07050301u),
                 __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), __builtin_amdgcn_perm(v[3], v[2], 0x07050301u)};
     }
@@ -369,6 +383,61 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     for (int i = 0; i < T::FN; ++i) dw[i] = *(const uint32_t*)(src + (wn * (BN / 2) + i * 32) * 16);
 #pragma unroll
     for (int j = 0; j < T::FM; ++j) da[j] = *(const uint32_t*)(src + (BN + wm * (BM / 2) + j * 32) * 16);
+  };
+
+  // Four buffers: the scales bypass LDS (an LDS read that no load in flight can
+  // alias makes the compiler wait for all of them). Lane (r, q) loads bytes
+  // 32q..32q+31 of the 64 of its row (2048 K values); one v_permlane32_swap of the
+  // even and the odd blocks of a unit leaves each half of the wave with the words
+  // of its own parity: unit i from the lower lanes, unit 4 + i from the upper.
+  constexpr int FS = NBUF == 4 ? T::FN + T::FM : 1;
+  u32x4 raw_d[FS][2];
+  uint32_t word[FS][8];
+  auto fetch_direct = [&](int super) {
+    const bool whole = 64 * super + 64 <= nblk;
+#pragma unroll
+    for (int x = 0; x < FS; ++x) {
+      const bool is_w = x < T::FN;
+      const uint8_t* base = is_w ? w_scb : a_scb;
+      const int r = is_w ? min(wn * (BN / 2) + x * 32 + lr, w_rows - 1)
+                         : min(wm * (BM / 2) + (x - T::FN) * 32 + lr, a_rows - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int b0 = 64 * super + 32 * lq + 16 * h;
+        const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
+        if (whole) raw_d[x][h] = load_sc16(base, off);
+        else raw_d[x][h] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
+      }
+    }
+  };
+  auto spread_direct = [&]() {
+#pragma unroll
+    for (int x = 0; x < FS; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = raw_d[x][i / 2][2 * (i % 2)], hi = raw_d[x][i / 2][2 * (i % 2) + 1];
+        const auto y = __builtin_amdgcn_permlane32_swap(__builtin_amdgcn_perm(hi, lo, 0x06040200u),
+                                                        __builtin_amdgcn_perm(hi, lo, 0x07050301u), false, false);
+        word[x][i] = y[0];
+        word[x][4 + i] = y[1];
+      }
+  };
+  // the words of turn t's two units into the operand sets; a new fetch every fourth turn
+  auto take_direct = [&](int t) {
+    if ((t & 3) == 0) {
+      spread_direct();
+      fetch_direct(t / 4 + 1);
+    }
+#pragma unroll
+    for (int x = 0; x < FS; ++x) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (x < T::FN) sw[h][x < T::FN ? x : 0] = word[x][h];
+        else sa[h][x < T::FN ? 0 : x - T::FN] = word[x][h];
+      }
+#pragma unroll
+      for (int i = 0; i < 6; ++i) word[x][i] = word[x][i + 2];
+    }
   };
 
   f32x16 acc[T::FN][T::FM];
@@ -465,32 +534,73 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     }                                                                    \
     pin();                                                               \
     mask_loads((NEXT) + 1);                                              \
-    __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */        \
+    wait_landed<0>();                                                    \
     asm volatile("s_barrier" ::: "memory");                              \
     __builtin_amdgcn_sched_barrier(0);                                   \
     if ((RSC) >= 0) read_scales(RSC, sa[RSS], sw[RSS]);                  \
     MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, 0, LH, CUR, (NEXT) + 1) \
   }
 
+  // The same with four buffers: the last step waits for the next stage only
+  // (the two after it may still be in flight) and loads stage NEXT + 3 into this one.
+#define MOE_MXL_STAGE4(CUR, OTHER, NEXT, SB0, SS)                        \
+  {                                                                      \
+    MOE_MXL_STEP(0, SB0, SS, CUR, 1, 0, 0, CUR, 0)                       \
+    pin();                                                               \
+    mask_loads((NEXT) + 3);                                              \
+    wait_landed<2 * LT>();                                               \
+    asm volatile("s_barrier" ::: "memory");                              \
+    __builtin_amdgcn_sched_barrier(0);                                   \
+    MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, 0, LT, CUR, (NEXT) + 3) \
+  }
+
   mask_loads(0);
-  fetch_scales(0);
+  if constexpr (NBUF == 4) fetch_direct(0);
+  else fetch_scales(0);
 #pragma unroll
   for (int q = 0; q < LT; ++q) load_piece(buf0, 0, q);
-  mask_loads(1);
+  if constexpr (NBUF == 4) {
+    mask_loads(1);
 #pragma unroll
-  for (int q = 0; q < LH; ++q) load_piece(buf1, 1, q);
-  publish_scales(0);
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    for (int q = 0; q < LT; ++q) load_piece(buf1, 1, q);
+    mask_loads(2);
+#pragma unroll
+    for (int q = 0; q < LT; ++q) load_piece(buf2, 2, q);
+    mask_loads(3);
+#pragma unroll
+    for (int q = 0; q < LT; ++q) load_piece(buf3, 3, q);
+  } else {
+    mask_loads(1);
+#pragma unroll
+    for (int q = 0; q < LH; ++q) load_piece(buf1, 1, q);
+  }
+  if constexpr (NBUF == 2) publish_scales(0);
+  wait_landed<NBUF == 4 ? 3 * LT : LH>();
   asm volatile("s_barrier" ::: "memory");
-  read_scales(0, sa[0], sw[0]);
+  if constexpr (NBUF == 2) read_scales(0, sa[0], sw[0]);
 #pragma unroll
   for (int i = 0; i < T::FN; ++i) read_w(buf0, 0, wv[0][i], i);
 #pragma unroll
   for (int j = 0; j < T::FM; ++j) read_a(buf0, 0, av[0][j], j);
-  if constexpr (BK == 256) {
+  if constexpr (NBUF == 4) {
+    // four stages = one scale group per turn
+    int t = 0;
+    for (; t < KS / 4; ++t) {
+      take_direct(t);
+      MOE_MXL_STAGE4(buf0, buf1, 4 * t + 1, 0, 0)
+      MOE_MXL_STAGE4(buf1, buf2, 4 * t + 2, 2, 0)
+      MOE_MXL_STAGE4(buf2, buf3, 4 * t + 3, 0, 1)
+      MOE_MXL_STAGE4(buf3, buf0, 4 * t + 4, 2, 1)
+      pin();
+    }
+    take_direct(t);
+    if ((KS & 3) > 0) MOE_MXL_STAGE4(buf0, buf1, 4 * t + 1, 0, 0)
+    if ((KS & 3) > 1) MOE_MXL_STAGE4(buf1, buf2, 4 * t + 2, 2, 0)
+    if ((KS & 3) > 2) MOE_MXL_STAGE4(buf2, buf3, 4 * t + 3, 0, 1)
+  } else if constexpr (BK == 256) {
     // two stages = one scale group per turn
     for (int t = 0; t < KS / 2; ++t) {
-      if (32 * (t + 1) < 2 * nblk) fetch_scales(t + 1);
+      if ((t + 1) % T::SP == 0) fetch_scales((t + 1) / T::SP);
       MOE_MXL_STAGE(buf0, buf1, 2 * t + 1, 0, 0, 2 * t + 1, 1)
       pin();
       publish_scales(t + 1);
@@ -501,7 +611,7 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     // two stages = one scale unit per turn, two turns per group; the last step
     // of a turn reads the next unit's words into the other set
     for (int t = 0; t < KS / 2; ++t) {
-      if (!(t & 1)) fetch_scales(t / 2 + 1);
+      if (t % (2 * T::SP) == 2 * T::SP - 2) fetch_scales((t / 2 + 1) / T::SP);
       MOE_MXL_STAGE(buf0, buf1, 2 * t + 1, 0, 0, -1, 0)
       pin();
       if (t & 1) publish_scales(t / 2 + 1);
@@ -513,12 +623,13 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
     }
     if (KS & 1) MOE_MXL_STAGE(buf0, buf1, KS, 0, 0, -1, 0)
   }
+#undef MOE_MXL_STAGE4
 #undef MOE_MXL_STAGE
 #undef MOE_MXL_STEP
 #undef MOE_MXL_MFMA
 
   // The last loads (of stages past the end) have landed and every wave has read its operands.
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  wait_landed<0>();
   asm volatile("s_barrier" ::: "memory");
   const int mw = m0 + wm * (BM / 2), nw = n0 + wn * (BN / 2);
   pin();
@@ -538,7 +649,9 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK>::WGS)) void k_tile(const
   // Rows that take no 16-byte accesses: each wave turns its block around
   // through its own part of the (now idle) buffers, 32 rows x EF column
   // fragments at a time, and stores value by value.
-  float* strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
+  float* strip;
+  if constexpr (NBUF == 4) strip = (float*)(wave < 2 ? wave == 0 ? buf0 : buf1 : wave == 2 ? buf2 : buf3);
+  else strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
   constexpr int CPR = T::EF * 8;       // 4-column pieces per strip row
   constexpr int RPP = 64 / CPR;        // rows per pass
 #pragma unroll
