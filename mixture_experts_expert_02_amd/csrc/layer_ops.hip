@@ -106,13 +106,13 @@ int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
   return MOE_OK;
 }
 
-template <int AF, int BM, int BN, int BK, int NBUF>
+template <int AF, int BM, int BN, int BK, int NBUF, int G = 1>
 int launch_tile(moe::mxl::Params& q, hipStream_t s) {
   q.mt = (q.M + BM - 1) / BM;
   q.nt = (q.N + BN - 1) / BN;
   const int64_t n = (int64_t)q.mt * q.nt;
   if (n > 0x7ffffff0) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF, G>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256 * G), 0, s, q);
   return launch_status();
 }
 

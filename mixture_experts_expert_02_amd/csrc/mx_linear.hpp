@@ -239,7 +239,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // (even and odd blocks of the first 256 K values, then of the second); a lane
 // reads one word per fragment and 256 K values, whose byte s is the scale of its
 // block in step s.
-template <int AF, int BM, int BN, int BK, int NBUF>
+template <int AF, int BM, int BN, int BK, int NBUF, int G>
 struct Tile {
   static constexpr int AB = AF == mxf::MXFP8 ? BK : BK / 2, WB = BK / 2;  // bytes of a row per stage
   static constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB;
@@ -248,12 +248,14 @@ struct Tile {
   static constexpr int FM = BM / 64, FN = BN / 64;         // 32 x 32 results of a wave
   static constexpr int AL = A_BYTES / 4096, WL = W_BYTES / 4096;  // loads per wave and stage
   static constexpr int ROWS = BM + BN;                     // scale rows: weights, then activations
-  static constexpr int SP = AF == mxf::MXFP8 && BK == 128 ? 2 : 4;  // 16-byte pieces of a scale row fetched at once
+  static constexpr int SP = AF == mxf::MXFP8 && BK == 128 && BN == 256 ? 2 : 4;  // 16-byte pieces of a scale row fetched at once
   static constexpr int SR = ROWS * SP / 256;               // per thread
   static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
   static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
-  static constexpr int WGS = NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 0) <= 80 * 1024 ? 2 : 1;  // workgroups per compute unit (160 KB of LDS)
-  static_assert(4 / NBUF * 32 * EROW * 4 <= STAGE, "epilogue staging: the waves share the buffers");
+  static constexpr int LDS = G * (NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 64));
+  static constexpr int WPS = G * (LDS <= 80 * 1024 ? 2 : 1);  // waves per SIMD (160 KB of LDS)
+  static_assert(4 / NBUF * 32 * EROW * 4 <= G * STAGE, "epilogue staging: the waves share the buffers");
+  static_assert((G - 1) * BM * BN * 4 <= NBUF * G * STAGE, "partial sums meet in the buffers");
   static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && BK == 128, "a scale word holds 256 K values");
   static_assert(NBUF == 4 || BN % (256 / SP) == 0, "an instruction fetches scale rows of one operand");
 };
@@ -264,18 +266,28 @@ __device__ __forceinline__ int slot_of(int c, int r) {
   return RB == 256 ? c ^ (r & 15) : RB == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int AF, int BM, int BN, int BK, int NBUF>
-__global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile(const Params p) {
-  using T = Tile<AF, BM, BN, BK, NBUF>;
-  __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t buf1[T::STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t buf2[NBUF == 4 ? T::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t buf3[NBUF == 4 ? T::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2][NBUF == 4 ? 16 : T::ROWS * 16];
-  const int tid = threadIdx.x, lane = tid & 63;
+template <int AF, int BM, int BN, int BK, int NBUF, int G>
+__global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void k_tile(const Params p) {
+  using T = Tile<AF, BM, BN, BK, NBUF, G>;
+  __shared__ __attribute__((aligned(16))) uint8_t all0[G * T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t all1[G * T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t all2[NBUF == 4 ? G * T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t all3[NBUF == 4 ? G * T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[G][2][NBUF == 4 ? 16 : T::ROWS * 16];
+  const int lane = threadIdx.x & 63;
+  const int tid = threadIdx.x & 255;     // within the group
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = G == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8);
   const int wm = wave & 1, wn = wave >> 1;
   const int lr = lane & 31, lq = lane >> 5;
+  uint8_t* const buf0 = all0 + grp * T::STAGE;
+  uint8_t* const buf1 = all1 + grp * T::STAGE;
+  uint8_t* buf2 = nullptr;
+  uint8_t* buf3 = nullptr;
+  if constexpr (NBUF == 4) {
+    buf2 = all2 + grp * T::STAGE;
+    buf3 = all3 + grp * T::STAGE;
+  }
 
   // Workgroup b runs on XCD b mod 8; each XCD takes a contiguous run of the
   // tiles, ordered in groups of 4 row tiles, columns outer inside a group, so
@@ -289,12 +301,19 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   const int m0 = __builtin_amdgcn_readfirstlane((4 * g + in % gm) * BM);
   const int n0 = __builtin_amdgcn_readfirstlane(in / gm * BN);
 
-  const int KS = (p.K + BK - 1) / BK;    // stages
-  const int nblk = p.K >> 5;
-  const uint32_t a_row = AF == mxf::MXFP8 ? (uint32_t)p.K : (uint32_t)p.K / 2, w_row = (uint32_t)p.K / 2;
+  // K range of this group: KS stages (the last group's may lie past the end:
+  // zeros), a_row and w_row bytes and nblk scale blocks of each row
+  const int KS = ((p.K + BK - 1) / BK + G - 1) / G;
+  const int row_blk = p.K >> 5;
+  const int blk0 = grp * KS * (BK / 32);
+  const int nblk = max(0, min(row_blk - blk0, KS * (BK / 32)));
+  const uint32_t a_row = (uint32_t)nblk * (AF == mxf::MXFP8 ? 32u : 16u), w_row = (uint32_t)nblk * 16u;
+  const uint32_t w_ld = (uint32_t)row_blk * 16u;
   const int a_rows = min(BM, p.M - m0), w_rows = min(BN, p.N - n0);
-  const __amdgpu_buffer_rsrc_t rsA = rsrc(p.a + (size_t)m0 * p.lda, (uint32_t)((a_rows - 1) * p.lda + a_row));
-  const __amdgpu_buffer_rsrc_t rsW = rsrc(p.w + (size_t)n0 * w_row, (uint32_t)w_rows * w_row);
+  const __amdgpu_buffer_rsrc_t rsA =
+      rsrc(p.a + (size_t)m0 * p.lda + (size_t)grp * KS * T::AB, (uint32_t)((a_rows - 1) * p.lda + a_row));
+  const __amdgpu_buffer_rsrc_t rsW =
+      rsrc(p.w + (size_t)n0 * w_ld + (size_t)grp * KS * T::WB, (uint32_t)(w_rows - 1) * w_ld + w_row);
 
   // load assignment: wave w fills the w-th quarter of each operand
   uint32_t a_off[T::AL], w_off[T::WL];
@@ -311,10 +330,11 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
     const int at = wave * (T::W_BYTES / 4) + i * 1024 + lane * 16;
     const int r = at / T::WB;
     w_ch[i] = 16u * slot_of<T::WB>((at % T::WB) / 16, r);
-    w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_ch[i] : kNoLoad;
+    w_off[i] = r < w_rows ? (uint32_t)r * w_ld + w_ch[i] : kNoLoad;
   }
   // Load instruction q of stage s into buf: first the activations', then the
   // weights'. The stage's place in K goes into the scalar offset, which the range
+  // check does not cover: mask_loads moves the lanes that would pass the row's
   // check does not cover: mask_loads moves the lanes that would pass the row's
   // end in the last stage, and all of them after it, out of range.
   // (Its arguments are plain variables: with array elements or template constants
@@ -333,7 +353,7 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
     }
   };
   auto mask_loads = [&](int s) {  // before the first load of stage s
-    if (s < KS - 1) return;
+    if ((s + 1) * (BK / 32) <= nblk) return;
 #pragma unroll
     for (int i = 0; i < T::AL; ++i)
       if ((uint32_t)s * T::AB + a_ch[i] >= a_row) a_off[i] = kNoLoad;
@@ -346,10 +366,12 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   // last (their results are never stored). SP lanes fetch SP consecutive 16-byte
   // pieces of one row (SP * 512 K values) in one go: what bounds the loads is
   // the number of 128-byte lines asked for, and a 16-byte piece costs a whole one.
-  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
-  const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
-  const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
-  const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
+  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as + blk0;
+  const uint8_t* w_scb = p.w_sc + (size_t)n0 * row_blk + blk0;
+  const uint32_t a_tot =
+      (uint32_t)max((int64_t)0, min((int64_t)(p.M - 1 - m0) * p.ld_as + row_blk - blk0, (int64_t)0x7fffffff));
+  const uint32_t w_tot =
+      (uint32_t)max((int64_t)0, min((int64_t)(p.N - n0) * row_blk - blk0, (int64_t)0x7fffffff));
   constexpr int RPI = 256 / T::SP;  // rows per instruction
   const int piece = tid % T::SP, prow = tid / T::SP;
   u32x4 raw[T::SR];
@@ -361,24 +383,24 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
       const bool is_w = i * RPI < BN;
       const uint8_t* base = is_w ? w_scb : a_scb;
       const int r = is_w ? min(i * RPI + prow, w_rows - 1) : min(i * RPI - BN + prow, a_rows - 1);
-      const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
+      const uint32_t off = (uint32_t)(r * (is_w ? row_blk : (int)p.ld_as) + b0);
       if (whole) raw[i] = load_sc16(base, off);
       else raw[i] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
     }
   };
-  auto publish_scales = [&](int grp) {
-    if (piece != grp % T::SP) return;
+  auto publish_scales = [&](int g) {
+    if (piece != g % T::SP) return;
 #pragma unroll
     for (int i = 0; i < T::SR; ++i) {
       const u32x4 v = raw[i];
-      *(u32x4*)(scales[grp & 1] + (i * RPI + prow) * 16) =
+      *(u32x4*)(scales[grp][g & 1] + (i * RPI + prow) * 16) =
           u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x06040200u), __builtin_amdgcn_perm(v[1], v[0], 0x07050301u),
                 __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), __builtin_amdgcn_perm(v[3], v[2], 0x07050301u)};
     }
   };
   uint32_t sa[2][T::FM], sw[2][T::FN];  // scale words of a 256-K unit, and of the next
   auto read_scales = [&](int unit, uint32_t (&da)[T::FM], uint32_t (&dw)[T::FN]) {
-    const uint8_t* src = scales[(unit >> 1) & 1] + (unit & 1) * 8 + 4 * lq + lr * 16;
+    const uint8_t* src = scales[grp][(unit >> 1) & 1] + (unit & 1) * 8 + 4 * lq + lr * 16;
 #pragma unroll
     for (int i = 0; i < T::FN; ++i) dw[i] = *(const uint32_t*)(src + (wn * (BN / 2) + i * 32) * 16);
 #pragma unroll
@@ -404,7 +426,7 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int b0 = 64 * super + 32 * lq + 16 * h;
-        const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
+        const uint32_t off = (uint32_t)(r * (is_w ? row_blk : (int)p.ld_as) + b0);
         if (whole) raw_d[x][h] = load_sc16(base, off);
         else raw_d[x][h] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
       }
@@ -477,7 +499,7 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   // spare they come in the order they are wanted; else each weight fragment
   // takes its predecessor's registers once that is used up.
   auto read_row = [&](const uint8_t* buf, int st, i32x4 (&dw)[T::FN], i32x8 (&da)[T::FM], int i) {
-    if constexpr (T::WGS == 2) {
+    if constexpr (T::WPS >= 2) {
       read_w(buf, st, dw[i], i);
 #pragma unroll
       for (int j = i; j < T::FM; j += T::FN) read_a(buf, st, da[j], j);
@@ -633,6 +655,46 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   asm volatile("s_barrier" ::: "memory");
   const int mw = m0 + wm * (BM / 2), nw = n0 + wn * (BN / 2);
   pin();
+  if constexpr (G > 1) {
+    // The groups' partial sums meet in the (now idle) buffers, added in group order.
+    // Four values a lane at a time: piece x of group g's wave w at ((g - 1) * PIECES + x) * 4 + w KB.
+    constexpr int PIECES = T::FN * T::FM * 4;
+    constexpr int BUF_KB = G * T::STAGE / 1024;  // KB of each buffer array
+    auto at = [&](int kb) {
+      uint8_t* base = kb < BUF_KB ? all0 : all1;
+      if constexpr (NBUF == 4)
+        if (kb >= 2 * BUF_KB) base = kb < 3 * BUF_KB ? all2 : all3;
+      return (f32x4*)(base + (kb % BUF_KB) * 1024) + lane;
+    };
+    if (grp > 0) {
+#pragma unroll
+      for (int x = 0; x < PIECES; ++x) {
+        const f32x16& c = acc[x / 4 / T::FM][x / 4 % T::FM];
+        *at(((grp - 1) * PIECES + x) * 4 + wave) = f32x4{c[4 * (x % 4)], c[4 * (x % 4) + 1], c[4 * (x % 4) + 2], c[4 * (x % 4) + 3]};
+      }
+    }
+    wait_landed<0>();
+    asm volatile("s_barrier" ::: "memory");
+    if (grp == 0) {
+#pragma unroll
+      for (int x = 0; x < PIECES; ++x) {
+        f32x16& c = acc[x / 4 / T::FM][x / 4 % T::FM];
+#pragma unroll
+        for (int g1 = 0; g1 < G - 1; ++g1) {
+          const f32x4 v = *at((g1 * PIECES + x) * 4 + wave);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[4 * (x % 4) + k] += v[k];
+        }
+      }
+    }
+    if (!p.vec) {  // the value-by-value stores below reuse the buffers
+      wait_landed<0>();
+      asm volatile("s_barrier" ::: "memory");
+    }
+    if (grp > 0) return;
+    __builtin_amdgcn_sched_barrier(0);
+    pin();
+  }
   if (p.vec) {
     const bool extra = p.bias || p.add;
 #define MOE_MXL_STORE(DT)                                                          \
@@ -650,8 +712,8 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   // through its own part of the (now idle) buffers, 32 rows x EF column
   // fragments at a time, and stores value by value.
   float* strip;
-  if constexpr (NBUF == 4) strip = (float*)(wave < 2 ? wave == 0 ? buf0 : buf1 : wave == 2 ? buf2 : buf3);
-  else strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
+  if constexpr (NBUF == 4) strip = (float*)(wave < 2 ? wave == 0 ? all0 : all1 : wave == 2 ? all2 : all3);
+  else strip = (float*)((wave < 2 ? all0 : all1) + (wave & 1) * 32 * T::EROW * 4);
   constexpr int CPR = T::EF * 8;       // 4-column pieces per strip row
   constexpr int RPP = 64 / CPR;        // rows per pass
 #pragma unroll
