@@ -150,14 +150,20 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
 // ----------------------------------------------------------------- routing
 template <int DT>
 void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
-#define MOE_ROUTE_TOPK(L, PER)                                                                                 \
-  hipLaunchKernelGGL((moe::k_route_topk<DT, L, PER>), dim3((unsigned)((q.T + 256 / L - 1) / (256 / L))), dim3(256), 0, \
-                     s, q)
-  if (q.E <= 64) MOE_ROUTE_TOPK(16, 4);
-  else if (q.E <= 128) MOE_ROUTE_TOPK(16, 8);
-  else if (q.E <= 256) MOE_ROUTE_TOPK(16, 16);
-  else if (q.E <= 512) MOE_ROUTE_TOPK(64, 8);
-  else MOE_ROUTE_TOPK(64, 16);
+  const bool row16 = aligned(q.logits, 16) && q.ld * moe::elem_size(DT) % 16 == 0;
+#define MOE_ROUTE_TOPK(L, PER)                                                                              \
+  {                                                                                                         \
+    const dim3 g((unsigned)((q.T + 256 / L - 1) / (256 / L)));                                              \
+    if (PER >= 8 && row16 && q.E % PER == 0)                                                                \
+      hipLaunchKernelGGL((moe::k_route_topk<DT, L, PER, PER >= 8>), g, dim3(256), 0, s, q);                 \
+    else                                                                                                    \
+      hipLaunchKernelGGL((moe::k_route_topk<DT, L, PER, false>), g, dim3(256), 0, s, q);                    \
+  }
+  if (q.E <= 64) MOE_ROUTE_TOPK(16, 4)
+  else if (q.E <= 128) MOE_ROUTE_TOPK(16, 8)
+  else if (q.E <= 256) MOE_ROUTE_TOPK(16, 16)
+  else if (q.E <= 512) MOE_ROUTE_TOPK(64, 8)
+  else MOE_ROUTE_TOPK(64, 16)
 #undef MOE_ROUTE_TOPK
 }
 

@@ -8,10 +8,18 @@
 // picks do not depend on how the work is split over lanes.
 //
 // L lanes per token (16: four tokens per wave, up to 256 experts; 64: up to
-// 1024), lane l holding experts l, l + L, ... (PER of them). Cross-lane steps
-// stay inside the token's lanes: with 16 they are four DPP rotations, so four
-// tokens share every instruction. Each of the k rounds takes the largest
-// order-preserving 32-bit key and, among its holders, the lowest index.
+// 1024), lane l holding experts PER l .. PER l + PER - 1, so that a group of
+// experts is a whole number of neighbouring lanes in the usual cases.
+// Cross-lane steps stay inside the token's lanes: with 16 they are four DPP
+// rotations, so four tokens share every instruction.
+//
+// Selection works on order-preserving 32-bit keys of the scores. The k-th
+// largest of the lanes' own maxima is at most the k-th largest key, so the picks
+// are among the keys that reach it, usually few more than k: those are
+// listed in LDS in index order and each counts the ones that beat it (a larger
+// key, or an equal one earlier in the list), which is its place in the output.
+// With more than kList of them (many equal scores) or k > L the wave takes the picks
+// one by one instead, each the largest key and among its holders the lowest index.
 #pragma once
 
 #include "elem.hpp"
@@ -73,84 +81,203 @@ __device__ __forceinline__ float token_maxf(float v) {
     return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
   }));
 }
+template <int N>
+__device__ __forceinline__ double row_ror_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)row_ror<N>((uint32_t)(u >> 32)) << 32 | row_ror<N>((uint32_t)u));
+}
 template <int L>
 __device__ __forceinline__ double token_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d);
+  v += row_ror_f64<8>(v);
+  v += row_ror_f64<4>(v);
+  v += row_ror_f64<2>(v);
+  v += row_ror_f64<1>(v);
+  if (L == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+// value of the lane N below within its 16, 0 for the first N
+template <int N>
+__device__ __forceinline__ int row_shr(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x110 + N, 0xf, 0xf, true);
+}
+// sum of v over the token's lanes up to this one
+template <int L>
+__device__ __forceinline__ int token_upto(int v, int l) {
+  v += row_shr<1>(v);
+  v += row_shr<2>(v);
+  v += row_shr<4>(v);
+  v += row_shr<8>(v);
+  if (L == 64) {
+    const int o = __shfl(v, (l & 48) - 1 < 0 ? 0 : (l & 48) - 1);  // the row before's sum
+    const int a = l >= 16 ? o : 0;
+    const int o2 = __shfl(v, 15), o3 = __shfl(v, 31);
+    v += l < 16 ? 0 : l < 32 ? a : l < 48 ? a + o2 : a + o2 + o3;
+  }
   return v;
 }
 
-constexpr int kTopkGroups = 64;
+// e^t for t <= 0 in double, to a few 2^-52: t = n ln 2 + r with |r| <= ln 2 / 2, e^r
+// by its Taylor sum to r^12 (the next term is below 2^-52). Below -120 the
+// result stays near 1e-52, which no fp32 score or sum can tell from 0.
+__device__ __forceinline__ double exp_neg(double t) {
+  t = fmax(t, -120.0);
+  const double n = __builtin_rint(t * 1.4426950408889634074);
+  double r = fma(n, -6.93147180369123816490e-01, t);  // ln 2 in two parts: n times the first is exact
+  r = fma(n, -1.90821492927058770002e-10, r);
+  double p = 1.0 / 479001600.0;
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
 
-template <int DT, int L, int PER>
+// 1 / v for v in [1, 2^11), to a few 2^-52: v_rcp_f64 and two Newton steps
+__device__ __forceinline__ double rcp_f64(double v) {
+  double y = __builtin_amdgcn_rcp(v);
+  y = fma(fma(-v, y, 1.0), y, y);
+  return fma(fma(-v, y, 1.0), y, y);
+}
+
+// the two largest of (a1 >= a2) and (b1 >= b2)
+__device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+
+constexpr int kTopkGroups = 64;
+constexpr int kList = 64;  // candidates listed per token
+
+// VEC: rows and row starts are 16-byte aligned and E is a multiple of PER
+template <int DT, int L, int PER, bool VEC>
 __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
   constexpr int TPW = 64 / L;      // tokens per wave
   constexpr int TPB = 4 * TPW;     // per workgroup
   __shared__ float sel_lds[TPB][L * PER + 4];
   __shared__ float grp_lds[TPB][kTopkGroups];
+  __shared__ __attribute__((aligned(16))) uint32_t max_lds[TPB][L];
+  __shared__ __attribute__((aligned(16))) uint64_t list[TPB][kList + 2];  // expert, key
   const int lane = threadIdx.x & 63, l = lane & (L - 1);
   const int slot = threadIdx.x / L;
   const int t_in = blockIdx.x * TPB + slot;
   const int t = min(t_in, p.T - 1);  // lanes past the last token repeat it and store nothing
   const size_t row = (size_t)t * p.ld;
+  const int e0 = l * PER;
   constexpr float kMax = 3.402823466e38f;
 
   float sc[PER];
-  uint32_t key[PER];
   float top = -kMax;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 8) {
+      float v[8] = {-kMax, -kMax, -kMax, -kMax, -kMax, -kMax, -kMax, -kMax};
+      if (e0 < p.E) load8<DT>(p.logits, row + e0 + i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sc[i + j] = v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      sc[i] = -kMax;
+      if (e0 + i < p.E) sc[i] = load1<DT>(p.logits, row + e0 + i);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = l + L * i;
-    float x = -kMax;
-    if (e < p.E) x = load1<DT>(p.logits, row + e);
-    sc[i] = x != x ? -kMax : fminf(fmaxf(x, -kMax), kMax);  // NaN counts as the most negative value
+    sc[i] = sc[i] != sc[i] ? -kMax : fminf(fmaxf(sc[i], -kMax), kMax);  // NaN counts as the most negative value
     top = fmaxf(top, sc[i]);
   }
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sc[i] = (float)(1.0 / (1.0 + exp(-(double)sc[i])));
+    for (int i = 0; i < PER; ++i) {  // 1 / (1 + e^-x), as e^x / (1 + e^x) for x < 0
+      const double ex = exp_neg(-fabs((double)sc[i]));
+      sc[i] = (float)((sc[i] < 0.f ? ex : 1.0) * rcp_f64(1.0 + ex));
+    }
   } else {
     top = token_maxf<L>(top);
     double ex[PER], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      ex[i] = l + L * i < p.E ? exp((double)sc[i] - (double)top) : 0.0;
+      ex[i] = exp_neg((double)sc[i] - (double)top);
+      if (e0 + i >= p.E) ex[i] = 0.0;
       sum += ex[i];
     }
-    sum = 1.0 / token_sum<L>(sum);
+    sum = rcp_f64(token_sum<L>(sum));
 #pragma unroll
     for (int i = 0; i < PER; ++i) sc[i] = (float)(ex[i] * sum);
+  }
+  // selection scores
+  float sel[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sel[i] = sc[i];
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sel[i] += p.bias[min(e0 + i, p.E - 1)];
   }
   auto wave_sync = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
-  // selection keys (0: not a candidate)
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = l + L * i;
-    float v = sc[i];
-    if (p.bias && e < p.E) v += p.bias[e];
-    key[i] = e < p.E ? max(route_key(v), 1u) : 0u;
-    if (p.n_group) sel_lds[slot][e] = v;
-  }
+  uint64_t kept = ~0ull;  // groups that stay
+  int G = 1;
+  bool lanes_whole = true;  // a lane's experts are all of one group
+  bool lane_kept = true;    // and that group stays
   if (p.n_group) {
-    wave_sync();
-    const int G = p.E / p.n_group;
-    for (int g = l; g < p.n_group; g += L) {
+    G = p.E / p.n_group;
+    const int span = G / PER;  // lanes of a group
+    lanes_whole = G % PER == 0 && (span & (span - 1)) == 0 && span <= L;
+    if (lanes_whole) {
       float m1 = -INFINITY, m2 = -INFINITY;
-      for (int j = 0; j < G; ++j) {
-        const float v = sel_lds[slot][g * G + j];
-        m2 = fmaxf(m2, fminf(m1, v));
-        m1 = fmaxf(m1, v);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) merge_top2(m1, m2, sel[i], -INFINITY);
+      for (int d = 1; d < span; d <<= 1) {
+        const float o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+        merge_top2(m1, m2, o1, o2);
       }
-      grp_lds[slot][g] = p.top2 ? m1 + m2 : m1;
+      const float score = p.top2 ? m1 + m2 : m1;  // the same in all lanes of the group
+      if constexpr (L == 16) {
+        // the group stays if fewer than topk_group groups beat it, counted by lanes
+        max_lds[slot][l] = __float_as_uint(e0 < p.E ? score : -INFINITY);
+        wave_sync();
+        const int first = l & ~(span - 1), lanes = p.E / PER;
+        int beat = 0;
+#pragma unroll
+        for (int m = 0; m < L; ++m) {
+          const float o = __uint_as_float(max_lds[slot][m]);
+          beat += m < lanes && (o > score || (o == score && m < first));
+        }
+        wave_sync();
+        lane_kept = beat < p.topk_group * span;
+      } else if (e0 < p.E && l % span == 0) {
+        grp_lds[slot][l / span] = score;
+      }
+    } else {  // groups that cut lanes apart: through LDS
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sel_lds[slot][e0 + i] = sel[i];
+      wave_sync();
+      for (int g = l; g < p.n_group; g += L) {
+        float m1 = -INFINITY, m2 = -INFINITY;
+        for (int j = 0; j < G; ++j) merge_top2(m1, m2, sel_lds[slot][g * G + j], -INFINITY);
+        grp_lds[slot][g] = p.top2 ? m1 + m2 : m1;
+      }
     }
     wave_sync();
     // a group stays if fewer than topk_group groups beat it (larger score, or equal and lower index)
-    uint64_t kept = 0;
-    for (int g0 = 0; g0 < p.n_group; g0 += L) {
+    const bool ranked = L == 16 && lanes_whole;
+    if (!ranked) kept = 0;
+    for (int g0 = ranked ? p.n_group : 0; g0 < p.n_group; g0 += L) {
       const int g = g0 + l;
       bool in = false;
       if (g < p.n_group) {
@@ -165,11 +292,85 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
       const uint64_t m = __ballot(in);
       kept |= (L == 64 ? m : (m >> (lane & ~(L - 1))) & ((1ull << (L & 63)) - 1)) << g0;
     }
+  }
+  uint32_t key[PER];  // 0: not a candidate
+  uint32_t top_key = 0;
+  if (L == 64 && p.n_group && lanes_whole) lane_kept = (kept >> (min(e0, p.E - 1) / G)) & 1ull;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = l + L * i;
-      if (e < p.E && !((kept >> (e / G)) & 1ull)) key[i] = 0u;
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i;
+    key[i] = e < p.E && lane_kept ? max(route_key(sel[i]), 1u) : 0u;
+  }
+  if (!lanes_whole) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (!((kept >> (min(e0 + i, p.E - 1) / G)) & 1ull)) key[i] = 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) top_key = max(top_key, key[i]);
+
+  // the k-th largest lane maximum, and how many keys reach it
+  uint32_t thr = 1u;
+  int upto = 0, mine = 0, count = kList + 1;
+  if (p.k <= L) {
+    max_lds[slot][l] = top_key;
+    wave_sync();
+    int above = 0;
+#pragma unroll
+    for (int m = 0; m < L; ++m) above += max_lds[slot][m] > top_key;
+    thr = max(token_min<L>(above < p.k ? top_key : 0xffffffffu), 1u);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine += key[i] >= thr;
+    upto = token_upto<L>(mine, l);
+    count = (int)token_max<L>((uint32_t)upto);
+  }
+  if (__all(count <= kList)) {
+    uint64_t* at = &list[slot][upto - mine];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] >= thr) *at++ = (uint64_t)key[i] << 32 | (uint32_t)(e0 + i);
+    if (l < 2) list[slot][count + l] = 0u;  // whole pairs below
+    if (p.bias) {  // the picks' weights are their scores without the bias
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sel_lds[slot][e0 + i] = sc[i];
     }
+    wave_sync();
+    double total = 0.0;
+    constexpr int CPL = kList / L;  // candidates per lane, nearly always one
+    int place[CPL], id[CPL];
+    float s[CPL];
+#pragma unroll
+    for (int h = 0; h < CPL; ++h) {
+      place[h] = -1;
+      if (!__any(L * h < count)) continue;
+      const int j = l + L * h;
+      const uint64_t c = j < count ? list[slot][j] : ~0ull;
+      const uint32_t ck = (uint32_t)(c >> 32);
+      id[h] = (int)(uint32_t)c;
+      int n = 0;
+      for (int x = 0; x < count; x += 2) {
+        const u32x4 o = *(const u32x4*)&list[slot][x];
+        n += o[1] > ck || (o[1] == ck && x < j);
+        n += o[3] > ck || (o[3] == ck && x + 1 < j);
+      }
+      if (j < count && n < p.k) {
+        place[h] = n;
+        s[h] = p.bias ? sel_lds[slot][id[h]]
+                      : __uint_as_float((ck & 0x80000000u) ? ck & 0x7fffffffu : ~ck);
+        total += (double)s[h];
+      }
+    }
+    if (p.renorm) total = token_sum<L>(total);
+    if (t_in >= p.T) return;
+#pragma unroll
+    for (int h = 0; h < CPL; ++h) {
+      if (place[h] < 0) continue;
+      float w = s[h];
+      if (p.renorm) w = total > 0.0 ? (float)((double)w / total) : 0.f;
+      p.ids[(size_t)t * p.k + place[h]] = id[h];
+      p.w[(size_t)t * p.k + place[h]] = w * p.scale;
+    }
+    return;
   }
 
   double total = 0.0;
@@ -183,16 +384,16 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
     uint32_t at = 0xffffffffu;
 #pragma unroll
     for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == best) at = (uint32_t)(l + L * i);
+      if (key[i] == best) at = (uint32_t)(e0 + i);
     at = token_min<L>(at);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (at == (uint32_t)(l + L * i)) {
+      if (at == (uint32_t)(e0 + i)) {
         s = sc[i];
         key[i] = 0u;
       }
-    s = __shfl(s, (int)((lane & ~(L - 1)) | (at & (L - 1))));
+    s = __shfl(s, (int)((lane & ~(L - 1)) | (at / PER & (L - 1))));
     total += (double)s;
     if (l == (r & (L - 1))) {
       my_id[r >= L] = (int)at;
