@@ -150,7 +150,7 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
 // ----------------------------------------------------------------- routing
 template <int DT>
 void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
-  const bool row16 = aligned(q.logits, 16) && q.ld * moe::elem_size(DT) % 16 == 0;
+  const bool row16 = aligned(q.logits, 16) && aligned(q.bias, 16) && q.ld * moe::elem_size(DT) % 16 == 0;
 #define MOE_ROUTE_TOPK(L, PER)                                                                              \
   {                                                                                                         \
     const dim3 g((unsigned)((q.T + 256 / L - 1) / (256 / L)));                                              \
@@ -323,6 +323,7 @@ int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const fl
   q.sigmoid = p->score == MOE_SCORE_SIGMOID;
   q.n_group = grouped ? p->n_group : 0;
   q.topk_group = p->topk_group;
+  q.per_group = grouped ? p->E / p->n_group : 0;
   q.top2 = p->group_score == MOE_GROUP_TOP2;
   q.renorm = p->renormalize;
   q.scale = p->routed_scaling_factor;

@@ -14,11 +14,11 @@
 // rotations, so four tokens share every instruction.
 //
 // Selection works on order-preserving 32-bit keys of the scores. The k-th
-// largest of the lanes' own maxima is at most the k-th largest key, so the picks
-// are among the keys that reach it, usually few more than k: those are
+// largest of the lanes' own maxima (or two largest) is at most the k-th largest key, so
+// the picks are among the keys that reach it, usually few more than k: those are
 // listed in LDS in index order and each counts the ones that beat it (a larger
 // key, or an equal one earlier in the list), which is its place in the output.
-// With more than kList of them (many equal scores) or k > L the wave takes the picks
+// With more than kList of them (many equal scores) the wave takes the picks
 // one by one instead, each the largest key and among its holders the lowest index.
 #pragma once
 
@@ -36,6 +36,7 @@ struct RouteTopkParams {
   int32_t T, E, k;
   int32_t sigmoid;     // scores: 1 sigmoid, 0 softmax
   int32_t n_group, topk_group;  // n_group 0: no groups
+  int32_t per_group;            // E / n_group
   int32_t top2;        // group score: 1 sum of the two largest, 0 the largest
   int32_t renorm;
   float scale;
@@ -119,11 +120,11 @@ __device__ __forceinline__ int token_upto(int v, int l) {
   return v;
 }
 
-// e^t for t <= 0 in double, to a few 2^-52: t = n ln 2 + r with |r| <= ln 2 / 2, e^r
-// by its Taylor sum to r^12 (the next term is below 2^-52). Below -120 the
-// result stays near 1e-52, which no fp32 score or sum can tell from 0.
-__device__ __forceinline__ double exp_neg(double t) {
-  t = fmax(t, -120.0);
+// e^t in double, to a few 2^-52: t = n ln 2 + r with |r| <= ln 2 / 2, e^r
+// by its Taylor sum to r^12 (the next term is below 2^-52). t is taken within
+// +-120: e^-120 is near 1e-52, which no fp32 score or sum can tell from 0.
+__device__ __forceinline__ double exp_120(double t) {
+  t = fmin(fmax(t, -120.0), 120.0);
   const double n = __builtin_rint(t * 1.4426950408889634074);
   double r = fma(n, -6.93147180369123816490e-01, t);  // ln 2 in two parts: n times the first is exact
   r = fma(n, -1.90821492927058770002e-10, r);
@@ -143,7 +144,7 @@ __device__ __forceinline__ double exp_neg(double t) {
   return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
-// 1 / v for v in [1, 2^11), to a few 2^-52: v_rcp_f64 and two Newton steps
+// 1 / v for v in [1, 2^200), to a few 2^-52: v_rcp_f64 and two Newton steps
 __device__ __forceinline__ double rcp_f64(double v) {
   double y = __builtin_amdgcn_rcp(v);
   y = fma(fma(-v, y, 1.0), y, y);
@@ -159,26 +160,37 @@ __device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float
 constexpr int kTopkGroups = 64;
 constexpr int kList = 64;  // candidates listed per token
 
-// VEC: rows and row starts are 16-byte aligned and E is a multiple of PER
+// VEC: rows, row starts and bias are 16-byte aligned and E is a multiple of PER
 template <int DT, int L, int PER, bool VEC>
 __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
   constexpr int TPW = 64 / L;      // tokens per wave
   constexpr int TPB = 4 * TPW;     // per workgroup
-  __shared__ float sel_lds[TPB][L * PER + 4];
-  __shared__ float grp_lds[TPB][kTopkGroups];
-  __shared__ __attribute__((aligned(16))) uint32_t max_lds[TPB][L];
-  __shared__ __attribute__((aligned(16))) uint64_t list[TPB][kList + 2];  // expert, key
-  const int lane = threadIdx.x & 63, l = lane & (L - 1);
   const int slot = threadIdx.x / L;
+  __shared__ float sel_lds[TPB][L * PER + 4];
+  __shared__ __attribute__((aligned(16))) uint32_t max_lds[TPB][2 * L];
+  __shared__ __attribute__((aligned(16))) uint64_t list[TPB][kList + 2];  // expert, key
+  float* const grp = (float*)list[slot];  // group scores, before the list
+  static_assert(kTopkGroups * 4 <= (kList + 2) * 8, "group scores fit the list");
+  const int lane = threadIdx.x & 63, l = lane & (L - 1);
   const int t_in = blockIdx.x * TPB + slot;
   const int t = min(t_in, p.T - 1);  // lanes past the last token repeat it and store nothing
   const size_t row = (size_t)t * p.ld;
   const int e0 = l * PER;
   constexpr float kMax = 3.402823466e38f;
 
-  float sc[PER];
+  float sc[PER], bias[PER];
   float top = -kMax;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) bias[i] = 0.f;
   if constexpr (VEC) {
+    if (p.bias && e0 < p.E) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        const f32x4 b = *(const f32x4*)(p.bias + e0 + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bias[i + j] = b[j];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < PER; i += 8) {
       float v[8] = {-kMax, -kMax, -kMax, -kMax, -kMax, -kMax, -kMax, -kMax};
@@ -189,27 +201,28 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      sc[i] = -kMax;
-      if (e0 + i < p.E) sc[i] = load1<DT>(p.logits, row + e0 + i);
+      sc[i] = load1<DT>(p.logits, row + min(e0 + i, p.E - 1));
+      if (e0 + i >= p.E) sc[i] = -kMax;
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) bias[i] = p.bias[min(e0 + i, p.E - 1)];
     }
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    sc[i] = sc[i] != sc[i] ? -kMax : fminf(fmaxf(sc[i], -kMax), kMax);  // NaN counts as the most negative value
+    sc[i] = fminf(fmaxf(sc[i], -kMax), kMax);  // NaN becomes the most negative value
     top = fmaxf(top, sc[i]);
   }
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {  // 1 / (1 + e^-x), as e^x / (1 + e^x) for x < 0
-      const double ex = exp_neg(-fabs((double)sc[i]));
-      sc[i] = (float)((sc[i] < 0.f ? ex : 1.0) * rcp_f64(1.0 + ex));
-    }
+    for (int i = 0; i < PER; ++i) sc[i] = (float)rcp_f64(1.0 + exp_120(-(double)sc[i]));
   } else {
     top = token_maxf<L>(top);
     double ex[PER], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      ex[i] = exp_neg((double)sc[i] - (double)top);
+      ex[i] = exp_120((double)sc[i] - (double)top);
       if (e0 + i >= p.E) ex[i] = 0.0;
       sum += ex[i];
     }
@@ -220,11 +233,7 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
   // selection scores
   float sel[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sel[i] = sc[i];
-  if (p.bias) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sel[i] += p.bias[min(e0 + i, p.E - 1)];
-  }
+  for (int i = 0; i < PER; ++i) sel[i] = sc[i] + bias[i];
   auto wave_sync = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -235,7 +244,7 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
   bool lanes_whole = true;  // a lane's experts are all of one group
   bool lane_kept = true;    // and that group stays
   if (p.n_group) {
-    G = p.E / p.n_group;
+    G = p.per_group;
     const int span = G / PER;  // lanes of a group
     lanes_whole = G % PER == 0 && (span & (span - 1)) == 0 && span <= L;
     if (lanes_whole) {
@@ -261,7 +270,7 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
         wave_sync();
         lane_kept = beat < p.topk_group * span;
       } else if (e0 < p.E && l % span == 0) {
-        grp_lds[slot][l / span] = score;
+        grp[l / span] = score;
       }
     } else {  // groups that cut lanes apart: through LDS
 #pragma unroll
@@ -270,7 +279,7 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
       for (int g = l; g < p.n_group; g += L) {
         float m1 = -INFINITY, m2 = -INFINITY;
         for (int j = 0; j < G; ++j) merge_top2(m1, m2, sel_lds[slot][g * G + j], -INFINITY);
-        grp_lds[slot][g] = p.top2 ? m1 + m2 : m1;
+        grp[g] = p.top2 ? m1 + m2 : m1;
       }
     }
     wave_sync();
@@ -281,10 +290,10 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
       const int g = g0 + l;
       bool in = false;
       if (g < p.n_group) {
-        const float mine = grp_lds[slot][g];
+        const float mine = grp[g];
         int beat = 0;
         for (int o = 0; o < p.n_group; ++o) {
-          const float v = grp_lds[slot][o];
+          const float v = grp[o];
           beat += v > mine || (v == mine && o < g);
         }
         in = beat < p.topk_group;
@@ -309,16 +318,40 @@ __global__ __launch_bounds__(256) void k_route_topk(const RouteTopkParams p) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) top_key = max(top_key, key[i]);
 
-  // the k-th largest lane maximum, and how many keys reach it
+  // A key that the picks reach: the k-th largest of the lanes' maxima, or, where
+  // those are few for k (only the kept groups' lanes have any), of their two largest.
   uint32_t thr = 1u;
   int upto = 0, mine = 0, count = kList + 1;
-  if (p.k <= L) {
-    max_lds[slot][l] = top_key;
-    wave_sync();
-    int above = 0;
+  const bool two = (L == 16 && p.n_group) || p.k > L / 2;
+  if (p.k <= 2 * L) {
+    if (!two) {
+      max_lds[slot][l] = top_key;
+      wave_sync();
+      int above = 0;
 #pragma unroll
-    for (int m = 0; m < L; ++m) above += max_lds[slot][m] > top_key;
-    thr = max(token_min<L>(above < p.k ? top_key : 0xffffffffu), 1u);
+      for (int m = 0; m < L; ++m) above += max_lds[slot][m] > top_key;
+      thr = token_min<L>(above < p.k ? top_key : 0xffffffffu);
+    } else {
+      uint32_t next = 0;
+      top_key = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        next = max(next, min(top_key, key[i]));
+        top_key = max(top_key, key[i]);
+      }
+      max_lds[slot][l] = top_key;
+      max_lds[slot][L + l] = next;
+      wave_sync();
+      int above = 0, above2 = 0;
+#pragma unroll
+      for (int m = 0; m < 2 * L; ++m) {
+        const uint32_t o = max_lds[slot][m];
+        above += o > top_key;
+        above2 += o > next;
+      }
+      thr = token_min<L>(above2 < p.k ? next : above < p.k ? top_key : 0xffffffffu);
+    }
+    thr = max(thr, 1u);
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine += key[i] >= thr;
     upto = token_upto<L>(mine, l);

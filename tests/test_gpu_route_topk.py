@@ -75,6 +75,20 @@ def test_ties_masks_and_nonfinite_logits():
     assert (gw == 0).all()
 
 
+@pytest.mark.parametrize("E,k", [(70, 5), (256, 8), (256, 32), (1000, 16), (1024, 32)])
+def test_many_equal_scores(E, k):
+    """More equal scores than the kernel lists candidates, with a few above and below them."""
+    l = torch.zeros(9, E)
+    l[1:, E // 2] = 1.0
+    l[2:, :3] = -1.0
+    l[3:, E - 1] = 30.0
+    l[4:, ::7] = 25.0                                           # sigmoid rounds these and the 30 to 1
+    for score in ("softmax", "sigmoid"):
+        check(l, k, None, score=score)
+        if E % 8 == 0:
+            check(l, k, None, score=score, n_group=8, topk_group=4, group_score="max")
+
+
 def test_minus_infinity_bias_masks_experts():
     b = np.zeros(64, np.float32)
     b[::2] = -np.inf
