@@ -145,9 +145,9 @@ __device__ __forceinline__ void store4(const Params& p, int row, int col, f32x4 
 // access covers 32 bytes of each of 32 rows and no LDS is needed. The accesses
 // go through buffer resources over the block's rows: one 32-bit offset per lane
 // (64-bit addresses for every row made the compiler spill), and rows past M
-// or columns past N lie outside them, read 0 and are not written. EXTRA: there is
-// a bias or an addend (one that is missing reads 0 through an empty resource).
-template <int DT, bool EXTRA, int FN, int FM>
+// or columns past N lie outside them, read 0 and are not written. EXTRA: 1 there is an
+// addend, 2 a bias and perhaps an addend (a missing one reads 0 through an empty resource).
+template <int DT, int EXTRA, int FN, int FM>
 __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][FM], int mw, int nw, int lane) {
   constexpr int FG = FN < 2 ? FN : 2;  // column fragments at a time
   constexpr uint32_t SZ = elem_size(DT);
@@ -159,58 +159,68 @@ __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][F
   const __amdgpu_buffer_rsrc_t rsD =
       rsrc((const uint8_t*)p.add + (size_t)mw * p.ld_add * SZ, p.add ? (uint32_t)(((rows - 1) * p.ld_add + p.N) * SZ) : 0u);
   const __amdgpu_buffer_rsrc_t rsB = rsrc(p.bias, p.bias ? 4u * (uint32_t)p.N : 0u);
-  uint32_t o = ((uint32_t)(lane & 31) * (uint32_t)p.ldo + (uint32_t)col0) * SZ;
-  uint32_t d = ((uint32_t)(lane & 31) * (uint32_t)p.ld_add + (uint32_t)col0) * SZ;
+  const uint32_t o = ((uint32_t)(lane & 31) * (uint32_t)p.ldo + (uint32_t)col0) * SZ;
+  const uint32_t d = ((uint32_t)(lane & 31) * (uint32_t)p.ld_add + (uint32_t)col0) * SZ;
+  // Strips of FG column fragments x 32 rows. Where the registers allow it (16-bit
+  // addend alone) the next strip's addend is loaded before this strip's stores.
+  constexpr bool AHEAD = EXTRA == 1 && SZ == 2;
+  constexpr int NI = FN / FG, NSTRIP = FM * NI;
+  u32x4 ad[AHEAD ? 2 : 1][2 * FG][SZ / 2], bi[2 * FG][2];
+  auto load_add = [&](int strip, u32x4 (&dst)[2 * FG][SZ / 2]) {
+    const int j = strip / NI, i0 = strip % NI * FG;
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
+    for (int q = 0; q < 2 * FG; ++q) {
+      const int c = 32 * i0 + 16 * q;  // past col0
+      const uint32_t at = col0 + c < p.N ? d + (uint32_t)j * 32u * (uint32_t)p.ld_add * SZ + c * SZ : kNoLoad;
 #pragma unroll
-    for (int i0 = 0; i0 < FN; i0 += FG) {
-      // results stay in AGPRs until they are wanted (moved to VGPRs as a whole they would spill)
-#pragma unroll
-      for (int i = 0; i < FG; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
-      u32x4 ad[2 * FG][SZ / 2], bi[2 * FG][2];
-      if constexpr (EXTRA) {
-#pragma unroll
-        for (int q = 0; q < 2 * FG; ++q) {
-          const int c = 32 * i0 + 16 * q;  // past col0
-          const bool in = col0 + c < p.N;
-#pragma unroll
-          for (uint32_t h = 0; h < SZ / 2; ++h)
-            ad[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsD, in ? d + c * SZ + 16 * h : kNoLoad, 0, 0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            bi[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsB, 4 * (uint32_t)(col0 + c) + 16 * h, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 2 * FG; ++q) {
-        const f32x16& a = acc[i0 + q / 2][j];
-        const int h = q & 1, c = 32 * i0 + 16 * q;
-        float v[8], x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[8 * h + k]),
-                                                          __float_as_uint(a[8 * h + 4 + k]), false, false);
-          v[k] = __uint_as_float(t[0]);
-          v[4 + k] = __uint_as_float(t[1]);
-        }
-        if constexpr (EXTRA) load8<DT>(ad[q], 0, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[k] *= p.alpha;
-          if constexpr (EXTRA) v[k] = v[k] + __uint_as_float(bi[q][k / 4][k % 4]) + x[k];
-        }
-        u32x4 r[SZ / 2];
-        store8<DT>(r, 0, v);
-        const bool in = col0 + c < p.N;
-#pragma unroll
-        for (uint32_t w = 0; w < SZ / 2; ++w)
-          __builtin_amdgcn_raw_buffer_store_b128(r[w], rsO, in ? o + c * SZ + 16 * w : kNoLoad, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // the registers hold no more than this much at once
+      for (uint32_t h = 0; h < SZ / 2; ++h) dst[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsD, at + 16 * h, 0, 0);
     }
-    o += 32 * (uint32_t)p.ldo * SZ;
-    d += 32 * (uint32_t)p.ld_add * SZ;
+  };
+  if constexpr (AHEAD) load_add(0, ad[0]);
+#pragma unroll
+  for (int strip = 0; strip < NSTRIP; ++strip) {
+    const int j = strip / NI, i0 = strip % NI * FG;
+    // results stay in AGPRs until they are wanted (moved to VGPRs as a whole they would spill)
+#pragma unroll
+    for (int i = 0; i < FG; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
+    if constexpr (AHEAD) {
+      if (strip + 1 < NSTRIP) load_add(strip + 1, ad[(strip + 1) & 1]);
+    } else if constexpr (EXTRA != 0) {
+      load_add(strip, ad[0]);
+    }
+    if constexpr (EXTRA == 2) {
+#pragma unroll
+      for (int q = 0; q < 2 * FG; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          bi[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rsB, 4 * (uint32_t)(col0 + 32 * i0 + 16 * q) + 16 * h, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 2 * FG; ++q) {
+      const f32x16& a = acc[i0 + q / 2][j];
+      const int h = q & 1, c = 32 * i0 + 16 * q;
+      float v[8], x[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[8 * h + k]),
+                                                        __float_as_uint(a[8 * h + 4 + k]), false, false);
+        v[k] = __uint_as_float(t[0]);
+        v[4 + k] = __uint_as_float(t[1]);
+      }
+      if constexpr (EXTRA != 0) load8<DT>(ad[AHEAD ? strip & 1 : 0][q], 0, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] *= p.alpha;
+        if constexpr (EXTRA == 2) v[k] += __uint_as_float(bi[q][k / 4][k % 4]);
+        if constexpr (EXTRA != 0) v[k] += x[k];
+      }
+      u32x4 r[SZ / 2];
+      store8<DT>(r, 0, v);
+      const uint32_t at = col0 + c < p.N ? o + (uint32_t)j * 32u * (uint32_t)p.ldo * SZ + c * SZ : kNoLoad;
+#pragma unroll
+      for (uint32_t w = 0; w < SZ / 2; ++w) __builtin_amdgcn_raw_buffer_store_b128(r[w], rsO, at + 16 * w, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // the registers hold no more than this much at once
   }
 }
 
@@ -239,7 +249,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // (even and odd blocks of the first 256 K values, then of the second); a lane
 // reads one word per fragment and 256 K values, whose byte s is the scale of its
 // block in step s.
-template <int AF, int BM, int BN, int BK, int NBUF, int G>
+template <int AF, int BM, int BN, int BK, int NBUF>
 struct Tile {
   static constexpr int AB = AF == mxf::MXFP8 ? BK : BK / 2, WB = BK / 2;  // bytes of a row per stage
   static constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB;
@@ -252,10 +262,9 @@ struct Tile {
   static constexpr int SR = ROWS * SP / 256;               // per thread
   static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
   static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
-  static constexpr int LDS = G * (NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 64));
-  static constexpr int WPS = G * (LDS <= 80 * 1024 ? 2 : 1);  // waves per SIMD (160 KB of LDS)
-  static_assert(4 / NBUF * 32 * EROW * 4 <= G * STAGE, "epilogue staging: the waves share the buffers");
-  static_assert((G - 1) * BM * BN * 4 <= NBUF * G * STAGE, "partial sums meet in the buffers");
+  static constexpr int LDS = NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 0);
+  static constexpr int WGS = LDS <= 80 * 1024 ? 2 : 1;     // workgroups per compute unit at least (160 KB of LDS)
+  static_assert(4 / NBUF * 32 * EROW * 4 <= STAGE, "epilogue staging: the waves share the buffers");
   static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && BK == 128, "a scale word holds 256 K values");
   static_assert(NBUF == 4 || BN % (256 / SP) == 0, "an instruction fetches scale rows of one operand");
 };
@@ -266,28 +275,18 @@ __device__ __forceinline__ int slot_of(int c, int r) {
   return RB == 256 ? c ^ (r & 15) : RB == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int AF, int BM, int BN, int BK, int NBUF, int G>
-__global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void k_tile(const Params p) {
-  using T = Tile<AF, BM, BN, BK, NBUF, G>;
-  __shared__ __attribute__((aligned(16))) uint8_t all0[G * T::STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t all1[G * T::STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t all2[NBUF == 4 ? G * T::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t all3[NBUF == 4 ? G * T::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[G][2][NBUF == 4 ? 16 : T::ROWS * 16];
-  const int lane = threadIdx.x & 63;
-  const int tid = threadIdx.x & 255;     // within the group
+template <int AF, int BM, int BN, int BK, int NBUF>
+__global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile(const Params p) {
+  using T = Tile<AF, BM, BN, BK, NBUF>;
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t buf2[NBUF == 4 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[NBUF == 4 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][NBUF == 4 ? 16 : T::ROWS * 16];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = G == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8);
   const int wm = wave & 1, wn = wave >> 1;
   const int lr = lane & 31, lq = lane >> 5;
-  uint8_t* const buf0 = all0 + grp * T::STAGE;
-  uint8_t* const buf1 = all1 + grp * T::STAGE;
-  uint8_t* buf2 = nullptr;
-  uint8_t* buf3 = nullptr;
-  if constexpr (NBUF == 4) {
-    buf2 = all2 + grp * T::STAGE;
-    buf3 = all3 + grp * T::STAGE;
-  }
 
   // Workgroup b runs on XCD b mod 8; each XCD takes a contiguous run of the
   // tiles, ordered in groups of 4 row tiles, columns outer inside a group, so
@@ -301,19 +300,13 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
   const int m0 = __builtin_amdgcn_readfirstlane((4 * g + in % gm) * BM);
   const int n0 = __builtin_amdgcn_readfirstlane(in / gm * BN);
 
-  // K range of this group: KS stages (the last group's may lie past the end:
-  // zeros), a_row and w_row bytes and nblk scale blocks of each row
-  const int KS = ((p.K + BK - 1) / BK + G - 1) / G;
-  const int row_blk = p.K >> 5;
-  const int blk0 = grp * KS * (BK / 32);
-  const int nblk = max(0, min(row_blk - blk0, KS * (BK / 32)));
-  const uint32_t a_row = (uint32_t)nblk * (AF == mxf::MXFP8 ? 32u : 16u), w_row = (uint32_t)nblk * 16u;
-  const uint32_t w_ld = (uint32_t)row_blk * 16u;
+  const int KS = (p.K + BK - 1) / BK;    // stages
+  const int nblk = p.K >> 5;
+  const uint32_t a_row = AF == mxf::MXFP8 ? (uint32_t)p.K : (uint32_t)p.K / 2, w_row = (uint32_t)p.K / 2;
+
   const int a_rows = min(BM, p.M - m0), w_rows = min(BN, p.N - n0);
-  const __amdgpu_buffer_rsrc_t rsA =
-      rsrc(p.a + (size_t)m0 * p.lda + (size_t)grp * KS * T::AB, (uint32_t)((a_rows - 1) * p.lda + a_row));
-  const __amdgpu_buffer_rsrc_t rsW =
-      rsrc(p.w + (size_t)n0 * w_ld + (size_t)grp * KS * T::WB, (uint32_t)(w_rows - 1) * w_ld + w_row);
+  const __amdgpu_buffer_rsrc_t rsA = rsrc(p.a + (size_t)m0 * p.lda, (uint32_t)((a_rows - 1) * p.lda + a_row));
+  const __amdgpu_buffer_rsrc_t rsW = rsrc(p.w + (size_t)n0 * w_row, (uint32_t)w_rows * w_row);
 
   // load assignment: wave w fills the w-th quarter of each operand
   uint32_t a_off[T::AL], w_off[T::WL];
@@ -330,11 +323,10 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
     const int at = wave * (T::W_BYTES / 4) + i * 1024 + lane * 16;
     const int r = at / T::WB;
     w_ch[i] = 16u * slot_of<T::WB>((at % T::WB) / 16, r);
-    w_off[i] = r < w_rows ? (uint32_t)r * w_ld + w_ch[i] : kNoLoad;
+    w_off[i] = r < w_rows ? (uint32_t)r * w_row + w_ch[i] : kNoLoad;
   }
   // Load instruction q of stage s into buf: first the activations', then the
   // weights'. The stage's place in K goes into the scalar offset, which the range
-  // check does not cover: mask_loads moves the lanes that would pass the row's
   // check does not cover: mask_loads moves the lanes that would pass the row's
   // end in the last stage, and all of them after it, out of range.
   // (Its arguments are plain variables: with array elements or template constants
@@ -366,12 +358,10 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
   // last (their results are never stored). SP lanes fetch SP consecutive 16-byte
   // pieces of one row (SP * 512 K values) in one go: what bounds the loads is
   // the number of 128-byte lines asked for, and a 16-byte piece costs a whole one.
-  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as + blk0;
-  const uint8_t* w_scb = p.w_sc + (size_t)n0 * row_blk + blk0;
-  const uint32_t a_tot =
-      (uint32_t)max((int64_t)0, min((int64_t)(p.M - 1 - m0) * p.ld_as + row_blk - blk0, (int64_t)0x7fffffff));
-  const uint32_t w_tot =
-      (uint32_t)max((int64_t)0, min((int64_t)(p.N - n0) * row_blk - blk0, (int64_t)0x7fffffff));
+  const uint8_t* a_scb = p.a_sc + (size_t)m0 * p.ld_as;
+  const uint8_t* w_scb = p.w_sc + (size_t)n0 * nblk;
+  const uint32_t a_tot = (uint32_t)min((int64_t)(p.M - 1 - m0) * p.ld_as + nblk, (int64_t)0x7fffffff);
+  const uint32_t w_tot = (uint32_t)min((int64_t)(p.N - n0) * nblk, (int64_t)0x7fffffff);
   constexpr int RPI = 256 / T::SP;  // rows per instruction
   const int piece = tid % T::SP, prow = tid / T::SP;
   u32x4 raw[T::SR];
@@ -383,7 +373,7 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
       const bool is_w = i * RPI < BN;
       const uint8_t* base = is_w ? w_scb : a_scb;
       const int r = is_w ? min(i * RPI + prow, w_rows - 1) : min(i * RPI - BN + prow, a_rows - 1);
-      const uint32_t off = (uint32_t)(r * (is_w ? row_blk : (int)p.ld_as) + b0);
+      const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
       if (whole) raw[i] = load_sc16(base, off);
       else raw[i] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
     }
@@ -393,14 +383,14 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
 #pragma unroll
     for (int i = 0; i < T::SR; ++i) {
       const u32x4 v = raw[i];
-      *(u32x4*)(scales[grp][g & 1] + (i * RPI + prow) * 16) =
+      *(u32x4*)(scales[g & 1] + (i * RPI + prow) * 16) =
           u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x06040200u), __builtin_amdgcn_perm(v[1], v[0], 0x07050301u),
                 __builtin_amdgcn_perm(v[3], v[2], 0x06040200u), __builtin_amdgcn_perm(v[3], v[2], 0x07050301u)};
     }
   };
   uint32_t sa[2][T::FM], sw[2][T::FN];  // scale words of a 256-K unit, and of the next
   auto read_scales = [&](int unit, uint32_t (&da)[T::FM], uint32_t (&dw)[T::FN]) {
-    const uint8_t* src = scales[grp][(unit >> 1) & 1] + (unit & 1) * 8 + 4 * lq + lr * 16;
+    const uint8_t* src = scales[(unit >> 1) & 1] + (unit & 1) * 8 + 4 * lq + lr * 16;
 #pragma unroll
     for (int i = 0; i < T::FN; ++i) dw[i] = *(const uint32_t*)(src + (wn * (BN / 2) + i * 32) * 16);
 #pragma unroll
@@ -426,7 +416,7 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int b0 = 64 * super + 32 * lq + 16 * h;
-        const uint32_t off = (uint32_t)(r * (is_w ? row_blk : (int)p.ld_as) + b0);
+        const uint32_t off = (uint32_t)(r * (is_w ? nblk : (int)p.ld_as) + b0);
         if (whole) raw_d[x][h] = load_sc16(base, off);
         else raw_d[x][h] = load_sc_tail(base, off, is_w ? w_tot : a_tot, min(nblk - b0, 16));
       }
@@ -499,7 +489,7 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
   // spare they come in the order they are wanted; else each weight fragment
   // takes its predecessor's registers once that is used up.
   auto read_row = [&](const uint8_t* buf, int st, i32x4 (&dw)[T::FN], i32x8 (&da)[T::FM], int i) {
-    if constexpr (T::WPS >= 2) {
+    if constexpr (T::WGS == 2) {
       read_w(buf, st, dw[i], i);
 #pragma unroll
       for (int j = i; j < T::FM; j += T::FN) read_a(buf, st, da[j], j);
@@ -581,20 +571,16 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
   else fetch_scales(0);
 #pragma unroll
   for (int q = 0; q < LT; ++q) load_piece(buf0, 0, q);
-  if constexpr (NBUF == 4) {
-    mask_loads(1);
+  mask_loads(1);
 #pragma unroll
-    for (int q = 0; q < LT; ++q) load_piece(buf1, 1, q);
+  for (int q = 0; q < (NBUF == 4 ? LT : LH); ++q) load_piece(buf1, 1, q);
+  if constexpr (NBUF == 4) {
     mask_loads(2);
 #pragma unroll
     for (int q = 0; q < LT; ++q) load_piece(buf2, 2, q);
     mask_loads(3);
 #pragma unroll
     for (int q = 0; q < LT; ++q) load_piece(buf3, 3, q);
-  } else {
-    mask_loads(1);
-#pragma unroll
-    for (int q = 0; q < LH; ++q) load_piece(buf1, 1, q);
   }
   if constexpr (NBUF == 2) publish_scales(0);
   wait_landed<NBUF == 4 ? 3 * LT : LH>();
@@ -650,57 +636,18 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
 #undef MOE_MXL_STEP
 #undef MOE_MXL_MFMA
 
-  // The last loads (of stages past the end) have landed and every wave has read its operands.
+  // The last loads (of stages past the end) have landed and every wave has read
+  // its operands: the buffers are free.
   wait_landed<0>();
   asm volatile("s_barrier" ::: "memory");
   const int mw = m0 + wm * (BM / 2), nw = n0 + wn * (BN / 2);
   pin();
-  if constexpr (G > 1) {
-    // The groups' partial sums meet in the (now idle) buffers, added in group order.
-    // Four values a lane at a time: piece x of group g's wave w at ((g - 1) * PIECES + x) * 4 + w KB.
-    constexpr int PIECES = T::FN * T::FM * 4;
-    constexpr int BUF_KB = G * T::STAGE / 1024;  // KB of each buffer array
-    auto at = [&](int kb) {
-      uint8_t* base = kb < BUF_KB ? all0 : all1;
-      if constexpr (NBUF == 4)
-        if (kb >= 2 * BUF_KB) base = kb < 3 * BUF_KB ? all2 : all3;
-      return (f32x4*)(base + (kb % BUF_KB) * 1024) + lane;
-    };
-    if (grp > 0) {
-#pragma unroll
-      for (int x = 0; x < PIECES; ++x) {
-        const f32x16& c = acc[x / 4 / T::FM][x / 4 % T::FM];
-        *at(((grp - 1) * PIECES + x) * 4 + wave) = f32x4{c[4 * (x % 4)], c[4 * (x % 4) + 1], c[4 * (x % 4) + 2], c[4 * (x % 4) + 3]};
-      }
-    }
-    wait_landed<0>();
-    asm volatile("s_barrier" ::: "memory");
-    if (grp == 0) {
-#pragma unroll
-      for (int x = 0; x < PIECES; ++x) {
-        f32x16& c = acc[x / 4 / T::FM][x / 4 % T::FM];
-#pragma unroll
-        for (int g1 = 0; g1 < G - 1; ++g1) {
-          const f32x4 v = *at((g1 * PIECES + x) * 4 + wave);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) c[4 * (x % 4) + k] += v[k];
-        }
-      }
-    }
-    if (!p.vec) {  // the value-by-value stores below reuse the buffers
-      wait_landed<0>();
-      asm volatile("s_barrier" ::: "memory");
-    }
-    if (grp > 0) return;
-    __builtin_amdgcn_sched_barrier(0);
-    pin();
-  }
   if (p.vec) {
-    const bool extra = p.bias || p.add;
 #define MOE_MXL_STORE(DT)                                                          \
   {                                                                                \
-    if (extra) store_block<DT, true, T::FN, T::FM>(p, acc, mw, nw, lane);          \
-    else store_block<DT, false, T::FN, T::FM>(p, acc, mw, nw, lane);               \
+    if (p.bias) store_block<DT, 2, T::FN, T::FM>(p, acc, mw, nw, lane);            \
+    else if (p.add) store_block<DT, 1, T::FN, T::FM>(p, acc, mw, nw, lane);        \
+    else store_block<DT, 0, T::FN, T::FM>(p, acc, mw, nw, lane);                   \
   }
     if (p.out_type == T_BF16) MOE_MXL_STORE(T_BF16)
     else if (p.out_type == T_FP16) MOE_MXL_STORE(T_FP16)
@@ -709,11 +656,11 @@ __global__ __launch_bounds__(256 * G, (Tile<AF, BM, BN, BK, NBUF, G>::WPS)) void
     return;
   }
   // Rows that take no 16-byte accesses: each wave turns its block around
-  // through its own part of the (now idle) buffers, 32 rows x EF column
-  // fragments at a time, and stores value by value.
+  // through its own part of the buffers, 32 rows x EF column fragments at a
+  // time, and stores value by value.
   float* strip;
-  if constexpr (NBUF == 4) strip = (float*)(wave < 2 ? wave == 0 ? all0 : all1 : wave == 2 ? all2 : all3);
-  else strip = (float*)((wave < 2 ? all0 : all1) + (wave & 1) * 32 * T::EROW * 4);
+  if constexpr (NBUF == 4) strip = (float*)(wave < 2 ? wave == 0 ? buf0 : buf1 : wave == 2 ? buf2 : buf3);
+  else strip = (float*)((wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * T::EROW * 4);
   constexpr int CPR = T::EF * 8;       // 4-column pieces per strip row
   constexpr int RPP = 64 / CPR;        // rows per pass
 #pragma unroll
