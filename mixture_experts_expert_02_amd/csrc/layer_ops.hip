@@ -22,6 +22,8 @@ bool type_ok(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP16 || t == MOE_
 int64_t or_default(int64_t ld, int64_t d) { return ld ? ld : d; }
 
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int kMaxRows = 1 << 24;                        // 256 threads to a row still count in 32 bits
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;     // workgroups of 256 threads
 
 // rows of n values of the type, ld elements apart: 16-byte accesses at every multiple of 8
 int check_rows(const void* p, int64_t ld, int64_t n, int32_t type) {
@@ -90,7 +92,7 @@ void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
 int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
   if (!p || p->M < 0 || p->N <= 0 || p->K <= 0 || !type_ok(p->out_type) || !std::isfinite(p->alpha)) return MOE_EINVAL;
   if (p->a_fmt != MOE_MX_FP4 && p->a_fmt != MOE_MX_FP8) return MOE_EINVAL;
-  if (p->K % 32 || p->K > 1 << 20) return MOE_ENOTSUP;
+  if (p->K % 32 || p->K > 1 << 20 || p->M >= kMaxRows || p->N >= kMaxRows) return MOE_ENOTSUP;
   const int64_t cb = moe::mxf::code_bytes(p->a_fmt, p->K);
   q.lda = or_default(p->lda, cb);
   q.ld_as = or_default(p->ld_as, p->K / 32);
@@ -110,41 +112,44 @@ template <int AF, int BM, int BN, int BK, int NBUF>
 int launch_tile(moe::mxl::Params& q, hipStream_t s) {
   q.mt = (q.M + BM - 1) / BM;
   q.nt = (q.N + BN - 1) / BN;
-  const int64_t n = (int64_t)q.mt * q.nt;
-  if (n > 0x7ffffff0) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, s, q);
+  const int64_t n = ((int64_t)q.mt * q.nt + 7) / 8 * 8;
+  if (n > kMaxGrid) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF>), dim3((unsigned)n), dim3(256), 0, s, q);
   return launch_status();
 }
 
-template <int AF, int S, int MT>
+template <int AF, int S, int FN, int FM, bool LITE>
 int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
-  q.nt = (q.N + 15) / 16;
-  q.mt = (q.M + 16 * MT - 1) / (16 * MT);
-  const int64_t n = (int64_t)q.mt * q.nt;
-  if (n > 0x7ffffff0) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, MT>), dim3((unsigned)n), dim3(64 * S), 0, s, q);
+  q.nt = (q.N + 16 * FN - 1) / (16 * FN);
+  q.mt = (q.M + 16 * FM - 1) / (16 * FM);
+  hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, FN, FM, LITE>), dim3((unsigned)(q.mt * q.nt)), dim3(64 * S), 0, s, q);
   return launch_status();
-}
-
-template <int AF, int MT>
-int launch_skinny_split(moe::mxl::Params& q, hipStream_t s) {
-  const int nt = (q.N + 15) / 16, kt = (q.K + 127) / 128;
-  if (nt >= 512 || kt <= 8) return launch_skinny<AF, 4, MT>(q, s);
-  if (nt >= 256 || kt <= 32) return launch_skinny<AF, 8, MT>(q, s);
-  return launch_skinny<AF, 16, MT>(q, s);
 }
 
 template <int AF>
 int launch_linear(moe::mxl::Params& q, hipStream_t s) {
-  if (q.M <= 16) return launch_skinny_split<AF, 1>(q, s);
-  if (q.M <= 32) return launch_skinny_split<AF, 2>(q, s);
+  constexpr bool F8 = AF == moe::mxf::MXFP8;
+  auto tiles = [&](int bm, int bn) { return (int64_t)((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
+  // Few rows: k_skinny; four waves, eight where that gives a compute unit at most
+  // one workgroup. us at M = 1: 2048 x 7168 (N x K) 5.6 with eight, 6.3 with four, 7168 x 2048 6.2 and 5.1. M = 16:
+  // 14336 x 4096 9.9 with 32 columns to a workgroup, 10.6 with 16; 2880 x 2880 6.8 and 5.2.
+  const bool few = q.N <= 16 * 256;
+  if (q.M <= (F8 ? 4 : 8))
+    return few ? launch_skinny<AF, 8, 1, 1, true>(q, s) : launch_skinny<AF, 4, 1, 1, true>(q, s);
+  if (q.M <= 16) return few ? launch_skinny<AF, 8, 1, 1, false>(q, s) : launch_skinny<AF, 4, 2, 1, false>(q, s);
+  // More of them while such workgroups of 32 x 16 find place on the chip at once (96 KiB of LDS
+  // for MXFP8, 56 for MXFP4): 32 x 4096 x 14336 MXFP8 15 where 32 columns to a workgroup take 17, 128 x 1024 x 7168 9.4
+  // where tiles of 64 x 64 take 13.5; MXFP4 7.8 and 12.7. With twice as many 128 x 2048 x 7168 MXFP8 17 and 13.6.
+  if (tiles(32, 16) <= (F8 ? 256 : 512)) return launch_skinny<AF, 4, 1, 2, false>(q, s);
+  // 24 x 7168 x 7168 MXFP8 12.3 where 16 columns take 17.7; 64 x 7168 x 7168 17 where tiles of 64 x 64 take 21,
+  // but 33 x 7168 x 2048 8.3 and 6.3, 64 x 14336 x 4096 21 and 14.
+  if (q.M <= 32 || (q.M <= 64 && q.K > 4096 && tiles(64, 64) <= 128))
+    return launch_skinny<AF, F8 ? 2 : 4, 2, 2, false>(q, s);
   // The largest tile that still gives most compute units one. Measured at 160-256
   // tiles (us, the tile taken against the next smaller): 300 x 7168 x 7168 MXFP8 29
   // against 33, 1024 x 4096 x 4096 MXFP8 21 against 22, MXFP4 16 against 21; below: 512 x 4096 x 4096
   // with 128 tiles of 128 x 128 17 against 13, 128 x 7168 x 7168 MXFP4 with 112 of 64 x 128 16 against 13.
-  constexpr bool F8 = AF == moe::mxf::MXFP8;
   constexpr int BM = F8 ? 128 : 256;
-  auto tiles = [&](int bm, int bn) { return (int64_t)((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
   if (tiles(BM, 256) >= 192) return launch_tile<AF, BM, 256, F8 ? 128 : 256, 2>(q, s);
   if (tiles(128, 128) >= 160) return launch_tile<AF, 128, 128, 128, 4>(q, s);
   if (tiles(64, 128) >= 160) return launch_tile<AF, 64, 128, 128, 4>(q, s);
@@ -233,7 +238,7 @@ int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residu
   if (!std::isfinite(p->eps) || p->eps < 0.f) return MOE_EINVAL;
   if (p->mx_fmt != MOE_MX_NONE && p->mx_fmt != MOE_MX_FP4 && p->mx_fmt != MOE_MX_FP8) return MOE_EINVAL;
   const bool mx = p->mx_fmt != MOE_MX_NONE;
-  if (p->H > 16384 || p->H % (mx ? 32 : 8)) return MOE_ENOTSUP;
+  if (p->T >= kMaxRows || p->H > 16384 || p->H % (mx ? 32 : 8)) return MOE_ENOTSUP;
   if (p->T == 0) return MOE_OK;
   if (!x || !weight || !aligned(weight, 16) || !residual != !residual_out || (!y && !mx)) return MOE_EINVAL;
   moe::NormParams q{};
@@ -301,7 +306,7 @@ int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const fl
   if (p->group_score != MOE_GROUP_MAX && p->group_score != MOE_GROUP_TOP2) return MOE_EINVAL;
   if (p->renormalize != 0 && p->renormalize != 1) return MOE_EINVAL;
   if (p->n_group < 0 || !std::isfinite(p->routed_scaling_factor)) return MOE_EINVAL;
-  if (p->E > moe::kRouteMaxE || p->k > moe::kRouteMaxK || p->n_group > moe::kTopkGroups) return MOE_ENOTSUP;
+  if (p->T >= kMaxRows || p->E > moe::kRouteMaxE || p->k > moe::kRouteMaxK || p->n_group > moe::kTopkGroups) return MOE_ENOTSUP;
   const bool grouped = p->n_group > 1;
   if (grouped && (p->E % p->n_group || p->topk_group < 1 || p->topk_group > p->n_group ||
                   (p->group_score == MOE_GROUP_TOP2 && p->E / p->n_group < 2) ||

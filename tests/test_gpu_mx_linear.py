@@ -9,7 +9,16 @@ so the sum is within K * 2^-23 * S (|alpha| S with alpha). At most 16 partial su
 are joined, and alpha, bias and add round once each: 20 more such terms; then
 half a step of the output type. (K / 64 in place of K, one rounding per block product
 of 64, was the first reading and is too small by this count: one case came
-to 2.2 times it.)"""
+to 2.2 times it.)
+
+MXFP8 has one more term. The MFMA with an e4m3 operand adds the products of eight
+consecutive K values after cutting each, toward zero, to a multiple of
+u = 2^-13 2^e, e the largest sum of the two exponents in the eight (test_cut_of_small_products
+pins it: 256 beside 2^-7 in the same eight gives 256, in the next eight 256 + 2^-7). Significands are in [1, 2),
+so u <= 2^-13 max|p|, and a product p, an integer times lsb(a) lsb(w), loses nothing where that is a
+multiple of u and less than min(|p|, u) otherwise: `cut` sums this over K. The products of
+e2m1 with e2m1 span less than the 13 bits, so MXFP4 has no such term. (K 2^-23 S alone was
+passed by 1% at 200 x 1501 x 160, where a row's S is little more than one product.)"""
 import numpy as np
 import pytest
 import torch
@@ -34,18 +43,41 @@ def operands(seed, M, N, K, fmt):
     return a, sc, w, ws
 
 
+def cut(A, W, a, sc, ws):
+    """Bound of what the cut of small products loses, for e4m3 codes a of the values A [M, K], W [N, K]."""
+    M, K = A.shape
+    N = W.shape[0]
+    x = np.maximum((a.numpy().astype(np.int32) & 0x7F) >> 3, 1) - 10             # exponent of an e4m3 code's last bit
+    la = np.ldexp(1.0, x + np.repeat(sc.numpy().astype(np.int32) - 127, 32, axis=1))
+    lw = np.ldexp(0.5, np.repeat(ws.numpy().astype(np.int32) - 127, 32, axis=1))   # e2m1: multiples of 0.5
+    A, W, la, lw = [torch.from_numpy(np.abs(v)).float().to(DEV) for v in (A, W, la, lw)]
+    res = torch.empty(M, N, dtype=torch.float64)
+    step = max(1, (1 << 26) // (N * K))
+    for m in range(0, M, step):
+        p = A[m:m + step, None, :] * W
+        u = p.view(-1, N, K // 8, 8).amax(-1).mul(2.0 ** -13).repeat_interleave(8, dim=-1)
+        p = torch.where(la[m:m + step, None, :] * lw < u, torch.minimum(p, u), 0.0)
+        res[m:m + step] = p.sum(-1, dtype=torch.float64).cpu()
+    return res.numpy()
+
+
+def sums(A, W, a, sc, w, ws, fmt):
+    """What the tolerance counts: S and the cut."""
+    return np.abs(A) @ np.abs(W).T, cut(A, W, a, sc, ws) if fmt == "mxfp8" else 0.0
+
+
 def reference(a, sc, w, ws, fmt, **kw):
     A, W = L.mx_values(a.numpy(), sc.numpy(), fmt), L.mx_values(w.numpy(), ws.numpy(), "mxfp4")
-    ref = L.mx_linear(A, W, **kw)
-    return ref, np.abs(A) @ np.abs(W).T
+    return L.mx_linear(A, W, **kw), sums(A, W, a, sc, w, ws, fmt)
 
 
 def check(out, ref, S, K, alpha=1.0, extra=0.0):
+    S, lost = S
     dt = out.dtype
     u = torch.finfo(dt).eps / 2
     tiny = torch.finfo(dt).smallest_normal * u
     got = out.double().cpu().numpy()
-    acc = (K + 20) * 2.0 ** -23 * (abs(alpha) * S + extra)
+    acc = (K + 20) * 2.0 ** -23 * (abs(alpha) * S + extra) + abs(alpha) * lost
     bound = np.abs(ref) * u + acc * (1 + u) + tiny
     err = np.abs(got - ref)
     assert np.isfinite(got).all()
@@ -75,10 +107,10 @@ def test_many_tiles(M, N, K, fmt):
     print(f"[mx_linear] {M}x{N}x{K} {fmt}", flush=True)
     ops = operands(3, M, N, K, fmt)
     out = moe.mx_linear(*[t.to(DEV) for t in ops], a_fmt=fmt, dtype=torch.float32)
-    A = torch.from_numpy(L.mx_values(ops[0].numpy(), ops[1].numpy(), fmt)).to(DEV)
-    W = torch.from_numpy(L.mx_values(ops[2].numpy(), ops[3].numpy(), "mxfp4")).to(DEV)
-    ref = (A @ W.t().contiguous()).cpu().numpy()
-    S = (A.abs() @ W.abs().t().contiguous()).cpu().numpy()
+    A, W = L.mx_values(ops[0].numpy(), ops[1].numpy(), fmt), L.mx_values(ops[2].numpy(), ops[3].numpy(), "mxfp4")
+    a, w = torch.from_numpy(A).to(DEV), torch.from_numpy(W).to(DEV)
+    ref = (a @ w.t().contiguous()).cpu().numpy()
+    S = (a.abs() @ w.abs().t().contiguous()).cpu().numpy(), cut(A, W, ops[0], ops[1], ops[3]) if fmt == "mxfp8" else 0.0
     check(out, ref, S, K)
 
 
@@ -146,9 +178,23 @@ def test_extreme_scales():
     out = moe.mx_linear(a.to(DEV), sc.to(DEV), w.to(DEV), ws.to(DEV), dtype=torch.float32).cpu()
     A, W = L.mx_values(a.numpy(), sc.numpy(), "mxfp8"), L.mx_values(w.numpy(), ws.numpy(), "mxfp4")
     ref = A @ W.T
-    S = np.abs(A) @ np.abs(W).T
+    S, lost = sums(A, W, a, sc, w, ws, "mxfp8")
     row = 1                                                     # 2^-127 times 2^-126 and 2^127
-    check(out[row:row + 1], ref[row:row + 1], S[row:row + 1], 128)
+    check(out[row:row + 1], ref[row:row + 1], (S[row:row + 1], lost[row:row + 1]), 128)
+
+
+@pytest.mark.parametrize("M", [1, 20, 2100])
+def test_cut_of_small_products(M):
+    """256 beside 2^-7 among eight consecutive K values, in the next eight, and beside 1.5 * 2^-5 (cut to 2^-5)."""
+    a, w = torch.zeros(M, 64, dtype=torch.uint8), torch.zeros(64, 64, dtype=torch.uint8)
+    a[:, 18], w[:, 18] = 0x78, 2                                # 256 times 1
+    s = torch.full((2100, 2), 127, dtype=torch.uint8, device=DEV)
+    for k, code, want in ((23, 0x08, 256.0), (24, 0x08, 256.0 + 2.0 ** -7), (16, 0x1C, 256.0 + 2.0 ** -5)):
+        x, v = a.clone(), w.clone()
+        x[:, k], v[:, k] = code, 1                              # times 0.5
+        packed = (v[:, 0::2] | (v[:, 1::2] << 4)).contiguous()
+        out = moe.mx_linear(x.to(DEV), s[:M], packed.to(DEV), s[:64], a_fmt="mxfp8", dtype=torch.float32)
+        assert (out == want).all(), (k, out[0, 0].item())
 
 
 def test_repeat_is_bitwise_the_same_and_rows_are_independent():
@@ -161,6 +207,47 @@ def test_repeat_is_bitwise_the_same_and_rows_are_independent():
     two = moe.mx_linear(a2, sc, w, ws, a_fmt="mxfp4")
     keep = torch.arange(40, device=DEV) != 7
     assert torch.equal(one[keep], two[keep])
+
+
+# few rows: one and two column blocks to a workgroup, slices of more than 2048 K values, odd numbers of
+# stages; then the tiles of 64 x 64, 64 x 128 and 128 x 128 with whole and with ragged ends
+KERNELS = [(1, 4112, 288), (4, 40, 20000), (8, 4300, 4128), (12, 4200, 352), (13, 90, 20000), (16, 5, 5152),
+           (25, 4200, 96), (40, 100, 9120), (60, 5000, 4160), (33, 2800, 4448), (200, 1500, 288), (200, 1501, 160),
+           (70, 7000, 544), (300, 4100, 352), (520, 4200, 160), (600, 4203, 96)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_every_kernel(M, N, K, fmt):
+    print(f"[mx_linear] kernels {M}x{N}x{K} {fmt}", flush=True)
+    ops = operands(M + 3 * N + K, M, N, K, fmt)
+    dtype = TYPES[(M + N + K // 32) % 3]
+    g = torch.Generator().manual_seed(M)
+    bias, add = torch.randn(N, generator=g), (3 * torch.randn(M, N, generator=g)).to(dtype)
+    dev = [t.to(DEV) for t in ops]
+    plain = moe.mx_linear(*dev, a_fmt=fmt, dtype=dtype)
+    out = torch.full((M + 2, N + 24), 7.0, dtype=dtype, device=DEV)
+    moe.mx_linear(*dev, a_fmt=fmt, bias=bias.to(DEV), add=add.to(DEV), alpha=1.5, out=out[1:M + 1, 8:N + 8])
+    torch.cuda.synchronize()
+    ref, S = reference(*ops, fmt)
+    check(plain, ref, S, K)
+    b, d = bias.double().numpy(), add.double().numpy()
+    check(out[1:M + 1, 8:N + 8], 1.5 * ref + b + d, S, K, 1.5, np.abs(b) + np.abs(d))
+    out[1:M + 1, 8:N + 8] = 7.0
+    assert (out == 7.0).all()                                   # nothing written beside the result
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", [(3, 4200, 96), (30, 4200, 96), (50, 4200, 4128), (200, 2100, 96), (600, 4200, 96)])
+def test_nan_scale_in_every_kernel(M, N, K, fmt):
+    print(f"[mx_linear] nan {M}x{N}x{K} {fmt}", flush=True)
+    a, sc, w, ws = operands(71, M, N, K, fmt)
+    sc[2, -1] = 255
+    ws[69, 0] = 255
+    out = moe.mx_linear(a.to(DEV), sc.to(DEV), w.to(DEV), ws.to(DEV), a_fmt=fmt).cpu()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[2], want[:, 69] = True, True
+    assert torch.equal(torch.isnan(out), want)
 
 
 def test_refusals():

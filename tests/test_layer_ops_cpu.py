@@ -153,6 +153,7 @@ NORM = dict(x=OK, residual=OK, weight=OK, residual_out=OK, y=OK, codes=0, scales
     (dict(eps=math.nan), {}, B.MOE_EINVAL),
     (dict(H=68), {}, B.MOE_ENOTSUP),
     (dict(H=16392), {}, B.MOE_ENOTSUP),
+    (dict(T=1 << 24), {}, B.MOE_ENOTSUP),
     (dict(H=72, mx_fmt=1), dict(codes=OK, scales=OK), B.MOE_ENOTSUP),
     ({}, dict(x=0), B.MOE_EINVAL),
     ({}, dict(weight=0), B.MOE_EINVAL),
@@ -182,6 +183,8 @@ def test_norm_refusals(kw, ptrs, code):
     (dict(K=0), {}, B.MOE_EINVAL),
     (dict(K=40), {}, B.MOE_ENOTSUP),
     (dict(K=(1 << 20) + 32), {}, B.MOE_ENOTSUP),
+    (dict(M=1 << 24), {}, B.MOE_ENOTSUP),
+    (dict(N=1 << 24), {}, B.MOE_ENOTSUP),
     (dict(a_fmt=0), {}, B.MOE_EINVAL),
     (dict(out_type=3), {}, B.MOE_EINVAL),
     (dict(alpha=math.inf), {}, B.MOE_EINVAL),
@@ -216,6 +219,7 @@ def test_linear_refusals(kw, ptrs, code):
     (dict(k=0), {}, B.MOE_EINVAL),
     (dict(k=17), {}, B.MOE_EINVAL),
     (dict(E=1025), {}, B.MOE_ENOTSUP),
+    (dict(T=1 << 24), {}, B.MOE_ENOTSUP),
     (dict(E=64, k=33), {}, B.MOE_ENOTSUP),
     (dict(type=3), {}, B.MOE_EINVAL),
     (dict(score=2), {}, B.MOE_EINVAL),
