@@ -78,7 +78,9 @@ void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
   if (n8 <= 64) MOE_NORM(64, 1);
   else if (n8 <= 128) MOE_NORM(128, 1);
   else if (n8 <= 256) MOE_NORM(256, 1);
-  else if (T <= 512) {  // too few rows to fill the card: a row's chunks side by side
+  else if (T <= 512) {
+    // Too few rows to fill the card: a row's chunks side by side, against several to a thread as below
+    // (us, MXFP8 output): 1 x 7168 3.4 and 5.0, 64 x 14336 4.7 and 8.0, 512 x 7168 6.4 and 7.4, 1024 x 7168 12.0 and 11.1.
     if (n8 <= 512) MOE_NORM(512, 1);
     else if (n8 <= 1024) MOE_NORM(1024, 1);
     else MOE_NORM(1024, 2);
@@ -157,6 +159,11 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
 }
 
 // ----------------------------------------------------------------- routing
+// A token takes 16 lanes, four tokens to a wave, where tokens are many: us with 16 and with 64 lanes:
+// 65536 x 256 softmax, top 8, 37 and 61, 4096 x 128 4.3 and 6.9. Up to 256 experts 16 lanes hold 16
+// each, and few tokens wait for that chain: 1 x 256 sigmoid in 8 groups 6.6 and 4.9, 2048 x 256 7.3 and 6.3, 4096 x 256
+// 7.5 and 8.5; with 128 experts 16 lanes are never behind (1 x 128 3.8 and 4.2). Vector
+// loads of 8 or more: 65536 x 256 41 -> 37.
 template <int DT>
 void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
   const bool row16 = aligned(q.logits, 16) && aligned(q.bias, 16) && q.ld * moe::elem_size(DT) % 16 == 0;
@@ -170,6 +177,7 @@ void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
   }
   if (q.E <= 64) MOE_ROUTE_TOPK(16, 4)
   else if (q.E <= 128) MOE_ROUTE_TOPK(16, 8)
+  else if (q.E <= 256 && q.T <= 2048) MOE_ROUTE_TOPK(64, 4)
   else if (q.E <= 256) MOE_ROUTE_TOPK(16, 16)
   else if (q.E <= 512) MOE_ROUTE_TOPK(64, 8)
   else MOE_ROUTE_TOPK(64, 16)

@@ -2,8 +2,10 @@
 //
 // A thread takes 8 consecutive values (16 or 32 bytes), so a quad of lanes
 // holds one block of 32: its largest magnitude is two DPP maxima away, no LDS,
-// and a wave reads and writes whole contiguous lines. Each thread does U chunks
-// 256 chunks apart with all loads issued first. Both kernels are bound by HBM.
+// and a wave reads and writes whole contiguous lines. Each thread does kUnroll
+// chunks, 256 chunks apart, with all loads issued first. Both kernels are bound by HBM:
+// bf16 14336 x 16384 to MXFP4 98 us (6.1 TB/s read and written), to MXFP8 118 us (6.0), a copy
+// of 1 GiB runs at 5.1. Chunks per thread 1 / 2 / 4 / 8: 99 / 98 / 104 / 110 us, 64 x 7168 2.3 / 2.4 / 2.6 / 3.5.
 #pragma once
 
 #include "elem.hpp"
@@ -12,7 +14,7 @@
 namespace moe {
 namespace mxf {
 
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
 struct RowsParams {
   const void* x;      // quantize: values in; dequantize: unused

@@ -8,7 +8,9 @@
 // scaling (one read of x and residual), sums in fp32. The microscaled output
 // is quantized from the fp32 y, so its elements are rounded once. A thread
 // holds C chunks of 8 values, NT chunks apart; a block of 32 values is one
-// quad of lanes, as in the quantizer.
+// quad of lanes, as in the quantizer. Bound by HBM where rows are many: 8192 x 7168 bf16 with
+// residual and MXFP8 output 80 us, 413 MB at 5.2 TB/s; few rows by the chain load, sum, scale, store:
+// 1 x 7168 3.4 us, where an empty kernel in a graph takes 2.
 #pragma once
 
 #include "elem.hpp"

@@ -89,6 +89,20 @@ def test_many_equal_scores(E, k):
             check(l, k, None, score=score, n_group=8, topk_group=4, group_score="max")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,G,keep", [(2049, 256, 8, 8, 4), (2300, 160, 6, 8, 3), (2050, 131, 16, 0, 0), (2100, 256, 32, 0, 0)])
+def test_more_than_2048_tokens(T, E, k, G, keep, score):
+    """Up to 256 experts take other lanes from there on; some rows hold many equal scores."""
+    print(f"[route_topk] T={T} E={E} k={k} groups {G}/{keep} {score}", flush=True)
+    l = logits(T + E, T, E, torch.float32)
+    l[:40] = 0.0
+    l[20:40, ::5] = 1.0
+    l[30:40, E // 2:] = -float("inf")
+    b = 0.05 * np.random.default_rng(E).standard_normal(E).astype(np.float32)
+    for bias in (b, None):
+        check(l, k, bias, score=score, n_group=G, topk_group=keep)
+
+
 def test_minus_infinity_bias_masks_experts():
     b = np.zeros(64, np.float32)
     b[::2] = -np.inf
