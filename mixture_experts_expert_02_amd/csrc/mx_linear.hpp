@@ -274,7 +274,7 @@ struct Tile {
   static constexpr int LDS = NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 0);
   static constexpr int WGS = LDS <= 80 * 1024 ? 2 : 1;     // workgroups per compute unit at least (160 KB of LDS)
   static_assert(4 / NBUF * 32 * EROW * 4 <= STAGE, "epilogue staging: the waves share the buffers");
-  static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && BK == 128, "a scale word holds 256 K values");
+  static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && (BK == 128 || BK == 256), "a scale word holds 256 K values");
   static_assert(NBUF == 4 || BN % (256 / SP) == 0, "an instruction fetches scale rows of one operand");
 };
 
@@ -443,21 +443,18 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
         word[x][4 + i] = y[1];
       }
   };
-  // the words of turn t's two units into the operand sets; a new fetch every fourth turn
-  auto take_direct = [&](int t) {
-    if ((t & 3) == 0) {
+  // the words of unit u into the operand set; a new fetch every eighth unit
+  auto take_direct = [&](int u) {
+    if ((u & 7) == 0) {
       spread_direct();
-      fetch_direct(t / 4 + 1);
+      fetch_direct(u / 8 + 1);
     }
 #pragma unroll
     for (int x = 0; x < FS; ++x) {
+      if (x < T::FN) sw[0][x < T::FN ? x : 0] = word[x][0];
+      else sa[0][x < T::FN ? 0 : x - T::FN] = word[x][0];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (x < T::FN) sw[h][x < T::FN ? x : 0] = word[x][h];
-        else sa[h][x < T::FN ? 0 : x - T::FN] = word[x][h];
-      }
-#pragma unroll
-      for (int i = 0; i < 6; ++i) word[x][i] = word[x][i + 2];
+      for (int i = 0; i < 7; ++i) word[x][i] = word[x][i + 1];
     }
   };
 
@@ -564,15 +561,23 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 
   // The same with four buffers: the last step waits for the next stage only
   // (the two after it may still be in flight) and loads stage NEXT + 3 into this one.
-#define MOE_MXL_STAGE4(CUR, OTHER, NEXT, SB0, SS)                        \
+#define MOE_MXL_STAGE4(CUR, OTHER, NEXT, SB0)                            \
   {                                                                      \
-    MOE_MXL_STEP(0, SB0, SS, CUR, 1, 0, 0, CUR, 0)                       \
+    if constexpr (T::NS == 4) {                                          \
+      pin();                                                             \
+      take_direct((NEXT) - 1);                                           \
+    }                                                                    \
+    MOE_MXL_STEP(0, SB0, 0, CUR, 1, 0, 0, CUR, 0)                        \
+    if constexpr (T::NS == 4) {                                          \
+      MOE_MXL_STEP(1, SB0 + 1, 0, CUR, 2, 0, 0, CUR, 0)                  \
+      MOE_MXL_STEP(2, SB0 + 2, 0, CUR, 3, 0, 0, CUR, 0)                  \
+    }                                                                    \
     pin();                                                               \
     mask_loads((NEXT) + 3);                                              \
     wait_landed<2 * LT>();                                               \
     asm volatile("s_barrier" ::: "memory");                              \
     __builtin_amdgcn_sched_barrier(0);                                   \
-    MOE_MXL_STEP(1, SB0 + T::NS - 1, SS, OTHER, 0, 0, LT, CUR, (NEXT) + 3) \
+    MOE_MXL_STEP(1, SB0 + T::NS - 1, 0, OTHER, 0, 0, LT, CUR, (NEXT) + 3) \
   }
 
   mask_loads(0);
@@ -600,20 +605,28 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 #pragma unroll
   for (int j = 0; j < T::FM; ++j) read_a(buf0, 0, av[0][j], j);
   if constexpr (NBUF == 4) {
-    // four stages = one scale group per turn
+    constexpr int H = T::NS == 4 ? 0 : 2;  // scale byte of the second stage of a pair
     int t = 0;
-    for (; t < KS / 4; ++t) {
-      take_direct(t);
-      MOE_MXL_STAGE4(buf0, buf1, 4 * t + 1, 0, 0)
-      MOE_MXL_STAGE4(buf1, buf2, 4 * t + 2, 2, 0)
-      MOE_MXL_STAGE4(buf2, buf3, 4 * t + 3, 0, 1)
-      MOE_MXL_STAGE4(buf3, buf0, 4 * t + 4, 2, 1)
+    for (; t + 4 <= KS; t += 4) {
+      if constexpr (T::NS == 2) take_direct(t / 2);
+      MOE_MXL_STAGE4(buf0, buf1, t + 1, 0)
+      MOE_MXL_STAGE4(buf1, buf2, t + 2, H)
+      if constexpr (T::NS == 2) {
+        pin();
+        take_direct(t / 2 + 1);
+      }
+      MOE_MXL_STAGE4(buf2, buf3, t + 3, 0)
+      MOE_MXL_STAGE4(buf3, buf0, t + 4, H)
       pin();
     }
-    take_direct(t);
-    if ((KS & 3) > 0) MOE_MXL_STAGE4(buf0, buf1, 4 * t + 1, 0, 0)
-    if ((KS & 3) > 1) MOE_MXL_STAGE4(buf1, buf2, 4 * t + 2, 2, 0)
-    if ((KS & 3) > 2) MOE_MXL_STAGE4(buf2, buf3, 4 * t + 3, 0, 1)
+    if constexpr (T::NS == 2) take_direct(t / 2);
+    if (t < KS) MOE_MXL_STAGE4(buf0, buf1, t + 1, 0)
+    if (t + 1 < KS) MOE_MXL_STAGE4(buf1, buf2, t + 2, H)
+    if constexpr (T::NS == 2) {
+      pin();
+      take_direct(t / 2 + 1);
+    }
+    if (t + 2 < KS) MOE_MXL_STAGE4(buf2, buf3, t + 3, 0)
   } else if constexpr (BK == 256) {
     // two stages = one scale group per turn
     for (int t = 0; t < KS / 2; ++t) {

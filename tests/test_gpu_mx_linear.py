@@ -210,10 +210,12 @@ def test_repeat_is_bitwise_the_same_and_rows_are_independent():
 
 
 # few rows: one and two column blocks to a workgroup, slices of more than 2048 K values, odd numbers of
-# stages; then the tiles of 64 x 64, 64 x 128 and 128 x 128 with whole and with ragged ends
+# stages; then the tiles of 64 x 64, 64 x 128 and 128 x 128 with whole and with ragged ends, up to
+# three turns of four stages and more than one fetch of scales
 KERNELS = [(1, 4112, 288), (4, 40, 20000), (8, 4300, 4128), (12, 4200, 352), (13, 90, 20000), (16, 5, 5152),
            (25, 4200, 96), (40, 100, 9120), (60, 5000, 4160), (33, 2800, 4448), (200, 1500, 288), (200, 1501, 160),
-           (70, 7000, 544), (300, 4100, 352), (520, 4200, 160), (600, 4203, 96)]
+           (70, 7000, 544), (300, 4100, 352), (520, 4200, 160), (600, 4203, 96),
+           (300, 1600, 2304), (330, 2805, 2336), (70, 9000, 2080), (260, 6000, 1024), (1100, 2400, 4384)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
