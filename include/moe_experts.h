@@ -516,7 +516,7 @@ typedef struct {
  *   residual_out (device) [T, H]: h; given exactly when residual is; may be
  *                residual itself, or x
  *   y            (device) [T, H], y rounded to the type, or NULL; may be x
- *   codes, scales (device) with mx_fmt: float32 y as microscaled rows, else ignored
+ *   codes, scales (device) with mx_fmt: y before its rounding to the type as microscaled rows, else ignored
  * At least one of y and the microscaled output is asked for. */
 int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight,
                     void* residual_out, void* y, void* codes, uint8_t* scales, moe_stream_t stream);

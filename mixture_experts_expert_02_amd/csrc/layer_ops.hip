@@ -80,7 +80,7 @@ void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
   else if (n8 <= 256) MOE_NORM(256, 1);
   else if (T <= 512) {
     // Too few rows to fill the card: a row's chunks side by side, against several to a thread as below
-    // (us, MXFP8 output): 1 x 7168 3.4 and 5.0, 64 x 14336 4.7 and 8.0, 512 x 7168 6.4 and 7.4, 1024 x 7168 12.0 and 11.1.
+    // (us, MXFP8 output): 1 x 7168 3.9 and 5.3, 64 x 14336 5.3 and 8.6, 512 x 7168 7.4 and 8.0, 1024 x 7168 13.3 and 12.2.
     if (n8 <= 512) MOE_NORM(512, 1);
     else if (n8 <= 1024) MOE_NORM(1024, 1);
     else MOE_NORM(1024, 2);
@@ -270,6 +270,7 @@ int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residu
   q.H = p->H;
   q.w_type = p->w_type;
   q.eps = p->eps;
+  q.inv_h = 1.0 / p->H;
   int rc = check_rows(x, q.ldx, p->H, p->type);
   if (!rc && residual) rc = check_rows(residual, q.ld_res, p->H, p->type);
   if (!rc && residual) rc = check_rows(residual_out, q.ld_res_out, p->H, p->type);

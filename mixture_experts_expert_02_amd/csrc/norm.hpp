@@ -5,12 +5,16 @@
 //   y = h * rsqrt(mean(h^2) + eps) * w
 //
 // One workgroup per row, the row kept in registers between the sum and the
-// scaling (one read of x and residual), sums in fp32. The microscaled output
-// is quantized from the fp32 y, so its elements are rounded once. A thread
+// scaling (one read of x and residual). Squares are added in fp32 by eights and
+// in double from there, the root is taken in double; h * w is exact for 16-bit
+// types, so y is off by the rounding of its last product and of r alone. The microscaled
+// output is quantized from the fp32 y rounded to odd (below), so that its elements are
+// the nearest ones to h * w * r, not to a y rounded before. A thread
 // holds C chunks of 8 values, NT chunks apart; a block of 32 values is one
 // quad of lanes, as in the quantizer. Bound by HBM where rows are many: 8192 x 7168 bf16 with
-// residual and MXFP8 output 80 us, 413 MB at 5.2 TB/s; few rows by the chain load, sum, scale, store:
-// 1 x 7168 3.4 us, where an empty kernel in a graph takes 2.
+// residual and MXFP8 output 84 us, 413 MB at 4.9 TB/s; few rows by the chain load, sum, scale, store:
+// 1 x 7168 3.9 us, where an empty kernel in a graph takes 2. The sums and the root in fp32 and y rounded
+// to nearest took 3.5 and 82.5 us and put four times as many elements on the other side of a tie.
 #pragma once
 
 #include "elem.hpp"
@@ -29,20 +33,35 @@ struct NormParams {
   int64_t ldx, ld_res, ld_res_out, ldy, ld_codes, ld_scales;
   int32_t H, w_type;
   float eps;
+  double inv_h;       // 1 / H
 };
 
 template <int NT>
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[NT / 64];
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double part[NT / 64];
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
   if (NT == 64) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
+  double s = 0.0;
 #pragma unroll
   for (int i = 0; i < NT / 64; ++i) s += part[i];
   return s;
+}
+
+// 1 / sqrt(v): one Newton step on the hardware's estimate; 0 and infinity keep theirs.
+__device__ __forceinline__ double rsqrt_f64(double v) {
+  const double y = __builtin_amdgcn_rsq(v);
+  const double z = fma(0.5 * fma(-v * y, y, 1.0), y, y);
+  return v > 0.0 && v < (double)INFINITY ? z : y;
+}
+
+// v + e, |e| at most half a step of v, cut toward zero with the last bit set if
+// anything was cut off: rounding that to fewer bits gives what rounding v + e would.
+__device__ __forceinline__ float to_odd(float v, float e) {
+  const int b = __float_as_int(v);
+  return e != 0.f ? __int_as_float((b + ((b ^ __float_as_int(e)) >> 31)) | 1) : v;
 }
 
 template <int DT, int FMT, int NT, int C>
@@ -50,7 +69,7 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(const NormParams p) {
   const size_t t = blockIdx.x;
   const int n8 = p.H / 8;
   float h[C][8];
-  float sq = 0.f;
+  double sq = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (int)threadIdx.x + c * NT;
@@ -76,10 +95,14 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(const NormParams p) {
     }
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    float q = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq += h[c][j] * h[c][j];
-  const float r = 1.f / sqrtf(block_sum<NT>(sq) / (float)p.H + p.eps);
+    for (int j = 0; j < 8; ++j) q += h[c][j] * h[c][j];
+    sq += (double)q;
+  }
+  const double rd = rsqrt_f64(fma(block_sum<NT>(sq), p.inv_h, (double)p.eps));
+  const float r = (float)rd, r_lo = (float)(rd - (double)r);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (int)threadIdx.x + c * NT;
@@ -87,9 +110,14 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(const NormParams p) {
     float w[8], y[8];
     load8_as(p.w_type, p.w, 8 * (size_t)i, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = h[c][j] * r * w[j];
+    for (int j = 0; j < 8; ++j) {
+      h[c][j] *= w[j];
+      y[j] = h[c][j] * r;
+    }
     if (p.y) store8<DT>(p.y, t * p.ldy + 8 * (size_t)i, y);
     if constexpr (FMT != 0) {  // H is a multiple of 32: quads are whole
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = to_odd(y[j], fmaf(h[c][j], r_lo, fmaf(h[c][j], r, -y[j])));
       const int code = mxf::scale_code<FMT>(mxf::quad_amax(y));
       uint32_t q[2];
       mxf::encode8<FMT>(y, code, q);
