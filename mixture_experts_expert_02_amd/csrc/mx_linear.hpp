@@ -243,7 +243,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // Tile kernel. A workgroup of 4 waves computes BM rows x BN columns; a stage is
 // BK values of K: BM rows of activation codes and BN rows of weight codes, loaded
 // HBM -> LDS with buffer_load ... lds into one of two buffers while the other is
-// multiplied. Rows past M or N and K past the row's end read zeros through the
+// multiplied (small tiles: four buffers, three stages ahead). Rows past M or N and K past the row's end read zeros through the
 // buffer's range check. The 16-byte chunks of a row are swizzled by its index so
 // that the 16 rows of one ds_read_b128 pass fall on distinct banks.
 //
@@ -252,6 +252,12 @@ __device__ __forceinline__ void wave_lds_sync() {
 // one output row. 32x32x64 operands, group q = lane >> 5: e2m1 K values
 // 32q..32q+31 (16 bytes); e4m3 16q..16q+15 and 32+16q..32+16q+15; the lane
 // gives the scale of block q.
+//
+// Bound by the matrix instruction at the clock that the card's power leaves: 8192 x 8192 x 8192
+// MXFP4 273 us (4.03 PFLOP/s, the bare instruction 6.3), MXFP8 414 us (2.66, bare 3.8); beside it by a
+// tile's start and end, 17k cycles of 60k at K = 4096, and by the last round of tiles: 4096 x 14336 x 4096
+// MXFP4 139 us (3.45), 8192 x 7168 x 2048 MXFP8 with an addend 142 us (1.69). Tiles smaller than the
+// largest wait for barriers and LDS: 300 x 7168 x 7168 MXFP8 28 us, MXFP4 23.5.
 //
 // Scales: a thread loads 16 scale bytes of one row (512 K values) at a time,
 // splits them into even and odd blocks and puts them into LDS as four words
@@ -718,8 +724,9 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 // through two buffers of its own, so nothing but its own loads is ever waited
 // for, and the partial sums meet in LDS in wave order. What bounds it is the number
 // of lines a compute unit can have in flight: register loads in operand layout
-// (16 rows x 64 bytes an instruction) take twice the requests and ran
-// 32 x 4096 x 14336 in 22 us. LITE: the activation rows fit one load instruction
+// (16 rows x 64 bytes an instruction) take twice the requests: 32 x 4096 x 14336 MXFP8 24 us, now
+// 15 (2.1 TB/s of weights; the 32 rows come again for every 16 columns), 1 x 32768 x 7168 MXFP4 36, now 27
+// (4.7 TB/s), 1 x 7168 x 2048 7.8, now 5.1. LITE: the activation rows fit one load instruction
 // (4 MXFP8 or 8 MXFP4 rows).
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4, weights as the A operand: group q = lane >> 4
