@@ -540,6 +540,7 @@ typedef struct {
  *   bias        (device) float32 [N] or NULL
  *   add         (device) [M, N] or NULL; may be out itself (with ld_add == ldo)
  *   out         (device) [M, N], overwritten
+ * The same call gives the same bits; the order of a sum depends on M, N, K and a_fmt.
  * out and add need their type's alignment only; N is free. A row of a with a NaN
  * scale gives a NaN row of out. Sums are float32, with one property of the matrix
  * instruction: with MXFP8 rows the products of K values 8j..8j+7 are cut, toward zero, to

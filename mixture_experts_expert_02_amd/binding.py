@@ -494,6 +494,17 @@ def _ld(t, shape, dtypes, dev: int, where: str, name: str) -> int:
     _refuse(where, f"{name} has type {t.dtype}")
 
 
+def _rows(t, where: str, name: str):
+    """(rows, columns, device index, elements between rows) of a GPU matrix of values."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _TYPE and t.is_contiguous():
+        dev = t.get_device()
+        if dev >= 0:
+            r, c = t.shape
+            return r, c, dev, 0
+    r, c, dev = _matrix(t, where, name)
+    return r, c, dev, _ld(t, (r, c), _TYPE, dev, where, name)
+
+
 def _vector(t, n: int, dtypes, dev: int, where: str, name: str) -> int:
     """Address of a contiguous vector of n values."""
     if not (isinstance(t, torch.Tensor) and t.shape == (n,) and t.is_contiguous()):
@@ -508,10 +519,12 @@ def _vector(t, n: int, dtypes, dev: int, where: str, name: str) -> int:
 # The current stream's handle by device index, without building a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# The current device's index; whoever has a GPU tensor has initialised the runtime.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(fn, where: str, dev: int, *args) -> None:
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -544,11 +557,11 @@ def _mx_out(like, codes, scales, rows: int, K: int, fmt: int, dev: int, where: s
     cols = K // 2 if fmt == MOE_MX_FP4 else K
     lc = ls = 0
     if codes is None:
-        codes = like.new_empty((rows, cols), dtype=torch.uint8)
+        codes = like.new_empty(rows, cols, dtype=torch.uint8)
     else:
         lc = _ld(codes, (rows, cols), _U8, dev, where, "codes")
     if scales is None:
-        scales = like.new_empty((rows, nb), dtype=torch.uint8)
+        scales = like.new_empty(rows, nb, dtype=torch.uint8)
     else:
         ls = _ld(scales, (rows, nb), _U8, dev, where, "scales")
     return codes, lc, scales, ls
@@ -560,8 +573,7 @@ def mx_quantize(x, fmt: str = "mxfp4", codes=None, scales=None):
     uint8 [rows, K/32]). See moe_mx_quantize."""
     where = "mx_quantize"
     f = _mx_fmt(fmt, where)
-    rows, K, dev = _matrix(x, where, "x")
-    ld = _ld(x, (rows, K), _TYPE, dev, where, "x")
+    rows, K, dev, ld = _rows(x, where, "x")
     codes, lc, scales, ls = _mx_out(x, codes, scales, rows, K, f, dev, where)
     p = MoeMxRows(rows, K, _TYPE[x.dtype], f, ld, lc, ls)
     _run(lib().moe_mx_quantize, "moe_mx_quantize", dev, ctypes.byref(p), x.data_ptr(), codes.data_ptr(),
@@ -581,7 +593,7 @@ def mx_dequantize(codes, scales, fmt: str = "mxfp4", dtype=torch.bfloat16, out=N
     if out is None:
         if dtype not in _TYPE:
             _refuse(where, f"unsupported type {dtype}", MOE_ENOTSUP)
-        out = codes.new_empty((rows, K), dtype=dtype)
+        out = codes.new_empty(rows, K, dtype=dtype)
     else:
         ld = _ld(out, (rows, K), _TYPE, dev, where, "out")
     p = MoeMxRows(rows, K, _TYPE[out.dtype], f, ld, lc, ls)
@@ -596,9 +608,8 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, want_y: bool = True
     x's type (unless want_y is false) and, with mx "mxfp8" or "mxfp4", as
     microscaled rows. See moe_add_rmsnorm."""
     where = "add_rmsnorm"
-    T, H, dev = _matrix(x, where, "x")
+    T, H, dev, ldx = _rows(x, where, "x")
     shape = (T, H)
-    ldx = _ld(x, shape, _TYPE, dev, where, "x")
     same = (x.dtype,)
     f = MOE_MX_NONE if mx is None else _mx_fmt(mx, where)
     if f == MOE_MX_NONE:
@@ -612,7 +623,7 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, want_y: bool = True
         ld_res = _ld(residual, shape, same, dev, where, "residual")
         res_ptr = residual.data_ptr()
         if residual_out is None:
-            residual_out = x.new_empty(shape)
+            residual_out = torch.empty_like(x)
         else:
             ld_out = _ld(residual_out, shape, same, dev, where, "residual_out")
         out_ptr = residual_out.data_ptr()
@@ -622,7 +633,7 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, want_y: bool = True
         ldy = _ld(y, shape, same, dev, where, "y")
         y_ptr = y.data_ptr()
     elif want_y:
-        y = x.new_empty(shape)
+        y = torch.empty_like(x)
         y_ptr = y.data_ptr()
     if f != MOE_MX_NONE:
         codes, lc, scales, ls = _mx_out(x, codes, scales, T, H, f, dev, where)
@@ -642,14 +653,28 @@ def mx_linear(a, a_scales, w, w_scales, a_fmt: str = "mxfp8", bias=None, add=Non
     (out may be add). See moe_mx_linear."""
     where = "mx_linear"
     f = _mx_fmt(a_fmt, where)
-    M, cols, dev = _matrix(a, where, "a")
-    N, half, _ = _matrix(w, where, "w")
-    K = 2 * half
-    nb = _blocks(K, where)
-    lda = _ld(a, (M, half if f == MOE_MX_FP4 else K), _U8, dev, where, "a")
-    ld_as = _ld(a_scales, (M, nb), _U8, dev, where, "a_scales")
-    if _ld(w, (N, half), _U8, dev, where, "w") or _ld(w_scales, (N, nb), _U8, dev, where, "w_scales"):
-        _refuse(where, "w and w_scales must be contiguous")
+    lda = ld_as = 0
+    # A call takes less time on the GPU than its checks take here, so the usual case (all
+    # contiguous) is looked over in one expression; what fails it is checked one by one.
+    try:
+        (M, cols), (N, half), dev, u8 = a.shape, w.shape, a.get_device(), torch.uint8
+        K, nb = 2 * half, half >> 4
+        plain = (dev >= 0 and cols == (half if f == MOE_MX_FP4 else K) and not half & 15
+                 and a.dtype is u8 and w.dtype is u8 and a_scales.dtype is u8 and w_scales.dtype is u8
+                 and a_scales.shape == (M, nb) and w_scales.shape == (N, nb)
+                 and w.get_device() == dev and a_scales.get_device() == dev and w_scales.get_device() == dev
+                 and a.is_contiguous() and w.is_contiguous() and a_scales.is_contiguous() and w_scales.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        M, cols, dev = _matrix(a, where, "a")
+        N, half, _ = _matrix(w, where, "w")
+        K = 2 * half
+        nb = _blocks(K, where)
+        lda = _ld(a, (M, half if f == MOE_MX_FP4 else K), _U8, dev, where, "a")
+        ld_as = _ld(a_scales, (M, nb), _U8, dev, where, "a_scales")
+        if _ld(w, (N, half), _U8, dev, where, "w") or _ld(w_scales, (N, nb), _U8, dev, where, "w_scales"):
+            _refuse(where, "w and w_scales must be contiguous")
     b_ptr = None if bias is None else _vector(bias, N, _F32, dev, where, "bias")
     ldo = ld_add = 0
     if out is not None:
@@ -662,7 +687,7 @@ def mx_linear(a, a_scales, w, w_scales, a_fmt: str = "mxfp8", bias=None, add=Non
         ld_add = _ld(add, (M, N), (dtype,), dev, where, "add")
         add_ptr = add.data_ptr()
     if out is None:
-        out = a.new_empty((M, N), dtype=dtype)
+        out = a.new_empty(M, N, dtype=dtype)
     p = MoeMxLinearProblem(M, N, K, f, _TYPE[dtype], alpha, lda, ld_as, ldo, ld_add)
     _run(lib().moe_mx_linear, "moe_mx_linear", dev, ctypes.byref(p), a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
          w_scales.data_ptr(), b_ptr, add_ptr, out.data_ptr())
@@ -675,8 +700,7 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
     """Top-k experts of logits [T, E] (bf16, float16 or float32; rows may be
     strided): (ids int32 [T, k], weights float32 [T, k]). See moe_route_topk."""
     where = "route_topk"
-    T, E, dev = _matrix(logits, where, "logits")
-    ld = _ld(logits, (T, E), _TYPE, dev, where, "logits")
+    T, E, dev, ld = _rows(logits, where, "logits")
     if score not in _SCORE:
         _refuse(where, f"unknown score {score!r}")
     if group_score not in _GROUP:
@@ -685,11 +709,11 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
         _refuse(where, "k must be a positive integer")
     b_ptr = None if bias is None else _vector(bias, E, _F32, dev, where, "bias")
     if ids is None:
-        ids = logits.new_empty((T, k), dtype=torch.int32)
+        ids = logits.new_empty(T, k, dtype=torch.int32)
     elif _ld(ids, (T, k), _I32, dev, where, "ids"):
         _refuse(where, "ids must be contiguous")
     if weights is None:
-        weights = logits.new_empty((T, k), dtype=torch.float32)
+        weights = logits.new_empty(T, k, dtype=torch.float32)
     elif _ld(weights, (T, k), _F32, dev, where, "weights"):
         _refuse(where, "weights must be contiguous")
     p = MoeRouteTopkProblem(T, E, k, _TYPE[logits.dtype], _SCORE[score], n_group, topk_group, _GROUP[group_score],

@@ -139,7 +139,7 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
   if (q.M <= (F8 ? 4 : 8))
     return few ? launch_skinny<AF, 8, 1, 1, true>(q, s) : launch_skinny<AF, 4, 1, 1, true>(q, s);
   if (q.M <= 16) return few ? launch_skinny<AF, 8, 1, 1, false>(q, s) : launch_skinny<AF, 4, 2, 1, false>(q, s);
-  // More of them while such workgroups of 32 x 16 find place on the chip at once (96 KiB of LDS
+  // More of them while such workgroups of 32 x 16 find place on the chip at once (88 KiB of LDS
   // for MXFP8, 56 for MXFP4): 32 x 4096 x 14336 MXFP8 15 where 32 columns to a workgroup take 17, 128 x 1024 x 7168 9.4
   // where tiles of 64 x 64 take 13.5; MXFP4 7.9 and 11.1, with 512 workgroups 64 x 4096 x 14336 19.5 and 24,
   // 128 x 2048 x 7168 10.9 and 11.2. MXFP8 with 512: 128 x 2048 x 7168 17 and 13.6.

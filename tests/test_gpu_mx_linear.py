@@ -252,6 +252,17 @@ def test_nan_scale_in_every_kernel(M, N, K, fmt):
     assert torch.equal(torch.isnan(out), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (30, 4200, 96), (600, 4200, 160)])
+def test_nan_code_stays_in_its_row(M, N, K):
+    a, sc, w, ws = operands(81, M, N, K, "mxfp8")
+    a[2, 70] = 0x7F
+    w[:, 35] = 0                                                # zero weights meet it
+    out = moe.mx_linear(a.to(DEV), sc.to(DEV), w.to(DEV), ws.to(DEV)).cpu()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[2] = True
+    assert torch.equal(torch.isnan(out), want)
+
+
 def test_refusals():
     a, sc, w, ws = [t.to(DEV) for t in operands(61, 4, 32, 128, "mxfp8")]
     bad = [
