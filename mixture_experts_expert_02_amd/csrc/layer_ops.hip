@@ -319,7 +319,8 @@ int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const fl
   if (p->group_score != MOE_GROUP_MAX && p->group_score != MOE_GROUP_TOP2) return MOE_EINVAL;
   if (p->renormalize != 0 && p->renormalize != 1) return MOE_EINVAL;
   if (p->n_group < 0 || !std::isfinite(p->routed_scaling_factor)) return MOE_EINVAL;
-  if (p->T >= kMaxRows || p->E > moe::kRouteMaxE || p->k > moe::kRouteMaxK || p->n_group > moe::kTopkGroups) return MOE_ENOTSUP;
+  if (p->T >= kMaxRows || p->E > moe::kRouteMaxE || p->k > moe::kRouteMaxK || p->n_group > moe::kTopkGroups)
+    return MOE_ENOTSUP;
   const bool grouped = p->n_group > 1;
   if (grouped && (p->E % p->n_group || p->topk_group < 1 || p->topk_group > p->n_group ||
                   (p->group_score == MOE_GROUP_TOP2 && p->E / p->n_group < 2) ||

@@ -244,9 +244,10 @@ __device__ __forceinline__ void wave_lds_sync() {
 // Tile kernel. A workgroup of 4 waves computes BM rows x BN columns; a stage is
 // BK values of K: BM rows of activation codes and BN rows of weight codes, loaded
 // HBM -> LDS with buffer_load ... lds into one of two buffers while the other is
-// multiplied (small tiles: four buffers, three stages ahead). Rows past M or N and K past the row's end read zeros through the
-// buffer's range check. The 16-byte chunks of a row are swizzled by its index so
-// that the 16 rows of one ds_read_b128 pass fall on distinct banks.
+// multiplied (small tiles: four buffers, three stages ahead). Rows past M or N and
+// K past the row's end read zeros through the buffer's range check. The 16-byte
+// chunks of a row are swizzled by its index so that the 16 rows of one ds_read_b128
+// pass fall on distinct banks.
 //
 // The weights are the MFMA's A operand (row lane & 31), the activations its B
 // operand (column lane & 31), so a lane's results are 4 consecutive columns of
@@ -257,7 +258,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // Bound by the matrix instruction at the clock that the card's power leaves: 8192 x 8192 x 8192
 // MXFP4 273 us (4.03 PFLOP/s, the bare instruction 6.3), MXFP8 414 us (2.66, bare 3.8); beside it by a
 // tile's start and end, 17k cycles of 60k at K = 4096, and by the last round of tiles: 4096 x 14336 x 4096
-// MXFP4 139 us (3.45), 8192 x 7168 x 2048 MXFP8 with an addend 142 us (1.69). Tiles smaller than the
+// MXFP4 139 us (3.45), 8192 x 7168 x 2048 MXFP8 with an addend 139 us (1.73). Tiles smaller than the
 // largest wait for barriers and LDS: 300 x 7168 x 7168 MXFP8 28 us, MXFP4 23.5.
 //
 // Scales: a thread loads 16 scale bytes of one row (512 K values) at a time,
@@ -274,14 +275,15 @@ struct Tile {
   static constexpr int FM = BM / 64, FN = BN / 64;         // 32 x 32 results of a wave
   static constexpr int AL = A_BYTES / 4096, WL = W_BYTES / 4096;  // loads per wave and stage
   static constexpr int ROWS = BM + BN;                     // scale rows: weights, then activations
-  static constexpr int SP = AF == mxf::MXFP8 && BK == 128 && BN == 256 ? 2 : 4;  // 16-byte pieces of a scale row fetched at once
+  // 16-byte pieces of a scale row fetched at once
+  static constexpr int SP = AF == mxf::MXFP8 && BK == 128 && BN == 256 ? 2 : 4;
   static constexpr int SR = ROWS * SP / 256;               // per thread
   static constexpr int EF = FN < 2 ? FN : 2;               // column fragments per epilogue strip
   static constexpr int EROW = EF * 32 + 4;                 // floats per strip row
   static constexpr int LDS = NBUF * STAGE + (NBUF == 2 ? 32 * ROWS : 0);
   static constexpr int WGS = LDS <= 80 * 1024 ? 2 : 1;     // workgroups per compute unit at least (160 KB of LDS)
   static_assert(4 / NBUF * 32 * EROW * 4 <= STAGE, "epilogue staging: the waves share the buffers");
-  static_assert(NBUF == 2 ? BK == 128 || BK == 256 : NBUF == 4 && (BK == 128 || BK == 256), "a scale word holds 256 K values");
+  static_assert((NBUF == 2 || NBUF == 4) && (BK == 128 || BK == 256), "a scale word holds 256 K values");
   static_assert(NBUF == 4 || BN % (256 / SP) == 0, "an instruction fetches scale rows of one operand");
 };
 

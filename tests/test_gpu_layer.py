@@ -42,7 +42,8 @@ class Layer:
         u8 = lambda *s: e(*s, dtype=torch.uint8)  # noqa: E731
         self.w, self.x, self.res = w, e(T, H), e(T, H)
         self.y, self.codes, self.sc = e(T, H), u8(T, H), u8(T, H // 32)
-        self.logits, self.ids, self.wt = e(T, E, dtype=torch.float32), e(T, K, dtype=torch.int32), e(T, K, dtype=torch.float32)
+        self.logits, self.wt = e(T, E, dtype=torch.float32), e(T, K, dtype=torch.float32)
+        self.ids = e(T, K, dtype=torch.int32)
         self.hid, self.hc, self.hs = e(T, I), u8(T, I), u8(T, I // 32)
         self.routed, self.out = e(T, H), e(T, H)
         p = moe.problem(T, H, I, E, K, "mxfp4", ACT["act"], ACT["alpha"], ACT["beta"], ACT["limit"], act_fmt="mxfp8")

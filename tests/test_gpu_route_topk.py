@@ -90,7 +90,8 @@ def test_many_equal_scores(E, k):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("T,E,k,G,keep", [(2049, 256, 8, 8, 4), (2300, 160, 6, 8, 3), (2050, 131, 16, 0, 0), (2100, 256, 32, 0, 0)])
+@pytest.mark.parametrize("T,E,k,G,keep", [(2049, 256, 8, 8, 4), (2300, 160, 6, 8, 3), (2050, 131, 16, 0, 0),
+                                          (2100, 256, 32, 0, 0)])
 def test_more_than_2048_tokens(T, E, k, G, keep, score):
     """Up to 256 experts take other lanes from there on; some rows hold many equal scores."""
     print(f"[route_topk] T={T} E={E} k={k} groups {G}/{keep} {score}", flush=True)
