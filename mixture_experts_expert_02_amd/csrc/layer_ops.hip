@@ -116,7 +116,13 @@ int launch_tile(moe::mxl::Params& q, hipStream_t s) {
   q.nt = (q.N + BN - 1) / BN;
   const int64_t n = ((int64_t)q.mt * q.nt + 7) / 8 * 8;
   if (n > kMaxGrid) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF>), dim3((unsigned)n), dim3(256), 0, s, q);
+  if constexpr (AF == moe::mxf::MXFP8 && NBUF == 4) {
+    if (q.out_type == MOE_T_FP32) {
+      hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF, true>), dim3((unsigned)n), dim3(256), 0, s, q);
+      return launch_status();
+    }
+  }
+  hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF, false>), dim3((unsigned)n), dim3(256), 0, s, q);
   return launch_status();
 }
 
@@ -124,7 +130,14 @@ template <int AF, int S, int FN, int FM, bool LITE>
 int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
   q.nt = (q.N + 16 * FN - 1) / (16 * FN);
   q.mt = (q.M + 16 * FM - 1) / (16 * FM);
-  hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, FN, FM, LITE>), dim3((unsigned)(q.mt * q.nt)), dim3(64 * S), 0, s, q);
+  const dim3 g((unsigned)(q.mt * q.nt));
+  if constexpr (AF == moe::mxf::MXFP8) {
+    if (q.out_type == MOE_T_FP32) {
+      hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, FN, FM, LITE, true>), g, dim3(64 * S), 0, s, q);
+      return launch_status();
+    }
+  }
+  hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, FN, FM, LITE, false>), g, dim3(64 * S), 0, s, q);
   return launch_status();
 }
 
@@ -156,7 +169,8 @@ int launch_linear(moe::mxl::Params& q, hipStream_t s) {
   // 128 x 7168 x 7168 19.6 -> 15.4 (half the barriers, whole lines of a weight row); 64 x 128 and 64 x 64 MXFP8 gain
   // nothing (200 x 14336 x 4096 20.7 and 20.9, 512 x 4096 x 4096 12.9 and 13.8).
   constexpr int BM = F8 ? 128 : 256, BK = F8 ? 128 : 256;
-  if (tiles(BM, 256) >= 192) return launch_tile<AF, BM, 256, BK, 2>(q, s);
+  const bool exact = F8 && q.out_type == MOE_T_FP32;  // no registers for the split codes in the largest
+  if (tiles(BM, 256) >= 192 && !exact) return launch_tile<AF, BM, 256, BK, 2>(q, s);
   if (tiles(128, 128) >= 160) return launch_tile<AF, 128, 128, BK, 4>(q, s);
   if (tiles(64, 128) >= 160) return launch_tile<AF, 64, 128, BK, 4>(q, s);
   return launch_tile<AF, 64, 64, BK, 4>(q, s);

@@ -8,8 +8,12 @@
 // eight consecutive K values are cut toward zero to multiples of 2^(e - 13), e
 // the largest exponent sum among them, before their sum joins the fp32 one (measured
 // lane by lane, the same for 16x16x128 and 32x32x64; e2m1 products span fewer bits and are
-// exact). Beside the 2^-4 of the codes this is kept: an exact sum would take the
-// bf16 instructions, at a quarter of the rate.
+// exact). e4m3 codes with bit 6 span eight exponents and so do those without: products of either kind
+// alone, lowest bit 2^(ea - 4) against the largest 2^(ea + 7 + 2), lose nothing. So two instructions, one on each
+// kind (split_e4m3), are exact; EXACT kernels run both, for float32 results. 16-bit results keep the
+// cut: beside their own rounding it is small, and exactness costs (us, float32 results, with the
+// cut and without): 1 x 7168 x 2048 5.3 and 5.7, 32 x 4096 x 14336 15 and 18.6, 1024 x 4096 x 4096 22 and 37,
+// 8192 x 7168 x 2048 134 and 273 (without the largest tile, whose registers are full).
 #pragma once
 
 #include <type_traits>
@@ -49,6 +53,16 @@ struct Params {
 };
 
 constexpr uint32_t kNoLoad = 0x80000000u;  // buffer offset past any operand: reads 0
+
+// Four e4m3 codes: those with bit 6, and the others; zeros (of their signs) in the places left.
+__device__ __forceinline__ void split_e4m3(i32x8 v, i32x8& hi, i32x8& lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = (uint32_t)v[i], t = x & 0x40404040u, m = (t << 1) - (t >> 6);
+    hi[i] = (int)(x & (m | 0x80808080u));
+    lo[i] = (int)(x & ~m);
+  }
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
@@ -293,7 +307,7 @@ __device__ __forceinline__ int slot_of(int c, int r) {
   return RB == 256 ? c ^ (r & 15) : RB == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int AF, int BM, int BN, int BK, int NBUF>
+template <int AF, int BM, int BN, int BK, int NBUF, bool EXACT>
 __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile(const Params p) {
   using T = Tile<AF, BM, BN, BK, NBUF>;
   __shared__ __attribute__((aligned(16))) uint8_t buf0[T::STAGE];
@@ -486,7 +500,7 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
   }
 
   // Operands of one step, two sets: while one is multiplied the other loads.
-  i32x8 av[2][T::FM];
+  i32x8 av[2][T::FM], hi[EXACT ? T::FM : 1];
   i32x4 wv[2][T::FN];
   auto read_a = [&](const uint8_t* buf, int st, i32x8& d, int j) {
     const i32x4 lo = *(const i32x4*)(buf + a_rd[st][0] + j * 32 * T::AB);
@@ -534,11 +548,19 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 #define MOE_MXL_MFMA(S, SB, SS, i)                                                                          \
   {                                                                                                         \
     const i32x8 w8 = __builtin_shufflevector(wv[(S) & 1][i], wv[(S) & 1][i], 0, 1, 2, 3, -1, -1, -1, -1);   \
+    if constexpr (EXACT) {                                                                                  \
+      _Pragma("unroll") for (int j = 0; j < T::FM; ++j)                                                     \
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, hi[j], acc[i][j], 4, 0, SB,         \
+                                                                    (int)sw[SS][i], SB, (int)sa[SS][j]);    \
+    }                                                                                                       \
     _Pragma("unroll") for (int j = 0; j < T::FM; ++j)                                                       \
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                          \
           w8, av[(S) & 1][j], acc[i][j], 4, AF == mxf::MXFP8 ? 0 : 4, SB, (int)sw[SS][i], SB, (int)sa[SS][j]); \
   }
 #define MOE_MXL_STEP(S, SB, SS, RD, RS, L0, L1, LBUF, LST)                                   \
+  if constexpr (EXACT) {                                                                     \
+    _Pragma("unroll") for (int j = 0; j < T::FM; ++j) split_e4m3(av[(S) & 1][j], hi[j], av[(S) & 1][j]); \
+  }                                                                                          \
   _Pragma("unroll") for (int i = 0; i < T::FN; ++i) {                                        \
     MOE_MXL_MFMA(S, SB, SS, i)                                                               \
     read_row(RD, RS, wv[((S) + 1) & 1], av[((S) + 1) & 1], i);                               \
@@ -745,7 +767,7 @@ struct Skinny {
   static constexpr int AL = ROWS * RB / 1024, WL = 2 * FN, LT = WL + AL;  // loads per stage
 };
 
-template <int AF, int S, int FN, int FM, bool LITE>
+template <int AF, int S, int FN, int FM, bool LITE, bool EXACT>
 __global__ __launch_bounds__(64 * S) void k_skinny(const Params p) {
   using T = Skinny<AF, FN, FM, LITE>;
   constexpr bool F8 = T::F8;
@@ -858,11 +880,16 @@ __global__ __launch_bounds__(64 * S) void k_skinny(const Params p) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         i32x8 a8;
+        i32x8 hi;
         if constexpr (F8) a8 = __builtin_shufflevector(av[i][u][0], av[i][u][1], 0, 1, 2, 3, 4, 5, 6, 7);
         else a8 = __builtin_shufflevector(av[i][u][0], av[i][u][0], 0, 1, 2, 3, -1, -1, -1, -1);
+        if constexpr (EXACT) split_e4m3(a8, hi, a8);
 #pragma unroll
         for (int n = 0; n < FN; ++n) {
           const i32x8 w8 = __builtin_shufflevector(wv[n][u], wv[n][u], 0, 1, 2, 3, -1, -1, -1, -1);
+          if constexpr (EXACT)
+            acc[i * FN + n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, hi, acc[i * FN + n], 4, 0, 0,
+                                                                               sw[n][u], 0, sa[i][u]);
           acc[i * FN + n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, acc[i * FN + n], 4, F8 ? 0 : 4, 0,
                                                                              sw[n][u], 0, sa[i][u]);
         }
