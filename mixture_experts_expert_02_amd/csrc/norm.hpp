@@ -59,9 +59,11 @@ __device__ __forceinline__ double rsqrt_f64(double v) {
 
 // v + e, |e| at most half a step of v, cut toward zero with the last bit set if
 // anything was cut off: rounding that to fewer bits gives what rounding v + e would.
+// An infinity or NaN stays (e is the other infinity or NaN then): its block becomes a NaN block.
 __device__ __forceinline__ float to_odd(float v, float e) {
   const int b = __float_as_int(v);
-  return e != 0.f ? __int_as_float((b + ((b ^ __float_as_int(e)) >> 31)) | 1) : v;
+  const bool cut = e != 0.f && (b & 0x7f800000) != 0x7f800000;
+  return cut ? __int_as_float((b + ((b ^ __float_as_int(e)) >> 31)) | 1) : v;
 }
 
 template <int DT, int FMT, int NT, int C>
