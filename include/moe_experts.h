@@ -509,14 +509,16 @@ typedef struct {
 /* Residual addition and root-mean-square norm of the rows that enter the
  * router and the experts:
  *   h = x + residual rounded to the type (h = x without a residual)
- *   y = h * weight / sqrt(mean(h^2) + eps), in float32
+ *   y = h * weight / sqrt(mean(h^2) + eps), in float32 (the mean and the root in double, so that rows of
+ *       any finite size have theirs; y past float32 is infinite)
  *   x            (device) [T, H]
  *   residual     (device) [T, H] or NULL
  *   weight       (device) [H]
  *   residual_out (device) [T, H]: h; given exactly when residual is; may be
  *                residual itself, or x
  *   y            (device) [T, H], y rounded to the type, or NULL; may be x
- *   codes, scales (device) with mx_fmt: y before its rounding to the type as microscaled rows, else ignored
+ *   codes, scales (device) with mx_fmt: y before any rounding as microscaled rows (a block with an infinite y:
+ *                the NaN block), else ignored
  * At least one of y and the microscaled output is asked for. */
 int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight,
                     void* residual_out, void* y, void* codes, uint8_t* scales, moe_stream_t stream);

@@ -5,16 +5,18 @@
 //   y = h * rsqrt(mean(h^2) + eps) * w
 //
 // One workgroup per row, the row kept in registers between the sum and the
-// scaling (one read of x and residual). Squares are added in fp32 by eights and
-// in double from there, the root is taken in double; h * w is exact for 16-bit
-// types, so y is off by the rounding of its last product and of r alone. The microscaled
-// output is quantized from the fp32 y rounded to odd (below), so that its elements are
-// the nearest ones to h * w * r, not to a y rounded before. A thread
+// scaling (one read of x and residual). Squares, their sum and the root are
+// doubles, where the square of every float32 is in range (sums in fp32 lost rows above 2^64 and below
+// 2^-75, and half the bits of r). The root is split into 2^k m, m in [1, 2): h 2^k is at most sqrt(H), so the
+// products with w and m pass float32 only if y does. The microscaled output and a float32 y
+// carry the roundings of both products and of m along (e below); the former is quantized from y
+// rounded to odd, so that its elements are the nearest ones to h * w * r, not to a y rounded before.
+// A 16-bit y takes the plain products. A thread
 // holds C chunks of 8 values, NT chunks apart; a block of 32 values is one
 // quad of lanes, as in the quantizer. Bound by HBM where rows are many: 8192 x 7168 bf16 with
-// residual and MXFP8 output 84 us, 413 MB at 4.9 TB/s; few rows by the chain load, sum, scale, store:
-// 1 x 7168 3.9 us, where an empty kernel in a graph takes 2. The sums and the root in fp32 and y rounded
-// to nearest took 3.5 and 82.5 us and put four times as many elements on the other side of a tie.
+// residual and MXFP8 output 83 us, 413 MB at 5.0 TB/s; few rows by the chain load, sum, scale, store:
+// 1 x 7168 4.1 us, where an empty kernel in a graph takes 2. Squares and products in fp32, the carried bits without
+// w's, took 82.5 and 3.9 us; every product in double 92 and 4.3.
 #pragma once
 
 #include "elem.hpp"
@@ -44,26 +46,28 @@ __device__ __forceinline__ double block_sum(double v) {
   if (NT == 64) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
-  double s = 0.0;
+  double s[2] = {0.0, 0.0};
 #pragma unroll
-  for (int i = 0; i < NT / 64; ++i) s += part[i];
-  return s;
+  for (int i = 0; i < NT / 64; ++i) s[i & 1] += part[i];
+  return s[0] + s[1];
 }
 
-// 1 / sqrt(v): one Newton step on the hardware's estimate; 0 and infinity keep theirs.
+// 1 / sqrt(v): the hardware's estimate y, off by 2^-23 or less, times (1 - e)^(-1/2) with e = 1 - v y^2,
+// by the series to e^2 (the next term is below 2^-66); 0 and infinity keep theirs.
 __device__ __forceinline__ double rsqrt_f64(double v) {
   const double y = __builtin_amdgcn_rsq(v);
-  const double z = fma(0.5 * fma(-v * y, y, 1.0), y, y);
+  const double e = fma(-v * y, y, 1.0);
+  const double z = fma(y * e, fma(0.375, e, 0.5), y);
   return v > 0.0 && v < (double)INFINITY ? z : y;
 }
 
 // v + e, |e| at most half a step of v, cut toward zero with the last bit set if
 // anything was cut off: rounding that to fewer bits gives what rounding v + e would.
-// An infinity or NaN stays (e is the other infinity or NaN then): its block becomes a NaN block.
+// An infinity or NaN stays (e is an infinity or NaN then, by v's own subtraction): its block becomes a NaN block.
 __device__ __forceinline__ float to_odd(float v, float e) {
+  constexpr int kFiniteNotZero = 0x198;  // normal and subnormal numbers of either sign
   const int b = __float_as_int(v);
-  const bool cut = e != 0.f && (b & 0x7f800000) != 0x7f800000;
-  return cut ? __int_as_float((b + ((b ^ __float_as_int(e)) >> 31)) | 1) : v;
+  return __builtin_amdgcn_classf(e, kFiniteNotZero) ? __int_as_float((b + ((b ^ __float_as_int(e)) >> 31)) | 1) : v;
 }
 
 template <int DT, int FMT, int NT, int C>
@@ -71,7 +75,6 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(const NormParams p) {
   const size_t t = blockIdx.x;
   const int n8 = p.H / 8;
   float h[C][8];
-  double sq = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (int)threadIdx.x + c * NT;
@@ -96,33 +99,38 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(const NormParams p) {
       if (i < n8) store8<DT>(p.res_out, t * p.ld_res_out + 8 * (size_t)i, h[c]);
     }
   }
+  double sq[2] = {0.0, 0.0};
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    float q = 0.f;
+  for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q += h[c][j] * h[c][j];
-    sq += (double)q;
-  }
-  const double rd = rsqrt_f64(fma(block_sum<NT>(sq), p.inv_h, (double)p.eps));
-  const float r = (float)rd, r_lo = (float)(rd - (double)r);
+    for (int j = 0; j < 8; ++j) sq[j & 1] = fma((double)h[c][j], (double)h[c][j], sq[j & 1]);
+  const double rd = rsqrt_f64(fma(block_sum<NT>(sq[0] + sq[1]), p.inv_h, (double)p.eps));
+  const int k = __builtin_amdgcn_frexp_exp(rd) - 1;  // rd = 2^k m, m in [1, 2) (0, infinity and NaN: themselves)
+  const double m = __builtin_amdgcn_ldexp(rd, -k);
+  const float r = (float)m, r_lo = (float)(m - (double)r);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (int)threadIdx.x + c * NT;
     if (i >= n8) break;
-    float w[8], y[8];
+    float w[8], y[8], odd[8];
     load8_as(p.w_type, p.w, 8 * (size_t)i, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      h[c][j] *= w[j];
-      y[j] = h[c][j] * r;
+      const float u = __builtin_amdgcn_ldexpf(h[c][j], k);
+      const float hw = u * w[j];
+      y[j] = hw * r;
+      if constexpr (FMT != 0 || DT == T_FP32) {
+        const float e = fmaf(hw, r_lo, fmaf(u, w[j], -hw) * r);
+        const float v = fmaf(hw, r, e);
+        if (FMT != 0) odd[j] = to_odd(v, fmaf(hw, r, -v) + e);
+        if (DT == T_FP32) y[j] = fabsf(y[j]) < INFINITY ? v : y[j];  // e is NaN beside an infinite hw
+      }
     }
     if (p.y) store8<DT>(p.y, t * p.ldy + 8 * (size_t)i, y);
     if constexpr (FMT != 0) {  // H is a multiple of 32: quads are whole
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = to_odd(y[j], fmaf(h[c][j], r_lo, fmaf(h[c][j], r, -y[j])));
-      const int code = mxf::scale_code<FMT>(mxf::quad_amax(y));
+      const int code = mxf::scale_code<FMT>(mxf::quad_amax(odd));
       uint32_t q[2];
-      mxf::encode8<FMT>(y, code, q);
+      mxf::encode8<FMT>(odd, code, q);
       mxf::store_codes<FMT>(p.codes + t * p.ld_codes, i, q);
       if ((threadIdx.x & 3) == 0) p.scales[t * p.ld_scales + i / 4] = (uint8_t)code;
     }
