@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -466,6 +467,26 @@ def _refuse(where: str, what: str, status: int = MOE_EINVAL):
     raise MoeError(status, f"{where}: {what}")
 
 
+# Sizes are 32-bit in the problem structures, and ctypes keeps the low bits of a larger number.
+_INT_MAX = 2 ** 31 - 1
+
+
+def _size(n: int, where: str) -> int:
+    if n > _INT_MAX:
+        _refuse(where, f"a size of {n} is too large", MOE_ENOTSUP)
+    return n
+
+
+def _count(n, where: str, name: str) -> int:
+    try:
+        n = operator.index(n)
+    except TypeError:
+        _refuse(where, f"{name} must be an integer")
+    if not -_INT_MAX <= n <= _INT_MAX:
+        _refuse(where, f"{name} is out of range")
+    return n
+
+
 def _matrix(t, where: str, name: str):
     """(rows, columns, device index) of a GPU matrix."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -474,7 +495,7 @@ def _matrix(t, where: str, name: str):
     if dev < 0:
         _refuse(where, f"{name} must be on a GPU")
     r, c = t.shape
-    return r, c, dev
+    return _size(r, where), _size(c, where), dev
 
 
 def _ld(t, shape, dtypes, dev: int, where: str, name: str) -> int:
@@ -498,8 +519,8 @@ def _rows(t, where: str, name: str):
     """(rows, columns, device index, elements between rows) of a GPU matrix of values."""
     if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _TYPE and t.is_contiguous():
         dev = t.get_device()
-        if dev >= 0:
-            r, c = t.shape
+        r, c = t.shape
+        if dev >= 0 and r <= _INT_MAX and c <= _INT_MAX:
             return r, c, dev, 0
     r, c, dev = _matrix(t, where, name)
     return r, c, dev, _ld(t, (r, c), _TYPE, dev, where, name)
@@ -548,7 +569,7 @@ def _mx_fmt(fmt, where: str) -> int:
 def _blocks(K: int, where: str) -> int:
     if K % 32:
         _refuse(where, "rows of a multiple of 32 values are needed", MOE_ENOTSUP)
-    return K // 32
+    return _size(K, where) // 32
 
 
 def _mx_out(like, codes, scales, rows: int, K: int, fmt: int, dev: int, where: str):
@@ -659,7 +680,7 @@ def mx_linear(a, a_scales, w, w_scales, a_fmt: str = "mxfp8", bias=None, add=Non
     try:
         (M, cols), (N, half), dev, u8 = a.shape, w.shape, a.get_device(), torch.uint8
         K, nb = 2 * half, half >> 4
-        plain = (dev >= 0 and cols == (half if f == MOE_MX_FP4 else K) and not half & 15
+        plain = (dev >= 0 and max(M, N, K) <= _INT_MAX and cols == (half if f == MOE_MX_FP4 else K) and not half & 15
                  and a.dtype is u8 and w.dtype is u8 and a_scales.dtype is u8 and w_scales.dtype is u8
                  and a_scales.shape == (M, nb) and w_scales.shape == (N, nb)
                  and w.get_device() == dev and a_scales.get_device() == dev and w_scales.get_device() == dev
@@ -705,8 +726,9 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
         _refuse(where, f"unknown score {score!r}")
     if group_score not in _GROUP:
         _refuse(where, f"unknown group score {group_score!r}")
-    if not isinstance(k, int) or k <= 0:
+    if not isinstance(k, int) or _count(k, where, "k") <= 0:
         _refuse(where, "k must be a positive integer")
+    n_group, topk_group = _count(n_group, where, "n_group"), _count(topk_group, where, "topk_group")
     b_ptr = None if bias is None else _vector(bias, E, _F32, dev, where, "bias")
     if ids is None:
         ids = logits.new_empty(T, k, dtype=torch.int32)
