@@ -9,6 +9,7 @@
 
 #include "../../include/moe_experts.h"
 #include "mx_linear.hpp"
+#include "mx_linear_rule.hpp"
 #include "mx_quant.hpp"
 #include "norm.hpp"
 #include "route_topk.hpp"
@@ -144,36 +145,24 @@ int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
 template <int AF>
 int launch_linear(moe::mxl::Params& q, hipStream_t s) {
   constexpr bool F8 = AF == moe::mxf::MXFP8;
-  auto tiles = [&](int bm, int bn) { return (int64_t)((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
-  // Few rows: k_skinny; four waves, eight where that gives a compute unit at most
-  // one workgroup. us at M = 1: 2048 x 7168 (N x K) 5.6 with eight, 6.3 with four, 7168 x 2048 6.2 and 5.1. M = 16:
-  // 14336 x 4096 9.9 with 32 columns to a workgroup, 10.6 with 16; 2880 x 2880 6.8 and 5.2.
-  const bool few = q.N <= 16 * 256;
-  if (q.M <= (F8 ? 4 : 8))
-    return few ? launch_skinny<AF, 8, 1, 1, true>(q, s) : launch_skinny<AF, 4, 1, 1, true>(q, s);
-  if (q.M <= 16) return few ? launch_skinny<AF, 8, 1, 1, false>(q, s) : launch_skinny<AF, 4, 2, 1, false>(q, s);
-  // More of them while such workgroups of 32 x 16 find place on the chip at once (88 KiB of LDS
-  // for MXFP8, 56 for MXFP4): 32 x 4096 x 14336 MXFP8 15 where 32 columns to a workgroup take 17, 128 x 1024 x 7168 9.4
-  // where tiles of 64 x 64 take 13.5; MXFP4 7.9 and 11.1, with 512 workgroups 64 x 4096 x 14336 19.5 and 24,
-  // 128 x 2048 x 7168 10.9 and 11.2. MXFP8 with 512: 128 x 2048 x 7168 17 and 13.6.
-  if (tiles(32, 16) <= (F8 ? 256 : 512)) return launch_skinny<AF, 4, 1, 2, false>(q, s);
-  // 24 x 7168 x 7168 MXFP8 12.3 where 16 columns take 17.7; 64 x 7168 x 7168 17 where tiles of 64 x 64 take 21,
-  // but 33 x 7168 x 2048 8.3 and 6.3, 64 x 14336 x 4096 21 and 14; MXFP4 33 x 6000 x 6016 14.8 and 13.1.
-  if (q.M <= 32 || (F8 && q.M <= 64 && q.K > 4096 && tiles(64, 64) <= 128))
-    return launch_skinny<AF, F8 ? 2 : 4, 2, 2, false>(q, s);
-  // The largest tile that still gives most compute units one. Measured at 160-256
-  // tiles (us, the tile taken against the next smaller): 300 x 7168 x 7168 MXFP8 29
-  // against 33, 1024 x 4096 x 4096 MXFP8 21 against 22, MXFP4 16 against 21; below: 512 x 4096 x 4096
-  // with 128 tiles of 128 x 128 17 against 13, 128 x 7168 x 7168 MXFP4 with 112 of 64 x 128 16 against 13.
   // Stages of 256 K values where they take the room of 128 MXFP8 ones: 300 x 7168 x 7168 MXFP4 27.5 -> 23.5,
   // 128 x 7168 x 7168 19.6 -> 15.4 (half the barriers, whole lines of a weight row); 64 x 128 and 64 x 64 MXFP8 gain
   // nothing (200 x 14336 x 4096 20.7 and 20.9, 512 x 4096 x 4096 12.9 and 13.8).
   constexpr int BM = F8 ? 128 : 256, BK = F8 ? 128 : 256;
-  const bool exact = F8 && q.out_type == MOE_T_FP32;  // no registers for the split codes in the largest
-  if (tiles(BM, 256) >= 192 && !exact) return launch_tile<AF, BM, 256, BK, 2>(q, s);
-  if (tiles(128, 128) >= 160) return launch_tile<AF, 128, 128, BK, 4>(q, s);
-  if (tiles(64, 128) >= 160) return launch_tile<AF, 64, 128, BK, 4>(q, s);
-  return launch_tile<AF, 64, 64, BK, 4>(q, s);
+  using moe::mxl::Kernel;
+  switch (moe::mxl::choose(F8, F8 && q.out_type == MOE_T_FP32, q.M, q.N, q.K)) {
+    case Kernel::SKINNY_8_1_1_LITE: return launch_skinny<AF, 8, 1, 1, true>(q, s);
+    case Kernel::SKINNY_4_1_1_LITE: return launch_skinny<AF, 4, 1, 1, true>(q, s);
+    case Kernel::SKINNY_8_1_1: return launch_skinny<AF, 8, 1, 1, false>(q, s);
+    case Kernel::SKINNY_4_2_1: return launch_skinny<AF, 4, 2, 1, false>(q, s);
+    case Kernel::SKINNY_4_1_2: return launch_skinny<AF, 4, 1, 2, false>(q, s);
+    case Kernel::SKINNY_X_2_2: return launch_skinny<AF, F8 ? 2 : 4, 2, 2, false>(q, s);
+    case Kernel::TILE_LARGEST: return launch_tile<AF, BM, 256, BK, 2>(q, s);
+    case Kernel::TILE_128_128: return launch_tile<AF, 128, 128, BK, 4>(q, s);
+    case Kernel::TILE_64_128: return launch_tile<AF, 64, 128, BK, 4>(q, s);
+    case Kernel::TILE_64_64: return launch_tile<AF, 64, 64, BK, 4>(q, s);
+  }
+  return MOE_EINVAL;
 }
 
 // ----------------------------------------------------------------- routing

@@ -1,0 +1,45 @@
+"""Which kernel of moe_mx_linear the tests' sizes reach, by the library's own rule,
+compiled for the host: a change of the rule that leaves a kernel untested fails here."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import mx_linear_cases as C
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mixture_experts_expert_02_amd", "csrc")
+KERNELS = ("SKINNY_8_1_1_LITE", "SKINNY_4_1_1_LITE", "SKINNY_8_1_1", "SKINNY_4_2_1", "SKINNY_4_1_2", "SKINNY_X_2_2",
+           "TILE_LARGEST", "TILE_128_128", "TILE_64_128", "TILE_64_64")
+MAIN = """#include <cstdio>
+#include "mx_linear_rule.hpp"
+int main() {
+  using moe::mxl::Kernel;
+  int f8, exact, M, N, K;
+  while (scanf("%%d %%d %%d %%d %%d", &f8, &exact, &M, &N, &K) == 5) switch (moe::mxl::choose(f8, exact, M, N, K)) {
+%s
+  }
+}
+""" % "\n".join(f'    case Kernel::{k}: puts("{k}"); break;' for k in KERNELS)
+
+
+@pytest.fixture(scope="module")
+def chosen(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("clang++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    d = tmp_path_factory.mktemp("rule")
+    (d / "main.cpp").write_text(MAIN)
+    subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror=switch", "-I", CSRC, str(d / "main.cpp"), "-o", str(d / "rule")],
+                   check=True, timeout=60)
+
+    def ask(fmt, exact, *shapes):
+        lines = "".join(f"{int(fmt == 'mxfp8')} {int(exact)} {M} {N} {K}\n" for M, N, K in shapes)
+        return subprocess.run([str(d / "rule")], input=lines, capture_output=True, text=True, check=True,
+                              timeout=60).stdout.split()
+    return ask
+
+
+def test_largest_tiles(chosen):
+    for fmt, shapes in C.LARGEST.items():
+        assert chosen(fmt, False, *shapes) == ["TILE_LARGEST"] * len(shapes)
