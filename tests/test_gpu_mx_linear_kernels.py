@@ -70,3 +70,29 @@ def test_largest_tiles(fmt, M, N, K):
         out = moe.mx_linear(*p.dev, a_fmt=fmt, dtype=dtype)
         torch.cuda.synchronize()
         p.check(out)
+
+
+@pytest.mark.parametrize("vec", [True, False])
+@pytest.mark.parametrize("kernel,fmt,M,widths", C.EPILOGUE)
+def test_every_epilogue(kernel, fmt, M, widths, vec):
+    """Bias and addend, each alone, both and neither, of every type; an addend alone also in place."""
+    N, K = widths[0 if vec else 1], C.EPILOGUE_K
+    p = Product(M + N, M, N, K, fmt)
+    g = torch.Generator().manual_seed(M)
+    bias, add32 = torch.randn(N, generator=g).to(DEV), (3 * torch.randn(M, N, generator=g)).to(DEV)
+    for dtype in TYPES:
+        add = add32.to(dtype)
+        for b, d in ((None, None), (bias, None), (None, add), (bias, add)):
+            print(f"[mx_linear] {kernel} {M}x{N}x{K} {fmt} {dtype} bias={b is not None} add={d is not None}", flush=True)
+            alpha = 1.0 if b is None else -0.75
+            out = torch.full((M + 2, N + 16), 7.0, dtype=dtype, device=DEV)
+            moe.mx_linear(*p.dev, a_fmt=fmt, bias=b, add=d, alpha=alpha, out=out[1:M + 1, 8:N + 8])
+            torch.cuda.synchronize()
+            p.check(out[1:M + 1, 8:N + 8], alpha, b, d)
+            if b is None and d is not None:
+                acc = add.clone()
+                moe.mx_linear(*p.dev, a_fmt=fmt, add=acc, out=acc)
+                torch.cuda.synchronize()
+                assert torch.equal(acc, out[1:M + 1, 8:N + 8])
+            out[1:M + 1, 8:N + 8] = 7.0
+            assert (out == 7.0).all()                           # nothing written beside the result

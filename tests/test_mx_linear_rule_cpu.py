@@ -43,3 +43,10 @@ def chosen(tmp_path_factory):
 def test_largest_tiles(chosen):
     for fmt, shapes in C.LARGEST.items():
         assert chosen(fmt, False, *shapes) == ["TILE_LARGEST"] * len(shapes)
+
+
+def test_epilogues(chosen):
+    for kernel, fmt, M, widths in C.EPILOGUE:
+        assert widths[0] % 8 == 0 and widths[1] % 8 != 0
+        assert chosen(fmt, False, *[(M, N, C.EPILOGUE_K) for N in widths]) == [kernel] * 2
+    assert {(k, f) for k, f, _, _ in C.EPILOGUE} == {(k, f) for k in KERNELS if k.startswith("TILE") for f in C.LARGEST}
