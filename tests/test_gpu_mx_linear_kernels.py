@@ -72,6 +72,16 @@ def test_largest_tiles(fmt, M, N, K):
         p.check(out)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("kernel,M,N,K", C.OTHERS + [("TILE_128_128", 1500, 4100, 2336)])
+def test_float32_results(kernel, M, N, K, fmt):
+    print(f"[mx_linear] {kernel} {M}x{N}x{K} {fmt}", flush=True)
+    p = Product(M + N + K, M, N, K, fmt)
+    out = moe.mx_linear(*p.dev, a_fmt=fmt, dtype=torch.float32)
+    torch.cuda.synchronize()
+    p.check(out)
+
+
 @pytest.mark.parametrize("vec", [True, False])
 @pytest.mark.parametrize("kernel,fmt,M,widths", C.EPILOGUE)
 def test_every_epilogue(kernel, fmt, M, widths, vec):
@@ -96,3 +106,19 @@ def test_every_epilogue(kernel, fmt, M, widths, vec):
                 assert torch.equal(acc, out[1:M + 1, 8:N + 8])
             out[1:M + 1, 8:N + 8] = 7.0
             assert (out == 7.0).all()                           # nothing written beside the result
+
+
+@pytest.mark.parametrize("kernel,M,N", C.EXACT)
+def test_small_products_in_every_exact_kernel(kernel, M, N):
+    """Beside 256 among eight consecutive K values a product 2^15 times smaller stays, wherever the eight lie."""
+    K = C.EXACT_K
+    print(f"[mx_linear] {kernel} {M}x{N}x{K}", flush=True)
+    s = torch.full((max(M, N), K // 32), 127, dtype=torch.uint8, device=DEV)
+    for base in (0, 200, 264, 632):
+        a, w = torch.zeros(M, K, dtype=torch.uint8), torch.zeros(N, K, dtype=torch.uint8)
+        a[:, base + 2], w[:, base + 2] = 0x78, 2                # 256 times 1
+        a[:, base + 7], w[:, base + 7] = 0x08, 1                # 2^-6 times 0.5
+        packed = (w[:, 0::2] | (w[:, 1::2] << 4)).contiguous()
+        out = moe.mx_linear(a.to(DEV), s[:M], packed.to(DEV), s[:N], dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert (out == 256.0 + 2.0 ** -7).all()

@@ -45,8 +45,21 @@ def test_largest_tiles(chosen):
         assert chosen(fmt, False, *shapes) == ["TILE_LARGEST"] * len(shapes)
 
 
+@pytest.mark.parametrize("fmt,exact", [("mxfp8", True), ("mxfp8", False), ("mxfp4", False)])
+def test_other_kernels(chosen, fmt, exact):
+    got = chosen(fmt, exact, *[c[1:] for c in C.OTHERS])
+    assert got == [c[0] for c in C.OTHERS]
+    assert set(got) == set(KERNELS) - {"TILE_LARGEST"}
+
+
 def test_epilogues(chosen):
     for kernel, fmt, M, widths in C.EPILOGUE:
         assert widths[0] % 8 == 0 and widths[1] % 8 != 0
         assert chosen(fmt, False, *[(M, N, C.EPILOGUE_K) for N in widths]) == [kernel] * 2
     assert {(k, f) for k, f, _, _ in C.EPILOGUE} == {(k, f) for k in KERNELS if k.startswith("TILE") for f in C.LARGEST}
+
+
+def test_exact_kernels(chosen):
+    got = chosen("mxfp8", True, *[(M, N, C.EXACT_K) for _, M, N in C.EXACT])
+    assert got == [c[0] for c in C.EXACT] and set(got) == set(KERNELS) - {"TILE_LARGEST"}
+    assert "TILE_LARGEST" not in chosen("mxfp8", True, *C.LARGEST["mxfp8"])
