@@ -92,9 +92,9 @@ void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ linear
-int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
+int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q, bool& exact) {
   if (!p || p->M < 0 || p->N <= 0 || p->K <= 0 || !type_ok(p->out_type) || !std::isfinite(p->alpha)) return MOE_EINVAL;
-  if (p->a_fmt != MOE_MX_FP4 && p->a_fmt != MOE_MX_FP8) return MOE_EINVAL;
+  if ((p->a_fmt != MOE_MX_FP4 && p->a_fmt != MOE_MX_FP8) || (p->exact != 0 && p->exact != 1)) return MOE_EINVAL;
   if (p->K % 32 || p->K > 1 << 20 || p->M >= kMaxRows || p->N >= kMaxRows) return MOE_ENOTSUP;
   const int64_t cb = moe::mxf::code_bytes(p->a_fmt, p->K);
   q.lda = or_default(p->lda, cb);
@@ -108,17 +108,18 @@ int mx_linear_params(const moe_mx_linear_problem* p, moe::mxl::Params& q) {
   q.K = p->K;
   q.out_type = p->out_type;
   q.alpha = p->alpha;
+  exact = p->a_fmt == MOE_MX_FP8 && (p->exact || p->out_type == MOE_T_FP32);
   return MOE_OK;
 }
 
 template <int AF, int BM, int BN, int BK, int NBUF>
-int launch_tile(moe::mxl::Params& q, hipStream_t s) {
+int launch_tile(moe::mxl::Params& q, bool exact, hipStream_t s) {
   q.mt = (q.M + BM - 1) / BM;
   q.nt = (q.N + BN - 1) / BN;
   const int64_t n = ((int64_t)q.mt * q.nt + 7) / 8 * 8;
   if (n > kMaxGrid) return MOE_ENOTSUP;
   if constexpr (AF == moe::mxf::MXFP8 && NBUF == 4) {
-    if (q.out_type == MOE_T_FP32) {
+    if (exact) {
       hipLaunchKernelGGL((moe::mxl::k_tile<AF, BM, BN, BK, NBUF, true>), dim3((unsigned)n), dim3(256), 0, s, q);
       return launch_status();
     }
@@ -128,12 +129,12 @@ int launch_tile(moe::mxl::Params& q, hipStream_t s) {
 }
 
 template <int AF, int S, int FN, int FM, bool LITE>
-int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
+int launch_skinny(moe::mxl::Params& q, bool exact, hipStream_t s) {
   q.nt = (q.N + 16 * FN - 1) / (16 * FN);
   q.mt = (q.M + 16 * FM - 1) / (16 * FM);
   const dim3 g((unsigned)(q.mt * q.nt));
   if constexpr (AF == moe::mxf::MXFP8) {
-    if (q.out_type == MOE_T_FP32) {
+    if (exact) {
       hipLaunchKernelGGL((moe::mxl::k_skinny<AF, S, FN, FM, LITE, true>), g, dim3(64 * S), 0, s, q);
       return launch_status();
     }
@@ -143,24 +144,24 @@ int launch_skinny(moe::mxl::Params& q, hipStream_t s) {
 }
 
 template <int AF>
-int launch_linear(moe::mxl::Params& q, hipStream_t s) {
+int launch_linear(moe::mxl::Params& q, bool exact, hipStream_t s) {
   constexpr bool F8 = AF == moe::mxf::MXFP8;
   // Stages of 256 K values where they take the room of 128 MXFP8 ones: 300 x 7168 x 7168 MXFP4 27.5 -> 23.5,
   // 128 x 7168 x 7168 19.6 -> 15.4 (half the barriers, whole lines of a weight row); 64 x 128 and 64 x 64 MXFP8 gain
   // nothing (200 x 14336 x 4096 20.7 and 20.9, 512 x 4096 x 4096 12.9 and 13.8).
   constexpr int BM = F8 ? 128 : 256, BK = F8 ? 128 : 256;
   using moe::mxl::Kernel;
-  switch (moe::mxl::choose(F8, F8 && q.out_type == MOE_T_FP32, q.M, q.N, q.K)) {
-    case Kernel::SKINNY_8_1_1_LITE: return launch_skinny<AF, 8, 1, 1, true>(q, s);
-    case Kernel::SKINNY_4_1_1_LITE: return launch_skinny<AF, 4, 1, 1, true>(q, s);
-    case Kernel::SKINNY_8_1_1: return launch_skinny<AF, 8, 1, 1, false>(q, s);
-    case Kernel::SKINNY_4_2_1: return launch_skinny<AF, 4, 2, 1, false>(q, s);
-    case Kernel::SKINNY_4_1_2: return launch_skinny<AF, 4, 1, 2, false>(q, s);
-    case Kernel::SKINNY_X_2_2: return launch_skinny<AF, F8 ? 2 : 4, 2, 2, false>(q, s);
-    case Kernel::TILE_LARGEST: return launch_tile<AF, BM, 256, BK, 2>(q, s);
-    case Kernel::TILE_128_128: return launch_tile<AF, 128, 128, BK, 4>(q, s);
-    case Kernel::TILE_64_128: return launch_tile<AF, 64, 128, BK, 4>(q, s);
-    case Kernel::TILE_64_64: return launch_tile<AF, 64, 64, BK, 4>(q, s);
+  switch (moe::mxl::choose(F8, exact, q.M, q.N, q.K)) {
+    case Kernel::SKINNY_8_1_1_LITE: return launch_skinny<AF, 8, 1, 1, true>(q, exact, s);
+    case Kernel::SKINNY_4_1_1_LITE: return launch_skinny<AF, 4, 1, 1, true>(q, exact, s);
+    case Kernel::SKINNY_8_1_1: return launch_skinny<AF, 8, 1, 1, false>(q, exact, s);
+    case Kernel::SKINNY_4_2_1: return launch_skinny<AF, 4, 2, 1, false>(q, exact, s);
+    case Kernel::SKINNY_4_1_2: return launch_skinny<AF, 4, 1, 2, false>(q, exact, s);
+    case Kernel::SKINNY_X_2_2: return launch_skinny<AF, F8 ? 2 : 4, 2, 2, false>(q, exact, s);
+    case Kernel::TILE_LARGEST: return launch_tile<AF, BM, 256, BK, 2>(q, exact, s);
+    case Kernel::TILE_128_128: return launch_tile<AF, 128, 128, BK, 4>(q, exact, s);
+    case Kernel::TILE_64_128: return launch_tile<AF, 64, 128, BK, 4>(q, exact, s);
+    case Kernel::TILE_64_64: return launch_tile<AF, 64, 64, BK, 4>(q, exact, s);
   }
   return MOE_EINVAL;
 }
@@ -293,7 +294,8 @@ int moe_add_rmsnorm(const moe_norm_problem* p, const void* x, const void* residu
 int moe_mx_linear(const moe_mx_linear_problem* p, const void* a, const uint8_t* a_scales, const void* w,
                   const uint8_t* w_scales, const float* bias, const void* add, void* out, moe_stream_t stream) {
   moe::mxl::Params q{};
-  int rc = mx_linear_params(p, q);
+  bool exact = false;
+  int rc = mx_linear_params(p, q, exact);
   if (rc) return rc;
   if (p->M == 0) return MOE_OK;
   if (!a || !a_scales || !w || !w_scales || !out) return MOE_EINVAL;
@@ -312,7 +314,7 @@ int moe_mx_linear(const moe_mx_linear_problem* p, const void* a, const uint8_t* 
   };
   q.vec = q.N % 8 == 0 && wide(out, q.ldo) && aligned(bias, 16) && (!add || wide(add, q.ld_add));
   hipStream_t s = (hipStream_t)stream;
-  return p->a_fmt == MOE_MX_FP8 ? launch_linear<moe::mxf::MXFP8>(q, s) : launch_linear<moe::mxf::MXFP4>(q, s);
+  return p->a_fmt == MOE_MX_FP8 ? launch_linear<moe::mxf::MXFP8>(q, exact, s) : launch_linear<moe::mxf::MXFP4>(q, exact, s);
 }
 
 int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const float* bias, int32_t* topk_ids,

@@ -10,10 +10,12 @@
 // lane by lane, the same for 16x16x128 and 32x32x64; e2m1 products span fewer bits and are
 // exact). e4m3 codes with bit 6 span eight exponents and so do those without: products of either kind
 // alone, lowest bit 2^(ea - 4) against the largest 2^(ea + 7 + 2), lose nothing. So two instructions, one on each
-// kind (split_e4m3), are exact; EXACT kernels run both, for float32 results. 16-bit results keep the
-// cut: beside their own rounding it is small, and exactness costs (us, float32 results, with the
-// cut and without): 1 x 7168 x 2048 5.3 and 5.7, 32 x 4096 x 14336 15 and 18.6, 1024 x 4096 x 4096 22 and 37,
-// 8192 x 7168 x 2048 134 and 273 (without the largest tile, whose registers are full).
+// kind (split_e4m3), are exact; EXACT kernels run both, for float32 results and for 16-bit ones whose caller
+// asks for it. Else 16-bit results keep the cut: it moves a sum by 1.5e-5 of its size (root mean square, random
+// rows), a bf16 rounding by 1.1e-3, and it matters where large products cancel. What exactness costs
+// (us, bf16 results with the cut and without): 1 x 7168 x 2048 5.2 and 5.7, 32 x 4096 x 14336 15 and 18.7,
+// 300 x 7168 x 7168 30 and 58, 1024 x 4096 x 4096 20.7 and 38, 8192 x 256 x 7168 22 and 33, 8192 x 7168 x 2048 112 and
+// 248 (without the largest tile, whose registers are full).
 #pragma once
 
 #include <type_traits>

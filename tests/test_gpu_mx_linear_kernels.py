@@ -122,3 +122,41 @@ def test_small_products_in_every_exact_kernel(kernel, M, N):
         out = moe.mx_linear(a.to(DEV), s[:M], packed.to(DEV), s[:N], dtype=torch.float32)
         torch.cuda.synchronize()
         assert (out == 256.0 + 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("kernel,M,N", C.EXACT)
+def test_16_bit_results_without_the_cut(kernel, M, N, dtype):
+    """exact=True: where 256 and -256 cancel, 1.5 * 2^-5 beside them stays whole."""
+    K = C.EXACT_K
+    print(f"[mx_linear] exact {kernel} {M}x{N}x{K} {dtype}", flush=True)
+    s = torch.full((max(M, N), K // 32), 127, dtype=torch.uint8, device=DEV)
+    for base in (0, 264, 632):
+        a, w = torch.zeros(M, K, dtype=torch.uint8), torch.zeros(N, K, dtype=torch.uint8)
+        for k, ac, wc in ((2, 0x78, 2), (3, 0x78, 10), (7, 0x1C, 1)):
+            a[:, base + k], w[:, base + k] = ac, wc
+        packed = (w[:, 0::2] | (w[:, 1::2] << 4)).contiguous()
+        out = moe.mx_linear(a.to(DEV), s[:M], packed.to(DEV), s[:N], dtype=dtype, exact=True)
+        torch.cuda.synchronize()
+        assert (out == 1.5 * 2.0 ** -5).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kernel,M,N,K", C.OTHERS + [("TILE_128_128", 1500, 4104, 2336)])
+def test_exact_results(kernel, M, N, K, dtype):
+    """Of 16 bits: the exact float32 result, rounded; of float32 and of MXFP4 rows: what there is without it."""
+    print(f"[mx_linear] exact {kernel} {M}x{N}x{K} {dtype}", flush=True)
+    p = Product(M + N + K, M, N, K, "mxfp8")
+    g = torch.Generator().manual_seed(K)
+    bias, add = torch.randn(N, generator=g).to(DEV), torch.randn(M, N, generator=g).to(dtype).to(DEV)
+    plain = moe.mx_linear(*p.dev, dtype=dtype, exact=True)
+    out = moe.mx_linear(*p.dev, bias=bias, add=add, alpha=0.5, dtype=dtype, exact=True)
+    f32 = moe.mx_linear(*p.dev, dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert torch.equal(plain, f32.to(dtype))
+    p.check(plain, exact=True)
+    p.check(out, 0.5, bias, add, exact=True)
+    if dtype == torch.bfloat16:
+        four = Product(M + N + K, M, N, K, "mxfp4")
+        one, two = (moe.mx_linear(*four.dev, a_fmt="mxfp4", dtype=dtype, exact=e) for e in (False, True))
+        assert torch.equal(one, two)
