@@ -124,13 +124,14 @@ __device__ __forceinline__ int token_upto(int v, int l) {
 }
 
 // e^t in double, to a few 2^-52: t = n ln 2 + r with |r| <= ln 2 / 2, e^r
-// by its Taylor sum to r^12 (the next term is below 2^-52). t is taken within
+// by its Taylor sum to r^12 (the next term is below 2^-52). n ln 2 is subtracted in two parts, as Cody and Waite
+// do it: ln 2 rounded to a multiple of 2^-42, whose product with n (8 bits) is exact, and the rest. t is taken within
 // +-120: e^-120 is near 1e-52, which no fp32 score or sum can tell from 0.
 __device__ __forceinline__ double exp_120(double t) {
   t = fmin(fmax(t, -120.0), 120.0);
   const double n = __builtin_rint(t * 1.4426950408889634074);
-  double r = fma(n, -6.93147180369123816490e-01, t);  // ln 2 in two parts: n times the first is exact
-  r = fma(n, -1.90821492927058770002e-10, r);
+  double r = fma(n, -0x1.62e42fefa38p-1, t);
+  r = fma(n, -0x1.ef35793c7673p-45, r);
   double p = 1.0 / 479001600.0;
   p = fma(p, r, 1.0 / 39916800.0);
   p = fma(p, r, 1.0 / 3628800.0);
