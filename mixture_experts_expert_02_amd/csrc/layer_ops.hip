@@ -79,15 +79,17 @@ void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
   if (n8 <= 64) MOE_NORM(64, 1);
   else if (n8 <= 128) MOE_NORM(128, 1);
   else if (n8 <= 256) MOE_NORM(256, 1);
+  // Rows of more than 8192 values: two chunks to a thread (us, MXFP8 output, against four on 512 threads and
+  // eight on 256): 1024 x 8224 17.4, 17.1 and 20.9, 4096 x 14336 80, 86 and 112, 4096 x 16384 91, 95 and 124.
+  else if (n8 > 1024) MOE_NORM(1024, 2);
   else if (T <= 512) {
     // Too few rows to fill the card: a row's chunks side by side, against several to a thread as below
-    // (us, MXFP8 output): 1 x 7168 3.9 and 5.3, 64 x 14336 5.3 and 8.6, 512 x 7168 7.4 and 8.0, 1024 x 7168 13.3 and 12.2.
+    // (us, MXFP8 output): 1 x 7168 4.1 and 5.7, 64 x 7168 4.4 and 6.0, 512 x 7168 7.8 and 8.3; 1024 x 7168 14.1 and 13.4,
+    // 8192 x 7168 91 and 86 (y alone: 82 and 89), 1024 x 4096 the same.
     if (n8 <= 512) MOE_NORM(512, 1);
-    else if (n8 <= 1024) MOE_NORM(1024, 1);
-    else MOE_NORM(1024, 2);
+    else MOE_NORM(1024, 1);
   } else if (n8 <= 512) MOE_NORM(256, 2);
-  else if (n8 <= 1024) MOE_NORM(256, 4);
-  else MOE_NORM(256, 8);
+  else MOE_NORM(256, 4);
 #undef MOE_NORM
 }
 
