@@ -451,9 +451,10 @@ int moe_check_expert_params(const moe_problem* p, const float* alpha_e, const fl
                             const float* limit_e, const float* fc1_alpha, const float* fc2_alpha);
 
 /* ------------------------------------------------------------------------
- * Operators around the experts step. Each enqueues one kernel on `stream`,
- * needs no workspace and allocates nothing, so it may be captured into a HIP
- * graph and calls may overlap as long as their outputs are distinct. A leading
+ * Operators around the experts step. Each enqueues one kernel on `stream`
+ * (moe_add_rmsnorm one for every 2^21 rows), needs no workspace and allocates
+ * nothing, so it may be captured into a HIP graph and calls may overlap as long
+ * as their outputs are distinct. A leading
  * dimension of 0 means contiguous rows. Unless said otherwise, value pointers
  * and codes are 16-byte aligned (else MOE_EINVAL) and the byte distance of
  * their rows is a multiple of 16 (else MOE_ENOTSUP); outputs do not overlap

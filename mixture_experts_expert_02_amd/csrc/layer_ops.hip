@@ -23,7 +23,7 @@ bool type_ok(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP16 || t == MOE_
 int64_t or_default(int64_t ld, int64_t d) { return ld ? ld : d; }
 
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
-constexpr int kMaxRows = 1 << 24;                        // 256 threads to a row still count in 32 bits
+constexpr int kMaxRows = 1 << 24;                        // routing: 64 threads to a row still count in 32 bits
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;     // workgroups of 256 threads
 
 // rows of n values of the type, ld elements apart: 16-byte accesses at every multiple of 8
@@ -71,8 +71,28 @@ int check_mx_rows(const moe_mx_rows* p, const moe::mxf::RowsParams& q, const voi
 }
 
 // ------------------------------------------------------------------- norm
+constexpr int kNormRows = 1 << 21;  // rows to a launch: a grid's threads count in 32 bits, up to 1024 to a row
+
+// the rows from row t on
+template <int DT>
+moe::NormParams norm_from(const moe::NormParams& p, int64_t t) {
+  moe::NormParams q = p;
+  auto at = [&](const void* base, int64_t ld) { return base ? (uint8_t*)base + t * ld * moe::elem_size(DT) : nullptr; };
+  q.x = at(p.x, p.ldx);
+  q.res = at(p.res, p.ld_res);
+  q.res_out = at(p.res_out, p.ld_res_out);
+  q.y = at(p.y, p.ldy);
+  q.codes = p.codes ? p.codes + t * p.ld_codes : nullptr;
+  q.scales = p.scales ? p.scales + t * p.ld_scales : nullptr;
+  return q;
+}
+
 template <int DT, int FMT>
 void launch_norm(const moe::NormParams& q, int T, hipStream_t s) {
+  if (T > kNormRows) {
+    for (int t = 0; t < T; t += kNormRows) launch_norm<DT, FMT>(norm_from<DT>(q, t), std::min(T - t, kNormRows), s);
+    return;
+  }
   const int n8 = q.H / 8;
   const dim3 g((unsigned)T);
 #define MOE_NORM(NT, C) hipLaunchKernelGGL((moe::k_add_rmsnorm<DT, FMT, NT, C>), g, dim3(NT), 0, s, q)

@@ -140,3 +140,22 @@ def test_elements_beside_their_borders(dtype, fmt):
         got = np.stack([L.E2M1[c & 15], L.E2M1[c >> 4]], -1).reshape(-1) if fmt == "mxfp4" else L.e4m3_values()[c]
         assert np.array_equal(got[sure], elem[0][sure])
     assert near > T * H // 4
+
+
+@pytest.mark.parametrize("T,H", [(2 ** 22 + 5, 8224), (2 ** 23 + 1, 64)])
+def test_more_rows_than_a_grid_dimension_holds(T, H):
+    """Rows times threads pass 32 bits, offsets too; the rows around the borders are looked at."""
+    print(f"[norm] {T}x{H}", flush=True)
+    need = T * H * 2.6
+    if torch.cuda.mem_get_info()[0] < 1.2 * need:
+        pytest.skip("not enough memory")
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+    at = [r for b in (0, 2 ** 21, 2 ** 22, T) for r in (b - 2, b - 1, b, b + 1) if 0 <= r < T]
+    rows = torch.randn(len(at), H, generator=torch.Generator().manual_seed(1)).bfloat16()
+    x[at] = rows.to(DEV)
+    w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    o = moe.add_rmsnorm(x, w, want_y=False, mx="mxfp4")
+    torch.cuda.synchronize()
+    want = moe.add_rmsnorm(rows.to(DEV), w, want_y=False, mx="mxfp4")
+    assert torch.equal(o.codes[at], want.codes) and torch.equal(o.scales[at], want.scales)
+    check_mx(want.codes, want.scales, L.rmsnorm(rows.double().numpy(), np.ones(H), float(np.float32(1e-6))), "mxfp4")
