@@ -190,10 +190,11 @@ int launch_linear(moe::mxl::Params& q, bool exact, hipStream_t s) {
 
 // ----------------------------------------------------------------- routing
 // A token takes 16 lanes, four tokens to a wave, where tokens are many: us with 16 and with 64 lanes:
-// 65536 x 256 softmax, top 8, 37 and 61, 4096 x 128 4.3 and 6.9. Up to 256 experts 16 lanes hold 16
-// each, and few tokens wait for that chain: 1 x 256 sigmoid in 8 groups 6.6 and 4.9, 2048 x 256 7.3 and 6.3, 4096 x 256
-// 7.5 and 8.5; with 128 experts 16 lanes are never behind (1 x 128 3.8 and 4.2). Vector
-// loads of 8 or more: 65536 x 256 41 -> 37.
+// 65536 x 256 softmax, top 8, 34 and 60, 16384 x 256 sigmoid in 8 groups 14.5 and 22, 65536 x 128 20 and 50, 4096 x 128
+// 4.4 and 6.0, 4096 x 64 4.1 and 5.4. Up to 256 experts 16 lanes hold 16 each, and few tokens wait for that chain:
+// 1 x 256 sigmoid in 8 groups 6.6 and 4.8, 2048 x 256 7.4 and 6.3, 4096 x 256 7.4 and 8.5; with 128 experts 16 lanes
+// are not behind (1 x 128 3.7 and 3.7). Vector loads of 8 or more, against value by value: 65536 x 256 34 and 61,
+// 1 x 128 3.7 and 5.1.
 template <int DT>
 void launch_route(const moe::RouteTopkParams& q, hipStream_t s) {
   const bool row16 = aligned(q.logits, 16) && aligned(q.bias, 16) && q.ld * moe::elem_size(DT) % 16 == 0;

@@ -210,7 +210,9 @@ __device__ __forceinline__ void store_block(const Params& p, f32x16 (&acc)[FN][F
 #pragma unroll
   for (int strip = 0; strip < NSTRIP; ++strip) {
     const int j = strip / NI, i0 = strip % NI * FG;
-    // results stay in AGPRs until they are wanted (moved to VGPRs as a whole they would spill)
+    // results stay in AGPRs until they are wanted (moved to VGPRs as a whole they would spill). The 128 x 256 tile
+    // of MXFP8 rows still spills one fragment before the branch over the epilogues: 16 registers a lane, 29 MB written
+    // and read again at 8192 x 7168 x 2048.
 #pragma unroll
     for (int i = 0; i < FG; ++i) asm volatile("" : "+a"(acc[i0 + i][j]));
     if constexpr (EXTRA != 0 && !AHEAD) load_add(strip, ad[0]);
@@ -324,7 +326,8 @@ __global__ __launch_bounds__(256, (Tile<AF, BM, BN, BK, NBUF>::WGS)) void k_tile
 
   // Workgroup b runs on XCD b mod 8; each XCD takes a contiguous run of the
   // tiles, ordered in groups of 4 row tiles, columns outer inside a group, so
-  // the tiles it holds at one time share operand panels in its L2.
+  // the tiles it holds at one time share operand panels in its L2. us with groups of 4, 8 and 16: 8192 x 7168 x 2048
+  // MXFP8 121, 124 and 128, 8192 x 4096 x 7168 190, 195 and 198, 4096 x 4096 x 14336 MXFP4 113, 115 and 119.
   const int n_tiles = p.mt * p.nt;
   const int per = (n_tiles + 7) >> 3;
   const int item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);

@@ -21,8 +21,8 @@
 // With more than kList of them (many equal scores) the wave takes the picks
 // one by one instead, each the largest key and among its holders the lowest index.
 //
-// Bound by instructions: 16384 x 256 fp32 in 8 groups 14.7 us (17.8 MB, 1.2 TB/s), most of it the
-// sigmoids in double; 65536 x 256 softmax 37 us (2 TB/s); 32 x 128 4.1 us, the chain of one token.
+// Bound by instructions: 16384 x 256 fp32 in 8 groups 14.5 us (17.8 MB, 1.2 TB/s), most of it the
+// sigmoids in double; 65536 x 256 softmax 34 us (2.1 TB/s); 32 x 128 4.0 us, the chain of one token.
 #pragma once
 
 #include "elem.hpp"
