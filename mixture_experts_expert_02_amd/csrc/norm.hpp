@@ -8,9 +8,10 @@
 // scaling (one read of x and residual). Squares, their sum and the root are
 // doubles, where the square of every float32 is in range (sums in fp32 lost rows above 2^64 and below
 // 2^-75, and half the bits of r). The root is split into 2^k m, m in [1, 2): h 2^k is at most sqrt(H), so the
-// products with w and m pass float32 only if y does. The microscaled output and a float32 y
-// carry the roundings of both products and of m along (e below); the former is quantized from y
-// rounded to odd, so that its elements are the nearest ones to h * w * r, not to a y rounded before.
+// products with w and m pass float32 only if y does (and an h 2^k below 2^-126 rounds as float32 does there).
+// The microscaled output and a float32 y carry the roundings of both products and of m along (e below); the
+// former is quantized from y rounded to odd, so that its elements are the nearest ones to h * w * r, not to a
+// y rounded before.
 // A 16-bit y takes the plain products. A thread
 // holds C chunks of 8 values, NT chunks apart; a block of 32 values is one
 // quad of lanes, as in the quantizer. Bound by HBM where rows are many: 8192 x 7168 bf16 with
