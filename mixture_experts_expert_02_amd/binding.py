@@ -681,7 +681,7 @@ def mx_linear(a, a_scales, w, w_scales, a_fmt: str = "mxfp8", bias=None, add=Non
     try:
         (M, cols), (N, half), dev, u8 = a.shape, w.shape, a.get_device(), torch.uint8
         K, nb = 2 * half, half >> 4
-        plain = (dev >= 0 and max(M, N, K) <= _INT_MAX and cols == (half if f == MOE_MX_FP4 else K) and not half & 15
+        plain = (dev >= 0 and M | N | K <= _INT_MAX and cols == (half if f == MOE_MX_FP4 else K) and not half & 15
                  and a.dtype is u8 and w.dtype is u8 and a_scales.dtype is u8 and w_scales.dtype is u8
                  and a_scales.shape == (M, nb) and w_scales.shape == (N, nb)
                  and w.get_device() == dev and a_scales.get_device() == dev and w_scales.get_device() == dev
@@ -727,9 +727,10 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
         _refuse(where, f"unknown score {score!r}")
     if group_score not in _GROUP:
         _refuse(where, f"unknown group score {group_score!r}")
-    if not isinstance(k, int) or _count(k, where, "k") <= 0:
+    if not isinstance(k, int) or not 0 < k <= _INT_MAX:
         _refuse(where, "k must be a positive integer")
-    n_group, topk_group = _count(n_group, where, "n_group"), _count(topk_group, where, "topk_group")
+    if n_group or topk_group:
+        n_group, topk_group = _count(n_group, where, "n_group"), _count(topk_group, where, "topk_group")
     b_ptr = None if bias is None else _vector(bias, E, _F32, dev, where, "bias")
     if ids is None:
         ids = logits.new_empty(T, k, dtype=torch.int32)
