@@ -4,7 +4,8 @@
  * The library runs the experts step of a mixture-of-experts layer on one GPU
  * (and, optionally, the router step before it, moe_route, and the operators
  * around it in a layer: row norm, microscaled quantization, a dense product
- * with MXFP4 weights and general routing, at the end of this file):
+ * with MXFP4 weights, general routing, a gated block of 16-bit weights with its
+ * backward pass and projections with adapters, at the end of this file):
  * group the router's top-k slots by expert (histogram, prefix sum to segment
  * end offsets, stable permutation), a grouped GEMM for the gate and up
  * projections with the activation and route weight applied in its epilogue,
@@ -589,6 +590,103 @@ typedef struct {
  * (MOE_EINVAL otherwise). */
 int moe_route_topk(const moe_route_topk_problem* p, const void* logits, const float* bias, int32_t* topk_ids,
                    float* topk_weights, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Dense 16-bit projections beside the routed experts: the gated block of a
+ * shared expert (or of a dense layer), its backward pass, and projections with
+ * low-rank adapters of many requests. A leading dimension of 0 means
+ * contiguous rows. Unless said otherwise pointers to 16-bit values are 16-byte
+ * aligned (else MOE_EINVAL) and their leading dimensions multiples of 8, at
+ * most 2^21 (else MOE_ENOTSUP); outputs do not overlap inputs or each other. The
+ * caller owns the workspace (16-byte aligned; NULL where 0 bytes are asked
+ * for); its contents before the call do not matter, and calls that share one must be ordered, by
+ * their stream or otherwise. The same call gives the same bits. Nothing is allocated
+ * and only kernels are enqueued, so a call may be captured into a HIP graph.
+ * Results are accumulated in float32 and rounded once.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t M;           /* rows, < 2^24 */
+  int32_t H, I;        /* width in and out; multiples of 8, at most 2^20, H * I at most 2^32 (else MOE_ENOTSUP) */
+  int32_t type;        /* moe_dtype: MOE_T_BF16 or MOE_T_FP16 (MOE_T_FP32: MOE_ENOTSUP) */
+  int32_t act;         /* moe_act, with alpha, beta and limit as in moe_problem */
+  float alpha, beta, limit;
+  int64_t ldx, ld_wg, ld_wu, ld_out, ld_gate, ld_up; /* elements between rows */
+} moe_gated_problem;
+
+/* Workspace bytes of moe_gated_linear on *p; 0 if it needs none or *p is invalid. */
+size_t moe_gated_linear_workspace_bytes(const moe_gated_problem* p);
+
+/* The gated block of moonep_experts page, module docstring (gate and up
+ * projections and their gated product), on all rows:
+ *   g = x w_gate^T + bias_gate, u = x w_up^T + bias_up, out = f(g, u), f as for moe_act
+ * (a NaN passes through f's clamps).
+ *   x               (device) [M, H]
+ *   w_gate, w_up    (device) [I, H]
+ *   bias_gate, bias_up (device) float32 [I], both or neither (NULL), 4-byte aligned
+ *   out             (device) [M, I], overwritten
+ *   gate, up        (device) [M, I]: g and u rounded to the type, for the backward
+ *                   pass; both or neither (NULL). out comes from the unrounded ones. */
+int moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_gate, const void* w_up,
+                     const float* bias_gate, const float* bias_up, void* out, void* gate, void* up, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream);
+
+typedef struct {
+  moe_gated_problem fwd;  /* of the forward call; ld_out: of dout */
+  int32_t dw_type;        /* moe_dtype of dw_gate and dw_up: fwd.type or MOE_T_FP32 */
+  int32_t accumulate;     /* 1: the weights' and biases' gradients are added to what dw_gate, dw_up, dbias_gate and
+                             dbias_up hold; 0: these are overwritten */
+  int64_t ld_dx, ld_dwg, ld_dwu; /* elements between rows; ld_dwg, ld_dwu with float32 at most 2^40, multiples of 4 */
+} moe_gated_grad_problem;
+
+size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p);
+
+/* Gradients of moe_gated_linear from dout, the gradient of out, and the gate and up it kept:
+ *   dg = dout df/dg, du = dout df/du   (f's clamps pass gradients on their limits and none beyond)
+ *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dbias_gate = sum_m dg, dbias_up = sum_m du
+ * dg and du are rounded to the type for the products (to half a step of each value; the biases' sums take them
+ * unrounded), so dx, dw_gate and dw_up carry that beside their own rounding, with dw_type MOE_T_FP32 too.
+ *   dout             (device) [M, I]
+ *   dx               (device) [M, H], overwritten, or NULL
+ *   dw_gate, dw_up   (device) [I, H] of dw_type, both or neither (NULL)
+ *   dbias_gate, dbias_up (device) float32 [I], both or neither (NULL)
+ * x may be NULL without dw_gate, w_gate and w_up without dx. At least one gradient is asked for. With M = 0 the weights'
+ * and biases' gradients are zero (unless accumulated). */
+int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout, const void* x, const void* w_gate,
+                              const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,
+                              float* dbias_gate, float* dbias_up, void* workspace, size_t workspace_bytes,
+                              moe_stream_t stream);
+
+typedef struct {
+  int32_t M, N, K;     /* rows (< 2^24), width out (at most 2^20), width in (a multiple of 8, at most 2^20) */
+  int32_t R, L;        /* rank (a multiple of 8, at most 256) and number of adapters (at most 4096) (else MOE_ENOTSUP) */
+  int32_t type;        /* MOE_T_BF16 or MOE_T_FP16 */
+  int64_t ldx, ldw;    /* elements between rows */
+  int64_t ld_out, ld_add; /* elements between rows, any up to 2^40 */
+} moe_lora_problem;
+
+size_t moe_lora_linear_workspace_bytes(const moe_lora_problem* p);
+
+/* A projection with a low-rank adapter of its own for every row, for the rows of
+ * many requests at once:
+ *   out_m = x_m w^T + bias + add_m + scales[a] (x_m lora_a[a]^T) lora_b[a]^T,  a = ids[m]
+ * A row whose id lies outside [0, L) has no adapter. w may be NULL: the adapters' part alone, to be
+ * added to a projection computed elsewhere (moe_mx_linear's, through add). Adapters whose
+ * rank is smaller than R are padded with zeros.
+ *   x       (device) [M, K]
+ *   w       (device) [N, K] or NULL
+ *   lora_a  (device) [L, R, K], contiguous
+ *   lora_b  (device) [L, N, R], contiguous
+ *   ids     (device) int32 [M]
+ *   scales  (device) float32 [L]
+ *   bias    (device) float32 [N] or NULL
+ *   add     (device) [M, N] or NULL; may be out itself (with ld_add == ld_out)
+ *   out     (device) [M, N], overwritten
+ * out and add need their type's alignment only; N is free. x lora_a^T is carried in two 16-bit parts of a row's own
+ * power of two (16 significand bits and more). What an adapter holds reaches its own rows only. */
+int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, const void* lora_a, const void* lora_b,
+                    const int32_t* ids, const float* scales, const float* bias, const void* add, void* out,
+                    void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* Static description of a status code. */
 const char* moe_strerror(int status);

@@ -33,7 +33,9 @@ EXPORTED = (
     "moe_strerror", "moe_route", "moe_experts_forward_grouped_timed", "moe_experts_forward_noalloc",
     "moe_check_expert_params", "moe_mx_packed_bytes", "moe_mx_pack_weights", "moe_bf16_packed_bytes",
     "moe_bf16_pack_weights", "moe_mx_quantize", "moe_mx_dequantize", "moe_add_rmsnorm", "moe_mx_linear",
-    "moe_route_topk",
+    "moe_route_topk", "moe_gated_linear_workspace_bytes", "moe_gated_linear",
+    "moe_gated_linear_backward_workspace_bytes", "moe_gated_linear_backward", "moe_lora_linear_workspace_bytes",
+    "moe_lora_linear",
 )
 MOE_ROUTE_RENORMALIZE, MOE_ROUTE_DEEPSEEK_V3 = 0, 1
 _ROUTE = {"renormalize": MOE_ROUTE_RENORMALIZE, "deepseek_v3": MOE_ROUTE_DEEPSEEK_V3}
@@ -86,6 +88,24 @@ class MoeRouteTopkProblem(ctypes.Structure):
                 ("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
                 ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("routed_scaling_factor", ctypes.c_float), ("ld", ctypes.c_int64)]
+
+
+class MoeGatedProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("limit", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ld_wg", ctypes.c_int64), ("ld_wu", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("ld_gate", ctypes.c_int64), ("ld_up", ctypes.c_int64)]
+
+
+class MoeGatedGradProblem(ctypes.Structure):
+    _fields_ = [("fwd", MoeGatedProblem), ("dw_type", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("ld_dx", ctypes.c_int64), ("ld_dwg", ctypes.c_int64), ("ld_dwu", ctypes.c_int64)]
+
+
+class MoeLoraProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("R", ctypes.c_int32),
+                ("L", ctypes.c_int32), ("type", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("ld_add", ctypes.c_int64)]
 
 
 class MoeWsLayout(ctypes.Structure):
@@ -159,6 +179,13 @@ def lib() -> ctypes.CDLL:
         L.moe_mx_linear.restype = ctypes.c_int
         L.moe_route_topk.argtypes = [ctypes.POINTER(MoeRouteTopkProblem), vp, vp, vp, vp, vp]
         L.moe_route_topk.restype = ctypes.c_int
+        for name, P, n in (("moe_gated_linear", MoeGatedProblem, 8),
+                           ("moe_gated_linear_backward", MoeGatedGradProblem, 11), ("moe_lora_linear", MoeLoraProblem, 9)):
+            fn, size = getattr(L, name), getattr(L, name + "_workspace_bytes")
+            fn.argtypes = [ctypes.POINTER(P)] + [vp] * n + [vp, sz, vp]
+            fn.restype = ctypes.c_int
+            size.argtypes = [ctypes.POINTER(P)]
+            size.restype = sz
         L.moe_strerror.argtypes = [ctypes.c_int]
         L.moe_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -359,6 +386,39 @@ def moe_mx_linear(p: MoeMxLinearProblem, a, a_scales, w, w_scales, bias, add, ou
 def moe_route_topk(p: MoeRouteTopkProblem, logits, bias, topk_ids, topk_weights, stream=None) -> int:
     return lib().moe_route_topk(ctypes.byref(p), _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights),
                                 _stream(stream))
+
+
+def _ws(workspace):
+    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def moe_gated_linear_workspace_bytes(p: MoeGatedProblem) -> int:
+    return lib().moe_gated_linear_workspace_bytes(ctypes.byref(p))
+
+
+def moe_gated_linear(p: MoeGatedProblem, x, w_gate, w_up, bias_gate, bias_up, out, gate, up, workspace, stream=None) -> int:
+    return lib().moe_gated_linear(ctypes.byref(p), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(bias_gate), _ptr(bias_up),
+                                  _ptr(out), _ptr(gate), _ptr(up), *_ws(workspace), _stream(stream))
+
+
+def moe_gated_linear_backward_workspace_bytes(p: MoeGatedGradProblem) -> int:
+    return lib().moe_gated_linear_backward_workspace_bytes(ctypes.byref(p))
+
+
+def moe_gated_linear_backward(p: MoeGatedGradProblem, dout, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, dbias_gate,
+                              dbias_up, workspace, stream=None) -> int:
+    return lib().moe_gated_linear_backward(ctypes.byref(p), _ptr(dout), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate),
+                                           _ptr(up), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(dbias_gate),
+                                           _ptr(dbias_up), *_ws(workspace), _stream(stream))
+
+
+def moe_lora_linear_workspace_bytes(p: MoeLoraProblem) -> int:
+    return lib().moe_lora_linear_workspace_bytes(ctypes.byref(p))
+
+
+def moe_lora_linear(p: MoeLoraProblem, x, w, lora_a, lora_b, ids, scales, bias, add, out, workspace, stream=None) -> int:
+    return lib().moe_lora_linear(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b), _ptr(ids), _ptr(scales),
+                                 _ptr(bias), _ptr(add), _ptr(out), *_ws(workspace), _stream(stream))
 
 
 # ---------------------------------------------------------------- torch conveniences
@@ -745,3 +805,181 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, n_group: int =
     _run(lib().moe_route_topk, "moe_route_topk", dev, ctypes.byref(p), logits.data_ptr(), b_ptr, ids.data_ptr(),
          weights.data_ptr())
     return ids, weights
+
+
+# ---------------------------------------------------------------- dense 16-bit projections beside the experts
+class GatedOut(NamedTuple):
+    """gated_linear's results; gate and up are None unless they were asked for."""
+    out: torch.Tensor
+    gate: Optional[torch.Tensor]
+    up: Optional[torch.Tensor]
+
+
+class GatedGrads(NamedTuple):
+    """gated_linear_backward's results; what was not asked for is None."""
+    dx: Optional[torch.Tensor]
+    dw_gate: Optional[torch.Tensor]
+    dw_up: Optional[torch.Tensor]
+    dbias_gate: Optional[torch.Tensor]
+    dbias_up: Optional[torch.Tensor]
+
+
+_T16 = (torch.bfloat16, torch.float16)
+
+
+def _rows16(t, where: str, name: str):
+    r, c, dev, ld = _rows(t, where, name)
+    if t.dtype not in _T16:
+        _refuse(where, f"{name} has type {t.dtype}: bfloat16 or float16 is needed", MOE_ENOTSUP)
+    return r, c, dev, ld
+
+
+def _both(a, b, where: str, names: str) -> bool:
+    if (a is None) != (b is None):
+        _refuse(where, f"{names} come together")
+    return a is not None
+
+
+def _act(act, where: str) -> int:
+    a = _ACT.get(act) if isinstance(act, str) else None
+    if a is None:
+        _refuse(where, f"unknown activation {act!r}")
+    return a
+
+
+def _workspace(workspace, need: int, like, dev: int, where: str):
+    """(address, bytes) of the given workspace, or of a new one; the tensor to keep alive."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, "workspace must be a contiguous tensor on the GPU of the other tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: float = 0.0, limit: float = math.inf,
+                 bias_gate=None, bias_up=None, save: bool = False, out=None, gate=None, up=None,
+                 workspace=None) -> GatedOut:
+    """f(x w_gate^T + bias_gate, x w_up^T + bias_up) for x [M, H] and weights [I, H] of one type (bf16 or
+    float16; rows may be strided), float32 biases [I]. save (or gate and up given): the two
+    projections [M, I] as well, for gated_linear_backward. See moe_gated_linear."""
+    where = "gated_linear"
+    M, H, dev, ldx = _rows16(x, where, "x")
+    I, _, _ = _matrix(w_gate, where, "w_gate")
+    same = (x.dtype,)
+    ld_wg = _ld(w_gate, (I, H), same, dev, where, "w_gate")
+    ld_wu = _ld(w_up, (I, H), same, dev, where, "w_up")
+    bg = bu = None
+    if _both(bias_gate, bias_up, where, "bias_gate and bias_up"):
+        bg = _vector(bias_gate, I, _F32, dev, where, "bias_gate")
+        bu = _vector(bias_up, I, _F32, dev, where, "bias_up")
+    shape = (M, I)
+    ldo = ld_g = ld_u = 0
+    g_ptr = u_ptr = None
+    if _both(gate, up, where, "gate and up"):
+        ld_g = _ld(gate, shape, same, dev, where, "gate")
+        ld_u = _ld(up, shape, same, dev, where, "up")
+    elif save:
+        gate, up = x.new_empty(shape), x.new_empty(shape)
+    if gate is not None:
+        g_ptr, u_ptr = gate.data_ptr(), up.data_ptr()
+    if out is None:
+        out = x.new_empty(shape)
+    else:
+        ldo = _ld(out, shape, same, dev, where, "out")
+    p = MoeGatedProblem(M, H, I, _TYPE[x.dtype], _act(act, where), alpha, beta, limit, ldx, ld_wg, ld_wu, ldo, ld_g, ld_u)
+    ref = ctypes.byref(p)
+    ws, size, keep = _workspace(workspace, lib().moe_gated_linear_workspace_bytes(ref), x, dev, where)
+    _run(lib().moe_gated_linear, "moe_gated_linear", dev, ref, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), bg, bu,
+         out.data_ptr(), g_ptr, u_ptr, ws, size)
+    return GatedOut(out, gate, up)
+
+
+def gated_linear_backward(dout, x, w_gate, w_up, gate, up, act: str = "silu", alpha: float = 1.0, beta: float = 0.0,
+                          limit: float = math.inf, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = False,
+                          accumulate: bool = False, dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None,
+                          workspace=None) -> GatedGrads:
+    """Gradients of gated_linear from dout [M, I] and the gate and up [M, I] it kept: dx [M, H], dw_gate and
+    dw_up [I, H] (given tensors may be float32), float32 dbias_gate and dbias_up [I]. accumulate: the
+    weights' and biases' gradients are added to the given tensors. See moe_gated_linear_backward."""
+    where = "gated_linear_backward"
+    M, I, dev, ldo = _rows16(dout, where, "dout")
+    _, H, _ = _matrix(x, where, "x")
+    same = (dout.dtype,)
+    shape = (M, I)
+    ldx = _ld(x, (M, H), same, dev, where, "x")
+    ld_wg = _ld(w_gate, (I, H), same, dev, where, "w_gate")
+    ld_wu = _ld(w_up, (I, H), same, dev, where, "w_up")
+    ld_g = _ld(gate, shape, same, dev, where, "gate")
+    ld_u = _ld(up, shape, same, dev, where, "up")
+    ld_dx = ld_dwg = ld_dwu = 0
+    dw_type = dout.dtype
+    if dx is not None:
+        ld_dx = _ld(dx, (M, H), same, dev, where, "dx")
+    elif want_dx:
+        dx = dout.new_empty(M, H)
+    if _both(dw_gate, dw_up, where, "dw_gate and dw_up"):
+        ld_dwg = _ld(dw_gate, (I, H), (dout.dtype, torch.float32), dev, where, "dw_gate")
+        dw_type = dw_gate.dtype
+        ld_dwu = _ld(dw_up, (I, H), (dw_type,), dev, where, "dw_up")
+    elif want_dw:
+        if accumulate:
+            _refuse(where, "accumulate needs dw_gate and dw_up")
+        dw_gate, dw_up = dout.new_empty(I, H), dout.new_empty(I, H)
+    if _both(dbias_gate, dbias_up, where, "dbias_gate and dbias_up"):
+        _vector(dbias_gate, I, _F32, dev, where, "dbias_gate")
+        _vector(dbias_up, I, _F32, dev, where, "dbias_up")
+    elif want_dbias:
+        if accumulate:
+            _refuse(where, "accumulate needs dbias_gate and dbias_up")
+        dbias_gate, dbias_up = (dout.new_empty(I, dtype=torch.float32) for _ in range(2))
+    f = MoeGatedProblem(M, H, I, _TYPE[dout.dtype], _act(act, where), alpha, beta, limit, ldx, ld_wg, ld_wu, ldo, ld_g, ld_u)
+    p = MoeGatedGradProblem(f, _TYPE[dw_type], 1 if accumulate else 0, ld_dx, ld_dwg, ld_dwu)
+    ref = ctypes.byref(p)
+    ws, size, keep = _workspace(workspace, lib().moe_gated_linear_backward_workspace_bytes(ref), dout, dev, where)
+    at = [None if t is None else t.data_ptr() for t in (dx, dw_gate, dw_up, dbias_gate, dbias_up)]
+    _run(lib().moe_gated_linear_backward, "moe_gated_linear_backward", dev, ref, dout.data_ptr(), x.data_ptr(),
+         w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(), *at, ws, size)
+    return GatedGrads(dx, dw_gate, dw_up, dbias_gate, dbias_up)
+
+
+def lora_linear(x, w, lora_a, lora_b, ids, scales, bias=None, add=None, out=None, workspace=None) -> torch.Tensor:
+    """x w^T + bias + add + scales[a] (x lora_a[a]^T) lora_b[a]^T with a = ids[m] for row m of x [M, K]; a row whose
+    id is outside [0, L) has no adapter. w [N, K] or None, lora_a [L, R, K], lora_b [L, N, R], all of x's type (bf16 or
+    float16); ids int32 [M], scales float32 [L], bias float32 [N]; add and out [M, N] (out may be add).
+    See moe_lora_linear."""
+    where = "lora_linear"
+    M, K, dev, ldx = _rows16(x, where, "x")
+    same = (x.dtype,)
+    for t, name in ((lora_a, "lora_a"), (lora_b, "lora_b")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_contiguous():
+            _refuse(where, f"{name} must be a contiguous tensor of three dimensions")
+        if t.dtype != x.dtype:
+            _refuse(where, f"{name} has type {t.dtype}")
+        if t.get_device() != dev:
+            _refuse(where, f"{name} must be on the GPU of the other tensors")
+    L, R, _ = lora_a.shape
+    N = lora_b.shape[1]
+    if lora_a.shape[2] != K or lora_b.shape[0] != L or lora_b.shape[2] != R:
+        _refuse(where, f"lora_a {tuple(lora_a.shape)} and lora_b {tuple(lora_b.shape)} do not fit rows of {K}")
+    _size(max(N, L, R), where)
+    ldw = 0 if w is None else _ld(w, (N, K), same, dev, where, "w")
+    i_ptr = _vector(ids, M, _I32, dev, where, "ids")
+    s_ptr = _vector(scales, L, _F32, dev, where, "scales")
+    b_ptr = None if bias is None else _vector(bias, N, _F32, dev, where, "bias")
+    ldo = ld_add = 0
+    if out is None:
+        out = x.new_empty(M, N)
+    else:
+        ldo = _ld(out, (M, N), same, dev, where, "out")
+    if add is not None:
+        ld_add = _ld(add, (M, N), same, dev, where, "add")
+    p = MoeLoraProblem(M, N, K, R, L, _TYPE[x.dtype], ldx, ldw, ldo, ld_add)
+    ref = ctypes.byref(p)
+    ws, size, keep = _workspace(workspace, lib().moe_lora_linear_workspace_bytes(ref), x, dev, where)
+    _run(lib().moe_lora_linear, "moe_lora_linear", dev, ref, x.data_ptr(), None if w is None else w.data_ptr(),
+         lora_a.data_ptr(), lora_b.data_ptr(), i_ptr, s_ptr, b_ptr, None if add is None else add.data_ptr(),
+         out.data_ptr(), ws, size)
+    return out

@@ -7,7 +7,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", n) for n in ("moe_experts.hip", "layer_ops.hip")]
+SRCS = [os.path.join(HERE, "csrc", n) for n in ("moe_experts.hip", "layer_ops.hip", "dense_ops.hip")]
 LIB = os.path.join(HERE, "libmoe_experts.so")
 
 HIPCC_FLAGS = [

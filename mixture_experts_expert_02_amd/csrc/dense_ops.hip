@@ -1,0 +1,375 @@
+// Host side of the dense 16-bit projections: the gated block, its backward pass and
+// projections with adapters. Argument checks, workspace and launches; no
+// host synchronisation.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_experts.h"
+#include "dense16.hpp"
+#include "gated_grad.hpp"
+#include "lora.hpp"
+
+namespace {
+
+using namespace moe::d16;
+
+int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+int64_t or_default(int64_t ld, int64_t d) { return ld ? ld : d; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxWidth = 1 << 20;
+constexpr int64_t kMaxLd = (int64_t)1 << 21, kMaxLdOut = (int64_t)1 << 40;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;  // workgroups: threads count in 32 bits
+
+int check_ld(int64_t ld, int64_t n, int64_t per = 8, int64_t most = kMaxLd) {
+  if (ld < n) return MOE_EINVAL;
+  return ld % per || ld > most ? MOE_ENOTSUP : MOE_OK;
+}
+int first_of(std::initializer_list<int> rcs) {
+  for (int rc : rcs)
+    if (rc) return rc;
+  return MOE_OK;
+}
+bool given16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p || !aligned(p, 16)) return false;
+  return true;
+}
+
+int type16(int32_t t) {
+  if (t == MOE_T_BF16 || t == MOE_T_FP16) return MOE_OK;
+  return t == MOE_T_FP32 ? MOE_ENOTSUP : MOE_EINVAL;
+}
+
+int check_act(const moe_gated_problem& p) {
+  if (p.act != MOE_ACT_SILU && p.act != MOE_ACT_SWIGLU_OAI && p.act != MOE_ACT_SITU) return MOE_EINVAL;
+  if (p.act == MOE_ACT_SILU) return MOE_OK;
+  if (!std::isfinite(p.alpha) || !std::isfinite(p.beta)) return MOE_EINVAL;
+  if (p.act == MOE_ACT_SITU) return p.alpha > 0.f && p.beta > 0.f ? MOE_OK : MOE_ENOTSUP;
+  if (std::isnan(p.limit)) return MOE_EINVAL;
+  return p.limit > 0.f ? MOE_OK : MOE_ENOTSUP;
+}
+
+// sizes, type and activation of a gated problem, and its leading dimensions
+struct Gated {
+  int64_t ldx, ld_wg, ld_wu, ld_out, ld_gate, ld_up;
+};
+int gated_sizes(const moe_gated_problem* p, Gated& g) {
+  if (!p || p->M < 0 || p->H <= 0 || p->I <= 0) return MOE_EINVAL;
+  int rc = first_of({type16(p->type), check_act(*p)});
+  if (rc) return rc;
+  if (p->M >= kMaxRows || p->H % 8 || p->I % 8 || p->H > kMaxWidth || p->I > kMaxWidth ||
+      (int64_t)p->H * p->I > (int64_t)1 << 32)
+    return MOE_ENOTSUP;
+  g = {or_default(p->ldx, p->H),     or_default(p->ld_wg, p->H),   or_default(p->ld_wu, p->H),
+       or_default(p->ld_out, p->I), or_default(p->ld_gate, p->I), or_default(p->ld_up, p->I)};
+  return first_of({check_ld(g.ldx, p->H), check_ld(g.ld_wg, p->H), check_ld(g.ld_wu, p->H), check_ld(g.ld_out, p->I),
+                   check_ld(g.ld_gate, p->I), check_ld(g.ld_up, p->I)});
+}
+
+moe::ActParams act_of(const moe_gated_problem& p) { return {p.act, p.alpha, p.beta, p.limit}; }
+
+template <class F>
+int with_type16(int32_t type, F f) {
+  if (type == MOE_T_BF16) return f(std::integral_constant<int, moe::T_BF16>{});
+  return f(std::integral_constant<int, moe::T_FP16>{});
+}
+
+template <int DT, int MODE, int BM, int BN, int NBUF>
+int launch_tile(Params& q, hipStream_t s) {
+  q.mt = (int)cdiv(q.M, BM);
+  q.nt = (int)cdiv(q.N, MODE == GATED ? BN / 2 : BN);
+  const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : q.splits), 8) * 8;
+  if (n > kMaxGrid) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((k_tile<DT, MODE, BM, BN, NBUF>), dim3((unsigned)n), dim3(256), 0, s, q);
+  return launch_status();
+}
+
+template <int DT, int MODE>
+int launch(Params& q, hipStream_t s) {
+  return launch_tile<DT, MODE, 128, 128, 4>(q, s);
+}
+
+// ------------------------------------------------------------ backward workspace
+struct GradLayout {
+  size_t dg, du, sums, part, bytes;
+};
+GradLayout grad_layout(const moe_gated_problem& p) {
+  GradLayout l;
+  const size_t mi = up256((size_t)p.M * p.I * 2);
+  l.dg = 0;
+  l.du = mi;
+  l.sums = 2 * mi;
+  l.part = l.sums + up256((size_t)cdiv(p.M, kGradRows) * 2 * p.I * 4);
+  l.bytes = l.part;
+  return l;
+}
+
+int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_t& ld_dwg, int64_t& ld_dwu) {
+  if (!p) return MOE_EINVAL;
+  int rc = gated_sizes(&p->fwd, g);
+  if (rc) return rc;
+  if (p->accumulate != 0 && p->accumulate != 1) return MOE_EINVAL;
+  const bool f32 = p->dw_type == MOE_T_FP32;
+  if (!f32 && p->dw_type != p->fwd.type) return p->dw_type == MOE_T_BF16 || p->dw_type == MOE_T_FP16 ? MOE_ENOTSUP : MOE_EINVAL;
+  const int H = p->fwd.H;
+  ld_dx = or_default(p->ld_dx, H);
+  ld_dwg = or_default(p->ld_dwg, H);
+  ld_dwu = or_default(p->ld_dwu, H);
+  return first_of({check_ld(ld_dx, H, 8, kMaxLdOut), check_ld(ld_dwg, H, f32 ? 4 : 8, kMaxLdOut),
+                   check_ld(ld_dwu, H, f32 ? 4 : 8, kMaxLdOut)});
+}
+
+// ------------------------------------------------------------ adapters
+// Rows of x are read by 32-bit offsets from its start, so a call of more goes in parts.
+int lora_rows(const moe_lora_problem& p, int64_t ldx) {
+  return (int)std::min<int64_t>({(int64_t)p.M, (0x7fffffff - 2 * (int64_t)p.K) / (2 * ldx) / 256 * 256, (int64_t)1 << 20});
+}
+struct LoraLayout {
+  size_t perm, sid, ends, tf, t, bytes;
+};
+LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
+  LoraLayout l;
+  l.perm = 0;
+  l.sid = up256((size_t)rows * 4);
+  l.ends = l.sid + up256((size_t)rows * 4);
+  l.tf = l.ends + up256((size_t)p.L * 4);
+  l.t = l.tf + up256((size_t)rows * 4);
+  l.bytes = l.t + up256((size_t)rows * 4 * p.R);
+  return l;
+}
+int lora_sizes(const moe_lora_problem* p, int64_t& ldx, int64_t& ldw, int64_t& ldo, int64_t& lda) {
+  if (!p || p->M < 0 || p->N <= 0 || p->K <= 0 || p->R <= 0 || p->L <= 0) return MOE_EINVAL;
+  int rc = type16(p->type);
+  if (rc) return rc;
+  if (p->M >= kMaxRows || p->N > kMaxWidth || p->K > kMaxWidth || p->K % 8 || p->R % 8 || p->R > kMaxRank ||
+      p->L > kMaxAdapters)
+    return MOE_ENOTSUP;
+  ldx = or_default(p->ldx, p->K);
+  ldw = or_default(p->ldw, p->K);
+  ldo = or_default(p->ld_out, p->N);
+  lda = or_default(p->ld_add, p->N);
+  return first_of({check_ld(ldx, p->K), check_ld(ldw, p->K), check_ld(ldo, p->N, 1, kMaxLdOut),
+                   check_ld(lda, p->N, 1, kMaxLdOut)});
+}
+
+template <int DT>
+void launch_shrink(const ShrinkParams& q, hipStream_t s) {
+  const dim3 g((unsigned)cdiv(q.M, 16)), b(512);
+  if (q.R <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), g, b, 0, s, q);
+  else if (q.R <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), g, b, 0, s, q);
+  else if (q.R <= 64) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), g, b, 0, s, q);
+  else if (q.R <= 128) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), g, b, 0, s, q);
+  else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), g, b, 0, s, q);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_gated_linear_workspace_bytes(const moe_gated_problem* p) {
+  Gated g;
+  if (gated_sizes(p, g)) return 0;
+  return 0;
+}
+
+int moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_gate, const void* w_up,
+                     const float* bias_gate, const float* bias_up, void* out, void* gate, void* up, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream) {
+  Gated g;
+  int rc = gated_sizes(p, g);
+  if (rc) return rc;
+  if (p->M == 0) return MOE_OK;
+  if (!given16({x, w_gate, w_up, out}) || !gate != !up || !aligned(gate, 16) || !aligned(up, 16) ||
+      !bias_gate != !bias_up || !aligned(bias_gate, 4) || !aligned(bias_up, 4))
+    return MOE_EINVAL;
+  const size_t need = moe_gated_linear_workspace_bytes(p);
+  if (need && (!workspace || !aligned(workspace, 16))) return MOE_EINVAL;
+  if (workspace_bytes < need) return MOE_ENOSPC;
+  Params q{};
+  q.m[0] = (const uint16_t*)x;
+  q.n[0] = (const uint16_t*)w_gate;
+  q.n[1] = (const uint16_t*)w_up;
+  q.ldm[0] = g.ldx;
+  q.ldn[0] = g.ld_wg;
+  q.ldn[1] = g.ld_wu;
+  q.out[0] = out;
+  q.ldo[0] = g.ld_out;
+  q.M = p->M;
+  q.N = p->I;
+  q.K = p->H;
+  q.splits = 1;
+  q.bias[0] = bias_gate;
+  q.bias[1] = bias_up;
+  q.keep[0] = gate;
+  q.keep[1] = up;
+  q.ld_keep[0] = g.ld_gate;
+  q.ld_keep[1] = g.ld_up;
+  q.act = act_of(*p);
+  hipStream_t s = (hipStream_t)stream;
+  return with_type16(p->type, [&](auto dt) { return launch<decltype(dt)::value, GATED>(q, s); });
+}
+
+size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p) {
+  Gated g;
+  int64_t a, b, c;
+  if (grad_sizes(p, g, a, b, c) || p->fwd.M == 0) return 0;
+  return grad_layout(p->fwd).bytes;
+}
+
+int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout, const void* x, const void* w_gate,
+                              const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,
+                              float* dbias_gate, float* dbias_up, void* workspace, size_t workspace_bytes,
+                              moe_stream_t stream) {
+  Gated g;
+  int64_t ld_dx, ld_dwg, ld_dwu;
+  int rc = grad_sizes(p, g, ld_dx, ld_dwg, ld_dwu);
+  if (rc) return rc;
+  if (!dw_gate != !dw_up || !dbias_gate != !dbias_up || (!dx && !dw_gate && !dbias_gate)) return MOE_EINVAL;
+  if (!aligned(dx, 16) || !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(dbias_gate, 4) || !aligned(dbias_up, 4))
+    return MOE_EINVAL;
+  const moe_gated_problem& f = p->fwd;
+  hipStream_t s = (hipStream_t)stream;
+  const bool f32 = p->dw_type == MOE_T_FP32;
+  if (f.M == 0) {
+    if (p->accumulate) return MOE_OK;
+    if (dw_gate) {
+      const dim3 grid((unsigned)cdiv((int64_t)f.I * f.H / 8, 256), 2);
+      if (f32) hipLaunchKernelGGL((k_zero_rows<moe::T_FP32>), grid, dim3(256), 0, s, dw_gate, dw_up, ld_dwg, ld_dwu, f.I, f.H);
+      else hipLaunchKernelGGL((k_zero_rows<moe::T_BF16>), grid, dim3(256), 0, s, dw_gate, dw_up, ld_dwg, ld_dwu, f.I, f.H);
+    }
+    if (dbias_gate)
+      hipLaunchKernelGGL(k_column_sums, dim3((unsigned)cdiv(f.I, 256), 2), dim3(256), 0, s, (const float*)nullptr, 0, f.I,
+                         dbias_gate, dbias_up, 0);
+    return launch_status();
+  }
+  if (!given16({dout, gate, up, workspace}) || (dw_gate && !given16({x})) || (dx && !given16({w_gate, w_up}))) return MOE_EINVAL;
+  const GradLayout l = grad_layout(f);
+  if (workspace_bytes < l.bytes) return MOE_ENOSPC;
+  uint8_t* ws = (uint8_t*)workspace;
+  GradParams r{};
+  r.dout = dout;
+  r.gate = gate;
+  r.up = up;
+  r.dg = ws + l.dg;
+  r.du = ws + l.du;
+  r.sums = dbias_gate ? (float*)(ws + l.sums) : nullptr;
+  r.ld_dout = g.ld_out;
+  r.ld_gate = g.ld_gate;
+  r.ld_up = g.ld_up;
+  r.M = f.M;
+  r.I = f.I;
+  r.act = act_of(f);
+  const int blocks = (int)cdiv(f.M, kGradRows);
+  Params q{};
+  q.m[0] = (const uint16_t*)r.dg;
+  q.m[1] = (const uint16_t*)r.du;
+  q.ldm[0] = q.ldm[1] = f.I;
+  q.splits = 1;
+  return with_type16(f.type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    hipLaunchKernelGGL((k_gated_grad<DT>), dim3((unsigned)blocks, (unsigned)cdiv(f.I, 512)), dim3(256), 0, s, r);
+    if (dbias_gate)
+      hipLaunchKernelGGL(k_column_sums, dim3((unsigned)cdiv(f.I, 256), 2), dim3(256), 0, s, (const float*)r.sums, blocks, f.I,
+                         dbias_gate, dbias_up, p->accumulate);
+    int rc = launch_status();
+    if (!rc && dx) {
+      Params d = q;
+      d.n[0] = (const uint16_t*)w_gate;
+      d.n[1] = (const uint16_t*)w_up;
+      d.ldn[0] = g.ld_wg;
+      d.ldn[1] = g.ld_wu;
+      d.out[0] = dx;
+      d.ldo[0] = ld_dx;
+      d.M = f.M;
+      d.N = f.H;
+      d.K = f.I;
+      rc = launch<DT, DX>(d, s);
+    }
+    if (!rc && dw_gate) {
+      Params d = q;
+      d.n[0] = (const uint16_t*)x;
+      d.ldn[0] = g.ldx;
+      d.out[0] = dw_gate;
+      d.out[1] = dw_up;
+      d.ldo[0] = ld_dwg;
+      d.ldo[1] = ld_dwu;
+      d.M = f.I;
+      d.N = f.H;
+      d.K = f.M;
+      d.f32_out = f32;
+      d.accumulate = p->accumulate;
+      rc = launch<DT, DW>(d, s);
+    }
+    return rc;
+  });
+}
+
+size_t moe_lora_linear_workspace_bytes(const moe_lora_problem* p) {
+  int64_t ldx, ldw, ldo, lda;
+  if (lora_sizes(p, ldx, ldw, ldo, lda) || p->M == 0) return 0;
+  return lora_layout(*p, lora_rows(*p, ldx)).bytes;
+}
+
+int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, const void* lora_a, const void* lora_b,
+                    const int32_t* ids, const float* scales, const float* bias, const void* add, void* out,
+                    void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int64_t ldx, ldw, ldo, lda;
+  int rc = lora_sizes(p, ldx, ldw, ldo, lda);
+  if (rc) return rc;
+  if (p->M == 0) return MOE_OK;
+  if (!given16({x, lora_a, lora_b, workspace}) || !aligned(w, 16) || !ids || !scales || !out || !aligned(ids, 4) ||
+      !aligned(scales, 4) || !aligned(bias, 4) || !aligned(add, 2) || !aligned(out, 2))
+    return MOE_EINVAL;
+  const int rows = lora_rows(*p, ldx);
+  const LoraLayout l = lora_layout(*p, rows);
+  if (workspace_bytes < l.bytes) return MOE_ENOSPC;
+  uint8_t* ws = (uint8_t*)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  Params q{};
+  q.n[0] = (const uint16_t*)w;
+  q.ldm[0] = ldx;
+  q.ldn[0] = ldw;
+  q.ldo[0] = ldo;
+  q.N = p->N;
+  q.K = w ? p->K : 0;
+  q.splits = 1;
+  q.bias[0] = bias;
+  q.ld_add = lda;
+  q.vec = aligned(out, 16) && ldo % 8 == 0 && (!add || (aligned(add, 16) && lda % 8 == 0));
+  q.R = p->R;
+  q.L = p->L;
+  q.t = (const uint16_t*)(ws + l.t);
+  q.tf = (const float*)(ws + l.tf);
+  q.b = (const uint16_t*)lora_b;
+  q.perm = (const int32_t*)(ws + l.perm);
+  q.sid = (const int32_t*)(ws + l.sid);
+  q.ends = (const int32_t*)(ws + l.ends);
+  return with_type16(p->type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    for (int64_t m = 0; m < p->M; m += rows) {
+      const int n = (int)std::min<int64_t>(rows, p->M - m);
+      q.m[0] = (const uint16_t*)x + m * ldx;
+      q.out[0] = (uint16_t*)out + m * ldo;
+      q.add = add ? (const uint16_t*)add + m * lda : nullptr;
+      q.M = n;
+      const SortParams sp{ids + m, (int32_t*)(ws + l.perm), (int32_t*)(ws + l.sid), (int32_t*)(ws + l.ends), n, p->L};
+      hipLaunchKernelGGL(k_lora_sort, dim3(1), dim3(1024), 0, s, sp);
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, q.perm, q.sid, q.ends, (uint16_t*)(ws + l.t),
+                            (float*)(ws + l.tf), ldx, n, p->K, p->R, p->L};
+      launch_shrink<DT>(sh, s);
+      int rc = launch_status();
+      if (!rc) rc = launch<DT, LORA>(q, s);
+      if (rc) return rc;
+    }
+    return (int)MOE_OK;
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,140 @@
+// Row-wise steps of the gated block: gradients of its pre-activations, sums of
+// columns, and the join of partial products.
+#pragma once
+
+#include "dense16.hpp"
+
+namespace moe {
+namespace d16 {
+
+// dg = dout f_g(g, u), du = dout f_u(g, u), rounded to the type: the matrix
+// instruction takes 16-bit operands, and each rounding is off by half a step of its own value, so a sum of
+// many carries an error of the size of its own last rounding. With sums != nullptr the columns'
+// sums over this workgroup's rows as well, from the unrounded values.
+// Memory-bound: three reads and two writes of 16 bits a value.
+constexpr int kGradRows = 32;  // rows of a workgroup (64 columns of 8 values x 4 rows at a time)
+struct GradParams {
+  const void *dout, *gate, *up;
+  void *dg, *du;      // [M, I] contiguous
+  float* sums;        // [row blocks][2][I] or nullptr
+  int64_t ld_dout, ld_gate, ld_up;
+  int32_t M, I;
+  ActParams act;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
+  __shared__ float part[2][4][64][8 + 1];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int col = (blockIdx.y * 64 + lane) * 8;
+  float sg[8], su[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.f;
+  if (col < p.I) {
+    with_act(p.act, [&](auto k) {
+#pragma unroll 2
+      for (int r = w; r < kGradRows; r += 4) {
+        const int64_t row = (int64_t)blockIdx.x * kGradRows + r;
+        if (row >= p.M) break;
+        float d[8], g[8], u[8];
+        load8<DT>(p.dout, (size_t)(row * p.ld_dout + col), d);
+        load8<DT>(p.gate, (size_t)(row * p.ld_gate + col), g);
+        load8<DT>(p.up, (size_t)(row * p.ld_up + col), u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float fg, fu;
+          act_df<decltype(k)::value>(p.act, g[j], u[j], fg, fu);
+          g[j] = d[j] * fg;
+          u[j] = d[j] * fu;
+          sg[j] += g[j];
+          su[j] += u[j];
+        }
+        store8<DT>(p.dg, (size_t)(row * p.I + col), g);
+        store8<DT>(p.du, (size_t)(row * p.I + col), u);
+      }
+    });
+  }
+  if (!p.sums) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    part[0][w][lane][j] = sg[j];
+    part[1][w][lane][j] = su[j];
+  }
+  __syncthreads();
+  // 1024 sums, four to a thread: which, column
+  for (int i = threadIdx.x; i < 1024; i += 256) {
+    const int which = i >> 9, c = i & 511, at = blockIdx.y * 512 + c;
+    if (at >= p.I) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s += part[which][q][c >> 3][c & 7];
+    p.sums[((size_t)blockIdx.x * 2 + which) * p.I + at] = s;
+  }
+}
+
+// dst[which][c] (+)= sum over blocks of sums[block][which][c], in the blocks' order
+__global__ __launch_bounds__(256) void k_column_sums(const float* sums, int blocks, int I, float* dg, float* du, int accumulate) {
+  const int c = blockIdx.x * 256 + threadIdx.x, which = blockIdx.y;
+  if (c >= I) return;
+  double s = 0;
+  for (int b = 0; b < blocks; ++b) s += sums[((size_t)b * 2 + which) * I + c];
+  float* dst = (which ? du : dg) + c;
+  *dst = (float)(accumulate ? s + *dst : s);
+}
+
+// Partial products joined in the order of their K ranges, eight columns to a thread.
+template <int DT, int MODE>
+__global__ __launch_bounds__(256) void k_join(const Params p) {
+  const int cpr = p.N / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * cpr) return;
+  const int row = (int)(i / cpr), col = (int)(i - (int64_t)row * cpr) * 8;
+  const size_t mn = (size_t)p.M * p.N, at = (size_t)row * p.N + col;
+  float v[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    float a[8];
+    load8<T_FP32>(p.part + (MODE == GATED ? 2 : 1) * s * mn, at, a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += a[j];
+    if constexpr (MODE == GATED) {
+      load8<T_FP32>(p.part + (2 * s + 1) * mn, at, a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += a[j];
+    }
+  }
+  if constexpr (MODE == GATED) {
+    if (p.bias[0]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] += p.bias[0][col + j];
+        u[j] += p.bias[1][col + j];
+      }
+    }
+    if (p.keep[0]) {
+      store8<DT>(p.keep[0], (size_t)(row * p.ld_keep[0] + col), v);
+      store8<DT>(p.keep[1], (size_t)(row * p.ld_keep[1] + col), u);
+    }
+    with_act(p.act, [&](auto k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_f<decltype(k)::value>(p.act, v[j], u[j]);
+    });
+  }
+  store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
+}
+
+// Gradients of weights where there are no rows: zeros, eight columns to a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void k_zero_rows(void* a, void* b, int64_t ld_a, int64_t ld_b, int rows, int cols) {
+  const int cpr = cols / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)rows * cpr) return;
+  const int64_t row = i / cpr, col = (i - row * cpr) * 8;
+  const float zero[8] = {};
+  if (blockIdx.y) store8<DT>(b, (size_t)(row * ld_b + col), zero);
+  else store8<DT>(a, (size_t)(row * ld_a + col), zero);
+}
+
+}  // namespace d16
+}  // namespace moe

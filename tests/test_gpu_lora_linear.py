@@ -1,0 +1,170 @@
+"""moe_lora_linear on the GPU against the float64 oracle.
+
+Tolerance, element by element, u = half a step of the type, e = 2^-23. Sums as in
+test_gpu_gated_linear.py: within acc(K, S) = (K + 66) e S of S = sum |a||b|. An adapter's x A^T is within acc(K, |x||A|),
+gets its scale (one rounding) and is carried in two parts of the type over the row's power of two, the second of
+which is rounded to half a step of a value that is half a step of the first: p = u^2 of the row's largest for
+bfloat16, and for float16 at least its smallest step, 2^-25 of it, as well. The second product adds
+acc(2 R, |t||B|). The row's power of two and the additions of the parts, bias and add: 8 more roundings of everything's
+magnitude. Then the last rounding."""
+import pytest
+import torch
+
+import mixture_experts_expert_02_amd as moe
+from oracle import dense16 as O
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda")
+E = 2.0 ** -23
+T16 = [torch.bfloat16, torch.float16]
+
+
+def make(seed, M, K, N, R, L, dt, w=True, bias=False, add=False, ids="token"):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    if ids == "token":
+        i = torch.randint(-1, L, (M,), generator=g, device=DEV)
+    else:
+        i = torch.randint(-1, L, (1 + M // 50,), generator=g, device=DEV).repeat_interleave(50)[:M].contiguous()
+    return dict(x=rn(M, K).to(dt), w=(rn(N, K) / K ** 0.5).to(dt) if w else None, lora_a=(rn(L, R, K) / K ** 0.5).to(dt),
+                lora_b=(0.3 * rn(L, N, R) / R ** 0.5).to(dt), ids=i.to(torch.int32),
+                scales=0.25 + 2 * torch.rand(L, generator=g, device=DEV), bias=rn(N) if bias else None,
+                add=rn(M, N).to(dt) if add else None)
+
+
+def bound(c):
+    x, dt = c["x"], c["x"].dtype
+    M, K = x.shape
+    R = c["lora_a"].shape[1]
+    u = torch.finfo(dt).eps / 2
+    X = x.double().abs()
+    y = X.new_zeros(M, c["lora_b"].shape[1])
+    mag = y.clone()
+    for i in range(c["lora_a"].shape[0]):
+        m = (c["ids"] == i).nonzero().flatten()
+        s, B = c["scales"][i].double(), c["lora_b"][i].double().abs()
+        T = s * (X[m] @ c["lora_a"][i].double().abs().t())
+        top = (s * (x[m].double() @ c["lora_a"][i].double().t())).abs().amax(-1, keepdim=True)
+        part = u * u * 2 * top + (2.0 ** -24 * top if dt == torch.float16 else 0)
+        y[m] += ((K + 67) * E * T + part) @ B.t() + (2 * R + 66) * E * (T @ B.t())
+        mag[m] += T @ B.t()
+    if c["w"] is not None:
+        S = X @ c["w"].double().abs().t()
+        y += (K + 66) * E * S
+        mag += S
+    if c["bias"] is not None:
+        mag += c["bias"].double().abs()
+    if c["add"] is not None:
+        mag += c["add"].double().abs()
+    return y + 8 * E * mag
+
+
+def check(got, c):
+    dt = c["x"].dtype
+    u = torch.finfo(dt).eps / 2
+    ref = O.lora(c["x"], c["w"], c["lora_a"], c["lora_b"], c["ids"], c["scales"], c["bias"], c["add"])
+    b = bound(c) * (1 + u) + u * ref.abs() + torch.finfo(dt).smallest_normal * u
+    assert torch.isfinite(got).all()
+    r = ((got.double() - ref).abs() / b).max().item()
+    assert r <= 1, r
+
+
+SHAPES = [(1, 64, 64, 8, 1), (1, 2048, 7168, 16, 8), (2, 8, 1, 8, 3), (3, 72, 33, 24, 2), (7, 1000, 200, 64, 5), (16, 264, 520, 128, 4),
+          (17, 128, 131, 256, 3), (33, 2880, 2895, 32, 32), (64, 512, 257, 16, 64), (65, 136, 72, 40, 70), (130, 776, 328, 64, 9),
+          (200, 64, 1000, 8, 1), (300, 1032, 515, 32, 16), (515, 520, 264, 16, 300), (1100, 264, 384, 64, 6)]
+
+
+@pytest.mark.parametrize("M,K,N,R,L", SHAPES)
+@pytest.mark.parametrize("dt", T16)
+def test_shapes(M, K, N, R, L, dt):
+    print(f"[lora] {M}x{K}x{N} R={R} L={L} {dt}", flush=True)
+    c = make(M + K + N, M, K, N, R, L, dt, w=(M + R // 8) % 3 != 0, bias=N % 2 == 0, add=M % 2 == 1,
+             ids="run" if R % 16 == 0 and M % 2 == 0 else "token")
+    out = moe.lora_linear(**c)
+    torch.cuda.synchronize()
+    check(out, c)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("w", [True, False])
+def test_in_place_addend_and_strides(M, w):
+    """out is add; rows apart in x, w, out and add; what lies between output rows stays."""
+    print(f"[lora] strides M={M} w={w}", flush=True)
+    K, N = 136, 203
+    c = make(11, M, K, N, 16, 5, torch.bfloat16, w=w, bias=True, add=True)
+    want = moe.lora_linear(**c)
+    check(want, c)
+
+    def wide(t, pad):
+        v = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=DEV)
+        v[:, : t.shape[1]] = t
+        return v[:, : t.shape[1]], v
+    for pad in (5, 6, 21):
+        o, whole = wide(c["add"], pad)
+        s = {**c, "x": wide(c["x"], 8)[0], "w": wide(c["w"], 16)[0] if w else None, "add": o}
+        got = moe.lora_linear(**s, out=o)
+        torch.cuda.synchronize()
+        assert got is o and torch.equal(o, want) and whole[:, N:].isnan().all()
+
+
+def test_ids_outside_and_no_adapter_at_all():
+    print("[lora] ids", flush=True)
+    c = make(3, 70, 264, 136, 16, 4, torch.bfloat16, add=True)
+    none = {**c, "ids": torch.full_like(c["ids"], -1)}
+    base = moe.lora_linear(**none)
+    check(base, none)
+    ids = c["ids"].clone()
+    ids[::5] = 4
+    ids[1::5] = -2 ** 31
+    ids[2::5] = 2 ** 31 - 1
+    c["ids"] = ids
+    got = moe.lora_linear(**c)
+    torch.cuda.synchronize()
+    out = (ids < 0) | (ids >= 4)
+    assert torch.equal(got[out], base[out])
+    check(got, c)
+
+
+@pytest.mark.parametrize("M", [5, 90, 400])
+def test_a_broken_adapter_stays_with_its_rows(M):
+    """Infinities and NaN in one adapter, and in rows without one."""
+    print(f"[lora] broken M={M}", flush=True)
+    c = make(4, M, 264, 200, 16, 3, torch.bfloat16)
+    ref = moe.lora_linear(**c)
+    b = {**c, "lora_a": c["lora_a"].clone(), "lora_b": c["lora_b"].clone(), "scales": c["scales"].clone()}
+    b["lora_b"][1, ::3] = float("inf")
+    b["lora_b"][1, 1::3] = float("nan")
+    b["lora_a"][1, 3] = float("nan")
+    got = moe.lora_linear(**b)
+    torch.cuda.synchronize()
+    mine = c["ids"] == 1
+    assert torch.equal(got[~mine], ref[~mine])
+    assert got[mine].isnan().all()
+    unused = {**c, "ids": torch.where(mine, -1, c["ids"])}
+    ref = moe.lora_linear(**unused)
+    got = moe.lora_linear(**{**b, "ids": unused["ids"]})
+    assert torch.equal(got, ref)
+
+
+def test_float16_parts_hold_large_and_small_products():
+    """x A^T beyond float16's ends: its row's power of two carries it."""
+    print("[lora] range", flush=True)
+    c = make(6, 40, 264, 136, 24, 3, torch.float16)
+    for up in (2.0 ** 8, 2.0 ** -8):
+        s = {**c, "x": (c["x"].float() * up).half(), "lora_a": (c["lora_a"].float() * up).half(), "w": None, "scales": c["scales"] / up ** 2}
+        check(moe.lora_linear(**s), s)
+        t = {**s, "scales": c["scales"], "lora_b": (c["lora_b"].float() * 2.0 ** -6).half() if up > 1 else c["lora_b"]}
+        check(moe.lora_linear(**t), t)
+
+
+def test_rows_do_not_depend_on_their_batch():
+    """A row's bits are the same whichever adapters the other rows of the call have."""
+    print("[lora] batch", flush=True)
+    c = make(8, 300, 512, 264, 32, 7, torch.bfloat16)
+    whole = moe.lora_linear(**c)
+    perm = torch.randperm(300, device=DEV)
+    got = moe.lora_linear(**{**c, "x": c["x"][perm].contiguous(), "ids": c["ids"][perm].contiguous()})
+    torch.cuda.synchronize()
+    assert torch.equal(got, whole[perm])
+    for _ in range(3):
+        assert torch.equal(moe.lora_linear(**c), whole)
