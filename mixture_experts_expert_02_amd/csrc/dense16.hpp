@@ -119,6 +119,12 @@ __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+// vmcnt(N) and every LDS access
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 __device__ __forceinline__ void wave_sync() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -167,6 +173,34 @@ struct Frag<true> {
     asm volatile("" : "+v"(b));
   }
   __device__ __forceinline__ u32x4 get() const { return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)}; }
+};
+
+// The same with the offset in the instruction (a K-major half of 128 columns).
+template <bool MAJOR>
+struct BigFrag {
+  u32x4 v;
+  template <int AT>
+  __device__ __forceinline__ void read(uint32_t addr) {
+    asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(AT));
+  }
+  __device__ __forceinline__ void tie() { asm volatile("" : "+v"(v)); }
+  __device__ __forceinline__ u32x4 get() const { return v; }
+};
+template <>
+struct BigFrag<true> {
+  uint64_t a, b;
+  template <int AT>
+  __device__ __forceinline__ void read(uint32_t addr) {
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(a) : "v"(addr), "n"(AT));
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(b) : "v"(addr), "n"(AT + 1024));
+  }
+  __device__ __forceinline__ void tie() {
+    asm volatile("" : "+v"(a));
+    asm volatile("" : "+v"(b));
+  }
+  __device__ __forceinline__ u32x4 get() const {
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  }
 };
 
 template <int DT>

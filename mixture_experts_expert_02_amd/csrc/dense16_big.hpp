@@ -1,0 +1,339 @@
+// The largest tiles of the dense 16-bit products: 256 x 256 outputs by eight waves
+// (GATED: 128 gate and the same 128 up columns).
+//
+// A stage of 64 K values is four half operands of 16 KB: M0, M1 (rows 0-127 and
+// 128-255) and N0, N1. Wave (wm, wn) of 2 x 4 owns 64 rows of each M half and 32
+// columns of each N half, so a stage is four phases of 64 x 32 x 64 products, eight
+// MFMAs a wave: M0 N0, M0 N1, M1 N1, M1 N0. While a phase multiplies, the wave reads
+// the operands of the next one from LDS (N1, M1, the next stage's M0, its N0: four or eight
+// fragments, each into registers that the last phases have used up) and loads the half
+// whose buffer the phase before has read for the last time, for the stage after the
+// next. So every half has six phases (3000 cycles at the MFMA rate) to arrive, 96 of the 128 KB of
+// buffers are in flight at any time, and a phase ends with one barrier, its reads done and the half
+// that the next one reads landed (all but the twelve youngest loads).
+#pragma once
+
+#include "dense16.hpp"
+
+namespace moe {
+namespace d16 {
+
+template <int DT, int MODE>
+__global__ __launch_bounds__(512) void k_big(const Params p) {
+  constexpr bool MM = MODE == DW, NM = MODE == DX || MODE == DW;  // K-major operands
+  constexpr int BM = 256, TN = MODE == GATED ? 128 : 256, HALF = 16384;
+  constexpr int N_AT = 4 * HALF;  // M halves [stage buffer][half], then N halves
+  __shared__ __attribute__((aligned(16))) uint8_t smem_arr[8 * HALF];
+  __shared__ int rows_lds[MODE == LORA ? BM : 1];
+  lds_u8* smem = (lds_u8*)smem_arr;
+  Item it;
+  if (!item_of(p, MODE == DW ? 2 : p.splits, it)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lk = lane >> 5;
+  const int m0 = it.mt * BM, n0 = it.nt * TN;
+  const int z = MODE == DW ? it.z : 0, split = MODE == DW ? 0 : it.z;
+  const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;
+  const int s_lo = (int)((int64_t)split * all / p.splits), nst = (int)((int64_t)(split + 1) * all / p.splits) - s_lo;
+
+  if constexpr (MODE == LORA) {
+    if (tid < BM) rows_lds[tid] = m0 + tid < p.M ? p.perm[m0 + tid] : 0;
+    __syncthreads();
+  }
+
+  // ---- loads: instructions 2 wave and 2 wave + 1 of the 16 of a half
+  // columns of N half h: 128 h + i where N is K-major or GATED (half = gate or up); else 32 columns of each half
+  // side by side, 64 (i / 32) + 32 h + i % 32, so that a wave's columns are 64 neighbours
+  int m_row[2], m_chunk[2], n_row[2], n_chunk[2];
+  uint32_t g_off[2][2];  // LORA: rows of x are gathered
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = 2 * wave + q, r = i * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+    if constexpr (MM) major_src<128>(i, lane, m_row[q], m_chunk[q]);
+    else {
+      m_row[q] = r;
+      m_chunk[q] = c;
+    }
+    if constexpr (NM) major_src<128>(i, lane, n_row[q], n_chunk[q]);
+    else {
+      n_row[q] = MODE == GATED ? r : (r >> 5) * 64 + (r & 31);
+      n_chunk[q] = c;
+    }
+    if constexpr (MODE == LORA) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        g_off[h][q] = m0 + h * 128 + r < p.M ? (uint32_t)rows_lds[h * 128 + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+    }
+  }
+  auto load_m = [&](int h, int st, int buf) {
+    const bool live = st < nst;
+    int s = s_lo + st, seg = 0;
+    if (MODE == DX && s >= kt) {
+      seg = 1;
+      s -= kt;
+    }
+    const int k0 = s * BK, mi = MODE == DX ? seg : z;
+    const int64_t ld = p.ldm[mi];
+    lds_u8* dst = smem + (buf * 2 + h) * HALF + wave * 2048;
+    if constexpr (MM) {
+      const auto rs = rsrc(p.m[mi] + (int64_t)k0 * ld + m0 + h * 128, live ? ((min(BK, p.K - k0) - 1) * ld + p.M - m0 - h * 128) * 2 : 0);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16, 0);
+    } else {
+      const auto rs = MODE == LORA ? rsrc(p.m[0], live ? 0x7fffffff : 0)
+                                   : rsrc(p.m[mi] + (int64_t)(m0 + h * 128) * ld,
+                                          live && p.M - m0 > h * 128 ? ((min(128, p.M - m0 - h * 128) - 1) * ld + p.K) * 2 : 0);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t off = MODE == LORA ? g_off[h][q] : m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16;
+        if (k0 + m_chunk[q] * 8 >= p.K) off = kNoLoad;
+        dma(rs, dst + q * 1024, off, k0 * 2);
+      }
+    }
+  };
+  auto load_n = [&](int h, int st, int buf) {
+    const bool live = st < nst;
+    int s = s_lo + st, seg = 0;
+    if (MODE == DX && s >= kt) {
+      seg = 1;
+      s -= kt;
+    }
+    const int k0 = s * BK, ni = MODE == GATED ? h : MODE == DX ? seg : 0;
+    const int64_t ld = p.ldn[ni];
+    lds_u8* dst = smem + N_AT + (buf * 2 + h) * HALF + wave * 2048;
+    if constexpr (NM) {
+      const auto rs = rsrc(p.n[ni] + (int64_t)k0 * ld + n0 + h * 128, live ? ((min(BK, p.K - k0) - 1) * ld + p.N - n0 - h * 128) * 2 : 0);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, n_row[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16, 0);
+    } else {
+      const int first = n0 + (MODE == GATED ? 0 : h * 32), rows = min(MODE == GATED ? 128 : 224, p.N - first);
+      const auto rs = rsrc(p.n[ni] + (int64_t)first * ld, live && rows > 0 ? ((rows - 1) * ld + p.K) * 2 : 0);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t off = n_row[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16;
+        if (k0 + n_chunk[q] * 8 >= p.K) off = kNoLoad;
+        dma(rs, dst + q * 1024, off, k0 * 2);
+      }
+    }
+  };
+
+  // ---- operand reads: bytes inside a half
+  const int tr = (lane >> 2) & 3;
+  auto major_at = [&](int col, int ks) {
+    const int cb = 2 * (col + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
+    return (uint32_t)((16 * ks + 8 * lk + tr) * 256 + (((cb >> 6) ^ tr) << 6) + (cb & 63));
+  };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  uint32_t m_at[MM ? 2 : 4], n_at[NM ? 1 : 4];  // K-major: by fragment; else by K step
+  if constexpr (MM) {
+    m_at[0] = lds0 + major_at(wm * 64, 0);
+    m_at[1] = lds0 + major_at(wm * 64 + 32, 0);
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) m_at[ks] = lds0 + 16 * row_slot(wm * 64 + lr, 2 * ks + lk);
+  }
+  if constexpr (NM) {
+    n_at[0] = lds0 + N_AT + major_at(wn * 32, 0);
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) n_at[ks] = lds0 + N_AT + 16 * row_slot(wn * 32 + lr, 2 * ks + lk);
+  }
+
+  f32x16 acc[2][2][2];  // [N half][M half][32 rows]
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[a][b][j][r] = 0.f;
+
+  BigFrag<MM> fm[2][2][4];  // [M half][32 rows][K step]
+  BigFrag<NM> fn[2][4];     // [set][K step]
+
+  // fragment x (0..7) of an M half, (0..3) of an N half; AT: constant byte offset of the half
+#define MOE_D16_READ_M(h, buf, x)                                                                                \
+  {                                                                                                              \
+    if constexpr (MM) fm[h][(x) & 1][(x) >> 1].template read<((buf) * 2 + (h)) * HALF + ((x) >> 1) * 4096>(m_at[(x) & 1]); \
+    else fm[h][(x) & 1][(x) >> 1].template read<((buf) * 2 + (h)) * HALF + ((x) & 1) * 4096>(m_at[(x) >> 1]);    \
+  }
+#define MOE_D16_READ_N(set, h, buf, x)                                                                 \
+  {                                                                                                    \
+    if constexpr (NM) fn[set][x].template read<((buf) * 2 + (h)) * HALF + (x) * 4096>(n_at[0]);        \
+    else fn[set][x].template read<((buf) * 2 + (h)) * HALF>(n_at[x]);                                  \
+  }
+#define MOE_D16_ALL_N(h) \
+  MOE_D16_READ_N(0, h, 0, 0) MOE_D16_READ_N(0, h, 0, 1) MOE_D16_READ_N(0, h, 0, 2) MOE_D16_READ_N(0, h, 0, 3)
+#define MOE_D16_ALL_M(h) \
+  MOE_D16_READ_M(h, 0, 0) MOE_D16_READ_M(h, 0, 1) MOE_D16_READ_M(h, 0, 2) MOE_D16_READ_M(h, 0, 3) \
+  MOE_D16_READ_M(h, 0, 4) MOE_D16_READ_M(h, 0, 5) MOE_D16_READ_M(h, 0, 6) MOE_D16_READ_M(h, 0, 7)
+#define MOE_D16_MFMA(hn, hm, set, x) \
+  acc[hn][hm][(x) & 1] = mfma<DT>(fn[set][(x) >> 1].get(), fm[hm][(x) & 1][(x) >> 1].get(), acc[hn][hm][(x) & 1]);
+  auto tie_m = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) fm[h][j][ks].tie();
+  };
+  auto tie_n = [&](int set) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) fn[set][ks].tie();
+  };
+
+  // ---- adapters of the tile's rows (see k_tile)
+  if constexpr (MODE == LORA) {
+    if (split == 0) {
+      int id[2][2];
+      float f[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int row = m0 + h * 128 + wm * 64 + j * 32 + lr;
+          id[h][j] = row < p.M ? p.sid[row] : p.L;
+          f[h][j] = row < p.M ? p.tf[row] : 0.f;
+        }
+      const int rc = p.R / 8, last = min(m0 + BM, p.M), rst = (2 * rc + 7) / 8;
+      const auto rs_t = rsrc(p.t + (int64_t)m0 * 2 * p.R, (int64_t)(last - m0) * 4 * p.R);
+      int pos = m0;
+      while (pos < last) {
+        const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
+        if (a >= p.L) break;
+        pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
+        const auto rs_b = rsrc(p.b + ((int64_t)a * p.N + n0) * p.R, (int64_t)min(TN, p.N - n0) * 2 * p.R);
+        for (int st = 0; st < rst; ++st) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int vm = st * 8 + m_chunk[q], vn = st * 8 + n_chunk[q];
+              dma(rs_t, smem + h * HALF + wave * 2048 + q * 1024, vm < 2 * rc ? (uint32_t)((h * 128 + m_row[q]) * 4 * p.R + vm * 16) : kNoLoad, 0);
+              dma(rs_b, smem + N_AT + h * HALF + wave * 2048 + q * 1024,
+                  vn < 2 * rc ? (uint32_t)((h * 32 + n_row[q]) * 2 * p.R + (vn < rc ? vn : vn - rc) * 16) : kNoLoad, 0);
+            }
+          wait_loads<0>();
+          barrier();
+#pragma unroll
+          for (int hn = 0; hn < 2; ++hn) {
+            if (hn == 0) { MOE_D16_ALL_N(0) } else { MOE_D16_ALL_N(1) }
+#pragma unroll
+            for (int hm = 0; hm < 2; ++hm) {
+              if (hm == 0) { MOE_D16_ALL_M(0) } else { MOE_D16_ALL_M(1) }
+              asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+              tie_n(0);
+              tie_m(hm);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (!__any(id[hm][j] == a)) continue;
+                f32x16 tmp;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) tmp[r] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) tmp = mfma<DT>(fn[0][ks].get(), fm[hm][j][ks].get(), tmp);
+                if (id[hm][j] == a) {
+#pragma unroll
+                  for (int r = 0; r < 16; ++r) acc[hn][hm][j][r] += tmp[r] * f[hm][j];
+                }
+              }
+            }
+          }
+          barrier();
+        }
+      }
+    }
+  }
+
+  // ---- main loop
+  // One phase: MFMAs 0..7, READS between the first, LOAD behind the fifth.
+#define MOE_D16_PHASE(hn, hm, set, R0, R1, R2, R3, LOAD, TIE)            \
+  {                                                                      \
+    MOE_D16_MFMA(hn, hm, set, 0) R0 __builtin_amdgcn_sched_barrier(0);   \
+    MOE_D16_MFMA(hn, hm, set, 1) R1 __builtin_amdgcn_sched_barrier(0);   \
+    MOE_D16_MFMA(hn, hm, set, 2) R2 __builtin_amdgcn_sched_barrier(0);   \
+    MOE_D16_MFMA(hn, hm, set, 3) R3 __builtin_amdgcn_sched_barrier(0);   \
+    MOE_D16_MFMA(hn, hm, set, 4) LOAD;                                   \
+    __builtin_amdgcn_sched_barrier(0);                                   \
+    MOE_D16_MFMA(hn, hm, set, 5)                                         \
+    MOE_D16_MFMA(hn, hm, set, 6)                                         \
+    MOE_D16_MFMA(hn, hm, set, 7)                                         \
+    __builtin_amdgcn_sched_barrier(0);                                   \
+    wait_all_but<12>();                                                  \
+    TIE;                                                                 \
+    barrier();                                                           \
+    __builtin_amdgcn_sched_barrier(0);                                   \
+  }
+  // Stage st in buffer B: N half 0 in set X, half 1 comes into set Y, which the next stage's half 0 takes over.
+#define MOE_D16_STAGE(st, B, X, Y)                                                                                   \
+  {                                                                                                                  \
+    MOE_D16_PHASE(0, 0, X, MOE_D16_READ_N(Y, 1, B, 0), MOE_D16_READ_N(Y, 1, B, 1), MOE_D16_READ_N(Y, 1, B, 2),       \
+                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + 2, B), tie_n(Y))                                      \
+    MOE_D16_PHASE(1, 0, Y, MOE_D16_READ_M(1, B, 0) MOE_D16_READ_M(1, B, 1), MOE_D16_READ_M(1, B, 2) MOE_D16_READ_M(1, B, 3), \
+                  MOE_D16_READ_M(1, B, 4) MOE_D16_READ_M(1, B, 5), MOE_D16_READ_M(1, B, 6) MOE_D16_READ_M(1, B, 7),  \
+                  load_n(1, (st) + 2, B), tie_m(1))                                                                  \
+    MOE_D16_PHASE(1, 1, Y, MOE_D16_READ_M(0, 1 - B, 0) MOE_D16_READ_M(0, 1 - B, 1),                                  \
+                  MOE_D16_READ_M(0, 1 - B, 2) MOE_D16_READ_M(0, 1 - B, 3),                                           \
+                  MOE_D16_READ_M(0, 1 - B, 4) MOE_D16_READ_M(0, 1 - B, 5),                                           \
+                  MOE_D16_READ_M(0, 1 - B, 6) MOE_D16_READ_M(0, 1 - B, 7), load_m(1, (st) + 2, B), tie_m(0))         \
+    MOE_D16_PHASE(0, 1, X, MOE_D16_READ_N(Y, 0, 1 - B, 0), MOE_D16_READ_N(Y, 0, 1 - B, 1), MOE_D16_READ_N(Y, 0, 1 - B, 2), \
+                  MOE_D16_READ_N(Y, 0, 1 - B, 3), load_m(0, (st) + 3, 1 - B), tie_n(Y))                              \
+  }
+  if (nst > 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      load_m(0, s, s);
+      load_n(0, s, s);
+      load_n(1, s, s);
+      load_m(1, s, s);
+    }
+    wait_loads<12>();
+    barrier();
+    MOE_D16_ALL_N(0)
+    MOE_D16_ALL_M(0)
+    wait_all_but<10>();
+    tie_n(0);
+    tie_m(0);
+    barrier();
+    load_m(0, 2, 0);
+    for (int s = 0; s < nst; s += 2) {
+      MOE_D16_STAGE(s, 0, 0, 1)
+      if (s + 1 >= nst) break;
+      MOE_D16_STAGE(s + 1, 1, 1, 0)
+    }
+    wait_loads<0>();
+    barrier();
+  }
+
+  // ---- epilogue: 32 rows at a time through the wave's part of the buffers
+  constexpr int COLS = NM ? 32 : 64;
+  float* strip = (float*)(smem_arr + wave * 32 * (64 + 4) * 4);
+#pragma unroll
+  for (int hm = 0; hm < 2; ++hm)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int hs = 0; hs < 64 / COLS; ++hs) {
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& c = acc[hs + i][hm][j];
+            *(f32x4*)(strip + lr * (COLS + 4) + i * 32 + 8 * q + 4 * lk) = f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+          }
+        wave_sync();
+        const int r = hm * 128 + wm * 64 + j * 32;
+        store_rows<DT, MODE, COLS>(p, strip, z, split, m0 + r, n0 + (MODE == GATED ? wn * 32 : NM ? hs * 128 + wn * 32 : wn * 64), lane,
+                                   rows_lds + (MODE == LORA ? r : 0));
+        wave_sync();
+      }
+#undef MOE_D16_STAGE
+#undef MOE_D16_PHASE
+#undef MOE_D16_ALL_M
+#undef MOE_D16_ALL_N
+#undef MOE_D16_MFMA
+#undef MOE_D16_READ_N
+#undef MOE_D16_READ_M
+}
+
+}  // namespace d16
+}  // namespace moe

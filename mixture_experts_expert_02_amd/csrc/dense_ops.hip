@@ -9,6 +9,7 @@
 
 #include "../../include/moe_experts.h"
 #include "dense16.hpp"
+#include "dense16_big.hpp"
 #include "gated_grad.hpp"
 #include "lora.hpp"
 
@@ -92,7 +93,18 @@ int launch_tile(Params& q, hipStream_t s) {
 }
 
 template <int DT, int MODE>
+int launch_big(Params& q, hipStream_t s) {
+  q.mt = (int)cdiv(q.M, 256);
+  q.nt = (int)cdiv(q.N, MODE == GATED ? 128 : 256);
+  const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : q.splits), 8) * 8;
+  if (n > kMaxGrid / 2) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((k_big<DT, MODE>), dim3((unsigned)n), dim3(512), 0, s, q);
+  return launch_status();
+}
+
+template <int DT, int MODE>
 int launch(Params& q, hipStream_t s) {
+  if (cdiv(q.M, 256) * cdiv(q.N, MODE == GATED ? 128 : 256) * (MODE == DW ? 2 : 1) >= 128) return launch_big<DT, MODE>(q, s);
   return launch_tile<DT, MODE, 128, 128, 4>(q, s);
 }
 

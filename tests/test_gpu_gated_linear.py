@@ -309,3 +309,20 @@ def test_repeats_are_bitwise_equal():
         again = moe.gated_linear_backward(*ops, want_dbias=True)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
         assert all(torch.equal(a, b) for a, b in zip(f1, moe.gated_linear(*ops[1:4], save=True)))
+
+
+@pytest.mark.parametrize("M,H,I", [(4099, 2056, 2088), (2500, 4104, 2048), (2560, 2048, 72 * 64), (8200, 72, 2120), (4099, 8, 2056)])
+@pytest.mark.parametrize("dt", T16)
+def test_many_rows(M, H, I, dt):
+    """Sizes that fill the chip with the largest tiles in one direction or all, with ends inside tiles."""
+    name = list(ACTS)[(M + H // 8) % 3]
+    print(f"[gated, grad] {M}x{H}x{I} {dt} {name}", flush=True)
+    ops = make(M + H, M, H, I, dt, bias=M % 2 == 0)
+    r = moe.gated_linear(*ops[:3], act=name, bias_gate=ops[3], bias_up=ops[4], save=True, **ACTS[name])
+    torch.cuda.synchronize()
+    check_forward(r, *ops, name, ACTS[name])
+    d = (torch.randn(M, I, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV) * 0.02).to(dt)
+    args = (d, *ops[:3], r.gate, r.up)
+    s = moe.gated_linear_backward(*args, act=name, want_dbias=True, **ACTS[name])
+    torch.cuda.synchronize()
+    check_grads(s, *args, name, ACTS[name])

@@ -168,3 +168,14 @@ def test_rows_do_not_depend_on_their_batch():
     assert torch.equal(got, whole[perm])
     for _ in range(3):
         assert torch.equal(moe.lora_linear(**c), whole)
+
+
+@pytest.mark.parametrize("M,K,N,R,L", [(4099, 520, 2900, 24, 5), (4096, 72, 2057, 40, 90), (2300, 2056, 4112, 128, 3), (9000, 64, 1100, 8, 12)])
+@pytest.mark.parametrize("dt", T16)
+@pytest.mark.parametrize("ids", ["token", "run"])
+def test_many_rows(M, K, N, R, L, dt, ids):
+    print(f"[lora] {M}x{K}x{N} R={R} L={L} {dt} {ids}", flush=True)
+    c = make(M + K + N, M, K, N, R, L, dt, w=N != 1100, bias=N % 2 == 0, add=M % 2 == 0, ids=ids)
+    out = moe.lora_linear(**c)
+    torch.cuda.synchronize()
+    check(out, c)
