@@ -1,0 +1,187 @@
+// Few rows (decode) of the dense 16-bit products: the weights stream from HBM once.
+//
+// A workgroup owns 16 FN weight rows (GATED: 8 FN gate and the same up rows, eight by
+// eight) and up to 8 XI rows of x; its S waves split K and work each for itself:
+// a wave's slice goes memory -> LDS in units of 64 K values, whole 128-byte lines of each row,
+// through a ring of D units of its own, so that it waits for nothing but its own oldest
+// unit; MFMA 16x16x32, and the partial sums meet in LDS in wave order.
+#pragma once
+
+#include "dense16.hpp"
+
+namespace moe {
+namespace d16 {
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == T_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ float load1(const void* base, size_t i) {
+  if constexpr (DT == T_BF16) return (float)((const __bf16*)base)[i];
+  else return (float)((const _Float16*)base)[i];
+}
+template <int DT>
+__device__ __forceinline__ void store1(void* base, size_t i, float v) {
+  if constexpr (DT == T_BF16) ((__bf16*)base)[i] = (__bf16)v;
+  else ((_Float16*)base)[i] = (_Float16)v;
+}
+
+// LORA here: p.tf holds the scaled x A^T in float32, [M, R] in the rows' own order, and p.sid the ids.
+template <int DT, int MODE, int S, int FN, int XI, int D>
+__global__ __launch_bounds__(64 * S) void k_few(const Params p) {
+  constexpr int FM = (XI + 1) / 2, NI = 2 * FN;  // 16-row fragments of x; load instructions of a unit's weights
+  constexpr int UNIT = (NI + XI) * 1024;
+  constexpr int COLS = MODE == GATED ? 8 * FN : 16 * FN;
+  constexpr int PART = FN * FM * 256;  // floats of a wave's partial sums
+  static_assert(S * D * UNIT <= 160 * 1024 && S * PART * 4 <= S * D * UNIT, "LDS");
+  __shared__ __attribute__((aligned(16))) uint8_t smem_arr[S * D * UNIT];
+  lds_u8* smem = (lds_u8*)smem_arr;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nt = blockIdx.x % p.nt, mt = blockIdx.x / p.nt;
+  const int n0 = nt * COLS, m0 = mt * 8 * XI;
+  const int units = (p.K + 63) / 64;
+  const int lo = wave * units / S, cnt = (wave + 1) * units / S - lo;
+  lds_u8* ring = smem + wave * (D * UNIT);
+
+  // lane's row in an instruction's eight, and the chunk it fetches for the slot it fills
+  const int r8 = lane >> 3;
+  int chunk[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) chunk[q] = (lane & 7) ^ (((q * 8 + r8) >> 1) & 7);
+  auto load = [&](int u, int slot) {
+    const bool live = u < cnt;
+    const int k0 = (lo + u) * 64;
+    lds_u8* dst = ring + slot * UNIT;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int w = MODE == GATED ? i & 1 : 0;
+      const int first = n0 + (MODE == GATED ? (i >> 1) * 8 : i * 8);
+      const int64_t ld = p.ldn[w];
+      const auto rs = rsrc(p.n[w] + (int64_t)first * ld, live && first < p.N ? ((min(8, p.N - first) - 1) * ld + p.K) * 2 : 0);
+      uint32_t off = (uint32_t)r8 * (uint32_t)(ld * 2) + chunk[i & 1] * 16;
+      if (k0 + chunk[i & 1] * 8 >= p.K) off = kNoLoad;
+      dma(rs, dst + i * 1024, off, k0 * 2);
+    }
+    const int64_t ld = p.ldm[0];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int first = m0 + i * 8;
+      const auto rs = rsrc(p.m[0] + (int64_t)first * ld, live && first < p.M ? ((min(8, p.M - first) - 1) * ld + p.K) * 2 : 0);
+      uint32_t off = (uint32_t)r8 * (uint32_t)(ld * 2) + chunk[i & 1] * 16;
+      if (k0 + chunk[i & 1] * 8 >= p.K) off = kNoLoad;
+      dma(rs, dst + (NI + i) * 1024, off, k0 * 2);
+    }
+  };
+
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t at[2];  // K halves of a unit
+  const int c = lane & 15;
+  // with eight rows of x the upper half of the fragment repeats the lower (its results are never used)
+  const int cx = XI == 1 ? c & 7 : c;
+  uint32_t at_x[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    at[h] = (uint32_t)(uintptr_t)ring + 16 * row_slot(c, 4 * h + (lane >> 4));
+    at_x[h] = (uint32_t)(uintptr_t)ring + NI * 1024 + 16 * row_slot(cx, 4 * h + (lane >> 4));
+  }
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u) load(u, u);
+  int slot = 0;
+  for (int u = 0; u < cnt; ++u) {
+    load(u + D - 1, slot == 0 ? D - 1 : slot - 1);  // the slot read in the last turn
+    wait_loads<(D - 1) * (NI + XI)>();
+    Frag<false> fw[2][FN], fx[2][FM];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fw[h][i].read(at[h] + slot * UNIT + i * 2048, 0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fx[h][j].read(at_x[h] + slot * UNIT + j * 2048, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fw[h][i].tie();
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fx[h][j].tie();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = mfma16<DT>(fw[h][i].get(), fx[h][j].get(), acc[i][j]);
+    slot = slot + 1 == D ? 0 : slot + 1;
+  }
+  wait_loads<0>();
+  __syncthreads();
+
+  // partial sums [wave][fragment][row of x][weight row]
+  float* part = (float*)smem_arr;
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) *(f32x4*)(part + wave * PART + (i * FM + j) * 256 + c * 16 + 4 * (lane >> 4)) = acc[i][j];
+  __syncthreads();
+  auto sum = [&](int i, int m, int r) {
+    const float* q = part + (i * FM + (m >> 4)) * 256 + (m & 15) * 16 + r;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < S; ++w) s += q[w * PART];
+    return s;
+  };
+  const int rows = min(8 * XI, p.M - m0);
+  for (int x = tid; x < rows * COLS; x += 64 * S) {
+    const int m = x / COLS, n = x % COLS, col = n0 + n;
+    const int64_t row = m0 + m;
+    if (col >= p.N) continue;
+    if constexpr (MODE == GATED) {
+      float g = sum(n >> 3, m, n & 7), u = sum(n >> 3, m, 8 + (n & 7));
+      if (p.bias[0]) {
+        g += p.bias[0][col];
+        u += p.bias[1][col];
+      }
+      if (p.keep[0]) {
+        store1<DT>(p.keep[0], (size_t)(row * p.ld_keep[0] + col), g);
+        store1<DT>(p.keep[1], (size_t)(row * p.ld_keep[1] + col), u);
+      }
+      float v = 0.f;
+      with_act(p.act, [&](auto k) { v = act_f<decltype(k)::value>(p.act, g, u); });
+      store1<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
+    } else {
+      float v = sum(n >> 4, m, n & 15);
+      const int a = p.sid[row];
+      if (a >= 0 && a < p.L) {
+        const float* t = p.tf + row * p.R;
+        const uint16_t* b = p.b + ((int64_t)a * p.N + col) * p.R;
+        float d = 0.f;
+#pragma unroll 4
+        for (int r = 0; r < p.R; r += 8) {
+          float bv[8], tv[8];
+          load8<DT>(b, r, bv);
+          load8<T_FP32>(t, r, tv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d = fmaf(tv[q], bv[q], d);
+        }
+        v += d;
+      }
+      if (p.bias[0]) v += p.bias[0][col];
+      if (p.add) v += load1<DT>(p.add, (size_t)(row * p.ld_add + col));
+      store1<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
+    }
+  }
+}
+
+}  // namespace d16
+}  // namespace moe

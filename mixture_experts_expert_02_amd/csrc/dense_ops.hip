@@ -108,6 +108,27 @@ int launch(Params& q, hipStream_t s) {
   return launch_tile<DT, MODE, 128, 128, 4>(q, s);
 }
 
+// ------------------------------------------------------------ few rows
+constexpr int kFewRows = 64;  // of a projection with adapters
+constexpr int kFewGated = 32;
+
+template <int DT, int MODE, int S, int FN, int XI, int D>
+int launch_few(Params& q, hipStream_t s) {
+  q.mt = (int)cdiv(q.M, 8 * XI);
+  q.nt = (int)cdiv(q.N, MODE == GATED ? 8 * FN : 16 * FN);
+  hipLaunchKernelGGL((k_few<DT, MODE, S, FN, XI, D>), dim3((unsigned)(q.mt * q.nt)), dim3(64 * S), 0, s, q);
+  return launch_status();
+}
+
+template <int DT, int MODE>
+int launch_rows(Params& q, hipStream_t s) {
+  const bool few = cdiv(q.N, MODE == GATED ? 8 : 16) <= 256;
+  if (q.M <= 8) return few ? launch_few<DT, MODE, 8, 1, 1, 6>(q, s) : launch_few<DT, MODE, 4, 2, 1, 3>(q, s);
+  if (q.M <= 16) return few ? launch_few<DT, MODE, 8, 1, 2, 4>(q, s) : launch_few<DT, MODE, 4, 2, 2, 3>(q, s);
+  if (q.M <= 32) return few ? launch_few<DT, MODE, 8, 1, 4, 3>(q, s) : launch_few<DT, MODE, 4, 2, 4, 2>(q, s);
+  return launch_few<DT, MODE, 4, 1, 8, 3>(q, s);
+}
+
 // ------------------------------------------------------------ backward workspace
 struct GradLayout {
   size_t dg, du, sums, part, bytes;
@@ -143,17 +164,31 @@ int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_
 int lora_rows(const moe_lora_problem& p, int64_t ldx) {
   return (int)std::min<int64_t>({(int64_t)p.M, (0x7fffffff - 2 * (int64_t)p.K) / (2 * ldx) / 256 * 256, (int64_t)1 << 20});
 }
+// K ranges of the first product: two workgroups to a compute unit, at least 16 steps of 32 to a range.
+int shrink_ranges(int64_t M, int K) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / cdiv(M, 16), cdiv(K, 32) / 16, 16}));
+}
+
 struct LoraLayout {
-  size_t perm, sid, ends, tf, t, bytes;
+  size_t perm, sid, ends, tf, t, part, bytes;
 };
 LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
-  LoraLayout l;
+  LoraLayout l{};
+  if (p.M <= kFewRows) {
+    l.bytes = (size_t)p.M * p.R * 4;
+    return l;
+  }
   l.perm = 0;
   l.sid = up256((size_t)rows * 4);
   l.ends = l.sid + up256((size_t)rows * 4);
   l.tf = l.ends + up256((size_t)p.L * 4);
   l.t = l.tf + up256((size_t)rows * 4);
-  l.bytes = l.t + up256((size_t)rows * 4 * p.R);
+  l.part = l.t + up256((size_t)rows * 4 * p.R);
+  // the last part of a call may be its smallest, with the most ranges
+  size_t part = 0;
+  for (int64_t n : {(int64_t)rows, (int64_t)p.M % rows})
+    if (n && shrink_ranges(n, p.K) > 1) part = std::max(part, (size_t)shrink_ranges(n, p.K) * n * p.R * 4);
+  l.bytes = l.part + up256(part);
   return l;
 }
 int lora_sizes(const moe_lora_problem* p, int64_t& ldx, int64_t& ldw, int64_t& ldo, int64_t& lda) {
@@ -173,12 +208,14 @@ int lora_sizes(const moe_lora_problem* p, int64_t& ldx, int64_t& ldw, int64_t& l
 
 template <int DT>
 void launch_shrink(const ShrinkParams& q, hipStream_t s) {
-  const dim3 g((unsigned)cdiv(q.M, 16)), b(512);
+  const int ranges = shrink_ranges(q.M, q.K);
+  const dim3 g((unsigned)cdiv(q.M, 16), (unsigned)ranges), b(512);
   if (q.R <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), g, b, 0, s, q);
   else if (q.R <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), g, b, 0, s, q);
   else if (q.R <= 64) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), g, b, 0, s, q);
   else if (q.R <= 128) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), g, b, 0, s, q);
   else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), g, b, 0, s, q);
+  if (ranges > 1) hipLaunchKernelGGL((k_lora_finish<DT>), dim3((unsigned)cdiv(q.M, 4)), dim3(256), 0, s, q, ranges);
 }
 
 }  // namespace
@@ -225,7 +262,10 @@ int moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_ga
   q.ld_keep[1] = g.ld_up;
   q.act = act_of(*p);
   hipStream_t s = (hipStream_t)stream;
-  return with_type16(p->type, [&](auto dt) { return launch<decltype(dt)::value, GATED>(q, s); });
+  return with_type16(p->type, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    return p->M <= kFewGated ? launch_rows<DT, GATED>(q, s) : launch<DT, GATED>(q, s);
+  });
 }
 
 size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p) {
@@ -363,6 +403,21 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
   q.perm = (const int32_t*)(ws + l.perm);
   q.sid = (const int32_t*)(ws + l.sid);
   q.ends = (const int32_t*)(ws + l.ends);
+  if (p->M <= kFewRows) {
+    q.m[0] = (const uint16_t*)x;
+    q.out[0] = out;
+    q.add = add;
+    q.M = p->M;
+    q.tf = (const float*)ws;
+    q.sid = ids;
+    return with_type16(p->type, [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, ids, nullptr, nullptr, (float*)ws, nullptr, ldx,
+                            p->M, p->K, p->R, p->L};
+      hipLaunchKernelGGL((k_lora_shrink_few<DT>), dim3((unsigned)p->M, (unsigned)p->R / 8), dim3(256), 0, s, sh);
+      return launch_rows<DT, LORA>(q, s);
+    });
+  }
   return with_type16(p->type, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     for (int64_t m = 0; m < p->M; m += rows) {
@@ -374,7 +429,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
       const SortParams sp{ids + m, (int32_t*)(ws + l.perm), (int32_t*)(ws + l.sid), (int32_t*)(ws + l.ends), n, p->L};
       hipLaunchKernelGGL(k_lora_sort, dim3(1), dim3(1024), 0, s, sp);
       const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, q.perm, q.sid, q.ends, (uint16_t*)(ws + l.t),
-                            (float*)(ws + l.tf), ldx, n, p->K, p->R, p->L};
+                            (float*)(ws + l.tf), (float*)(ws + l.part), ldx, n, p->K, p->R, p->L};
       launch_shrink<DT>(sh, s);
       int rc = launch_status();
       if (!rc) rc = launch<DT, LORA>(q, s);
