@@ -43,7 +43,7 @@ struct Params {
   int32_t M, N, K;         // K of one product
   int32_t mt, nt;          // row and column tiles
   int32_t splits;          // K ranges, each with a partial result of its own (1 = none)
-  float* part;             // partial results [splits][M][N] (GATED: [splits][2][M][N])
+  float* part;             // partial results
   const float* bias[2];
   void* keep[2];           // GATED: g and u, or nullptr
   int64_t ld_keep[2];
@@ -175,8 +175,8 @@ struct Frag<true> {
   __device__ __forceinline__ u32x4 get() const { return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)}; }
 };
 
-// The same with the offset in the instruction (a K-major half of 128 columns).
-template <bool MAJOR>
+// The same with the offset in the instruction; K-major: rows of W columns.
+template <bool MAJOR, int W>
 struct BigFrag {
   u32x4 v;
   template <int AT>
@@ -186,13 +186,13 @@ struct BigFrag {
   __device__ __forceinline__ void tie() { asm volatile("" : "+v"(v)); }
   __device__ __forceinline__ u32x4 get() const { return v; }
 };
-template <>
-struct BigFrag<true> {
+template <int W>
+struct BigFrag<true, W> {
   uint64_t a, b;
   template <int AT>
   __device__ __forceinline__ void read(uint32_t addr) {
     asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(a) : "v"(addr), "n"(AT));
-    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(b) : "v"(addr), "n"(AT + 1024));
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(b) : "v"(addr), "n"(AT + 8 * W));
   }
   __device__ __forceinline__ void tie() {
     asm volatile("" : "+v"(a));
@@ -230,10 +230,90 @@ __device__ __forceinline__ bool item_of(const Params& p, int nz, Item& it) {
   return true;
 }
 
+template <int DT>
+__device__ __forceinline__ float load1(const void* base, size_t i) {
+  if constexpr (DT == T_BF16) return (float)((const __bf16*)base)[i];
+  else return (float)((const _Float16*)base)[i];
+}
+template <int DT>
+__device__ __forceinline__ void store1(void* base, size_t i, float v) {
+  if constexpr (DT == T_BF16) ((__bf16*)base)[i] = (__bf16)v;
+  else ((_Float16*)base)[i] = (_Float16)v;
+}
+
 // ------------------------------------------------------------ epilogue
-// A wave's results of 32 rows, staged in LDS as float32 (rows of PITCH values),
-// come back eight columns to a lane, get their bias, addend or activation,
-// are rounded once and leave as 16-byte stores.
+// Eight neighbouring results of one output row (GATED: of both projections) get their bias, addend or
+// activation, are rounded once and stored. row: LORA's in the output's order, not the sorted one.
+template <int DT, int MODE>
+__device__ __forceinline__ void finish8(const Params& p, int z, int64_t row, int col, float (&v)[8], float (&u)[8]) {
+  if constexpr (MODE == GATED) {
+    if (p.bias[0]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] += p.bias[0][col + j];
+        u[j] += p.bias[1][col + j];
+      }
+    }
+    if (p.keep[0]) {
+      store8<DT>(p.keep[0], (size_t)(row * p.ld_keep[0] + col), v);
+      store8<DT>(p.keep[1], (size_t)(row * p.ld_keep[1] + col), u);
+    }
+    with_act(p.act, [&](auto k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_f<decltype(k)::value>(p.act, v[j], u[j]);
+    });
+    store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
+  } else if constexpr (MODE == DX) {
+    store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
+  } else if constexpr (MODE == DW) {
+    const size_t at = (size_t)(row * p.ldo[z] + col);
+    if (p.accumulate) {
+      float old[8];
+      if (p.f32_out) load8<T_FP32>(p.out[z], at, old);
+      else load8<DT>(p.out[z], at, old);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += old[j];
+    }
+    if (p.f32_out) store8<T_FP32>(p.out[z], at, v);
+    else store8<DT>(p.out[z], at, v);
+  } else {
+    uint16_t* out = (uint16_t*)p.out[0] + row * p.ldo[0] + col;
+    const uint16_t* add = p.add ? (const uint16_t*)p.add + row * p.ld_add + col : nullptr;
+    if (p.vec && col + 8 <= p.N) {
+      if (p.bias[0]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += p.bias[0][col + j];
+      }
+      if (add) {
+        float old[8];
+        load8<DT>(add, 0, old);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += old[j];
+      }
+      store8<DT>(out, 0, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (col + j >= p.N) break;
+        float s = v[j];
+        if (p.bias[0]) s += p.bias[0][col + j];
+        if (add) s += load1<DT>(add, j);
+        store1<DT>(out, j, s);
+      }
+    }
+  }
+}
+
+// Partial results: [K range][GATED: g, u; DW: half][row][columns rounded up to 8]
+template <int MODE>
+__device__ __forceinline__ float* part_of(const Params& p, int split, int which, int64_t row, int col) {
+  const int64_t np = (p.N + 7) & ~7;
+  const int planes = MODE == GATED || MODE == DW ? 2 : 1;
+  return p.part + ((int64_t)(planes * split + which) * p.M + row) * np + col;
+}
+
+// A wave's results of 32 rows, staged in LDS as float32 (rows of COLS + 4 values),
+// come back eight columns to a lane and leave as 16-byte stores.
 template <int DT, int MODE, int COLS>
 __device__ __forceinline__ void store_rows(const Params& p, const float* strip, int z, int split, int row0, int col0,
                                            int lane, const int* rows_lds) {
@@ -247,90 +327,40 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* strip, 
     const int row = row0 + r;
     if (row >= p.M) return;
     float v[8], u[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const f32x4 a = *(const f32x4*)(strip + r * PITCH + c + j);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[j + q] = a[q];
-      if constexpr (MODE == GATED) {
-        const f32x4 b = *(const f32x4*)(strip + r * PITCH + HALF + c + j);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) u[j + q] = b[q];
-      }
-    }
-    if (p.splits > 1) {  // N is a multiple of 8 here
-      const size_t mn = (size_t)p.M * p.N, at = (size_t)row * p.N + col;
-      if constexpr (MODE == GATED) {
-        store8<T_FP32>(p.part + (size_t)(2 * split) * mn, at, v);
-        store8<T_FP32>(p.part + (size_t)(2 * split + 1) * mn, at, u);
-      } else {
-        store8<T_FP32>(p.part + (size_t)split * mn, at, v);
-      }
-      continue;
-    }
-    if constexpr (MODE == GATED) {
-      if (p.bias[0]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] += p.bias[0][col + j];
-          u[j] += p.bias[1][col + j];
-        }
-      }
-      if (p.keep[0]) {
-        store8<DT>(p.keep[0], (size_t)(row * p.ld_keep[0] + col), v);
-        store8<DT>(p.keep[1], (size_t)(row * p.ld_keep[1] + col), u);
-      }
-      with_act(p.act, [&](auto k) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = act_f<decltype(k)::value>(p.act, v[j], u[j]);
-      });
-      store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
-    } else if constexpr (MODE == DX) {
-      store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
-    } else if constexpr (MODE == DW) {
-      const size_t at = (size_t)(row * p.ldo[z] + col);
-      if (p.accumulate) {
-        float old[8];
-        if (p.f32_out) load8<T_FP32>(p.out[z], at, old);
-        else load8<DT>(p.out[z], at, old);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += old[j];
-      }
-      if (p.f32_out) store8<T_FP32>(p.out[z], at, v);
-      else store8<DT>(p.out[z], at, v);
+    load8<T_FP32>(strip, r * PITCH + c, v);
+    if constexpr (MODE == GATED) load8<T_FP32>(strip, r * PITCH + HALF + c, u);
+    if (p.splits > 1) {
+      store8<T_FP32>(part_of<MODE>(p, split, z, row, col), 0, v);
+      if constexpr (MODE == GATED) store8<T_FP32>(part_of<MODE>(p, split, 1, row, col), 0, u);
     } else {
-      const int64_t orow = rows_lds[r];
-      uint16_t* out = (uint16_t*)p.out[0] + orow * p.ldo[0] + col;
-      const uint16_t* add = p.add ? (const uint16_t*)p.add + orow * p.ld_add + col : nullptr;
-      if (p.vec && col + 8 <= p.N) {
-        if (p.bias[0]) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += p.bias[0][col + j];
-        }
-        if (add) {
-          float old[8];
-          load8<DT>(add, 0, old);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += old[j];
-        }
-        store8<DT>(out, 0, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (col + j >= p.N) break;
-          float s = v[j];
-          if (p.bias[0]) s += p.bias[0][col + j];
-          if constexpr (DT == T_BF16) {
-            if (add) s += (float)((const __bf16*)add)[j];
-            ((__bf16*)out)[j] = (__bf16)s;
-          } else {
-            if (add) s += (float)((const _Float16*)add)[j];
-            ((_Float16*)out)[j] = (_Float16)s;
-          }
-        }
-      }
+      finish8<DT, MODE>(p, z, MODE == LORA ? rows_lds[r] : row, col, v, u);
     }
   }
+}
+
+// Partial results joined in the order of their K ranges, eight columns to a thread.
+template <int DT, int MODE>
+__global__ __launch_bounds__(256) void k_join(const Params p) {
+  const int cpr = (p.N + 7) / 8, z = blockIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * cpr) return;
+  const int row = (int)(i / cpr), col = (int)(i - (int64_t)row * cpr) * 8;
+  float v[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    float a[8];
+    load8<T_FP32>(part_of<MODE>(p, s, z, row, col), 0, a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += a[j];
+    if constexpr (MODE == GATED) {
+      load8<T_FP32>(part_of<MODE>(p, s, 1, row, col), 0, a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += a[j];
+    }
+  }
+  finish8<DT, MODE>(p, z, MODE == LORA ? p.perm[row] : row, col, v, u);
 }
 
 // ------------------------------------------------------------ tiles by four waves
@@ -348,13 +378,13 @@ __global__ __launch_bounds__(256) void k_tile(const Params p) {
   __shared__ int rows_lds[MODE == LORA ? BM : 1];
   lds_u8* smem = (lds_u8*)smem_arr;
   Item it;
-  if (!item_of(p, MODE == DW ? 2 : p.splits, it)) return;
+  if (!item_of(p, MODE == DW ? 2 * p.splits : p.splits, it)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, lr = lane & 31, lk = lane >> 5;
   constexpr int TN = MODE == GATED ? BN / 2 : BN;  // output columns of the tile
   const int m0 = it.mt * BM, n0 = it.nt * TN;
-  const int z = MODE == DW ? it.z : 0, split = MODE == DW ? 0 : it.z;
+  const int z = MODE == DW ? it.z & 1 : 0, split = MODE == DW ? it.z >> 1 : it.z;
 
   // stages of this workgroup's K range
   const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;

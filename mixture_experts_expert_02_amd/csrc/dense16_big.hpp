@@ -18,21 +18,23 @@
 namespace moe {
 namespace d16 {
 
-template <int DT, int MODE>
+template <int DT, int MODE, int BM>
 __global__ __launch_bounds__(512) void k_big(const Params p) {
   constexpr bool MM = MODE == DW, NM = MODE == DX || MODE == DW;  // K-major operands
-  constexpr int BM = 256, TN = MODE == GATED ? 128 : 256, HALF = 16384;
-  constexpr int N_AT = 4 * HALF;  // M halves [stage buffer][half], then N halves
-  __shared__ __attribute__((aligned(16))) uint8_t smem_arr[8 * HALF];
+  constexpr int HM = BM / 2, J = BM / 128, NB = BM == 256 ? 2 : 3;  // rows of an M half, a wave's 32-row fragments of it, buffers
+  constexpr int TN = MODE == GATED ? 128 : 256, HALF = 16384, HALF_M = HM * 128;
+  constexpr int N_AT = NB * 2 * HALF_M;  // M halves [stage buffer][half], then N halves
+  constexpr int LM = BM / 128, LN = 2, LS = 2 * (LM + LN);  // a wave's load instructions for a half, and for a stage
+  __shared__ __attribute__((aligned(16))) uint8_t smem_arr[NB * 2 * (HALF_M + HALF)];
   __shared__ int rows_lds[MODE == LORA ? BM : 1];
   lds_u8* smem = (lds_u8*)smem_arr;
   Item it;
-  if (!item_of(p, MODE == DW ? 2 : p.splits, it)) return;
+  if (!item_of(p, MODE == DW ? 2 * p.splits : p.splits, it)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lk = lane >> 5;
   const int m0 = it.mt * BM, n0 = it.nt * TN;
-  const int z = MODE == DW ? it.z : 0, split = MODE == DW ? 0 : it.z;
+  const int z = MODE == DW ? it.z & 1 : 0, split = MODE == DW ? it.z >> 1 : it.z;
   const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;
   const int s_lo = (int)((int64_t)split * all / p.splits), nst = (int)((int64_t)(split + 1) * all / p.splits) - s_lo;
 
@@ -41,28 +43,32 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     __syncthreads();
   }
 
-  // ---- loads: instructions 2 wave and 2 wave + 1 of the 16 of a half
+  // ---- loads: instructions 2 wave and 2 wave + 1 of the 16 of a half (BM = 128: instruction `wave` of the 8 of an M half)
   // columns of N half h: 128 h + i where N is K-major or GATED (half = gate or up); else 32 columns of each half
   // side by side, 64 (i / 32) + 32 h + i % 32, so that a wave's columns are 64 neighbours
-  int m_row[2], m_chunk[2], n_row[2], n_chunk[2];
-  uint32_t g_off[2][2];  // LORA: rows of x are gathered
+  int m_row[LM], m_chunk[LM], n_row[2], n_chunk[2];
+  uint32_t g_off[2][LM];  // LORA: rows of x are gathered
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = 2 * wave + q, r = i * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-    if constexpr (MM) major_src<128>(i, lane, m_row[q], m_chunk[q]);
+  for (int q = 0; q < LM; ++q) {
+    const int i = LM * wave + q, r = i * 8 + (lane >> 3);
+    if constexpr (MM) major_src<HM>(i, lane, m_row[q], m_chunk[q]);
     else {
       m_row[q] = r;
-      m_chunk[q] = c;
-    }
-    if constexpr (NM) major_src<128>(i, lane, n_row[q], n_chunk[q]);
-    else {
-      n_row[q] = MODE == GATED ? r : (r >> 5) * 64 + (r & 31);
-      n_chunk[q] = c;
+      m_chunk[q] = (lane & 7) ^ ((r >> 1) & 7);
     }
     if constexpr (MODE == LORA) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        g_off[h][q] = m0 + h * 128 + r < p.M ? (uint32_t)rows_lds[h * 128 + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+        g_off[h][q] = m0 + h * HM + r < p.M ? (uint32_t)rows_lds[h * HM + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = 2 * wave + q, r = i * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+    if constexpr (NM) major_src<128>(i, lane, n_row[q], n_chunk[q]);
+    else {
+      n_row[q] = MODE == GATED ? r : (r >> 5) * 64 + (r & 31);
+      n_chunk[q] = c;
     }
   }
   auto load_m = [&](int h, int st, int buf) {
@@ -74,17 +80,17 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     }
     const int k0 = s * BK, mi = MODE == DX ? seg : z;
     const int64_t ld = p.ldm[mi];
-    lds_u8* dst = smem + (buf * 2 + h) * HALF + wave * 2048;
+    lds_u8* dst = smem + (buf * 2 + h) * HALF_M + wave * LM * 1024;
     if constexpr (MM) {
-      const auto rs = rsrc(p.m[mi] + (int64_t)k0 * ld + m0 + h * 128, live ? ((min(BK, p.K - k0) - 1) * ld + p.M - m0 - h * 128) * 2 : 0);
+      const auto rs = rsrc(p.m[mi] + (int64_t)k0 * ld + m0 + h * HM, live ? ((min(BK, p.K - k0) - 1) * ld + p.M - m0 - h * HM) * 2 : 0);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16, 0);
+      for (int q = 0; q < LM; ++q) dma(rs, dst + q * 1024, m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16, 0);
     } else {
       const auto rs = MODE == LORA ? rsrc(p.m[0], live ? 0x7fffffff : 0)
-                                   : rsrc(p.m[mi] + (int64_t)(m0 + h * 128) * ld,
-                                          live && p.M - m0 > h * 128 ? ((min(128, p.M - m0 - h * 128) - 1) * ld + p.K) * 2 : 0);
+                                   : rsrc(p.m[mi] + (int64_t)(m0 + h * HM) * ld,
+                                          live && p.M - m0 > h * HM ? ((min(HM, p.M - m0 - h * HM) - 1) * ld + p.K) * 2 : 0);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < LM; ++q) {
         uint32_t off = MODE == LORA ? g_off[h][q] : m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16;
         if (k0 + m_chunk[q] * 8 >= p.K) off = kNoLoad;
         dma(rs, dst + q * 1024, off, k0 * 2);
@@ -119,60 +125,70 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 
   // ---- operand reads: bytes inside a half
   const int tr = (lane >> 2) & 3;
-  auto major_at = [&](int col, int ks) {
-    const int cb = 2 * (col + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-    return (uint32_t)((16 * ks + 8 * lk + tr) * 256 + (((cb >> 6) ^ tr) << 6) + (cb & 63));
+  auto major_at = [&](int col, bool narrow) {  // rows of 128 columns, or of 64
+    const int cb = 2 * (col + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)), k = 8 * lk + tr;
+    return (uint32_t)(k * (narrow ? 128 : 256) + (((cb >> 6) ^ (narrow ? tr >> 1 : tr)) << 6) + (cb & 63));
   };
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-  uint32_t m_at[MM ? 2 : 4], n_at[NM ? 1 : 4];  // K-major: by fragment; else by K step
+  // K-major: by fragment; else by K step. An instruction's offset reaches 64 KB: the third buffer's N halves have addresses of their own.
+  uint32_t m_at[MM ? J : 4], n_at[NB == 3 ? 2 : 1][NM ? 1 : 4];
   if constexpr (MM) {
-    m_at[0] = lds0 + major_at(wm * 64, 0);
-    m_at[1] = lds0 + major_at(wm * 64 + 32, 0);
+#pragma unroll
+    for (int j = 0; j < J; ++j) m_at[j] = lds0 + major_at(wm * (HM / 2) + j * 32, HM == 64);
   } else {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) m_at[ks] = lds0 + 16 * row_slot(wm * 64 + lr, 2 * ks + lk);
+    for (int ks = 0; ks < 4; ++ks) m_at[ks] = lds0 + 16 * row_slot(wm * (HM / 2) + lr, 2 * ks + lk);
   }
-  if constexpr (NM) {
-    n_at[0] = lds0 + N_AT + major_at(wn * 32, 0);
-  } else {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) n_at[ks] = lds0 + N_AT + 16 * row_slot(wn * 32 + lr, 2 * ks + lk);
+  for (int b = 0; b < (NB == 3 ? 2 : 1); ++b) {
+    if constexpr (NM) {
+      n_at[b][0] = lds0 + N_AT + b * 4 * HALF + major_at(wn * 32, false);
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) n_at[b][ks] = lds0 + N_AT + b * 4 * HALF + 16 * row_slot(wn * 32 + lr, 2 * ks + lk);
+    }
   }
 
-  f32x16 acc[2][2][2];  // [N half][M half][32 rows]
+  f32x16 acc[2][2][J];  // [N half][M half][32 rows]
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[a][b][j][r] = 0.f;
 
-  BigFrag<MM> fm[2][2][4];  // [M half][32 rows][K step]
-  BigFrag<NM> fn[2][4];     // [set][K step]
+  BigFrag<MM, HM> fm[2][J][4];  // [M half][32 rows][K step]
+  BigFrag<NM, 128> fn[2][4];     // [set][K step]
 
-  // fragment x (0..7) of an M half, (0..3) of an N half; AT: constant byte offset of the half
-#define MOE_D16_READ_M(h, buf, x)                                                                                \
-  {                                                                                                              \
-    if constexpr (MM) fm[h][(x) & 1][(x) >> 1].template read<((buf) * 2 + (h)) * HALF + ((x) >> 1) * 4096>(m_at[(x) & 1]); \
-    else fm[h][(x) & 1][(x) >> 1].template read<((buf) * 2 + (h)) * HALF + ((x) & 1) * 4096>(m_at[(x) >> 1]);    \
+  // fragment x (0 .. 4 J - 1) of an M half, (0..3) of an N half
+#define MOE_D16_READ_M(h, buf, x)                                                                                    \
+  {                                                                                                                  \
+    constexpr int j_ = (x) % J, k_ = (x) / J;                                                                        \
+    if constexpr (MM) fm[h][j_][k_].template read<((buf) * 2 + (h)) * HALF_M + k_ * 32 * HM>(m_at[j_]);               \
+    else fm[h][j_][k_].template read<((buf) * 2 + (h)) * HALF_M + j_ * 4096>(m_at[k_]);                              \
   }
-#define MOE_D16_READ_N(set, h, buf, x)                                                                 \
-  {                                                                                                    \
-    if constexpr (NM) fn[set][x].template read<((buf) * 2 + (h)) * HALF + (x) * 4096>(n_at[0]);        \
-    else fn[set][x].template read<((buf) * 2 + (h)) * HALF>(n_at[x]);                                  \
+#define MOE_D16_READ_N(set, h, buf, x)                                                                               \
+  {                                                                                                                  \
+    if constexpr (NM) fn[set][x].template read<(((buf) & 1) * 2 + (h)) * HALF + (x) * 4096>(n_at[(buf) >> 1][0]);     \
+    else fn[set][x].template read<(((buf) & 1) * 2 + (h)) * HALF>(n_at[(buf) >> 1][x]);                              \
+  }
+// two of an M half's reads in one slot (of four slots) where there are eight
+#define MOE_D16_READ_M2(h, buf, s)                                          \
+  {                                                                         \
+    if constexpr (J == 2) {                                                 \
+      MOE_D16_READ_M(h, buf, 2 * (s)) MOE_D16_READ_M(h, buf, 2 * (s) + 1)   \
+    } else MOE_D16_READ_M(h, buf, s)                                        \
   }
 #define MOE_D16_ALL_N(h) \
   MOE_D16_READ_N(0, h, 0, 0) MOE_D16_READ_N(0, h, 0, 1) MOE_D16_READ_N(0, h, 0, 2) MOE_D16_READ_N(0, h, 0, 3)
-#define MOE_D16_ALL_M(h) \
-  MOE_D16_READ_M(h, 0, 0) MOE_D16_READ_M(h, 0, 1) MOE_D16_READ_M(h, 0, 2) MOE_D16_READ_M(h, 0, 3) \
-  MOE_D16_READ_M(h, 0, 4) MOE_D16_READ_M(h, 0, 5) MOE_D16_READ_M(h, 0, 6) MOE_D16_READ_M(h, 0, 7)
+#define MOE_D16_ALL_M(h) MOE_D16_READ_M2(h, 0, 0) MOE_D16_READ_M2(h, 0, 1) MOE_D16_READ_M2(h, 0, 2) MOE_D16_READ_M2(h, 0, 3)
 #define MOE_D16_MFMA(hn, hm, set, x) \
-  acc[hn][hm][(x) & 1] = mfma<DT>(fn[set][(x) >> 1].get(), fm[hm][(x) & 1][(x) >> 1].get(), acc[hn][hm][(x) & 1]);
+  if constexpr ((x) < 4 * J) acc[hn][hm][(x) % J] = mfma<DT>(fn[set][(x) / J % 4].get(), fm[hm][(x) % J][(x) / J % 4].get(), acc[hn][hm][(x) % J]);
   auto tie_m = [&](int h) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) fm[h][j][ks].tie();
   };
@@ -184,13 +200,13 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // ---- adapters of the tile's rows (see k_tile)
   if constexpr (MODE == LORA) {
     if (split == 0) {
-      int id[2][2];
-      float f[2][2];
+      int id[2][J];
+      float f[2][J];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = m0 + h * 128 + wm * 64 + j * 32 + lr;
+        for (int j = 0; j < J; ++j) {
+          const int row = m0 + h * HM + wm * (HM / 2) + j * 32 + lr;
           id[h][j] = row < p.M ? p.sid[row] : p.L;
           f[h][j] = row < p.M ? p.tf[row] : 0.f;
         }
@@ -206,9 +222,15 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
+            for (int q = 0; q < LM; ++q) {
+              const int vm = st * 8 + m_chunk[q];
+              dma(rs_t, smem + h * HALF_M + (wave * LM + q) * 1024, vm < 2 * rc ? (uint32_t)((h * HM + m_row[q]) * 4 * p.R + vm * 16) : kNoLoad, 0);
+            }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int vm = st * 8 + m_chunk[q], vn = st * 8 + n_chunk[q];
-              dma(rs_t, smem + h * HALF + wave * 2048 + q * 1024, vm < 2 * rc ? (uint32_t)((h * 128 + m_row[q]) * 4 * p.R + vm * 16) : kNoLoad, 0);
+              const int vn = st * 8 + n_chunk[q];
               dma(rs_b, smem + N_AT + h * HALF + wave * 2048 + q * 1024,
                   vn < 2 * rc ? (uint32_t)((h * 32 + n_row[q]) * 2 * p.R + (vn < rc ? vn : vn - rc) * 16) : kNoLoad, 0);
             }
@@ -224,7 +246,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
               tie_n(0);
               tie_m(hm);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < J; ++j) {
                 if (!__any(id[hm][j] == a)) continue;
                 f32x16 tmp;
 #pragma unroll
@@ -245,8 +267,8 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   }
 
   // ---- main loop
-  // One phase: MFMAs 0..7, READS between the first, LOAD behind the fifth.
-#define MOE_D16_PHASE(hn, hm, set, R0, R1, R2, R3, LOAD, TIE)            \
+  // One phase: its MFMAs, a slot of READS behind each of the first four, the LOAD, and all loads but the LEFT youngest landed.
+#define MOE_D16_PHASE(hn, hm, set, R0, R1, R2, R3, LOAD, LEFT, TIE)      \
   {                                                                      \
     MOE_D16_MFMA(hn, hm, set, 0) R0 __builtin_amdgcn_sched_barrier(0);   \
     MOE_D16_MFMA(hn, hm, set, 1) R1 __builtin_amdgcn_sched_barrier(0);   \
@@ -258,47 +280,61 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     MOE_D16_MFMA(hn, hm, set, 6)                                         \
     MOE_D16_MFMA(hn, hm, set, 7)                                         \
     __builtin_amdgcn_sched_barrier(0);                                   \
-    wait_all_but<12>();                                                  \
+    wait_all_but<LEFT>();                                                \
     TIE;                                                                 \
     barrier();                                                           \
     __builtin_amdgcn_sched_barrier(0);                                   \
   }
-  // Stage st in buffer B: N half 0 in set X, half 1 comes into set Y, which the next stage's half 0 takes over.
-#define MOE_D16_STAGE(st, B, X, Y)                                                                                   \
+  // Stage st in buffer B (the next one's: C): N half 0 in set X, half 1 comes into set Y, which the next stage's
+  // half 0 takes over.
+#define MOE_D16_STAGE(st, B, C, X, Y)                                                                                \
   {                                                                                                                  \
     MOE_D16_PHASE(0, 0, X, MOE_D16_READ_N(Y, 1, B, 0), MOE_D16_READ_N(Y, 1, B, 1), MOE_D16_READ_N(Y, 1, B, 2),       \
-                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + 2, B), tie_n(Y))                                      \
-    MOE_D16_PHASE(1, 0, Y, MOE_D16_READ_M(1, B, 0) MOE_D16_READ_M(1, B, 1), MOE_D16_READ_M(1, B, 2) MOE_D16_READ_M(1, B, 3), \
-                  MOE_D16_READ_M(1, B, 4) MOE_D16_READ_M(1, B, 5), MOE_D16_READ_M(1, B, 6) MOE_D16_READ_M(1, B, 7),  \
-                  load_n(1, (st) + 2, B), tie_m(1))                                                                  \
-    MOE_D16_PHASE(1, 1, Y, MOE_D16_READ_M(0, 1 - B, 0) MOE_D16_READ_M(0, 1 - B, 1),                                  \
-                  MOE_D16_READ_M(0, 1 - B, 2) MOE_D16_READ_M(0, 1 - B, 3),                                           \
-                  MOE_D16_READ_M(0, 1 - B, 4) MOE_D16_READ_M(0, 1 - B, 5),                                           \
-                  MOE_D16_READ_M(0, 1 - B, 6) MOE_D16_READ_M(0, 1 - B, 7), load_m(1, (st) + 2, B), tie_m(0))         \
-    MOE_D16_PHASE(0, 1, X, MOE_D16_READ_N(Y, 0, 1 - B, 0), MOE_D16_READ_N(Y, 0, 1 - B, 1), MOE_D16_READ_N(Y, 0, 1 - B, 2), \
-                  MOE_D16_READ_N(Y, 0, 1 - B, 3), load_m(0, (st) + 3, 1 - B), tie_n(Y))                              \
+                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + NB, B), (NB - 1) * LS + LM + LN, tie_n(Y))            \
+    MOE_D16_PHASE(1, 0, Y, MOE_D16_READ_M2(1, B, 0), MOE_D16_READ_M2(1, B, 1), MOE_D16_READ_M2(1, B, 2),             \
+                  MOE_D16_READ_M2(1, B, 3), load_n(1, (st) + NB, B), (NB - 2) * LS + 2 * LM + 4 * LN, tie_m(1))      \
+    MOE_D16_PHASE(1, 1, Y, MOE_D16_READ_M2(0, C, 0), MOE_D16_READ_M2(0, C, 1), MOE_D16_READ_M2(0, C, 2),             \
+                  MOE_D16_READ_M2(0, C, 3), load_m(1, (st) + NB, B), (NB - 1) * LS + LM + LN, tie_m(0))              \
+    MOE_D16_PHASE(0, 1, X, MOE_D16_READ_N(Y, 0, C, 0), MOE_D16_READ_N(Y, 0, C, 1), MOE_D16_READ_N(Y, 0, C, 2),       \
+                  MOE_D16_READ_N(Y, 0, C, 3), load_m(0, (st) + 1 + NB, C), (NB - 1) * LS + 2 * LM, tie_n(Y))         \
   }
   if (nst > 0) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < NB; ++s) {
       load_m(0, s, s);
       load_n(0, s, s);
       load_n(1, s, s);
       load_m(1, s, s);
     }
-    wait_loads<12>();
+    wait_loads<NB * LS - LM - LN>();
     barrier();
     MOE_D16_ALL_N(0)
     MOE_D16_ALL_M(0)
-    wait_all_but<10>();
+    wait_all_but<NB * LS - LM - 2 * LN>();
     tie_n(0);
     tie_m(0);
     barrier();
-    load_m(0, 2, 0);
-    for (int s = 0; s < nst; s += 2) {
-      MOE_D16_STAGE(s, 0, 0, 1)
-      if (s + 1 >= nst) break;
-      MOE_D16_STAGE(s + 1, 1, 1, 0)
+    load_m(0, NB, 0);
+    if constexpr (NB == 2) {
+      for (int s = 0; s < nst; s += 2) {
+        MOE_D16_STAGE(s, 0, 1, 0, 1)
+        if (s + 1 >= nst) break;
+        MOE_D16_STAGE(s + 1, 1, 0, 1, 0)
+      }
+    } else {
+      for (int s = 0; s < nst; s += 6) {
+        MOE_D16_STAGE(s, 0, 1, 0, 1)
+        if (s + 1 >= nst) break;
+        MOE_D16_STAGE(s + 1, 1, 2, 1, 0)
+        if (s + 2 >= nst) break;
+        MOE_D16_STAGE(s + 2, 2, 0, 0, 1)
+        if (s + 3 >= nst) break;
+        MOE_D16_STAGE(s + 3, 0, 1, 1, 0)
+        if (s + 4 >= nst) break;
+        MOE_D16_STAGE(s + 4, 1, 2, 0, 1)
+        if (s + 5 >= nst) break;
+        MOE_D16_STAGE(s + 5, 2, 0, 1, 0)
+      }
     }
     wait_loads<0>();
     barrier();
@@ -310,7 +346,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #pragma unroll
   for (int hm = 0; hm < 2; ++hm)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int hs = 0; hs < 64 / COLS; ++hs) {
 #pragma unroll
@@ -321,7 +357,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
             *(f32x4*)(strip + lr * (COLS + 4) + i * 32 + 8 * q + 4 * lk) = f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
           }
         wave_sync();
-        const int r = hm * 128 + wm * 64 + j * 32;
+        const int r = hm * HM + wm * (HM / 2) + j * 32;
         store_rows<DT, MODE, COLS>(p, strip, z, split, m0 + r, n0 + (MODE == GATED ? wn * 32 : NM ? hs * 128 + wn * 32 : wn * 64), lane,
                                    rows_lds + (MODE == LORA ? r : 0));
         wave_sync();
@@ -332,6 +368,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #undef MOE_D16_ALL_N
 #undef MOE_D16_MFMA
 #undef MOE_D16_READ_N
+#undef MOE_D16_READ_M2
 #undef MOE_D16_READ_M
 }
 

@@ -20,17 +20,6 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-template <int DT>
-__device__ __forceinline__ float load1(const void* base, size_t i) {
-  if constexpr (DT == T_BF16) return (float)((const __bf16*)base)[i];
-  else return (float)((const _Float16*)base)[i];
-}
-template <int DT>
-__device__ __forceinline__ void store1(void* base, size_t i, float v) {
-  if constexpr (DT == T_BF16) ((__bf16*)base)[i] = (__bf16)v;
-  else ((_Float16*)base)[i] = (_Float16)v;
-}
-
 // LORA here: p.tf holds the scaled x A^T in float32, [M, R] in the rows' own order, and p.sid the ids.
 template <int DT, int MODE, int S, int FN, int XI, int D>
 __global__ __launch_bounds__(64 * S) void k_few(const Params p) {

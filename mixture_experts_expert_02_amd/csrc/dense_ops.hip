@@ -82,30 +82,52 @@ int with_type16(int32_t type, F f) {
   return f(std::integral_constant<int, moe::T_FP16>{});
 }
 
-template <int DT, int MODE, int BM, int BN, int NBUF>
-int launch_tile(Params& q, hipStream_t s) {
-  q.mt = (int)cdiv(q.M, BM);
-  q.nt = (int)cdiv(q.N, MODE == GATED ? BN / 2 : BN);
-  const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : q.splits), 8) * 8;
-  if (n > kMaxGrid) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((k_tile<DT, MODE, BM, BN, NBUF>), dim3((unsigned)n), dim3(256), 0, s, q);
-  return launch_status();
+// ------------------------------------------------------------ tiles
+struct Plan {
+  int bm, splits;
+  size_t part;  // bytes of partial results
+};
+// MODE's planes of results, columns of a tile, stages of all of K
+Plan plan_of(int mode, int64_t M, int64_t N, int64_t K) {
+  const int planes = mode == GATED || mode == DW ? 2 : 1, tn = mode == GATED ? 128 : 256;
+  const int64_t stages = cdiv(K, BK) * (mode == DX ? 2 : 1);
+  Plan best{256, 1, 0};
+  double least = 1e30;
+  for (int bm : {256, 128}) {
+    const int64_t tiles = cdiv(M, bm) * cdiv(N, tn) * (mode == DW ? 2 : 1);
+    for (int s = 1; s <= 16 && s * 4 <= std::max<int64_t>(stages, 4); ++s) {
+      const double rounds = (double)cdiv(tiles * s, 256);
+      const double part = s > 1 ? (double)s * planes * M * N * 4 : 0;
+      if (part > 256e6) break;
+      const double us = rounds * (cdiv(stages, s) * (bm == 256 ? 1.0 : 0.55) + (bm == 256 ? 8 : 6)) + (s > 1 ? 4 + part * 2 / 5e6 : 0);
+      if (us < least) {
+        least = us;
+        best = {bm, s, s > 1 ? up256((size_t)s * planes * M * ((N + 7) & ~7) * 4) : 0};
+      }
+    }
+  }
+  return best;
 }
 
-template <int DT, int MODE>
+template <int DT, int MODE, int BM>
 int launch_big(Params& q, hipStream_t s) {
-  q.mt = (int)cdiv(q.M, 256);
+  q.mt = (int)cdiv(q.M, BM);
   q.nt = (int)cdiv(q.N, MODE == GATED ? 128 : 256);
-  const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : q.splits), 8) * 8;
+  const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : 1) * q.splits, 8) * 8;
   if (n > kMaxGrid / 2) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((k_big<DT, MODE>), dim3((unsigned)n), dim3(512), 0, s, q);
+  hipLaunchKernelGGL((k_big<DT, MODE, BM>), dim3((unsigned)n), dim3(512), 0, s, q);
+  if (q.splits > 1)
+    hipLaunchKernelGGL((k_join<DT, MODE>), dim3((unsigned)cdiv((int64_t)q.M * ((q.N + 7) / 8), 256), MODE == DW ? 2 : 1), dim3(256), 0, s, q);
   return launch_status();
 }
 
+// q.K: of one product; part: room for plan_of's partial results
 template <int DT, int MODE>
-int launch(Params& q, hipStream_t s) {
-  if (cdiv(q.M, 256) * cdiv(q.N, MODE == GATED ? 128 : 256) * (MODE == DW ? 2 : 1) >= 128) return launch_big<DT, MODE>(q, s);
-  return launch_tile<DT, MODE, 128, 128, 4>(q, s);
+int launch(Params& q, void* part, hipStream_t s) {
+  const Plan plan = plan_of(MODE, q.M, q.N, q.K);
+  q.splits = plan.splits;
+  q.part = (float*)part;
+  return plan.bm == 256 ? launch_big<DT, MODE, 256>(q, s) : launch_big<DT, MODE, 128>(q, s);
 }
 
 // ------------------------------------------------------------ few rows
@@ -130,6 +152,8 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
+// Rows of k_gated_grad's workgroups.
+int grad_rows(int M) { return M >= 4096 ? 32 : 8; }
 struct GradLayout {
   size_t dg, du, sums, part, bytes;
 };
@@ -139,8 +163,8 @@ GradLayout grad_layout(const moe_gated_problem& p) {
   l.dg = 0;
   l.du = mi;
   l.sums = 2 * mi;
-  l.part = l.sums + up256((size_t)cdiv(p.M, kGradRows) * 2 * p.I * 4);
-  l.bytes = l.part;
+  l.part = l.sums + up256((size_t)cdiv(p.M, grad_rows(p.M)) * 2 * p.I * 4);
+  l.bytes = l.part + std::max(plan_of(DX, p.M, p.H, p.I).part, plan_of(DW, p.I, p.H, p.M).part);
   return l;
 }
 
@@ -184,10 +208,13 @@ LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
   l.tf = l.ends + up256((size_t)p.L * 4);
   l.t = l.tf + up256((size_t)rows * 4);
   l.part = l.t + up256((size_t)rows * 4 * p.R);
-  // the last part of a call may be its smallest, with the most ranges
+  // partial results of the first product, then of the second; the last part of a call may be its smallest, with the most ranges
   size_t part = 0;
   for (int64_t n : {(int64_t)rows, (int64_t)p.M % rows})
-    if (n && shrink_ranges(n, p.K) > 1) part = std::max(part, (size_t)shrink_ranges(n, p.K) * n * p.R * 4);
+    if (n) {
+      if (shrink_ranges(n, p.K) > 1) part = std::max(part, (size_t)shrink_ranges(n, p.K) * n * p.R * 4);
+      part = std::max(part, plan_of(LORA, n, p.N, p.K).part);
+    }
   l.bytes = l.part + up256(part);
   return l;
 }
@@ -224,8 +251,8 @@ extern "C" {
 
 size_t moe_gated_linear_workspace_bytes(const moe_gated_problem* p) {
   Gated g;
-  if (gated_sizes(p, g)) return 0;
-  return 0;
+  if (gated_sizes(p, g) || p->M <= kFewGated) return 0;
+  return plan_of(GATED, p->M, p->I, p->H).part;
 }
 
 int moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_gate, const void* w_up,
@@ -264,7 +291,7 @@ int moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_ga
   hipStream_t s = (hipStream_t)stream;
   return with_type16(p->type, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    return p->M <= kFewGated ? launch_rows<DT, GATED>(q, s) : launch<DT, GATED>(q, s);
+    return p->M <= kFewGated ? launch_rows<DT, GATED>(q, s) : launch<DT, GATED>(q, workspace, s);
   });
 }
 
@@ -317,8 +344,9 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.ld_up = g.ld_up;
   r.M = f.M;
   r.I = f.I;
+  r.rows = grad_rows(f.M);
   r.act = act_of(f);
-  const int blocks = (int)cdiv(f.M, kGradRows);
+  const int blocks = (int)cdiv(f.M, r.rows);
   Params q{};
   q.m[0] = (const uint16_t*)r.dg;
   q.m[1] = (const uint16_t*)r.du;
@@ -342,7 +370,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.M = f.M;
       d.N = f.H;
       d.K = f.I;
-      rc = launch<DT, DX>(d, s);
+      rc = launch<DT, DX>(d, ws + l.part, s);
     }
     if (!rc && dw_gate) {
       Params d = q;
@@ -357,7 +385,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.K = f.M;
       d.f32_out = f32;
       d.accumulate = p->accumulate;
-      rc = launch<DT, DW>(d, s);
+      rc = launch<DT, DW>(d, ws + l.part, s);
     }
     return rc;
   });
@@ -432,7 +460,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
                             (float*)(ws + l.tf), (float*)(ws + l.part), ldx, n, p->K, p->R, p->L};
       launch_shrink<DT>(sh, s);
       int rc = launch_status();
-      if (!rc) rc = launch<DT, LORA>(q, s);
+      if (!rc) rc = launch<DT, LORA>(q, ws + l.part, s);
       if (rc) return rc;
     }
     return (int)MOE_OK;

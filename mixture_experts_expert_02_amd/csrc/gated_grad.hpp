@@ -1,5 +1,5 @@
-// Row-wise steps of the gated block: gradients of its pre-activations, sums of
-// columns, and the join of partial products.
+// Row-wise steps of the gated block's backward pass: gradients of its
+// pre-activations and sums of columns.
 #pragma once
 
 #include "dense16.hpp"
@@ -12,13 +12,13 @@ namespace d16 {
 // many carries an error of the size of its own last rounding. With sums != nullptr the columns'
 // sums over this workgroup's rows as well, from the unrounded values.
 // Memory-bound: three reads and two writes of 16 bits a value.
-constexpr int kGradRows = 32;  // rows of a workgroup (64 columns of 8 values x 4 rows at a time)
 struct GradParams {
   const void *dout, *gate, *up;
   void *dg, *du;      // [M, I] contiguous
   float* sums;        // [row blocks][2][I] or nullptr
   int64_t ld_dout, ld_gate, ld_up;
   int32_t M, I;
+  int32_t rows;       // of a workgroup, a multiple of 4: 64 columns of 8 values x 4 rows at a time
   ActParams act;
 };
 
@@ -33,8 +33,8 @@ __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
   if (col < p.I) {
     with_act(p.act, [&](auto k) {
 #pragma unroll 2
-      for (int r = w; r < kGradRows; r += 4) {
-        const int64_t row = (int64_t)blockIdx.x * kGradRows + r;
+      for (int r = w; r < p.rows; r += 4) {
+        const int64_t row = (int64_t)blockIdx.x * p.rows + r;
         if (row >= p.M) break;
         float d[8], g[8], u[8];
         load8<DT>(p.dout, (size_t)(row * p.ld_dout + col), d);
@@ -80,48 +80,6 @@ __global__ __launch_bounds__(256) void k_column_sums(const float* sums, int bloc
   for (int b = 0; b < blocks; ++b) s += sums[((size_t)b * 2 + which) * I + c];
   float* dst = (which ? du : dg) + c;
   *dst = (float)(accumulate ? s + *dst : s);
-}
-
-// Partial products joined in the order of their K ranges, eight columns to a thread.
-template <int DT, int MODE>
-__global__ __launch_bounds__(256) void k_join(const Params p) {
-  const int cpr = p.N / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)p.M * cpr) return;
-  const int row = (int)(i / cpr), col = (int)(i - (int64_t)row * cpr) * 8;
-  const size_t mn = (size_t)p.M * p.N, at = (size_t)row * p.N + col;
-  float v[8], u[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    float a[8];
-    load8<T_FP32>(p.part + (MODE == GATED ? 2 : 1) * s * mn, at, a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += a[j];
-    if constexpr (MODE == GATED) {
-      load8<T_FP32>(p.part + (2 * s + 1) * mn, at, a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += a[j];
-    }
-  }
-  if constexpr (MODE == GATED) {
-    if (p.bias[0]) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] += p.bias[0][col + j];
-        u[j] += p.bias[1][col + j];
-      }
-    }
-    if (p.keep[0]) {
-      store8<DT>(p.keep[0], (size_t)(row * p.ld_keep[0] + col), v);
-      store8<DT>(p.keep[1], (size_t)(row * p.ld_keep[1] + col), u);
-    }
-    with_act(p.act, [&](auto k) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_f<decltype(k)::value>(p.act, v[j], u[j]);
-    });
-  }
-  store8<DT>(p.out[0], (size_t)(row * p.ldo[0] + col), v);
 }
 
 // Gradients of weights where there are no rows: zeros, eight columns to a thread.
