@@ -108,6 +108,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
 }
 
+// an address that is the same in all lanes, in scalar registers
+__device__ __forceinline__ const uint8_t* uniform(const void* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const uint8_t*)((uint64_t)hi << 32 | lo);
+}
+
 // 16 bytes to a lane, straight into LDS from dst on
 __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t rs, lds_u8* dst, uint32_t off, uint32_t uniform) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)dst, 16, (int)off, (int)uniform, 0, 0);
@@ -361,272 +368,6 @@ __global__ __launch_bounds__(256) void k_join(const Params p) {
     }
   }
   finish8<DT, MODE>(p, z, MODE == LORA ? p.perm[row] : row, col, v, u);
-}
-
-// ------------------------------------------------------------ tiles by four waves
-// BM x BN output tile (GATED: BN / 2 gate and the same up columns), waves 2 x 2.
-// NBUF stages in LDS: NBUF - 1 of them loading while one is multiplied.
-template <int DT, int MODE, int BM, int BN, int NBUF>
-__global__ __launch_bounds__(256) void k_tile(const Params p) {
-  constexpr bool MM = MODE == DW, NM = MODE == DX || MODE == DW;  // K-major operands
-  constexpr int FM = BM / 64, FN = BN / 64;                        // 32-wide fragments of a wave
-  constexpr int M_BYTES = BM * 128, STAGE = (BM + BN) * 128;
-  constexpr int LM = BM / 32, LN = BN / 32, LT = LM + LN;          // load instructions of a wave and stage
-  constexpr int COLS = FN * 32;
-  static_assert(4 * 32 * (COLS + 4) * 4 <= NBUF * STAGE, "epilogue strips");
-  __shared__ __attribute__((aligned(16))) uint8_t smem_arr[NBUF * STAGE];
-  __shared__ int rows_lds[MODE == LORA ? BM : 1];
-  lds_u8* smem = (lds_u8*)smem_arr;
-  Item it;
-  if (!item_of(p, MODE == DW ? 2 * p.splits : p.splits, it)) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1, lr = lane & 31, lk = lane >> 5;
-  constexpr int TN = MODE == GATED ? BN / 2 : BN;  // output columns of the tile
-  const int m0 = it.mt * BM, n0 = it.nt * TN;
-  const int z = MODE == DW ? it.z & 1 : 0, split = MODE == DW ? it.z >> 1 : it.z;
-
-  // stages of this workgroup's K range
-  const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;
-  const int s_lo = (int)((int64_t)split * all / p.splits), nst = (int)((int64_t)(split + 1) * all / p.splits) - s_lo;
-
-  if constexpr (MODE == LORA) {
-    for (int r = tid; r < BM; r += 256) rows_lds[r] = m0 + r < p.M ? p.perm[m0 + r] : 0;
-    __syncthreads();
-  }
-
-  // ---- loads of one stage
-  uint32_t m_row[LM];
-  int m_chunk[LM], n_rowi[LN], n_chunk[LN];
-#pragma unroll
-  for (int q = 0; q < LM; ++q) {
-    const int i = wave * LM + q;
-    if constexpr (MM) {
-      int k;
-      major_src<BM>(i, lane, k, m_chunk[q]);
-      m_row[q] = (uint32_t)k;
-    } else {
-      const int r = i * 8 + (lane >> 3);
-      m_chunk[q] = (lane & 7) ^ ((r >> 1) & 7);
-      m_row[q] = (uint32_t)r;
-      if constexpr (MODE == LORA) m_row[q] = m0 + r < p.M ? (uint32_t)rows_lds[r] : 0xffffffffu;
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < LN; ++q) {
-    const int i = wave * LN + q;
-    if constexpr (NM) {
-      major_src<BN>(i, lane, n_rowi[q], n_chunk[q]);
-    } else {
-      const int r = i * 8 + (lane >> 3);
-      n_chunk[q] = (lane & 7) ^ ((r >> 1) & 7);
-      n_rowi[q] = MODE == GATED ? r % TN : r;
-    }
-  }
-  auto load = [&](int st, int buf) {
-    const bool live = st < nst;
-    int s = s_lo + st, seg = 0;
-    if (MODE == DX && s >= kt) {
-      seg = 1;
-      s -= kt;
-    }
-    const int k0 = s * BK;
-    lds_u8* dst = smem + buf * STAGE;
-    {
-      const int mi = MODE == DX ? seg : MODE == DW ? z : 0;
-      const int64_t ld = p.ldm[mi];
-      if constexpr (MM) {
-        const auto rs = rsrc(p.m[mi] + (int64_t)k0 * ld + m0, live ? ((min(BK, p.K - k0) - 1) * ld + p.M - m0) * 2 : 0);
-#pragma unroll
-        for (int q = 0; q < LM; ++q)
-          dma(rs, dst + (wave * LM + q) * 1024, m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16, 0);
-      } else {
-        const int64_t base = MODE == LORA ? 0 : (int64_t)m0 * ld;
-        const int64_t rows = MODE == LORA ? (int64_t)1 << 30 : min(BM, p.M - m0);
-        const auto rs = rsrc(p.m[mi] + base, live ? ((rows - 1) * ld + p.K) * 2 : 0);
-#pragma unroll
-        for (int q = 0; q < LM; ++q) {
-          uint32_t off = m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16;
-          if (k0 + m_chunk[q] * 8 >= p.K || (MODE == LORA && m_row[q] == 0xffffffffu)) off = kNoLoad;
-          dma(rs, dst + (wave * LM + q) * 1024, off, k0 * 2);
-        }
-      }
-    }
-    dst += M_BYTES;
-    if constexpr (NM) {
-      const int64_t ld = p.ldn[seg];
-      const auto rs = rsrc(p.n[seg] + (int64_t)k0 * ld + n0, live ? ((min(BK, p.K - k0) - 1) * ld + p.N - n0) * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < LN; ++q)
-        dma(rs, dst + (wave * LN + q) * 1024, n_rowi[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16, 0);
-    } else {
-      // GATED: waves 0 and 1 load gate rows, 2 and 3 up rows
-      const int ni = MODE == GATED ? wave >> 1 : 0;
-      const int64_t ld = p.ldn[ni];
-      const auto rs = rsrc(p.n[ni] + (int64_t)n0 * ld, live ? ((min(TN, p.N - n0) - 1) * ld + p.K) * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < LN; ++q) {
-        uint32_t off = n_rowi[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16;
-        if (k0 + n_chunk[q] * 8 >= p.K) off = kNoLoad;
-        dma(rs, dst + (wave * LN + q) * 1024, off, k0 * 2);
-      }
-    }
-  };
-
-  // ---- operand reads: bytes inside a stage
-  auto m_col = [&](int j) { return wm * (BM / 2) + j * 32; };
-  auto n_col = [&](int i) { return MODE == GATED ? (i < FN / 2 ? 0 : TN) + wn * (TN / 2) + (i % (FN / 2)) * 32 : wn * (BN / 2) + i * 32; };
-  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-  const int tr = (lane >> 2) & 3;  // K row of a transposing read
-  auto major_at = [&](auto w, int col, int ks) {
-    constexpr int W = decltype(w)::value;
-    const int k = 16 * ks + 8 * lk + tr, cb = 2 * (col + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-    return (uint32_t)(k * 2 * W + (((cb >> 6) ^ major_xor<W>(k)) << 6) + (cb & 63));
-  };
-  auto m_at = [&](int j, int ks) {
-    if constexpr (MM) return major_at(std::integral_constant<int, BM>{}, m_col(j), ks);
-    else return 16 * row_slot(m_col(j) + lr, 2 * ks + lk);
-  };
-  auto n_at = [&](int i, int ks) {
-    if constexpr (NM) return major_at(std::integral_constant<int, BN>{}, n_col(i), ks);
-    else return 16 * row_slot(n_col(i) + lr, 2 * ks + lk);
-  };
-
-  f32x16 acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
-  Frag<MM> fm[2][FM];
-  Frag<NM> fn[2][FN];
-  auto read = [&](uint32_t at, int ks, int set) {
-#pragma unroll
-    for (int j = 0; j < FM; ++j) fm[set][j].read(at + m_at(j, ks), 4 * 2 * BM);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) fn[set][i].read(at + M_BYTES + n_at(i, ks), 4 * 2 * BN);
-  };
-  auto landed = [&](int set) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int j = 0; j < FM; ++j) fm[set][j].tie();
-#pragma unroll
-    for (int i = 0; i < FN; ++i) fn[set][i].tie();
-  };
-
-  // ---- adapters of this tile's rows, one after the other. Rows are sorted by adapter; a
-  // fragment that holds rows of several gets each one's product in registers
-  // of its own and adds it to the rows it belongs to, so that what an adapter
-  // holds (an infinity, say) reaches no other adapter's rows.
-  if constexpr (MODE == LORA) {
-    if (split == 0) {
-      int id[FM];
-      float f[FM];
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const int row = m0 + m_col(j) + lr;
-        id[j] = row < p.M ? p.sid[row] : p.L;
-        f[j] = row < p.M ? p.tf[row] : 0.f;
-      }
-      const int rc = p.R / 8, last = min(m0 + BM, p.M), rst = (2 * rc + 7) / 8;
-      const auto rs_t = rsrc(p.t + (int64_t)m0 * 2 * p.R, (int64_t)(last - m0) * 4 * p.R);
-      int pos = m0;
-      while (pos < last) {
-        const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
-        if (a >= p.L) break;
-        pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
-        const auto rs_b = rsrc(p.b + ((int64_t)a * p.N + n0) * p.R, (int64_t)min(BN, p.N - n0) * 2 * p.R);
-        for (int st0 = 0; st0 < rst; st0 += NBUF) {
-          const int some = min(NBUF, rst - st0);
-          for (int x = 0; x < some; ++x) {
-            lds_u8* dst = smem + x * STAGE;
-#pragma unroll
-            for (int q = 0; q < LM; ++q) {
-              const int r = (wave * LM + q) * 8 + (lane >> 3), v = (st0 + x) * 8 + m_chunk[q];
-              dma(rs_t, dst + (wave * LM + q) * 1024, v < 2 * rc ? (uint32_t)(r * 4 * p.R + v * 16) : kNoLoad, 0);
-            }
-#pragma unroll
-            for (int q = 0; q < LN; ++q) {
-              const int v = (st0 + x) * 8 + n_chunk[q];
-              dma(rs_b, dst + M_BYTES + (wave * LN + q) * 1024, v < 2 * rc ? (uint32_t)(n_rowi[q] * 2 * p.R + (v < rc ? v : v - rc) * 16) : kNoLoad, 0);
-            }
-          }
-          wait_loads<0>();
-          barrier();
-          for (int x = 0; x < some; ++x) {
-            f32x16 tmp[FN][FM];
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              read(lds0 + x * STAGE, ks, 0);
-              landed(0);
-#pragma unroll
-              for (int j = 0; j < FM; ++j)
-#pragma unroll
-                for (int i = 0; i < FN; ++i) {
-                  if (ks == 0) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) tmp[i][j][r] = 0.f;
-                  }
-                  tmp[i][j] = mfma<DT>(fn[0][i].get(), fm[0][j].get(), tmp[i][j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-              if (id[j] == a) {
-#pragma unroll
-                for (int i = 0; i < FN; ++i)
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) acc[i][j][r] += tmp[i][j][r] * f[j];
-              }
-          }
-          barrier();  // the buffers are free
-        }
-      }
-    }
-  }
-
-  // ---- main loop
-  if (nst > 0) {
-#pragma unroll
-    for (int s = 0; s < NBUF - 1; ++s) load(s, s);
-    int buf = 0;
-    for (int s = 0; s < nst; ++s) {
-      wait_loads<(NBUF - 2) * LT>();
-      barrier();  // stage s is there for all, and all have read stage s - 1
-      load(s + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
-      const uint32_t at = lds0 + buf * STAGE;
-      read(at, 0, 0);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        landed(ks & 1);
-        if (ks < 3) read(at, ks + 1, (ks + 1) & 1);
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int j = 0; j < FM; ++j) acc[i][j] = mfma<DT>(fn[ks & 1][i].get(), fm[ks & 1][j].get(), acc[i][j]);
-      }
-      buf = buf + 1 == NBUF ? 0 : buf + 1;
-    }
-    wait_loads<0>();
-    barrier();
-  }
-
-  float* strip = (float*)(smem_arr + wave * 32 * (COLS + 4) * 4);
-#pragma unroll
-  for (int j = 0; j < FM; ++j) {
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(f32x4*)(strip + lr * (COLS + 4) + i * 32 + 8 * q + 4 * lk) =
-            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    wave_sync();
-    store_rows<DT, MODE, COLS>(p, strip, z, split, m0 + m_col(j), n0 + (MODE == GATED ? wn * (TN / 2) : wn * (BN / 2)), lane,
-                               rows_lds + (MODE == LORA ? m_col(j) : 0));
-    wave_sync();
-  }
 }
 
 }  // namespace d16

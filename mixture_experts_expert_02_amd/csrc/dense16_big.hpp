@@ -71,55 +71,82 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       n_chunk[q] = c;
     }
   }
+  // Where each half's next stage begins: K value k of product seg, at the operand's row k (K-major) or its first row.
+  // Kept from stage to stage, in 32 bits where they suffice: 64-bit products and compares are the scalar unit's slowest.
+  struct Cursor {
+    const uint8_t* at;
+    int k, seg;
+  };
+  Cursor cm[2], cn[2];
+  const int seg0 = MODE == DX && s_lo >= kt ? 1 : 0, first_k = (s_lo - seg0 * kt) * BK;
+  const int mi0 = MODE == DX ? seg0 : z;
+  const uint32_t ldm2 = (uint32_t)(p.ldm[mi0] * 2), ldn2[2] = {(uint32_t)(p.ldn[0] * 2), (uint32_t)(p.ldn[1] * 2)};
+  const uint32_t m_step = __builtin_amdgcn_readfirstlane(ldm2 * BK);
+  const uint32_t n_step[2] = {(uint32_t)__builtin_amdgcn_readfirstlane(ldn2[0] * BK), (uint32_t)__builtin_amdgcn_readfirstlane(ldn2[1] * BK)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int ni = MODE == GATED ? h : seg0;
+    const int64_t m_at0 = MODE == LORA ? 0 : MM ? (int64_t)first_k * p.ldm[mi0] + m0 + h * HM : (int64_t)(m0 + h * HM) * p.ldm[mi0];
+    const int64_t n_at0 = NM ? (int64_t)first_k * p.ldn[ni] + n0 + h * 128 : (int64_t)(n0 + (MODE == GATED ? 0 : h * 32)) * p.ldn[ni];
+    cm[h] = {uniform(p.m[mi0] + m_at0), first_k, seg0};
+    cn[h] = {uniform(p.n[ni] + n_at0), first_k, seg0};
+  }
+  auto desc = [](const uint8_t* at, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), (short)0, bytes, 0x00020000);
+  };
   auto load_m = [&](int h, int st, int buf) {
+    Cursor& c = cm[h];
     const bool live = st < nst;
-    int s = s_lo + st, seg = 0;
-    if (MODE == DX && s >= kt) {
-      seg = 1;
-      s -= kt;
-    }
-    const int k0 = s * BK, mi = MODE == DX ? seg : z;
-    const int64_t ld = p.ldm[mi];
     lds_u8* dst = smem + (buf * 2 + h) * HALF_M + wave * LM * 1024;
     if constexpr (MM) {
-      const auto rs = rsrc(p.m[mi] + (int64_t)k0 * ld + m0 + h * HM, live ? ((min(BK, p.K - k0) - 1) * ld + p.M - m0 - h * HM) * 2 : 0);
+      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)ldm2 + (p.M - m0 - h * HM) * 2 : 0);
 #pragma unroll
-      for (int q = 0; q < LM; ++q) dma(rs, dst + q * 1024, m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16, 0);
+      for (int q = 0; q < LM; ++q) dma(rs, dst + q * 1024, __umul24(m_row[q], ldm2) + m_chunk[q] * 16, 0);
+      c.at += m_step;
+      c.k += BK;
     } else {
-      const auto rs = MODE == LORA ? rsrc(p.m[0], live ? 0x7fffffff : 0)
-                                   : rsrc(p.m[mi] + (int64_t)(m0 + h * HM) * ld,
-                                          live && p.M - m0 > h * HM ? ((min(HM, p.M - m0 - h * HM) - 1) * ld + p.K) * 2 : 0);
+      const int rows = min(HM, p.M - m0 - h * HM);
+      const auto rs = desc(c.at, !live ? 0 : MODE == LORA ? 0x7fffffff : rows > 0 ? (rows - 1) * (int)ldm2 + p.K * 2 : 0);
 #pragma unroll
       for (int q = 0; q < LM; ++q) {
-        uint32_t off = MODE == LORA ? g_off[h][q] : m_row[q] * (uint32_t)(ld * 2) + m_chunk[q] * 16;
-        if (k0 + m_chunk[q] * 8 >= p.K) off = kNoLoad;
-        dma(rs, dst + q * 1024, off, k0 * 2);
+        uint32_t off = MODE == LORA ? g_off[h][q] : __umul24(m_row[q], ldm2) + m_chunk[q] * 16;
+        if (c.k + m_chunk[q] * 8 >= p.K) off = kNoLoad;
+        dma(rs, dst + q * 1024, off, c.k * 2);
+      }
+      c.k += BK;
+      if (MODE == DX && c.k >= p.K && c.seg == 0) {
+        c.at += (const uint8_t*)p.m[1] - (const uint8_t*)p.m[0];
+        c.k = 0;
+        c.seg = 1;
       }
     }
   };
   auto load_n = [&](int h, int st, int buf) {
+    Cursor& c = cn[h];
     const bool live = st < nst;
-    int s = s_lo + st, seg = 0;
-    if (MODE == DX && s >= kt) {
-      seg = 1;
-      s -= kt;
-    }
-    const int k0 = s * BK, ni = MODE == GATED ? h : MODE == DX ? seg : 0;
-    const int64_t ld = p.ldn[ni];
     lds_u8* dst = smem + N_AT + (buf * 2 + h) * HALF + wave * 2048;
+    const uint32_t ld2 = MODE == GATED ? ldn2[h] : MODE == DX ? (c.seg ? ldn2[1] : ldn2[0]) : ldn2[0];
     if constexpr (NM) {
-      const auto rs = rsrc(p.n[ni] + (int64_t)k0 * ld + n0 + h * 128, live ? ((min(BK, p.K - k0) - 1) * ld + p.N - n0 - h * 128) * 2 : 0);
+      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)ld2 + (p.N - n0 - h * 128) * 2 : 0);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, n_row[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16, 0);
+      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, __umul24(n_row[q], ld2) + n_chunk[q] * 16, 0);
+      c.at += MODE == DX && c.seg ? n_step[1] : n_step[0];
+      c.k += BK;
+      if (MODE == DX && c.k >= p.K && c.seg == 0) {
+        c.at = (const uint8_t*)(p.n[1] + n0 + h * 128);
+        c.k = 0;
+        c.seg = 1;
+      }
     } else {
-      const int first = n0 + (MODE == GATED ? 0 : h * 32), rows = min(MODE == GATED ? 128 : 224, p.N - first);
-      const auto rs = rsrc(p.n[ni] + (int64_t)first * ld, live && rows > 0 ? ((rows - 1) * ld + p.K) * 2 : 0);
+      const int rows = min(MODE == GATED ? 128 : 224, p.N - n0 - (MODE == GATED ? 0 : h * 32));
+      const auto rs = desc(c.at, live && rows > 0 ? (rows - 1) * (int)ld2 + p.K * 2 : 0);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t off = n_row[q] * (uint32_t)(ld * 2) + n_chunk[q] * 16;
-        if (k0 + n_chunk[q] * 8 >= p.K) off = kNoLoad;
-        dma(rs, dst + q * 1024, off, k0 * 2);
+        uint32_t off = __umul24(n_row[q], ld2) + n_chunk[q] * 16;
+        if (c.k + n_chunk[q] * 8 >= p.K) off = kNoLoad;
+        dma(rs, dst + q * 1024, off, c.k * 2);
       }
+      c.k += BK;
     }
   };
 
@@ -161,6 +188,8 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 
   BigFrag<MM, HM> fm[2][J][4];  // [M half][32 rows][K step]
   BigFrag<NM, 128> fn[2][4];     // [set][K step]
+  BigFrag<MM, HM> gm[J == 1 ? 2 : 1][2][4];   // J = 1: [set][M half][K step]
+  BigFrag<NM, 128> gn[J == 1 ? 2 : 1][2][4];  // and [set][N half][K step]
 
   // fragment x (0 .. 4 J - 1) of an M half, (0..3) of an N half
 #define MOE_D16_READ_M(h, buf, x)                                                                                    \
@@ -290,52 +319,122 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #define MOE_D16_STAGE(st, B, C, X, Y)                                                                                \
   {                                                                                                                  \
     MOE_D16_PHASE(0, 0, X, MOE_D16_READ_N(Y, 1, B, 0), MOE_D16_READ_N(Y, 1, B, 1), MOE_D16_READ_N(Y, 1, B, 2),       \
-                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + NB, B), (NB - 1) * LS + LM + LN, tie_n(Y))            \
+                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + NB, B), 12, tie_n(Y))                                   \
     MOE_D16_PHASE(1, 0, Y, MOE_D16_READ_M2(1, B, 0), MOE_D16_READ_M2(1, B, 1), MOE_D16_READ_M2(1, B, 2),             \
-                  MOE_D16_READ_M2(1, B, 3), load_n(1, (st) + NB, B), (NB - 2) * LS + 2 * LM + 4 * LN, tie_m(1))      \
+                  MOE_D16_READ_M2(1, B, 3), load_n(1, (st) + NB, B), 12, tie_m(1))                                   \
     MOE_D16_PHASE(1, 1, Y, MOE_D16_READ_M2(0, C, 0), MOE_D16_READ_M2(0, C, 1), MOE_D16_READ_M2(0, C, 2),             \
-                  MOE_D16_READ_M2(0, C, 3), load_m(1, (st) + NB, B), (NB - 1) * LS + LM + LN, tie_m(0))              \
+                  MOE_D16_READ_M2(0, C, 3), load_m(1, (st) + NB, B), 12, tie_m(0))                                   \
     MOE_D16_PHASE(0, 1, X, MOE_D16_READ_N(Y, 0, C, 0), MOE_D16_READ_N(Y, 0, C, 1), MOE_D16_READ_N(Y, 0, C, 2),       \
-                  MOE_D16_READ_N(Y, 0, C, 3), load_m(0, (st) + 1 + NB, C), (NB - 1) * LS + 2 * LM, tie_n(Y))         \
+                  MOE_D16_READ_N(Y, 0, C, 3), load_m(0, (st) + 1 + NB, C), 12, tie_n(Y))                                 \
   }
-  if (nst > 0) {
+  if constexpr (J == 2) {
+    if (nst > 0) {
 #pragma unroll
-    for (int s = 0; s < NB; ++s) {
-      load_m(0, s, s);
-      load_n(0, s, s);
-      load_n(1, s, s);
-      load_m(1, s, s);
-    }
-    wait_loads<NB * LS - LM - LN>();
-    barrier();
-    MOE_D16_ALL_N(0)
-    MOE_D16_ALL_M(0)
-    wait_all_but<NB * LS - LM - 2 * LN>();
-    tie_n(0);
-    tie_m(0);
-    barrier();
-    load_m(0, NB, 0);
-    if constexpr (NB == 2) {
+      for (int s = 0; s < 2; ++s) {
+        load_m(0, s, s);
+        load_n(0, s, s);
+        load_n(1, s, s);
+        load_m(1, s, s);
+      }
+      wait_loads<12>();
+      barrier();
+      MOE_D16_ALL_N(0)
+      MOE_D16_ALL_M(0)
+      wait_all_but<10>();
+      tie_n(0);
+      tie_m(0);
+      barrier();
+      load_m(0, 2, 0);
       for (int s = 0; s < nst; s += 2) {
         MOE_D16_STAGE(s, 0, 1, 0, 1)
         if (s + 1 >= nst) break;
         MOE_D16_STAGE(s + 1, 1, 0, 1, 0)
       }
-    } else {
+    }
+  } else {
+    // A phase of 64 x 32 x 64 products by half as many MFMAs is over before its reads are done, so
+    // with 128 rows a stage is one phase: all of the next one's operands are read under its sixteen
+    // MFMAs, and the stage after the next but one loads into its buffer.
+#define MOE_D16_READ_G(set, B, x)                                                                                      \
+  {                                                                                                                    \
+    constexpr int k_ = (x) >> 2, h_ = (x) & 1;                                                                         \
+    if constexpr ((x) & 2) {                                                                                           \
+      if constexpr (NM) gn[set][h_][k_].template read<(((B) & 1) * 2 + h_) * HALF + k_ * 4096>(n_at[(B) >> 1][0]);      \
+      else gn[set][h_][k_].template read<(((B) & 1) * 2 + h_) * HALF>(n_at[(B) >> 1][k_]);                             \
+    } else {                                                                                                           \
+      if constexpr (MM) gm[set][h_][k_].template read<((B) * 2 + h_) * HALF_M + k_ * 32 * HM>(m_at[0]);                \
+      else gm[set][h_][k_].template read<((B) * 2 + h_) * HALF_M>(m_at[k_]);                                           \
+    }                                                                                                                  \
+  }
+#define MOE_D16_MFMA_G(set, x)                                                                                         \
+  {                                                                                                                    \
+    f32x16& c_ = acc[((x) >> 1) & 1][(x) & 1][0];                                                                      \
+    c_ = mfma<DT>(gn[set][((x) >> 1) & 1][(x) >> 2].get(), gm[set][(x) & 1][(x) >> 2].get(), c_);                       \
+  }
+#define MOE_D16_STEP_G(X, Y, C, x)                                                                                     \
+  MOE_D16_MFMA_G(X, x) MOE_D16_READ_G(Y, C, 2 * (x)) MOE_D16_READ_G(Y, C, 2 * (x) + 1) __builtin_amdgcn_sched_barrier(0);
+    auto tie_g = [&](int set) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          gm[set][h][ks].tie();
+          gn[set][h][ks].tie();
+        }
+    };
+#define MOE_D16_STAGE_G(st, B, C, X, Y)                                                                                \
+  {                                                                                                                    \
+    load_m(0, (st) + NB, B);                                                                                           \
+    load_n(0, (st) + NB, B);                                                                                           \
+    load_n(1, (st) + NB, B);                                                                                           \
+    load_m(1, (st) + NB, B);                                                                                           \
+    __builtin_amdgcn_sched_barrier(0);                                                                                 \
+    MOE_D16_STEP_G(X, Y, C, 0) MOE_D16_STEP_G(X, Y, C, 1) MOE_D16_STEP_G(X, Y, C, 2) MOE_D16_STEP_G(X, Y, C, 3)         \
+    MOE_D16_STEP_G(X, Y, C, 4) MOE_D16_STEP_G(X, Y, C, 5) MOE_D16_STEP_G(X, Y, C, 6) MOE_D16_STEP_G(X, Y, C, 7)         \
+    MOE_D16_MFMA_G(X, 8) MOE_D16_MFMA_G(X, 9) MOE_D16_MFMA_G(X, 10) MOE_D16_MFMA_G(X, 11)                              \
+    MOE_D16_MFMA_G(X, 12) MOE_D16_MFMA_G(X, 13) MOE_D16_MFMA_G(X, 14) MOE_D16_MFMA_G(X, 15)                            \
+    __builtin_amdgcn_sched_barrier(0);                                                                                 \
+    wait_all_but<LS>();                                                                                                \
+    tie_g(Y);                                                                                                          \
+    barrier();                                                                                                         \
+    __builtin_amdgcn_sched_barrier(0);                                                                                 \
+  }
+    if (nst > 0) {
+#pragma unroll
+      for (int s = 0; s < NB; ++s) {
+        load_m(0, s, s);
+        load_n(0, s, s);
+        load_n(1, s, s);
+        load_m(1, s, s);
+      }
+      wait_loads<2 * LS>();
+      barrier();
+#define MOE_D16_ALL_G(x) MOE_D16_READ_G(0, 0, x) MOE_D16_READ_G(0, 0, x + 1) MOE_D16_READ_G(0, 0, x + 2) MOE_D16_READ_G(0, 0, x + 3)
+      MOE_D16_ALL_G(0) MOE_D16_ALL_G(4) MOE_D16_ALL_G(8) MOE_D16_ALL_G(12)
+      wait_all_but<LS>();
+      tie_g(0);
+      barrier();
       for (int s = 0; s < nst; s += 6) {
-        MOE_D16_STAGE(s, 0, 1, 0, 1)
+        MOE_D16_STAGE_G(s, 0, 1, 0, 1)
         if (s + 1 >= nst) break;
-        MOE_D16_STAGE(s + 1, 1, 2, 1, 0)
+        MOE_D16_STAGE_G(s + 1, 1, 2, 1, 0)
         if (s + 2 >= nst) break;
-        MOE_D16_STAGE(s + 2, 2, 0, 0, 1)
+        MOE_D16_STAGE_G(s + 2, 2, 0, 0, 1)
         if (s + 3 >= nst) break;
-        MOE_D16_STAGE(s + 3, 0, 1, 1, 0)
+        MOE_D16_STAGE_G(s + 3, 0, 1, 1, 0)
         if (s + 4 >= nst) break;
-        MOE_D16_STAGE(s + 4, 1, 2, 0, 1)
+        MOE_D16_STAGE_G(s + 4, 1, 2, 0, 1)
         if (s + 5 >= nst) break;
-        MOE_D16_STAGE(s + 5, 2, 0, 1, 0)
+        MOE_D16_STAGE_G(s + 5, 2, 0, 1, 0)
       }
     }
+#undef MOE_D16_ALL_G
+#undef MOE_D16_STAGE_G
+#undef MOE_D16_STEP_G
+#undef MOE_D16_MFMA_G
+#undef MOE_D16_READ_G
+  }
+  if (nst > 0) {
     wait_loads<0>();
     barrier();
   }
