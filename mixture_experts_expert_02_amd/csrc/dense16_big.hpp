@@ -226,74 +226,67 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     for (int ks = 0; ks < 4; ++ks) fn[set][ks].tie();
   };
 
-  // ---- adapters of the tile's rows (see k_tile)
-  if constexpr (MODE == LORA) {
-    if (split == 0) {
-      int id[2][J];
-      float f[2][J];
+  // ---- adapters, a fragment of 32 sorted rows at a time, while the first stages load: both operands straight
+  // into registers (t and the factor's rows are as the MFMA wants them). A fragment that holds rows of
+  // several adapters gets each one's product in registers of its own and adds it to the rows it belongs to,
+  // so that what an adapter holds (an infinity, say) reaches no other adapter's rows.
+  auto adapters = [&]() {
+    u32x4 b[2][4];
+    int held = -1;  // whose factor b holds
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int hm = 0; hm < 2; ++hm)
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int row = m0 + h * HM + wm * (HM / 2) + j * 32 + lr;
-          id[h][j] = row < p.M ? p.sid[row] : p.L;
-          f[h][j] = row < p.M ? p.tf[row] : 0.f;
-        }
-      const int rc = p.R / 8, last = min(m0 + BM, p.M), rst = (2 * rc + 7) / 8;
-      const auto rs_t = rsrc(p.t + (int64_t)m0 * 2 * p.R, (int64_t)(last - m0) * 4 * p.R);
-      int pos = m0;
-      while (pos < last) {
-        const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
-        if (a >= p.L) break;
-        pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
-        const auto rs_b = rsrc(p.b + ((int64_t)a * p.N + n0) * p.R, (int64_t)min(TN, p.N - n0) * 2 * p.R);
-        for (int st = 0; st < rst; ++st) {
+      for (int j = 0; j < J; ++j) {
+        const int r0 = m0 + hm * HM + wm * (HM / 2) + j * 32, row = min(r0 + lr, p.M - 1), end = min(r0 + 32, p.M);
+        const int id = r0 + lr < p.M ? p.sid[row] : p.L;
+        const float f = p.tf[row];
+        const uint16_t* t = p.t + (int64_t)row * 2 * p.R;
+        int pos = r0;
+        while (pos < end) {
+          const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
+          if (a >= p.L) break;
+          pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
+          const bool mine = id == a;
+          for (int c0 = 0; c0 < p.R; c0 += 64) {
+            u32x4 hi[4], lo[4];
+            const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int ks = 0; ks < 4; ++ks) {
+              const int k = c0 + 16 * ks + 8 * lk;
+              hi[ks] = lo[ks] = zero;
+              if (k < p.R) {
+                hi[ks] = *(const u32x4*)(t + k);
+                lo[ks] = *(const u32x4*)(t + p.R + k);
+              }
+              if (held != a || p.R > 64) {
 #pragma unroll
-            for (int q = 0; q < LM; ++q) {
-              const int vm = st * 8 + m_chunk[q];
-              dma(rs_t, smem + h * HALF_M + (wave * LM + q) * 1024, vm < 2 * rc ? (uint32_t)((h * HM + m_row[q]) * 4 * p.R + vm * 16) : kNoLoad, 0);
-            }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int vn = st * 8 + n_chunk[q];
-              dma(rs_b, smem + N_AT + h * HALF + wave * 2048 + q * 1024,
-                  vn < 2 * rc ? (uint32_t)((h * 32 + n_row[q]) * 2 * p.R + (vn < rc ? vn : vn - rc) * 16) : kNoLoad, 0);
-            }
-          wait_loads<0>();
-          barrier();
-#pragma unroll
-          for (int hn = 0; hn < 2; ++hn) {
-            if (hn == 0) { MOE_D16_ALL_N(0) } else { MOE_D16_ALL_N(1) }
-#pragma unroll
-            for (int hm = 0; hm < 2; ++hm) {
-              if (hm == 0) { MOE_D16_ALL_M(0) } else { MOE_D16_ALL_M(1) }
-              asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-              tie_n(0);
-              tie_m(hm);
-#pragma unroll
-              for (int j = 0; j < J; ++j) {
-                if (!__any(id[hm][j] == a)) continue;
-                f32x16 tmp;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) tmp[r] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) tmp = mfma<DT>(fn[0][ks].get(), fm[hm][j][ks].get(), tmp);
-                if (id[hm][j] == a) {
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) acc[hn][hm][j][r] += tmp[r] * f[hm][j];
+                for (int hn = 0; hn < 2; ++hn) {
+                  const int col = n0 + wn * 64 + hn * 32 + lr;
+                  b[hn][ks] = zero;
+                  if (k < p.R && col < p.N) b[hn][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
                 }
               }
             }
+            held = a;
+#pragma unroll
+            for (int hn = 0; hn < 2; ++hn) {
+              f32x16 tmp;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) tmp[r] = 0.f;
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                tmp = mfma<DT>(b[hn][ks], hi[ks], tmp);
+                tmp = mfma<DT>(b[hn][ks], lo[ks], tmp);
+              }
+              if (mine) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[hn][hm][j][r] += tmp[r] * f;
+              }
+            }
           }
-          barrier();
         }
       }
-    }
-  }
+  };
 
   // ---- main loop
   // One phase: its MFMAs, a slot of READS behind each of the first four, the LOAD, and all loads but the LEFT youngest landed.
@@ -335,6 +328,9 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
         load_n(0, s, s);
         load_n(1, s, s);
         load_m(1, s, s);
+      }
+      if constexpr (MODE == LORA) {
+        if (split == 0) adapters();
       }
       wait_loads<12>();
       barrier();
@@ -406,6 +402,9 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
         load_n(0, s, s);
         load_n(1, s, s);
         load_m(1, s, s);
+      }
+      if constexpr (MODE == LORA) {
+        if (split == 0) adapters();
       }
       wait_loads<2 * LS>();
       barrier();

@@ -188,11 +188,12 @@ int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_
 int lora_rows(const moe_lora_problem& p, int64_t ldx) {
   return (int)std::min<int64_t>({(int64_t)p.M, (0x7fffffff - 2 * (int64_t)p.K) / (2 * ldx) / 256 * 256, (int64_t)1 << 20});
 }
-// K ranges of the first product: two workgroups to a compute unit, at least 16 steps of 32 to a range.
-int shrink_ranges(int64_t M, int K) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / cdiv(M, 16), cdiv(K, 32) / 16, 16}));
+// The first product: 16-row fragments of a workgroup, and K ranges: two workgroups to a compute unit, at least 16
+// steps of 32 to a range.
+int shrink_frags(int64_t M, int R) { return R <= 64 && M > 2048 ? 2 : 1; }
+int shrink_ranges(int64_t M, int K, int R) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / cdiv(M, 16 * shrink_frags(M, R)), cdiv(K, 32) / 16, 16}));
 }
-
 struct LoraLayout {
   size_t perm, sid, ends, tf, t, part, bytes;
 };
@@ -212,7 +213,7 @@ LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
   size_t part = 0;
   for (int64_t n : {(int64_t)rows, (int64_t)p.M % rows})
     if (n) {
-      if (shrink_ranges(n, p.K) > 1) part = std::max(part, (size_t)shrink_ranges(n, p.K) * n * p.R * 4);
+      if (shrink_ranges(n, p.K, p.R) > 1) part = std::max(part, (size_t)shrink_ranges(n, p.K, p.R) * n * p.R * 4);
       part = std::max(part, plan_of(LORA, n, p.N, p.K).part);
     }
   l.bytes = l.part + up256(part);
@@ -233,16 +234,37 @@ int lora_sizes(const moe_lora_problem* p, int64_t& ldx, int64_t& ldw, int64_t& l
                    check_ld(lda, p->N, 1, kMaxLdOut)});
 }
 
+template <int DT, int RF>
+void launch_shrink_of(const ShrinkParams& q, int ranges, hipStream_t s) {
+  if constexpr (RF <= 4) {
+    if (shrink_frags(q.M, q.R) == 2) {
+      hipLaunchKernelGGL((k_lora_shrink<DT, RF, 2>), dim3((unsigned)cdiv(q.M, 32), (unsigned)ranges), dim3(512), 0, s, q);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_lora_shrink<DT, RF, 1>), dim3((unsigned)cdiv(q.M, 16), (unsigned)ranges), dim3(512), 0, s, q);
+}
+
 template <int DT>
 void launch_shrink(const ShrinkParams& q, hipStream_t s) {
-  const int ranges = shrink_ranges(q.M, q.K);
-  const dim3 g((unsigned)cdiv(q.M, 16), (unsigned)ranges), b(512);
-  if (q.R <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), g, b, 0, s, q);
-  else if (q.R <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), g, b, 0, s, q);
-  else if (q.R <= 64) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), g, b, 0, s, q);
-  else if (q.R <= 128) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), g, b, 0, s, q);
-  else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), g, b, 0, s, q);
-  if (ranges > 1) hipLaunchKernelGGL((k_lora_finish<DT>), dim3((unsigned)cdiv(q.M, 4)), dim3(256), 0, s, q, ranges);
+  const int ranges = shrink_ranges(q.M, q.K, q.R);
+  if (q.R <= 16) launch_shrink_of<DT, 1>(q, ranges, s);
+  else if (q.R <= 32) launch_shrink_of<DT, 2>(q, ranges, s);
+  else if (q.R <= 64) launch_shrink_of<DT, 4>(q, ranges, s);
+  else if (q.R <= 128) launch_shrink_of<DT, 8>(q, ranges, s);
+  else launch_shrink_of<DT, 16>(q, ranges, s);
+  if (ranges == 1) return;
+  const dim3 g((unsigned)cdiv(q.M, 4)), b(256);
+  if (q.R <= 64) hipLaunchKernelGGL((k_lora_finish<DT, 1>), g, b, 0, s, q, ranges);
+  else if (q.R <= 128) hipLaunchKernelGGL((k_lora_finish<DT, 2>), g, b, 0, s, q, ranges);
+  else hipLaunchKernelGGL((k_lora_finish<DT, 4>), g, b, 0, s, q, ranges);
+}
+
+template <int DT>
+int launch_expand(const Params& q, hipStream_t s) {
+  const int frags = q.M >= 2048 ? 4 : 1;
+  hipLaunchKernelGGL((k_lora_expand<DT>), dim3((unsigned)cdiv(q.M, 16 * frags), (unsigned)cdiv(q.N, 256)), dim3(256), 0, s, q, frags);
+  return launch_status();
 }
 
 }  // namespace
@@ -460,7 +482,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
                             (float*)(ws + l.tf), (float*)(ws + l.part), ldx, n, p->K, p->R, p->L};
       launch_shrink<DT>(sh, s);
       int rc = launch_status();
-      if (!rc) rc = launch<DT, LORA>(q, ws + l.part, s);
+      if (!rc) rc = w ? launch<DT, LORA>(q, ws + l.part, s) : launch_expand<DT>(q, s);
       if (rc) return rc;
     }
     return (int)MOE_OK;

@@ -27,12 +27,13 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
   for (int i = tid; i <= p.L; i += 1024) at[i] = 0;
   __syncthreads();
   auto key = [&](int m) {
+    if (m >= p.M) return -1;
     const int a = p.ids[m];
     return a >= 0 && a < p.L ? a : p.L;
   };
-  // a wave whose rows share one adapter counts them at once
-  auto take = [&](int m, bool in) {
-    const int a = in ? key(m) : -1;
+  // one place for each lane with a key; a wave whose rows share one adapter counts them at once
+  auto take = [&](int a) {
+    const bool in = a >= 0;
     const uint64_t live = __ballot(in);
     const int first = __builtin_amdgcn_readfirstlane(a);
     const uint64_t same = __ballot(in && a == first);
@@ -45,8 +46,20 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
     }
     return place;
   };
-  const int steps = (p.M + 1023) / 1024;
-  for (int i = 0; i < steps; ++i) take(i * 1024 + tid, i * 1024 + tid < p.M);
+  // eight keys to a thread at a time, so that their loads overlap; the first 8192 rows' stay in registers
+  constexpr int KEYS = 8;
+  int keep[KEYS];
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) keep[i] = key(i * 1024 + tid);
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) take(keep[i]);
+  for (int m = KEYS * 1024; m < p.M; m += KEYS * 1024) {
+    int k[KEYS];
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) k[i] = key(m + i * 1024 + tid);
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) take(k[i]);
+  }
   __syncthreads();
   // exclusive running sum, five counters to a thread
   constexpr int PER = (kMaxAdapters + 1 + 1023) / 1024;
@@ -75,13 +88,20 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
     if (i < p.L) p.ends[i] = base;
   }
   __syncthreads();
-  for (int i = 0; i < steps; ++i) {
-    const int m = i * 1024 + tid;
-    const int place = take(m, m < p.M);
-    if (m < p.M) {
-      p.perm[place] = m;
-      p.sid[place] = key(m);
-    }
+  auto put = [&](int m, int a) {
+    const int place = take(a);
+    if (a < 0) return;
+    p.perm[place] = m;
+    p.sid[place] = a;
+  };
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) put(i * 1024 + tid, keep[i]);
+  for (int m = KEYS * 1024; m < p.M; m += KEYS * 1024) {
+    int k[KEYS];
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) k[i] = key(m + i * 1024 + tid);
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) put(m + i * 1024 + tid, k[i]);
   }
 }
 
@@ -129,45 +149,57 @@ __device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, uint16
   }
 }
 
-// 16 sorted rows to a workgroup (and a K range: blockIdx.y); its eight waves split K and join in LDS in wave order.
-// RF: fragments of 16 ranks.
-template <int DT, int RF>
+// 16 FX sorted rows to a workgroup (and a K range: blockIdx.y); its eight waves split K and join in LDS in wave
+// order. RF: fragments of 16 ranks.
+template <int DT, int RF, int FX>
 __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
-  constexpr int U = RF <= 2 ? 4 : RF == 4 ? 3 : RF == 8 ? 2 : 1;  // K steps whose loads are issued together
-  constexpr int RC = RF < 4 ? RF : 4;                             // fragments joined at a time
-  __shared__ float part[8][RC][16][17];
-  __shared__ float sum[RF * 16][17];
+  constexpr int ROWS = 16 * FX;
+  constexpr int U = RF + FX <= 4 ? 6 : RF + FX <= 6 ? 4 : RF + FX <= 10 ? 2 : 1;  // K steps whose loads are issued together
+  constexpr int RC = RF < 2 ? RF : 2;                                            // fragments joined at a time
+  __shared__ float part[8][RC][16][ROWS + 1];
+  __shared__ float sum[RF * 16][ROWS + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, kq = (lane >> 4) * 8;
-  const int m0 = blockIdx.x * 16, last = min(m0 + 16, p.M);
-  const int row = min(m0 + c, p.M - 1);
-  const int id = m0 + c < p.M ? p.sid[row] : p.L;
-  const uint16_t* xr = p.x + (int64_t)p.perm[row] * p.ldx;
+  const int m0 = blockIdx.x * ROWS, last = min(m0 + ROWS, p.M);
+  int id[FX];
+  const uint16_t* xr[FX];
+#pragma unroll
+  for (int j = 0; j < FX; ++j) {
+    const int row = min(m0 + j * 16 + c, p.M - 1);
+    id[j] = m0 + j * 16 + c < p.M ? p.sid[row] : p.L;
+    xr[j] = p.x + (int64_t)p.perm[row] * p.ldx;
+  }
   const int steps = (p.K + 31) / 32, nw = 8 * gridDim.y, w = blockIdx.y * 8 + wave;
   const int lo = (int)((int64_t)w * steps / nw), hi = (int)((int64_t)(w + 1) * steps / nw);
-  f32x4 acc[RF];
+  f32x4 acc[RF][FX];
 #pragma unroll
-  for (int i = 0; i < RF; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < RF; ++i)
+#pragma unroll
+    for (int j = 0; j < FX; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   int pos = m0;
   while (pos < last) {
     const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
     if (a >= p.L) break;
     pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
-    f32x4 tmp[RF];
+    f32x4 tmp[RF][FX];
     const uint16_t* ar[RF];
 #pragma unroll
     for (int i = 0; i < RF; ++i) {
-      tmp[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < FX; ++j) tmp[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       ar[i] = p.a + ((int64_t)a * p.R + min(i * 16 + c, p.R - 1)) * p.K;
     }
     for (int s = lo; s < hi; s += U) {
-      u32x4 xv[U], av[U][RF];
+      u32x4 xv[U][FX], av[U][RF];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = (s + u) * 32 + kq;
         const bool in = s + u < hi && k < p.K;
-        xv[u] = u32x4{0, 0, 0, 0};
-        if (in) xv[u] = *(const u32x4*)(xr + k);
+#pragma unroll
+        for (int j = 0; j < FX; ++j) {
+          xv[u][j] = u32x4{0, 0, 0, 0};
+          if (in) xv[u][j] = *(const u32x4*)(xr[j] + k);
+        }
 #pragma unroll
         for (int i = 0; i < RF; ++i) {
           av[u][i] = u32x4{0, 0, 0, 0};
@@ -177,24 +209,30 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < RF; ++i) tmp[i] = mfma16<DT>(av[u][i], xv[u], tmp[i]);
-    }
-    if (id == a) {
+        for (int i = 0; i < RF; ++i)
 #pragma unroll
-      for (int i = 0; i < RF; ++i) acc[i] = tmp[i];
+          for (int j = 0; j < FX; ++j) tmp[i][j] = mfma16<DT>(av[u][i], xv[u][j], tmp[i][j]);
     }
+#pragma unroll
+    for (int j = 0; j < FX; ++j)
+      if (id[j] == a) {
+#pragma unroll
+        for (int i = 0; i < RF; ++i) acc[i][j] = tmp[i][j];
+      }
   }
-  // rank 16 i + 4 (lane / 16) + q of row c
+  // rank 16 i + 4 (lane / 16) + q of row 16 j + c
 #pragma unroll
   for (int i0 = 0; i0 < RF; i0 += RC) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < RC; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) part[wave][i][4 * (lane >> 4) + q][c] = acc[i0 + i][q];
+      for (int j = 0; j < FX; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[wave][i][4 * (lane >> 4) + q][j * 16 + c] = acc[i0 + i][j][q];
     __syncthreads();
-    for (int x = tid; x < RC * 256; x += 512) {
-      const int i = x >> 8, r = (x >> 4) & 15, m = x & 15;
+    for (int x = tid; x < RC * 16 * ROWS; x += 512) {
+      const int i = x / (16 * ROWS), r = x / ROWS % 16, m = x % ROWS;
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < 8; ++v) s += part[v][i][r][m];
@@ -202,45 +240,43 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
     }
   }
   __syncthreads();
-  // 32 lanes to a row
-  const int m = tid >> 5, r0 = tid & 31;
+  // 512 / ROWS lanes to a row
+  constexpr int LANES = 512 / ROWS, N = (RF * 16 + LANES - 1) / LANES;
+  const int m = tid / LANES, r0 = tid % LANES;
   if (m0 + m >= p.M) return;
   const int a = p.sid[m0 + m];
-  constexpr int N = RF < 2 ? 1 : RF / 2;
   float v[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = r0 + 32 * i < p.R && a < p.L ? sum[min(r0 + 32 * i, RF * 16 - 1)][m] : 0.f;
+  for (int i = 0; i < N; ++i) v[i] = r0 + LANES * i < p.R && a < p.L ? sum[min(r0 + LANES * i, RF * 16 - 1)][m] : 0.f;
   if (gridDim.y > 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (r0 + 32 * i < p.R) p.part[((size_t)blockIdx.y * p.M + m0 + m) * p.R + r0 + 32 * i] = v[i];
+      if (r0 + LANES * i < p.R) p.part[((size_t)blockIdx.y * p.M + m0 + m) * p.R + r0 + LANES * i] = v[i];
     return;
   }
   const float sc = a < p.L ? p.scales[a] : 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] *= sc;
-  store_parts<DT, 32, N>(v, r0, p.R, p.t + (int64_t)(m0 + m) * 2 * p.R, p.tf + m0 + m);
+  store_parts<DT, LANES, N>(v, r0, p.R, p.t + (int64_t)(m0 + m) * 2 * p.R, p.tf + m0 + m);
 }
 
-// The K ranges' results joined in their order, a row to a wave.
-template <int DT>
+// The K ranges' results joined in their order, a row to a wave, N ranks to a lane.
+template <int DT, int N>
 __global__ __launch_bounds__(256) void k_lora_finish(const ShrinkParams p, int ranges) {
   const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (m >= p.M) return;
   const int a = p.sid[m];
   const float sc = a < p.L ? p.scales[a] : 0.f;
-  float v[kMaxRank / 64];
+  float v[N];
 #pragma unroll
-  for (int i = 0; i < kMaxRank / 64; ++i) v[i] = 0.f;
-  if (a < p.L) {
-    for (int k = 0; k < ranges; ++k)
-#pragma unroll
-      for (int i = 0; i < kMaxRank / 64; ++i)
-        if (lane + 64 * i < p.R) v[i] += p.part[((size_t)k * p.M + m) * p.R + lane + 64 * i];
-#pragma unroll
-    for (int i = 0; i < kMaxRank / 64; ++i) v[i] *= sc;
+  for (int i = 0; i < N; ++i) {
+    const int r = min(lane + 64 * i, p.R - 1);
+    float s = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < ranges; ++k) s += p.part[((size_t)k * p.M + m) * p.R + r];
+    v[i] = a < p.L && lane + 64 * i < p.R ? s * sc : 0.f;
   }
-  store_parts<DT, 64, kMaxRank / 64>(v, lane, p.R, p.t + (int64_t)m * 2 * p.R, p.tf + m);
+  store_parts<DT, 64, N>(v, lane, p.R, p.t + (int64_t)m * 2 * p.R, p.tf + m);
 }
 
 // Few rows: row blockIdx.x's products with eight ranks of its adapter, two to a wave, in float32, scaled;
@@ -271,6 +307,100 @@ __global__ __launch_bounds__(256) void k_lora_shrink_few(const ShrinkParams p) {
     s1 += __shfl_xor(s1, d);
   }
   if (lane < 2) p.tf[(int64_t)m * p.R + r + lane] = (lane ? s1 : s0) * p.scales[a];
+}
+
+// The adapters' part alone (no projection): out = bias + add + f_m (t_m B_a^T). A workgroup owns 16 `frags` sorted rows
+// and 256 columns, 64 to a wave; both operands go straight into registers in the MFMA's layout, the factor's
+// rows once for all fragments of the same adapter. Bound by the factors' and outputs' bytes.
+template <int DT>
+__global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int col0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
+  if (col0 >= p.N) return;
+  u32x4 b[4][2];
+  int held = -1;
+  for (int x = 0; x < frags; ++x) {
+    const int r0 = (blockIdx.x * frags + x) * 16, end = min(r0 + 16, p.M);
+    if (r0 >= p.M) return;
+    const int row = min(r0 + c, p.M - 1);
+    const int id = p.sid[row];
+    const float f = p.tf[row];
+    const uint16_t* t = p.t + (int64_t)row * 2 * p.R;
+    f32x4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int pos = r0;
+    while (pos < end) {
+      const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
+      if (a >= p.L) break;
+      pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
+      for (int c0 = 0; c0 < p.R; c0 += 64) {
+        u32x4 hi[2], lo[2];
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const int k = c0 + 32 * ks + 8 * g;
+          hi[ks] = lo[ks] = zero;
+          if (k < p.R) {
+            hi[ks] = *(const u32x4*)(t + k);
+            lo[ks] = *(const u32x4*)(t + p.R + k);
+          }
+          if (held != a || p.R > 64) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = col0 + i * 16 + c;
+              b[i][ks] = zero;
+              if (k < p.R && col < p.N) b[i][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
+            }
+          }
+        }
+        held = a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f32x4 tmp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            tmp = mfma16<DT>(b[i][ks], hi[ks], tmp);
+            tmp = mfma16<DT>(b[i][ks], lo[ks], tmp);
+          }
+          if (id == a) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][q] += tmp[q] * f;
+          }
+        }
+      }
+    }
+    if (r0 + c >= p.M) continue;
+    const int64_t orow = p.perm[row];
+    uint16_t* out = (uint16_t*)p.out[0] + orow * p.ldo[0];
+    const uint16_t* add = p.add ? (const uint16_t*)p.add + orow * p.ld_add : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = col0 + i * 16 + 4 * g;  // four neighbours
+      if (p.vec && col + 4 <= p.N) {
+        uint2 old = {0, 0}, res;
+        if (add) old = *(const uint2*)(add + col);
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = acc[i][q] + (p.bias[0] ? p.bias[0][col + q] : 0.f);
+        if (add) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += load1<DT>(&old, q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) store1<DT>(&res, q, v[q]);
+        *(uint2*)(out + col) = res;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (col + q >= p.N) break;
+          float v = acc[i][q] + (p.bias[0] ? p.bias[0][col + q] : 0.f);
+          if (add) v += load1<DT>(add, col + q);
+          store1<DT>(out, col + q, v);
+        }
+      }
+    }
+  }
 }
 
 }  // namespace d16
