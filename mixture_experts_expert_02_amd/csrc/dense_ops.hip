@@ -152,8 +152,8 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
-// Rows of k_gated_grad's workgroups.
-int grad_rows(int M) { return M >= 4096 ? 32 : 8; }
+// Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
+int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
   size_t dg, du, sums, part, bytes;
 };
@@ -188,11 +188,12 @@ int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_
 int lora_rows(const moe_lora_problem& p, int64_t ldx) {
   return (int)std::min<int64_t>({(int64_t)p.M, (0x7fffffff - 2 * (int64_t)p.K) / (2 * ldx) / 256 * 256, (int64_t)1 << 20});
 }
-// The first product: 16-row fragments of a workgroup, and K ranges: two workgroups to a compute unit, at least 16
-// steps of 32 to a range.
+// The first product: 16-row fragments of a workgroup, and K ranges: at most one workgroup to a compute unit (us of the
+// kernel: 1000 rows of 4096, rank 24, 64 adapters 31, 17, 8.7, 12.5 and 17 with 1, 2, 4, 8 and 16 ranges; 256 of 7168,
+// rank 64, 34, 19, 11.6, 7.6 and 6.0; 8192 of 2048 18.6, 21 and 28 with 1, 2 and 4), at least 16 steps of 32 to a range.
 int shrink_frags(int64_t M, int R) { return R <= 64 && M > 2048 ? 2 : 1; }
 int shrink_ranges(int64_t M, int K, int R) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / cdiv(M, 16 * shrink_frags(M, R)), cdiv(K, 32) / 16, 16}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({256 / cdiv(M, 16 * shrink_frags(M, R)), cdiv(K, 32) / 16, 16}));
 }
 struct LoraLayout {
   size_t perm, sid, ends, tf, t, part, bytes;
@@ -361,6 +362,9 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.dg = ws + l.dg;
   r.du = ws + l.du;
   r.sums = dbias_gate ? (float*)(ws + l.sums) : nullptr;
+  r.dbias[0] = dbias_gate;
+  r.dbias[1] = dbias_up;
+  r.accumulate = p->accumulate;
   r.ld_dout = g.ld_out;
   r.ld_gate = g.ld_gate;
   r.ld_up = g.ld_up;
@@ -376,8 +380,8 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   q.splits = 1;
   return with_type16(f.type, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    hipLaunchKernelGGL((k_gated_grad<DT>), dim3((unsigned)blocks, (unsigned)cdiv(f.I, 512)), dim3(256), 0, s, r);
-    if (dbias_gate)
+    hipLaunchKernelGGL((k_gated_grad<DT>), dim3((unsigned)blocks, (unsigned)cdiv(f.I, 64)), dim3(256), 0, s, r);
+    if (dbias_gate && blocks > 1)
       hipLaunchKernelGGL(k_column_sums, dim3((unsigned)cdiv(f.I, 256), 2), dim3(256), 0, s, (const float*)r.sums, blocks, f.I,
                          dbias_gate, dbias_up, p->accumulate);
     int rc = launch_status();

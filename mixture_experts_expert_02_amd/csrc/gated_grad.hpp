@@ -10,30 +10,33 @@ namespace d16 {
 // dg = dout f_g(g, u), du = dout f_u(g, u), rounded to the type: the matrix
 // instruction takes 16-bit operands, and each rounding is off by half a step of its own value, so a sum of
 // many carries an error of the size of its own last rounding. With sums != nullptr the columns'
-// sums over this workgroup's rows as well, from the unrounded values.
-// Memory-bound: three reads and two writes of 16 bits a value.
+// sums over this workgroup's rows as well, from the unrounded values: to their place where one workgroup
+// has all rows, else for k_column_sums.
+// Memory-bound: three reads and two writes of 16 bits a value. 64 columns to a workgroup, whole lines of 32 rows at a time.
 struct GradParams {
   const void *dout, *gate, *up;
   void *dg, *du;      // [M, I] contiguous
   float* sums;        // [row blocks][2][I] or nullptr
+  float* dbias[2];    // [I]
   int64_t ld_dout, ld_gate, ld_up;
   int32_t M, I;
-  int32_t rows;       // of a workgroup, a multiple of 4: 64 columns of 8 values x 4 rows at a time
+  int32_t rows;       // of a workgroup, a multiple of 32
+  int32_t accumulate;
   ActParams act;
 };
 
 template <int DT>
 __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
-  __shared__ float part[2][4][64][8 + 1];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int col = (blockIdx.y * 64 + lane) * 8;
+  __shared__ float part[2][32][64 + 1];
+  const int c8 = (threadIdx.x & 7) * 8, r0 = threadIdx.x >> 3;
+  const int col = blockIdx.y * 64 + c8;
   float sg[8], su[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.f;
   if (col < p.I) {
     with_act(p.act, [&](auto k) {
 #pragma unroll 2
-      for (int r = w; r < p.rows; r += 4) {
+      for (int r = r0; r < p.rows; r += 32) {
         const int64_t row = (int64_t)blockIdx.x * p.rows + r;
         if (row >= p.M) break;
         float d[8], g[8], u[8];
@@ -57,19 +60,17 @@ __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
   if (!p.sums) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    part[0][w][lane][j] = sg[j];
-    part[1][w][lane][j] = su[j];
+    part[0][r0][c8 + j] = sg[j];
+    part[1][r0][c8 + j] = su[j];
   }
   __syncthreads();
-  // 1024 sums, four to a thread: which, column
-  for (int i = threadIdx.x; i < 1024; i += 256) {
-    const int which = i >> 9, c = i & 511, at = blockIdx.y * 512 + c;
-    if (at >= p.I) continue;
-    float s = 0.f;
+  const int which = threadIdx.x >> 6, c = threadIdx.x & 63, at = blockIdx.y * 64 + c;
+  if (which > 1 || at >= p.I) return;
+  float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s += part[which][q][c >> 3][c & 7];
-    p.sums[((size_t)blockIdx.x * 2 + which) * p.I + at] = s;
-  }
+  for (int q = 0; q < 32; ++q) s += part[which][q][c];
+  if (gridDim.x == 1) p.dbias[which][at] = p.accumulate ? p.dbias[which][at] + s : s;
+  else p.sums[((size_t)blockIdx.x * 2 + which) * p.I + at] = s;
 }
 
 // dst[which][c] (+)= sum over blocks of sums[block][which][c], in the blocks' order
