@@ -186,40 +186,33 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[a][b][j][r] = 0.f;
 
-  BigFrag<MM, HM> fm[2][J][4];  // [M half][32 rows][K step]
-  BigFrag<NM, 128> fn[2][4];     // [set][K step]
-  BigFrag<MM, HM> gm[J == 1 ? 2 : 1][2][4];   // J = 1: [set][M half][K step]
-  BigFrag<NM, 128> gn[J == 1 ? 2 : 1][2][4];  // and [set][N half][K step]
+  BigFrag<MM, HM> fm[J][4];   // 256 rows: an M half's [32 rows][K step]
+  BigFrag<NM, 128> fn[3][4];  // and N halves' [set][K step]
+  BigFrag<MM, HM> gm[2][2];   // 128 rows: [M half][K step of a pair]
+  BigFrag<NM, 128> gn[2][2];  // and [N half][K step]
 
-  // fragment x (0 .. 4 J - 1) of an M half, (0..3) of an N half
-#define MOE_D16_READ_M(h, buf, x)                                                                                    \
-  {                                                                                                                  \
-    constexpr int j_ = (x) % J, k_ = (x) / J;                                                                        \
-    if constexpr (MM) fm[h][j_][k_].template read<((buf) * 2 + (h)) * HALF_M + k_ * 32 * HM>(m_at[j_]);               \
-    else fm[h][j_][k_].template read<((buf) * 2 + (h)) * HALF_M + j_ * 4096>(m_at[k_]);                              \
+  // fragment x (0..7) of an M half, (0..3) of an N half
+#define MOE_D16_READ_M(h, buf, x)                                                                             \
+  {                                                                                                           \
+    constexpr int j_ = (x) % J, k_ = (x) / J;                                                                 \
+    if constexpr (MM) fm[j_][k_].template read<((buf) * 2 + (h)) * HALF_M + k_ * 32 * HM>(m_at[j_]);          \
+    else fm[j_][k_].template read<((buf) * 2 + (h)) * HALF_M + j_ * 4096>(m_at[k_]);                         \
   }
-#define MOE_D16_READ_N(set, h, buf, x)                                                                               \
-  {                                                                                                                  \
-    if constexpr (NM) fn[set][x].template read<(((buf) & 1) * 2 + (h)) * HALF + (x) * 4096>(n_at[(buf) >> 1][0]);     \
-    else fn[set][x].template read<(((buf) & 1) * 2 + (h)) * HALF>(n_at[(buf) >> 1][x]);                              \
+#define MOE_D16_READ_N(set, h, buf, x)                                                                        \
+  {                                                                                                           \
+    if constexpr (NM) fn[set][x].template read<((buf) * 2 + (h)) * HALF + (x) * 4096>(n_at[0][0]);            \
+    else fn[set][x].template read<((buf) * 2 + (h)) * HALF>(n_at[0][x]);                                      \
   }
-// two of an M half's reads in one slot (of four slots) where there are eight
-#define MOE_D16_READ_M2(h, buf, s)                                          \
-  {                                                                         \
-    if constexpr (J == 2) {                                                 \
-      MOE_D16_READ_M(h, buf, 2 * (s)) MOE_D16_READ_M(h, buf, 2 * (s) + 1)   \
-    } else MOE_D16_READ_M(h, buf, s)                                        \
-  }
-#define MOE_D16_ALL_N(h) \
-  MOE_D16_READ_N(0, h, 0, 0) MOE_D16_READ_N(0, h, 0, 1) MOE_D16_READ_N(0, h, 0, 2) MOE_D16_READ_N(0, h, 0, 3)
-#define MOE_D16_ALL_M(h) MOE_D16_READ_M2(h, 0, 0) MOE_D16_READ_M2(h, 0, 1) MOE_D16_READ_M2(h, 0, 2) MOE_D16_READ_M2(h, 0, 3)
-#define MOE_D16_MFMA(hn, hm, set, x) \
-  if constexpr ((x) < 4 * J) acc[hn][hm][(x) % J] = mfma<DT>(fn[set][(x) / J % 4].get(), fm[hm][(x) % J][(x) / J % 4].get(), acc[hn][hm][(x) % J]);
-  auto tie_m = [&](int h) {
+#define MOE_D16_ALL_M(h, buf)                                                                                 \
+  MOE_D16_READ_M(h, buf, 0) MOE_D16_READ_M(h, buf, 1) MOE_D16_READ_M(h, buf, 2) MOE_D16_READ_M(h, buf, 3)     \
+  MOE_D16_READ_M(h, buf, 4) MOE_D16_READ_M(h, buf, 5) MOE_D16_READ_M(h, buf, 6) MOE_D16_READ_M(h, buf, 7)
+#define MOE_D16_ALL_N(set, h, buf) \
+  MOE_D16_READ_N(set, h, buf, 0) MOE_D16_READ_N(set, h, buf, 1) MOE_D16_READ_N(set, h, buf, 2) MOE_D16_READ_N(set, h, buf, 3)
+  auto tie_m = [&]() {
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) fm[h][j][ks].tie();
+      for (int ks = 0; ks < 4; ++ks) fm[j][ks].tie();
   };
   auto tie_n = [&](int set) {
 #pragma unroll
@@ -289,39 +282,87 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   };
 
   // ---- main loop
-  // One phase: its MFMAs, a slot of READS behind each of the first four, the LOAD, and all loads but the LEFT youngest landed.
-#define MOE_D16_PHASE(hn, hm, set, R0, R1, R2, R3, LOAD, LEFT, TIE)      \
-  {                                                                      \
-    MOE_D16_MFMA(hn, hm, set, 0) R0 __builtin_amdgcn_sched_barrier(0);   \
-    MOE_D16_MFMA(hn, hm, set, 1) R1 __builtin_amdgcn_sched_barrier(0);   \
-    MOE_D16_MFMA(hn, hm, set, 2) R2 __builtin_amdgcn_sched_barrier(0);   \
-    MOE_D16_MFMA(hn, hm, set, 3) R3 __builtin_amdgcn_sched_barrier(0);   \
-    MOE_D16_MFMA(hn, hm, set, 4) LOAD;                                   \
-    __builtin_amdgcn_sched_barrier(0);                                   \
-    MOE_D16_MFMA(hn, hm, set, 5)                                         \
-    MOE_D16_MFMA(hn, hm, set, 6)                                         \
-    MOE_D16_MFMA(hn, hm, set, 7)                                         \
-    __builtin_amdgcn_sched_barrier(0);                                   \
-    wait_all_but<LEFT>();                                                \
-    TIE;                                                                 \
-    barrier();                                                           \
-    __builtin_amdgcn_sched_barrier(0);                                   \
+  // The two waves of a SIMD (wm = 0 and 1) work half a phase apart: while one multiplies, the other reads the operands
+  // of its next phase and starts a half's loads, and a barrier ends each turn. Waves with wm = 1 begin one
+  // barrier later and end one earlier. Before the barrier behind its reads a wave has them all, and those of its loads
+  // have landed that the next phase's reads need.
+#define MOE_D16_PHASE(hn, hm, set, READS, LOAD, LEFT, TIE)                                             \
+  {                                                                                                    \
+    READS;                                                                                             \
+    LOAD;                                                                                              \
+    wait_all_but<LEFT>();                                                                              \
+    TIE;                                                                                               \
+    barrier();                                                                                         \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
+    __builtin_amdgcn_s_setprio(1);                                                                     \
+    _Pragma("unroll") for (int x = 0; x < 8; ++x) acc[hn][hm][x % J] =                                 \
+        mfma<DT>(fn[set][x / J % 4].get(), fm[x % J][x / J % 4].get(), acc[hn][hm][x % J]);            \
+    __builtin_amdgcn_s_setprio(0);                                                                     \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
+    barrier();                                                                                         \
   }
-  // Stage st in buffer B (the next one's: C): N half 0 in set X, half 1 comes into set Y, which the next stage's
-  // half 0 takes over.
-#define MOE_D16_STAGE(st, B, C, X, Y)                                                                                \
-  {                                                                                                                  \
-    MOE_D16_PHASE(0, 0, X, MOE_D16_READ_N(Y, 1, B, 0), MOE_D16_READ_N(Y, 1, B, 1), MOE_D16_READ_N(Y, 1, B, 2),       \
-                  MOE_D16_READ_N(Y, 1, B, 3), load_n(0, (st) + NB, B), 12, tie_n(Y))                                   \
-    MOE_D16_PHASE(1, 0, Y, MOE_D16_READ_M2(1, B, 0), MOE_D16_READ_M2(1, B, 1), MOE_D16_READ_M2(1, B, 2),             \
-                  MOE_D16_READ_M2(1, B, 3), load_n(1, (st) + NB, B), 12, tie_m(1))                                   \
-    MOE_D16_PHASE(1, 1, Y, MOE_D16_READ_M2(0, C, 0), MOE_D16_READ_M2(0, C, 1), MOE_D16_READ_M2(0, C, 2),             \
-                  MOE_D16_READ_M2(0, C, 3), load_m(1, (st) + NB, B), 12, tie_m(0))                                   \
-    MOE_D16_PHASE(0, 1, X, MOE_D16_READ_N(Y, 0, C, 0), MOE_D16_READ_N(Y, 0, C, 1), MOE_D16_READ_N(Y, 0, C, 2),       \
-                  MOE_D16_READ_N(Y, 0, C, 3), load_m(0, (st) + 1 + NB, C), 12, tie_n(Y))                                 \
+  // Stage st in buffer B: its N half 0 is in set X already, the next stage's comes into set Y. Every half is
+  // loaded for the stage after the next in the phase behind the one that read it.
+#define MOE_D16_STAGE(st, B, X, Y)                                                                     \
+  {                                                                                                    \
+    MOE_D16_PHASE(0, 0, X, MOE_D16_ALL_M(0, B), load_n(0, (st) + 2, B), 12, tie_m())                   \
+    MOE_D16_PHASE(1, 0, 2, MOE_D16_ALL_N(2, 1, B), load_m(0, (st) + 2, B), 12, tie_n(2))               \
+    MOE_D16_PHASE(1, 1, 2, MOE_D16_ALL_M(1, B), load_n(1, (st) + 2, B), 12, tie_m())                   \
+    MOE_D16_PHASE(0, 1, X, MOE_D16_ALL_N(Y, 0, 1 - B), load_m(1, (st) + 2, B), 12, tie_n(Y))           \
   }
-  if constexpr (J == 2) {
-    if (nst > 0) {
+  // 128 rows: a phase is all four blocks of two K steps, and a buffer is loaded anew, for the stage after the next
+  // but one, in the two phases behind its last read.
+#define MOE_D16_READ_P(B, p_)                                                                          \
+  _Pragma("unroll") for (int x = 0; x < 2; ++x) {                                                      \
+    if constexpr (MM) {                                                                                \
+      if (x == 0) { gm[0][0].template read<(B) * 2 * HALF_M + (2 * (p_)) * 32 * HM>(m_at[0]); gm[1][0].template read<((B) * 2 + 1) * HALF_M + (2 * (p_)) * 32 * HM>(m_at[0]); } \
+      else { gm[0][1].template read<(B) * 2 * HALF_M + (2 * (p_) + 1) * 32 * HM>(m_at[0]); gm[1][1].template read<((B) * 2 + 1) * HALF_M + (2 * (p_) + 1) * 32 * HM>(m_at[0]); } \
+    } else {                                                                                           \
+      gm[0][x].template read<(B) * 2 * HALF_M>(m_at[(2 * (p_) + x) % 4]);                                    \
+      gm[1][x].template read<((B) * 2 + 1) * HALF_M>(m_at[(2 * (p_) + x) % 4]);                              \
+    }                                                                                                  \
+    if constexpr (NM) {                                                                                \
+      if (x == 0) { gn[0][0].template read<((B) & 1) * 2 * HALF + (2 * (p_)) * 4096>(n_at[(B) >> 1][0]); gn[1][0].template read<(((B) & 1) * 2 + 1) * HALF + (2 * (p_)) * 4096>(n_at[(B) >> 1][0]); } \
+      else { gn[0][1].template read<((B) & 1) * 2 * HALF + (2 * (p_) + 1) * 4096>(n_at[(B) >> 1][0]); gn[1][1].template read<(((B) & 1) * 2 + 1) * HALF + (2 * (p_) + 1) * 4096>(n_at[(B) >> 1][0]); } \
+    } else {                                                                                           \
+      gn[0][x].template read<((B) & 1) * 2 * HALF>(n_at[(B) >> 1][(2 * (p_) + x) % 4]);                      \
+      gn[1][x].template read<(((B) & 1) * 2 + 1) * HALF>(n_at[(B) >> 1][(2 * (p_) + x) % 4]);                \
+    }                                                                                                  \
+  }
+#define MOE_D16_PHASE_P(B, p_, LOAD, LEFT)                                                             \
+  {                                                                                                    \
+    MOE_D16_READ_P(B, p_)                                                                              \
+    LOAD;                                                                                              \
+    wait_all_but<LEFT>();                                                                              \
+    _Pragma("unroll") for (int x = 0; x < 4; ++x) {                                                    \
+      gm[x >> 1][x & 1].tie();                                                                         \
+      gn[x >> 1][x & 1].tie();                                                                         \
+    }                                                                                                  \
+    barrier();                                                                                         \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
+    __builtin_amdgcn_s_setprio(1);                                                                     \
+    _Pragma("unroll") for (int x = 0; x < 8; ++x) acc[(x >> 1) & 1][x & 1][0] =                        \
+        mfma<DT>(gn[(x >> 1) & 1][x >> 2].get(), gm[x & 1][x >> 2].get(), acc[(x >> 1) & 1][x & 1][0]); \
+    __builtin_amdgcn_s_setprio(0);                                                                     \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
+    barrier();                                                                                         \
+  }
+  // stage st in buffer B, the last one read in buffer A
+#define MOE_D16_STAGE_P(st, B, A)                                                                      \
+  {                                                                                                    \
+    MOE_D16_PHASE_P(B, 0, { load_m(0, (st) + 2, A); load_n(0, (st) + 2, A); }, 9)                      \
+    MOE_D16_PHASE_P(B, 1, { load_n(1, (st) + 2, A); load_m(1, (st) + 2, A); }, 6)                      \
+  }
+  if (nst > 0) {
+    if constexpr (J == 2) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        load_n(0, s, s);
+        load_m(0, s, s);
+        load_n(1, s, s);
+        load_m(1, s, s);
+      }
+    } else {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         load_m(0, s, s);
@@ -329,114 +370,42 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
         load_n(1, s, s);
         load_m(1, s, s);
       }
-      if constexpr (MODE == LORA) {
-        if (split == 0) adapters();
-      }
+    }
+    if constexpr (MODE == LORA) {
+      if (split == 0) adapters();
+    }
+    if constexpr (J == 2) {
       wait_loads<12>();
       barrier();
-      MOE_D16_ALL_N(0)
-      MOE_D16_ALL_M(0)
-      wait_all_but<10>();
+      MOE_D16_ALL_N(0, 0, 0)
+      wait_all_but<12>();
       tie_n(0);
-      tie_m(0);
       barrier();
-      load_m(0, 2, 0);
+      if (wm) barrier();
       for (int s = 0; s < nst; s += 2) {
-        MOE_D16_STAGE(s, 0, 1, 0, 1)
+        MOE_D16_STAGE(s, 0, 0, 1)
         if (s + 1 >= nst) break;
-        MOE_D16_STAGE(s + 1, 1, 0, 1, 0)
+        MOE_D16_STAGE(s + 1, 1, 1, 0)
       }
-    }
-  } else {
-    // A phase of 64 x 32 x 64 products by half as many MFMAs is over before its reads are done, so
-    // with 128 rows a stage is one phase: all of the next one's operands are read under its sixteen
-    // MFMAs, and the stage after the next but one loads into its buffer.
-#define MOE_D16_READ_G(set, B, x)                                                                                      \
-  {                                                                                                                    \
-    constexpr int k_ = (x) >> 2, h_ = (x) & 1;                                                                         \
-    if constexpr ((x) & 2) {                                                                                           \
-      if constexpr (NM) gn[set][h_][k_].template read<(((B) & 1) * 2 + h_) * HALF + k_ * 4096>(n_at[(B) >> 1][0]);      \
-      else gn[set][h_][k_].template read<(((B) & 1) * 2 + h_) * HALF>(n_at[(B) >> 1][k_]);                             \
-    } else {                                                                                                           \
-      if constexpr (MM) gm[set][h_][k_].template read<((B) * 2 + h_) * HALF_M + k_ * 32 * HM>(m_at[0]);                \
-      else gm[set][h_][k_].template read<((B) * 2 + h_) * HALF_M>(m_at[k_]);                                           \
-    }                                                                                                                  \
-  }
-#define MOE_D16_MFMA_G(set, x)                                                                                         \
-  {                                                                                                                    \
-    f32x16& c_ = acc[((x) >> 1) & 1][(x) & 1][0];                                                                      \
-    c_ = mfma<DT>(gn[set][((x) >> 1) & 1][(x) >> 2].get(), gm[set][(x) & 1][(x) >> 2].get(), c_);                       \
-  }
-#define MOE_D16_STEP_G(X, Y, C, x)                                                                                     \
-  MOE_D16_MFMA_G(X, x) MOE_D16_READ_G(Y, C, 2 * (x)) MOE_D16_READ_G(Y, C, 2 * (x) + 1) __builtin_amdgcn_sched_barrier(0);
-    auto tie_g = [&](int set) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          gm[set][h][ks].tie();
-          gn[set][h][ks].tie();
-        }
-    };
-#define MOE_D16_STAGE_G(st, B, C, X, Y)                                                                                \
-  {                                                                                                                    \
-    load_m(0, (st) + NB, B);                                                                                           \
-    load_n(0, (st) + NB, B);                                                                                           \
-    load_n(1, (st) + NB, B);                                                                                           \
-    load_m(1, (st) + NB, B);                                                                                           \
-    __builtin_amdgcn_sched_barrier(0);                                                                                 \
-    MOE_D16_STEP_G(X, Y, C, 0) MOE_D16_STEP_G(X, Y, C, 1) MOE_D16_STEP_G(X, Y, C, 2) MOE_D16_STEP_G(X, Y, C, 3)         \
-    MOE_D16_STEP_G(X, Y, C, 4) MOE_D16_STEP_G(X, Y, C, 5) MOE_D16_STEP_G(X, Y, C, 6) MOE_D16_STEP_G(X, Y, C, 7)         \
-    MOE_D16_MFMA_G(X, 8) MOE_D16_MFMA_G(X, 9) MOE_D16_MFMA_G(X, 10) MOE_D16_MFMA_G(X, 11)                              \
-    MOE_D16_MFMA_G(X, 12) MOE_D16_MFMA_G(X, 13) MOE_D16_MFMA_G(X, 14) MOE_D16_MFMA_G(X, 15)                            \
-    __builtin_amdgcn_sched_barrier(0);                                                                                 \
-    wait_all_but<LS>();                                                                                                \
-    tie_g(Y);                                                                                                          \
-    barrier();                                                                                                         \
-    __builtin_amdgcn_sched_barrier(0);                                                                                 \
-  }
-    if (nst > 0) {
-#pragma unroll
-      for (int s = 0; s < NB; ++s) {
-        load_m(0, s, s);
-        load_n(0, s, s);
-        load_n(1, s, s);
-        load_m(1, s, s);
-      }
-      if constexpr (MODE == LORA) {
-        if (split == 0) adapters();
-      }
-      wait_loads<2 * LS>();
+    } else {
+      wait_loads<LS>();
       barrier();
-#define MOE_D16_ALL_G(x) MOE_D16_READ_G(0, 0, x) MOE_D16_READ_G(0, 0, x + 1) MOE_D16_READ_G(0, 0, x + 2) MOE_D16_READ_G(0, 0, x + 3)
-      MOE_D16_ALL_G(0) MOE_D16_ALL_G(4) MOE_D16_ALL_G(8) MOE_D16_ALL_G(12)
-      wait_all_but<LS>();
-      tie_g(0);
-      barrier();
-      for (int s = 0; s < nst; s += 6) {
-        MOE_D16_STAGE_G(s, 0, 1, 0, 1)
+      if (wm) barrier();
+      for (int s = 0; s < nst; s += 3) {
+        MOE_D16_STAGE_P(s, 0, 2)
         if (s + 1 >= nst) break;
-        MOE_D16_STAGE_G(s + 1, 1, 2, 1, 0)
+        MOE_D16_STAGE_P(s + 1, 1, 0)
         if (s + 2 >= nst) break;
-        MOE_D16_STAGE_G(s + 2, 2, 0, 0, 1)
-        if (s + 3 >= nst) break;
-        MOE_D16_STAGE_G(s + 3, 0, 1, 1, 0)
-        if (s + 4 >= nst) break;
-        MOE_D16_STAGE_G(s + 4, 1, 2, 0, 1)
-        if (s + 5 >= nst) break;
-        MOE_D16_STAGE_G(s + 5, 2, 0, 1, 0)
+        MOE_D16_STAGE_P(s + 2, 2, 1)
       }
     }
-#undef MOE_D16_ALL_G
-#undef MOE_D16_STAGE_G
-#undef MOE_D16_STEP_G
-#undef MOE_D16_MFMA_G
-#undef MOE_D16_READ_G
-  }
-  if (nst > 0) {
+    if (!wm) barrier();
     wait_loads<0>();
     barrier();
   }
+#undef MOE_D16_STAGE_P
+#undef MOE_D16_PHASE_P
+#undef MOE_D16_READ_P
 
   // ---- epilogue: 32 rows at a time through the wave's part of the buffers
   constexpr int COLS = NM ? 32 : 64;
@@ -464,9 +433,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #undef MOE_D16_PHASE
 #undef MOE_D16_ALL_M
 #undef MOE_D16_ALL_N
-#undef MOE_D16_MFMA
 #undef MOE_D16_READ_N
-#undef MOE_D16_READ_M2
 #undef MOE_D16_READ_M
 }
 
