@@ -115,6 +115,10 @@ __device__ __forceinline__ const uint8_t* uniform(const void* p) {
   return (const uint8_t*)((uint64_t)hi << 32 | lo);
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t desc(const uint8_t* at, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), (short)0, bytes, 0x00020000);
+}
+
 // 16 bytes to a lane, straight into LDS from dst on
 __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t rs, lds_u8* dst, uint32_t off, uint32_t uniform) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)dst, 16, (int)off, (int)uniform, 0, 0);

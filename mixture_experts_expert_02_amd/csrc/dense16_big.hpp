@@ -71,83 +71,62 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       n_chunk[q] = c;
     }
   }
-  // Where each half's next stage begins: K value k of product seg, at the operand's row k (K-major) or its first row.
-  // Kept from stage to stage, in 32 bits where they suffice: 64-bit products and compares are the scalar unit's slowest.
+  // Where each half's next stage begins, at the operand's row k (K-major) or at its first row; DX's operands change once,
+  // from the gate's product to the up one. All of it in scalar registers and in 32 bits where they suffice, for a
+  // wave's turn beside the other's 256 cycles of MFMAs is short (among the MFMAs the same instructions cost more:
+  // a stage 1.30 us in place of 1.10 for DX, 0.97 in place of 0.91 for GATED).
   struct Cursor {
     const uint8_t* at;
     int k, seg;
+    uint32_t ld2;   // bytes between rows
+    int bytes;      // K-contiguous: of the half; K-major: of a row from its first column on
   };
-  Cursor cm[2], cn[2];
   const int seg0 = MODE == DX && s_lo >= kt ? 1 : 0, first_k = (s_lo - seg0 * kt) * BK;
-  const int mi0 = MODE == DX ? seg0 : z;
-  const uint32_t ldm2 = (uint32_t)(p.ldm[mi0] * 2), ldn2[2] = {(uint32_t)(p.ldn[0] * 2), (uint32_t)(p.ldn[1] * 2)};
-  const uint32_t m_step = __builtin_amdgcn_readfirstlane(ldm2 * BK);
-  const uint32_t n_step[2] = {(uint32_t)__builtin_amdgcn_readfirstlane(ldn2[0] * BK), (uint32_t)__builtin_amdgcn_readfirstlane(ldn2[1] * BK)};
+  auto m_cursor = [&](int h, int seg, int k) {
+    const int i = MODE == DX ? seg : z;
+    const int64_t ld = p.ldm[i], at = MODE == LORA ? 0 : MM ? k * ld + m0 + h * HM : (m0 + h * HM) * ld;
+    const int rows = min(HM, p.M - m0 - h * HM);
+    const int bytes = MM ? (p.M - m0 - h * HM) * 2 : MODE == LORA ? 0x7fffffff : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
+    return Cursor{uniform(p.m[i] + at), k, seg, (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2), __builtin_amdgcn_readfirstlane(bytes)};
+  };
+  auto n_cursor = [&](int h, int seg, int k) {
+    const int i = MODE == GATED ? h : seg;
+    const int64_t ld = p.ldn[i], at = NM ? k * ld + n0 + h * 128 : (n0 + (MODE == GATED ? 0 : h * 32)) * ld;
+    const int rows = min(MODE == GATED ? 128 : 224, p.N - n0 - (MODE == GATED ? 0 : h * 32));
+    const int bytes = NM ? (p.N - n0 - h * 128) * 2 : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
+    return Cursor{uniform(p.n[i] + at), k, seg, (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2), __builtin_amdgcn_readfirstlane(bytes)};
+  };
+  Cursor cm[2] = {m_cursor(0, seg0, first_k), m_cursor(1, seg0, first_k)};
+  Cursor cn[2] = {n_cursor(0, seg0, first_k), n_cursor(1, seg0, first_k)};
+  // stage st's part of a half into LDS from dst on; `major`: the operand is K-major
+  auto load = [&](auto major, auto count, Cursor& c, const int (&row)[decltype(count)::value], const int (&chunk)[decltype(count)::value],
+                  const uint32_t* gathered, bool live, lds_u8* dst) {
+    constexpr int L = decltype(count)::value;
+    if constexpr (decltype(major)::value) {
+      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)c.ld2 + c.bytes : 0);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int ni = MODE == GATED ? h : seg0;
-    const int64_t m_at0 = MODE == LORA ? 0 : MM ? (int64_t)first_k * p.ldm[mi0] + m0 + h * HM : (int64_t)(m0 + h * HM) * p.ldm[mi0];
-    const int64_t n_at0 = NM ? (int64_t)first_k * p.ldn[ni] + n0 + h * 128 : (int64_t)(n0 + (MODE == GATED ? 0 : h * 32)) * p.ldn[ni];
-    cm[h] = {uniform(p.m[mi0] + m_at0), first_k, seg0};
-    cn[h] = {uniform(p.n[ni] + n_at0), first_k, seg0};
-  }
-  auto desc = [](const uint8_t* at, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), (short)0, bytes, 0x00020000);
+      for (int q = 0; q < L; ++q) dma(rs, dst + q * 1024, __umul24(row[q], c.ld2) + chunk[q] * 16, 0);
+      c.at += c.ld2 * BK;
+    } else {
+      const auto rs = desc(c.at, live ? c.bytes : 0);
+#pragma unroll
+      for (int q = 0; q < L; ++q) {
+        uint32_t off = gathered ? gathered[q] : __umul24(row[q], c.ld2) + chunk[q] * 16;
+        if (c.k + chunk[q] * 8 >= p.K) off = kNoLoad;
+        dma(rs, dst + q * 1024, off, c.k * 2);
+      }
+    }
+    c.k += BK;
   };
   auto load_m = [&](int h, int st, int buf) {
-    Cursor& c = cm[h];
-    const bool live = st < nst;
-    lds_u8* dst = smem + (buf * 2 + h) * HALF_M + wave * LM * 1024;
-    if constexpr (MM) {
-      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)ldm2 + (p.M - m0 - h * HM) * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < LM; ++q) dma(rs, dst + q * 1024, __umul24(m_row[q], ldm2) + m_chunk[q] * 16, 0);
-      c.at += m_step;
-      c.k += BK;
-    } else {
-      const int rows = min(HM, p.M - m0 - h * HM);
-      const auto rs = desc(c.at, !live ? 0 : MODE == LORA ? 0x7fffffff : rows > 0 ? (rows - 1) * (int)ldm2 + p.K * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < LM; ++q) {
-        uint32_t off = MODE == LORA ? g_off[h][q] : __umul24(m_row[q], ldm2) + m_chunk[q] * 16;
-        if (c.k + m_chunk[q] * 8 >= p.K) off = kNoLoad;
-        dma(rs, dst + q * 1024, off, c.k * 2);
-      }
-      c.k += BK;
-      if (MODE == DX && c.k >= p.K && c.seg == 0) {
-        c.at += (const uint8_t*)p.m[1] - (const uint8_t*)p.m[0];
-        c.k = 0;
-        c.seg = 1;
-      }
-    }
+    load(std::bool_constant<MM>{}, std::integral_constant<int, LM>{}, cm[h], m_row, m_chunk, MODE == LORA ? g_off[h] : nullptr, st < nst,
+         smem + (buf * 2 + h) * HALF_M + wave * LM * 1024);
+    if (MODE == DX && __builtin_expect(cm[h].k >= p.K && cm[h].seg == 0, 0)) cm[h] = m_cursor(h, 1, 0);
   };
   auto load_n = [&](int h, int st, int buf) {
-    Cursor& c = cn[h];
-    const bool live = st < nst;
-    lds_u8* dst = smem + N_AT + (buf * 2 + h) * HALF + wave * 2048;
-    const uint32_t ld2 = MODE == GATED ? ldn2[h] : MODE == DX ? (c.seg ? ldn2[1] : ldn2[0]) : ldn2[0];
-    if constexpr (NM) {
-      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)ld2 + (p.N - n0 - h * 128) * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) dma(rs, dst + q * 1024, __umul24(n_row[q], ld2) + n_chunk[q] * 16, 0);
-      c.at += MODE == DX && c.seg ? n_step[1] : n_step[0];
-      c.k += BK;
-      if (MODE == DX && c.k >= p.K && c.seg == 0) {
-        c.at = (const uint8_t*)(p.n[1] + n0 + h * 128);
-        c.k = 0;
-        c.seg = 1;
-      }
-    } else {
-      const int rows = min(MODE == GATED ? 128 : 224, p.N - n0 - (MODE == GATED ? 0 : h * 32));
-      const auto rs = desc(c.at, live && rows > 0 ? (rows - 1) * (int)ld2 + p.K * 2 : 0);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t off = __umul24(n_row[q], ld2) + n_chunk[q] * 16;
-        if (c.k + n_chunk[q] * 8 >= p.K) off = kNoLoad;
-        dma(rs, dst + q * 1024, off, c.k * 2);
-      }
-      c.k += BK;
-    }
+    load(std::bool_constant<NM>{}, std::integral_constant<int, 2>{}, cn[h], n_row, n_chunk, nullptr, st < nst,
+         smem + N_AT + (buf * 2 + h) * HALF + wave * 2048);
+    if (MODE == DX && __builtin_expect(cn[h].k >= p.K && cn[h].seg == 0, 0)) cn[h] = n_cursor(h, 1, 0);
   };
 
   // ---- operand reads: bytes inside a half
@@ -285,18 +264,19 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // The two waves of a SIMD (wm = 0 and 1) work half a phase apart: while one multiplies, the other reads the operands
   // of its next phase and starts a half's loads, and a barrier ends each turn. Waves with wm = 1 begin one
   // barrier later and end one earlier. Before the barrier behind its reads a wave has them all, and those of its loads
-  // have landed that the next phase's reads need.
-#define MOE_D16_PHASE(hn, hm, set, READS, LOAD, LEFT, TIE)                                             \
+  // have landed that the next phase's reads need: all but the twelve youngest.
+#define MOE_D16_MFMA(hn, hm, set, x) \
+  acc[hn][hm][(x) % J] = mfma<DT>(fn[set][(x) / J % 4].get(), fm[(x) % J][(x) / J % 4].get(), acc[hn][hm][(x) % J]);
+#define MOE_D16_PHASE(hn, hm, set, READS, LOAD, TIE)                                                   \
   {                                                                                                    \
     READS;                                                                                             \
     LOAD;                                                                                              \
-    wait_all_but<LEFT>();                                                                              \
+    wait_all_but<12>();                                                                                \
     TIE;                                                                                               \
     barrier();                                                                                         \
     __builtin_amdgcn_sched_barrier(0);                                                                 \
     __builtin_amdgcn_s_setprio(1);                                                                     \
-    _Pragma("unroll") for (int x = 0; x < 8; ++x) acc[hn][hm][x % J] =                                 \
-        mfma<DT>(fn[set][x / J % 4].get(), fm[x % J][x / J % 4].get(), acc[hn][hm][x % J]);            \
+    _Pragma("unroll") for (int x = 0; x < 8; ++x) MOE_D16_MFMA(hn, hm, set, x)                         \
     __builtin_amdgcn_s_setprio(0);                                                                     \
     __builtin_amdgcn_sched_barrier(0);                                                                 \
     barrier();                                                                                         \
@@ -305,10 +285,10 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // loaded for the stage after the next in the phase behind the one that read it.
 #define MOE_D16_STAGE(st, B, X, Y)                                                                     \
   {                                                                                                    \
-    MOE_D16_PHASE(0, 0, X, MOE_D16_ALL_M(0, B), load_n(0, (st) + 2, B), 12, tie_m())                   \
-    MOE_D16_PHASE(1, 0, 2, MOE_D16_ALL_N(2, 1, B), load_m(0, (st) + 2, B), 12, tie_n(2))               \
-    MOE_D16_PHASE(1, 1, 2, MOE_D16_ALL_M(1, B), load_n(1, (st) + 2, B), 12, tie_m())                   \
-    MOE_D16_PHASE(0, 1, X, MOE_D16_ALL_N(Y, 0, 1 - B), load_m(1, (st) + 2, B), 12, tie_n(Y))           \
+    MOE_D16_PHASE(0, 0, X, MOE_D16_ALL_M(0, B), load_n(0, (st) + 2, B), tie_m())                   \
+    MOE_D16_PHASE(1, 0, 2, MOE_D16_ALL_N(2, 1, B), load_m(0, (st) + 2, B), tie_n(2))               \
+    MOE_D16_PHASE(1, 1, 2, MOE_D16_ALL_M(1, B), load_n(1, (st) + 2, B), tie_m())                   \
+    MOE_D16_PHASE(0, 1, X, MOE_D16_ALL_N(Y, 0, 1 - B), load_m(1, (st) + 2, B), tie_n(Y))           \
   }
   // 128 rows: a phase is all four blocks of two K steps, and a buffer is loaded anew, for the stage after the next
   // but one, in the two phases behind its last read.
@@ -329,6 +309,8 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       gn[1][x].template read<(((B) & 1) * 2 + 1) * HALF>(n_at[(B) >> 1][(2 * (p_) + x) % 4]);                \
     }                                                                                                  \
   }
+#define MOE_D16_MFMA_P(x) \
+  acc[((x) >> 1) & 1][(x) & 1][0] = mfma<DT>(gn[((x) >> 1) & 1][(x) >> 2].get(), gm[(x) & 1][(x) >> 2].get(), acc[((x) >> 1) & 1][(x) & 1][0]);
 #define MOE_D16_PHASE_P(B, p_, LOAD, LEFT)                                                             \
   {                                                                                                    \
     MOE_D16_READ_P(B, p_)                                                                              \
@@ -341,8 +323,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     barrier();                                                                                         \
     __builtin_amdgcn_sched_barrier(0);                                                                 \
     __builtin_amdgcn_s_setprio(1);                                                                     \
-    _Pragma("unroll") for (int x = 0; x < 8; ++x) acc[(x >> 1) & 1][x & 1][0] =                        \
-        mfma<DT>(gn[(x >> 1) & 1][x >> 2].get(), gm[x & 1][x >> 2].get(), acc[(x >> 1) & 1][x & 1][0]); \
+    _Pragma("unroll") for (int x = 0; x < 8; ++x) MOE_D16_MFMA_P(x)                                    \
     __builtin_amdgcn_s_setprio(0);                                                                     \
     __builtin_amdgcn_sched_barrier(0);                                                                 \
     barrier();                                                                                         \
@@ -405,6 +386,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   }
 #undef MOE_D16_STAGE_P
 #undef MOE_D16_PHASE_P
+#undef MOE_D16_MFMA_P
 #undef MOE_D16_READ_P
 
   // ---- epilogue: 32 rows at a time through the wave's part of the buffers
@@ -431,6 +413,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       }
 #undef MOE_D16_STAGE
 #undef MOE_D16_PHASE
+#undef MOE_D16_MFMA
 #undef MOE_D16_ALL_M
 #undef MOE_D16_ALL_N
 #undef MOE_D16_READ_N
