@@ -77,56 +77,62 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // a stage 1.30 us in place of 1.10 for DX, 0.97 in place of 0.91 for GATED).
   struct Cursor {
     const uint8_t* at;
-    int k, seg;
+    int k, end;     // next K value, and the end of this workgroup's in the operand: beyond it nothing is loaded
     uint32_t ld2;   // bytes between rows
     int bytes;      // K-contiguous: of the half; K-major: of a row from its first column on
   };
-  const int seg0 = MODE == DX && s_lo >= kt ? 1 : 0, first_k = (s_lo - seg0 * kt) * BK;
-  auto m_cursor = [&](int h, int seg, int k) {
-    const int i = MODE == DX ? seg : z;
+  const int seg0 = MODE == DX && s_lo >= kt ? 1 : 0;
+  const int second = MODE == DX && !seg0 ? kt - s_lo : 0x7fffffff;  // the first stage of DX's second product
+  auto first_k = [&](int seg) { return seg == seg0 ? (s_lo - seg * kt) * BK : 0; };
+  auto end_k = [&](int seg) { return __builtin_amdgcn_readfirstlane(min(p.K, (s_lo + nst - seg * kt) * BK)); };
+  auto m_cursor = [&](int h, int seg) {
+    const int i = MODE == DX ? seg : z, k = first_k(seg);
     const int64_t ld = p.ldm[i], at = MODE == LORA ? 0 : MM ? k * ld + m0 + h * HM : (m0 + h * HM) * ld;
     const int rows = min(HM, p.M - m0 - h * HM);
     const int bytes = MM ? (p.M - m0 - h * HM) * 2 : MODE == LORA ? 0x7fffffff : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
-    return Cursor{uniform(p.m[i] + at), k, seg, (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2), __builtin_amdgcn_readfirstlane(bytes)};
+    return Cursor{uniform(p.m[i] + at), k, end_k(seg), (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2),
+                  __builtin_amdgcn_readfirstlane(bytes)};
   };
-  auto n_cursor = [&](int h, int seg, int k) {
-    const int i = MODE == GATED ? h : seg;
+  auto n_cursor = [&](int h, int seg) {
+    const int i = MODE == GATED ? h : seg, k = first_k(seg);
     const int64_t ld = p.ldn[i], at = NM ? k * ld + n0 + h * 128 : (n0 + (MODE == GATED ? 0 : h * 32)) * ld;
     const int rows = min(MODE == GATED ? 128 : 224, p.N - n0 - (MODE == GATED ? 0 : h * 32));
     const int bytes = NM ? (p.N - n0 - h * 128) * 2 : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
-    return Cursor{uniform(p.n[i] + at), k, seg, (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2), __builtin_amdgcn_readfirstlane(bytes)};
+    return Cursor{uniform(p.n[i] + at), k, end_k(seg), (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2),
+                  __builtin_amdgcn_readfirstlane(bytes)};
   };
-  Cursor cm[2] = {m_cursor(0, seg0, first_k), m_cursor(1, seg0, first_k)};
-  Cursor cn[2] = {n_cursor(0, seg0, first_k), n_cursor(1, seg0, first_k)};
-  // stage st's part of a half into LDS from dst on; `major`: the operand is K-major
+  Cursor cm[2] = {m_cursor(0, seg0), m_cursor(1, seg0)};
+  Cursor cn[2] = {n_cursor(0, seg0), n_cursor(1, seg0)};
+  // the next stage's part of a half into LDS from dst on; `major`: the operand is K-major
   auto load = [&](auto major, auto count, Cursor& c, const int (&row)[decltype(count)::value], const int (&chunk)[decltype(count)::value],
-                  const uint32_t* gathered, bool live, lds_u8* dst) {
+                  const uint32_t* gathered, lds_u8* dst) {
     constexpr int L = decltype(count)::value;
     if constexpr (decltype(major)::value) {
-      const auto rs = desc(c.at, live ? (min(BK, p.K - c.k) - 1) * (int)c.ld2 + c.bytes : 0);
+      // a row's bytes are at most those between rows, so without rows this is not positive
+      const auto rs = desc(c.at, max(0, (min(BK, c.end - c.k) - 1) * (int)c.ld2 + c.bytes));
 #pragma unroll
       for (int q = 0; q < L; ++q) dma(rs, dst + q * 1024, __umul24(row[q], c.ld2) + chunk[q] * 16, 0);
       c.at += c.ld2 * BK;
     } else {
-      const auto rs = desc(c.at, live ? c.bytes : 0);
+      const auto rs = desc(c.at, c.bytes);
 #pragma unroll
       for (int q = 0; q < L; ++q) {
         uint32_t off = gathered ? gathered[q] : __umul24(row[q], c.ld2) + chunk[q] * 16;
-        if (c.k + chunk[q] * 8 >= p.K) off = kNoLoad;
+        if (chunk[q] * 8 >= c.end - c.k) off = kNoLoad;
         dma(rs, dst + q * 1024, off, c.k * 2);
       }
     }
     c.k += BK;
   };
   auto load_m = [&](int h, int st, int buf) {
-    load(std::bool_constant<MM>{}, std::integral_constant<int, LM>{}, cm[h], m_row, m_chunk, MODE == LORA ? g_off[h] : nullptr, st < nst,
+    if (MODE == DX && st == second) cm[h] = m_cursor(h, 1);
+    load(std::bool_constant<MM>{}, std::integral_constant<int, LM>{}, cm[h], m_row, m_chunk, MODE == LORA ? g_off[h] : nullptr,
          smem + (buf * 2 + h) * HALF_M + wave * LM * 1024);
-    if (MODE == DX && __builtin_expect(cm[h].k >= p.K && cm[h].seg == 0, 0)) cm[h] = m_cursor(h, 1, 0);
   };
   auto load_n = [&](int h, int st, int buf) {
-    load(std::bool_constant<NM>{}, std::integral_constant<int, 2>{}, cn[h], n_row, n_chunk, nullptr, st < nst,
+    if (MODE == DX && st == second) cn[h] = n_cursor(h, 1);
+    load(std::bool_constant<NM>{}, std::integral_constant<int, 2>{}, cn[h], n_row, n_chunk, nullptr,
          smem + N_AT + (buf * 2 + h) * HALF + wave * 2048);
-    if (MODE == DX && __builtin_expect(cn[h].k >= p.K && cn[h].seg == 0, 0)) cn[h] = n_cursor(h, 1, 0);
   };
 
   // ---- operand reads: bytes inside a half
@@ -270,6 +276,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #define MOE_D16_PHASE(hn, hm, set, READS, LOAD, TIE)                                                   \
   {                                                                                                    \
     READS;                                                                                             \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
     LOAD;                                                                                              \
     wait_all_but<12>();                                                                                \
     TIE;                                                                                               \
@@ -314,6 +321,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #define MOE_D16_PHASE_P(B, p_, LOAD, LEFT)                                                             \
   {                                                                                                    \
     MOE_D16_READ_P(B, p_)                                                                              \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
     LOAD;                                                                                              \
     wait_all_but<LEFT>();                                                                              \
     _Pragma("unroll") for (int x = 0; x < 4; ++x) {                                                    \
