@@ -52,14 +52,14 @@ struct Params {
   // LORA
   const void* add;
   int64_t ld_add;
-  int32_t vec;             // out, add and bias take 16-byte accesses at multiples of 8 columns
+  int32_t vec;             // out and add take 16-byte accesses at multiples of 8 columns
+  int32_t N8;              // N rounded down to a multiple of 8
   int32_t R, L;
   const uint16_t* t;       // [M, 2R] upper and lower parts of the scaled x A^T, rows in sorted order
   const float* tf;         // [M] their rows' powers of two
   const uint16_t* b;       // [L, N, R]
   const int32_t* perm;     // sorted row -> row
   const int32_t* sid;      // adapter of the sorted row, L where it has none
-  const int32_t* ends;     // [L] sorted row behind an adapter's last
 };
 
 // ------------------------------------------------------------ activations
@@ -323,30 +323,35 @@ __device__ __forceinline__ float* part_of(const Params& p, int split, int which,
   return p.part + ((int64_t)(planes * split + which) * p.M + row) * np + col;
 }
 
-// A wave's results of 32 rows, staged in LDS as float32 (rows of COLS + 4 values),
-// come back eight columns to a lane and leave as 16-byte stores.
-template <int DT, int MODE, int COLS>
-__device__ __forceinline__ void store_rows(const Params& p, const float* strip, int z, int split, int row0, int col0,
-                                           int lane, const int* rows_lds) {
-  constexpr int HALF = MODE == GATED ? COLS / 2 : COLS;  // output columns
-  constexpr int PITCH = COLS + 4;
-  constexpr int CPR = HALF / 8, RPP = 64 / CPR;
-  const int c = 8 * (lane % CPR), col = col0 + c;
-  if (col >= p.N) return;
-#pragma unroll 1
-  for (int r = lane / CPR; r < 32; r += RPP) {
-    const int row = row0 + r;
-    if (row >= p.M) return;
-    float v[8], u[8];
-    load8<T_FP32>(strip, r * PITCH + c, v);
-    if constexpr (MODE == GATED) load8<T_FP32>(strip, r * PITCH + HALF + c, u);
-    if (p.splits > 1) {
-      store8<T_FP32>(part_of<MODE>(p, split, z, row, col), 0, v);
-      if constexpr (MODE == GATED) store8<T_FP32>(part_of<MODE>(p, split, 1, row, col), 0, u);
-    } else {
-      finish8<DT, MODE>(p, z, MODE == LORA ? rows_lds[r] : row, col, v, u);
-    }
+// Stores from a 32 x 32 result fragment (N operand first): the lane holds columns 8 q + 4 lk .. + 3 of row lr in registers
+// 4 q .. 4 q + 3. 16-bit values of an even q and the odd one behind it change places between the
+// halves of the wave, so that a lane stores eight neighbours: q's in the lower half, q + 1's in the upper.
+template <int DT>
+__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
+  uint2 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) store1<DT>(&r, j, v[j]);
+  return r;
+}
+__device__ __forceinline__ u32x4 swap_halves(uint2 even, uint2 odd) {
+  const auto a = __builtin_amdgcn_permlane32_swap(even.x, odd.x, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(even.y, odd.y, false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+// v[q][j]: 4 x 4 values of the lane; base: the row's first value of the fragment's columns; left: columns from there to the end,
+// a multiple of 8
+template <int DT>
+__device__ __forceinline__ void store_fragment(void* base, const float (&v)[4][4], int lk, int left, bool row_ok) {
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    const u32x4 x = swap_halves(pack4<DT>(v[q]), pack4<DT>(v[q + 1]));
+    if (row_ok && 8 * (q + lk) < left) *(u32x4*)((uint16_t*)base + 8 * (q + lk)) = x;
   }
+}
+__device__ __forceinline__ void store_fragment_f32(float* base, const float (&v)[4][4], int lk, int left, bool row_ok) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (row_ok && 8 * q + 4 * lk < left) *(f32x4*)(base + 8 * q + 4 * lk) = f32x4{v[q][0], v[q][1], v[q][2], v[q][3]};
 }
 
 // Partial results joined in the order of their K ranges, eight columns to a thread.

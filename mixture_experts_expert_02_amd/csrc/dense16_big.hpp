@@ -26,7 +26,6 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   constexpr int N_AT = NB * 2 * HALF_M;  // M halves [stage buffer][half], then N halves
   constexpr int LM = BM / 128, LN = 2, LS = 2 * (LM + LN);  // a wave's load instructions for a half, and for a stage
   __shared__ __attribute__((aligned(16))) uint8_t smem_arr[NB * 2 * (HALF_M + HALF)];
-  __shared__ int rows_lds[MODE == LORA ? BM : 1];
   lds_u8* smem = (lds_u8*)smem_arr;
   Item it;
   if (!item_of(p, MODE == DW ? 2 * p.splits : p.splits, it)) return;
@@ -37,11 +36,6 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   const int z = MODE == DW ? it.z & 1 : 0, split = MODE == DW ? it.z >> 1 : it.z;
   const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;
   const int s_lo = (int)((int64_t)split * all / p.splits), nst = (int)((int64_t)(split + 1) * all / p.splits) - s_lo;
-
-  if constexpr (MODE == LORA) {
-    if (tid < BM) rows_lds[tid] = m0 + tid < p.M ? p.perm[m0 + tid] : 0;
-    __syncthreads();
-  }
 
   // ---- loads: instructions 2 wave and 2 wave + 1 of the 16 of a half (BM = 128: instruction `wave` of the 8 of an M half)
   // columns of N half h: 128 h + i where N is K-major or GATED (half = gate or up); else 32 columns of each half
@@ -59,7 +53,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     if constexpr (MODE == LORA) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        g_off[h][q] = m0 + h * HM + r < p.M ? (uint32_t)rows_lds[h * HM + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+        g_off[h][q] = m0 + h * HM + r < p.M ? (uint32_t)p.perm[m0 + h * HM + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
     }
   }
 #pragma unroll
@@ -205,65 +199,75 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   };
 
   // ---- adapters, a fragment of 32 sorted rows at a time, while the first stages load: both operands straight
-  // into registers (t and the factor's rows are as the MFMA wants them). A fragment that holds rows of
-  // several adapters gets each one's product in registers of its own and adds it to the rows it belongs to,
-  // so that what an adapter holds (an infinity, say) reaches no other adapter's rows.
+  // into registers (t and the factor's rows are as the MFMA wants them). A fragment that holds rows of several adapters gets each one's product in registers of its own
+  // and adds it to the rows it belongs to, so that what an adapter holds (an infinity, say) reaches no other
+  // adapter's rows.
   auto adapters = [&]() {
-    u32x4 b[2][4];
+    constexpr int F = 2 * J;
+    int id[F];
+    float f[F];
+    u32x4 hi[4], lo[4], b[2][4];
+    const u32x4 zero = {0, 0, 0, 0};
+    auto first_row = [&](int x) { return m0 + (x / J) * HM + wm * (HM / 2) + (x % J) * 32; };
+    auto load_t = [&](int x, int c0) {
+      const uint16_t* t = p.t + (int64_t)min(first_row(x) + lr, p.M - 1) * 2 * p.R;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int k = c0 + 16 * ks + 8 * lk;
+        hi[ks] = lo[ks] = zero;
+        if (k < p.R) {
+          hi[ks] = *(const u32x4*)(t + k);
+          lo[ks] = *(const u32x4*)(t + p.R + k);
+        }
+      }
+    };
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+      const int row = first_row(x) + lr;
+      id[x] = row < p.M ? p.sid[row] : p.L;
+      f[x] = p.tf[min(row, p.M - 1)];
+    }
     int held = -1;  // whose factor b holds
 #pragma unroll
-    for (int hm = 0; hm < 2; ++hm)
+    for (int x = 0; x < F; ++x) {
+      load_t(x, 0);
+      uint64_t rows = __ballot(id[x] < p.L);
+      while (rows) {
+        const int a = __builtin_amdgcn_readlane(id[x], __builtin_ctzll(rows));
+        const bool mine = id[x] == a;
+        rows &= ~__ballot(mine);
+        for (int c0 = 0; c0 < p.R; c0 += 64) {
+          if (held != a || p.R > 64) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int r0 = m0 + hm * HM + wm * (HM / 2) + j * 32, row = min(r0 + lr, p.M - 1), end = min(r0 + 32, p.M);
-        const int id = r0 + lr < p.M ? p.sid[row] : p.L;
-        const float f = p.tf[row];
-        const uint16_t* t = p.t + (int64_t)row * 2 * p.R;
-        int pos = r0;
-        while (pos < end) {
-          const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
-          if (a >= p.L) break;
-          pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
-          const bool mine = id == a;
-          for (int c0 = 0; c0 < p.R; c0 += 64) {
-            u32x4 hi[4], lo[4];
-            const u32x4 zero = {0, 0, 0, 0};
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+              for (int hn = 0; hn < 2; ++hn) {
+                const int k = c0 + 16 * ks + 8 * lk, col = n0 + wn * 64 + hn * 32 + lr;
+                b[hn][ks] = zero;
+                if (k < p.R && col < p.N) b[hn][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
+              }
+            held = a;
+          }
+          if (p.R > 64) load_t(x, c0);
+#pragma unroll
+          for (int hn = 0; hn < 2; ++hn) {
+            f32x16 tmp;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) tmp[r] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              const int k = c0 + 16 * ks + 8 * lk;
-              hi[ks] = lo[ks] = zero;
-              if (k < p.R) {
-                hi[ks] = *(const u32x4*)(t + k);
-                lo[ks] = *(const u32x4*)(t + p.R + k);
-              }
-              if (held != a || p.R > 64) {
-#pragma unroll
-                for (int hn = 0; hn < 2; ++hn) {
-                  const int col = n0 + wn * 64 + hn * 32 + lr;
-                  b[hn][ks] = zero;
-                  if (k < p.R && col < p.N) b[hn][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
-                }
-              }
+              if (c0 + 16 * ks >= p.R) break;
+              tmp = mfma<DT>(b[hn][ks], hi[ks], tmp);
+              tmp = mfma<DT>(b[hn][ks], lo[ks], tmp);
             }
-            held = a;
+            if (mine) {
 #pragma unroll
-            for (int hn = 0; hn < 2; ++hn) {
-              f32x16 tmp;
-#pragma unroll
-              for (int r = 0; r < 16; ++r) tmp[r] = 0.f;
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                tmp = mfma<DT>(b[hn][ks], hi[ks], tmp);
-                tmp = mfma<DT>(b[hn][ks], lo[ks], tmp);
-              }
-              if (mine) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[hn][hm][j][r] += tmp[r] * f;
-              }
+              for (int r = 0; r < 16; ++r) acc[hn][x / J][x % J][r] += tmp[r] * f[x];
             }
           }
         }
       }
+    }
   };
 
   // ---- main loop
@@ -397,28 +401,120 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #undef MOE_D16_MFMA_P
 #undef MOE_D16_READ_P
 
-  // ---- epilogue: 32 rows at a time through the wave's part of the buffers
-  constexpr int COLS = NM ? 32 : 64;
-  float* strip = (float*)(smem_arr + wave * 32 * (64 + 4) * 4);
+  // ---- epilogue, from registers
+  const int colw = n0 + (MODE == GATED || NM ? wn * 32 : wn * 64);      // the wave's first column of N half 0
+  constexpr int STEP = NM ? 128 : 32;                                   // from there to half 1's (GATED: the same)
+  auto add_bias = [&](int w, int col, float (&v)[4][4]) {               // the lane's 16 columns from col on
 #pragma unroll
-  for (int hm = 0; hm < 2; ++hm)
+    for (int r = 0; r < 16; ++r) {
+      const int c = col + 8 * (r >> 2) + 4 * lk + (r & 3);
+      v[r >> 2][r & 3] += p.bias[w][min(c, p.N - 1)];
+    }
+  };
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+  for (int hm = 0; hm < 2; ++hm) {
+    uint2 old[J][2][4];  // LORA's addend, of both fragments before either is stored
+    int orow[J];
 #pragma unroll
-      for (int hs = 0; hs < 64 / COLS; ++hs) {
+    for (int j = 0; j < J; ++j) {
+      const int row = m0 + hm * HM + wm * (HM / 2) + j * 32 + lr;
+      orow[j] = MODE == LORA ? p.perm[min(row, p.M - 1)] : row;
+      if constexpr (MODE == LORA) {
+        if (p.add && p.vec && p.splits == 1 && row < p.M) {
 #pragma unroll
-        for (int i = 0; i < COLS / 32; ++i)
+          for (int hn = 0; hn < 2; ++hn)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x16& c = acc[hs + i][hm][j];
-            *(f32x4*)(strip + lr * (COLS + 4) + i * 32 + 8 * q + 4 * lk) = f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-          }
-        wave_sync();
-        const int r = hm * HM + wm * (HM / 2) + j * 32;
-        store_rows<DT, MODE, COLS>(p, strip, z, split, m0 + r, n0 + (MODE == GATED ? wn * 32 : NM ? hs * 128 + wn * 32 : wn * 64), lane,
-                                   rows_lds + (MODE == LORA ? r : 0));
-        wave_sync();
+            for (int q = 0; q < 4; ++q) {
+              const int c = colw + hn * STEP + 8 * q + 4 * lk;
+              old[j][hn][q] = {0, 0};  // columns behind the last multiple of 8 get theirs where they are stored
+              if (c < p.N8) old[j][hn][q] = *(const uint2*)((const uint16_t*)p.add + orow[j] * p.ld_add + c);
+            }
+        }
       }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int row = m0 + hm * HM + wm * (HM / 2) + j * 32 + lr;
+      const bool ok = row < p.M;
+      const int64_t o = orow[j];
+      float v[2][4][4];
+#pragma unroll
+      for (int hn = 0; hn < 2; ++hn)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[hn][r >> 2][r & 3] = acc[hn][hm][j][r];
+      if (p.splits > 1) {
+#pragma unroll
+        for (int hn = 0; hn < 2; ++hn) {
+          const int col = MODE == GATED ? colw : colw + hn * STEP;
+          store_fragment_f32(part_of<MODE>(p, split, MODE == GATED ? hn : z, row, col), v[hn], lk, p.N - col, ok);
+        }
+      } else if constexpr (MODE == GATED) {
+#pragma unroll
+        for (int hn = 0; hn < 2; ++hn) {
+          if (p.bias[0]) add_bias(hn, colw, v[hn]);
+          if (p.keep[0]) store_fragment<DT>((uint16_t*)p.keep[hn] + o * p.ld_keep[hn] + colw, v[hn], lk, p.N - colw, ok);
+        }
+        with_act(p.act, [&](auto k) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            v[0][r >> 2][r & 3] = act_f<decltype(k)::value>(p.act, v[0][r >> 2][r & 3], v[1][r >> 2][r & 3]);
+            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // more evaluations at once do not fit the registers
+          }
+        });
+        store_fragment<DT>((uint16_t*)p.out[0] + o * p.ldo[0] + colw, v[0], lk, p.N - colw, ok);
+      } else if constexpr (MODE == DX) {
+#pragma unroll
+        for (int hn = 0; hn < 2; ++hn)
+          store_fragment<DT>((uint16_t*)p.out[0] + o * p.ldo[0] + colw + hn * STEP, v[hn], lk, p.N - colw - hn * STEP, ok);
+      } else if constexpr (MODE == DW) {
+#pragma unroll
+        for (int hn = 0; hn < 2; ++hn) {
+          const int64_t at = o * p.ldo[z] + colw + hn * STEP;
+          const int left = p.N - colw - hn * STEP;
+          if (p.accumulate) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (!ok || 8 * q + 4 * lk >= left) continue;
+              if (p.f32_out) {
+                const f32x4 x = *(const f32x4*)((const float*)p.out[z] + at + 8 * q + 4 * lk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[hn][q][i] += x[i];
+              } else {
+                const uint2 x = *(const uint2*)((const uint16_t*)p.out[z] + at + 8 * q + 4 * lk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
+              }
+            }
+          }
+          if (p.f32_out) store_fragment_f32((float*)p.out[z] + at, v[hn], lk, left, ok);
+          else store_fragment<DT>((uint16_t*)p.out[z] + at, v[hn], lk, left, ok);
+        }
+      } else {
+#pragma unroll
+        for (int hn = 0; hn < 2; ++hn) {
+          const int col = colw + hn * STEP;
+          uint16_t* out = (uint16_t*)p.out[0] + o * p.ldo[0] + col;
+          if (p.bias[0]) add_bias(0, col, v[hn]);
+          if (p.vec) {
+            if (p.add) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) v[hn][r >> 2][r & 3] += load1<DT>(&old[j][hn][r >> 2], r & 3);
+            }
+            store_fragment<DT>(out, v[hn], lk, p.N8 - col, ok);
+          }
+          // what no 16-byte store takes: everything, or the columns behind the last multiple of 8
+          if (ok && (!p.vec || col + 32 > p.N8)) {
+            const uint16_t* add = p.add ? (const uint16_t*)p.add + o * p.ld_add + col : nullptr;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int c = 8 * (r >> 2) + 4 * lk + (r & 3);
+              if (col + c < p.N && (!p.vec || col + c >= p.N8)) store1<DT>(out, c, v[hn][r >> 2][r & 3] + (add ? load1<DT>(add, c) : 0.f));
+            }
+          }
+        }
+      }
+    }
+  }
 #undef MOE_D16_STAGE
 #undef MOE_D16_PHASE
 #undef MOE_D16_MFMA

@@ -196,7 +196,7 @@ int shrink_ranges(int64_t M, int K, int R) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({256 / cdiv(M, 16 * shrink_frags(M, R)), cdiv(K, 32) / 16, 16}));
 }
 struct LoraLayout {
-  size_t perm, sid, ends, tf, t, part, bytes;
+  size_t perm, sid, tf, t, part, bytes;
 };
 LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
   LoraLayout l{};
@@ -206,8 +206,7 @@ LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
   }
   l.perm = 0;
   l.sid = up256((size_t)rows * 4);
-  l.ends = l.sid + up256((size_t)rows * 4);
-  l.tf = l.ends + up256((size_t)p.L * 4);
+  l.tf = l.sid + up256((size_t)rows * 4);
   l.t = l.tf + up256((size_t)rows * 4);
   l.part = l.t + up256((size_t)rows * 4 * p.R);
   // partial results of the first product, then of the second; the last part of a call may be its smallest, with the most ranges
@@ -449,6 +448,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
   q.bias[0] = bias;
   q.ld_add = lda;
   q.vec = aligned(out, 16) && ldo % 8 == 0 && (!add || (aligned(add, 16) && lda % 8 == 0));
+  q.N8 = p->N / 8 * 8;
   q.R = p->R;
   q.L = p->L;
   q.t = (const uint16_t*)(ws + l.t);
@@ -456,7 +456,6 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
   q.b = (const uint16_t*)lora_b;
   q.perm = (const int32_t*)(ws + l.perm);
   q.sid = (const int32_t*)(ws + l.sid);
-  q.ends = (const int32_t*)(ws + l.ends);
   if (p->M <= kFewRows) {
     q.m[0] = (const uint16_t*)x;
     q.out[0] = out;
@@ -466,7 +465,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
     q.sid = ids;
     return with_type16(p->type, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
-      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, ids, nullptr, nullptr, (float*)ws, nullptr, ldx,
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, ids, nullptr, (float*)ws, nullptr, ldx,
                             p->M, p->K, p->R, p->L};
       hipLaunchKernelGGL((k_lora_shrink_few<DT>), dim3((unsigned)p->M, (unsigned)p->R / 8), dim3(256), 0, s, sh);
       return launch_rows<DT, LORA>(q, s);
@@ -480,9 +479,9 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
       q.out[0] = (uint16_t*)out + m * ldo;
       q.add = add ? (const uint16_t*)add + m * lda : nullptr;
       q.M = n;
-      const SortParams sp{ids + m, (int32_t*)(ws + l.perm), (int32_t*)(ws + l.sid), (int32_t*)(ws + l.ends), n, p->L};
+      const SortParams sp{ids + m, (int32_t*)(ws + l.perm), (int32_t*)(ws + l.sid), n, p->L};
       hipLaunchKernelGGL(k_lora_sort, dim3(1), dim3(1024), 0, s, sp);
-      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, q.perm, q.sid, q.ends, (uint16_t*)(ws + l.t),
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, q.perm, q.sid, (uint16_t*)(ws + l.t),
                             (float*)(ws + l.tf), (float*)(ws + l.part), ldx, n, p->K, p->R, p->L};
       launch_shrink<DT>(sh, s);
       int rc = launch_status();

@@ -14,7 +14,6 @@ constexpr int kMaxRank = 256;
 struct SortParams {
   const int32_t* ids;  // [M]; outside [0, L): no adapter
   int32_t *perm, *sid; // [M]
-  int32_t* ends;       // [L]
   int32_t M, L;
 };
 
@@ -31,19 +30,17 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
     const int a = p.ids[m];
     return a >= 0 && a < p.L ? a : p.L;
   };
-  // one place for each lane with a key; a wave whose rows share one adapter counts them at once
-  auto take = [&](int a) {
-    const bool in = a >= 0;
-    const uint64_t live = __ballot(in);
+  // one place for each lane with a key; a wave whose rows share one adapter counts them at once, by its first lane
+  auto shared_by = [&](int a) {
     const int first = __builtin_amdgcn_readfirstlane(a);
-    const uint64_t same = __ballot(in && a == first);
+    return __ballot(a >= 0 && a != first) == 0;
+  };
+  auto count = [&](int a) {
+    const bool all = shared_by(a);
+    const uint64_t live = __ballot(a >= 0);  // with all lanes active: in the branch below it would count the first alone
+    const int n = all ? __popcll(live) : 1;
     int place = 0;
-    if (first >= 0 && same == live) {
-      if (lane == 0) place = atomicAdd(&at[first], __popcll(live));
-      place = __builtin_amdgcn_readfirstlane(place) + __popcll(live & lanemask_lt());
-    } else if (in) {
-      place = atomicAdd(&at[a], 1);
-    }
+    if (a >= 0 && (!all || lane == 0)) place = atomicAdd(&at[a], n);
     return place;
   };
   // eight keys to a thread at a time, so that their loads overlap; the first 8192 rows' stay in registers
@@ -52,13 +49,13 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) keep[i] = key(i * 1024 + tid);
 #pragma unroll
-  for (int i = 0; i < KEYS; ++i) take(keep[i]);
+  for (int i = 0; i < KEYS; ++i) count(keep[i]);
   for (int m = KEYS * 1024; m < p.M; m += KEYS * 1024) {
     int k[KEYS];
 #pragma unroll
     for (int i = 0; i < KEYS; ++i) k[i] = key(m + i * 1024 + tid);
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) take(k[i]);
+    for (int i = 0; i < KEYS; ++i) count(k[i]);
   }
   __syncthreads();
   // exclusive running sum, five counters to a thread
@@ -85,23 +82,26 @@ __global__ __launch_bounds__(1024) void k_lora_sort(const SortParams p) {
     const int i = tid * PER + j;
     if (i <= p.L) at[i] = base;
     base += c[j];
-    if (i < p.L) p.ends[i] = base;
   }
   __syncthreads();
-  auto put = [&](int m, int a) {
-    const int place = take(a);
-    if (a < 0) return;
-    p.perm[place] = m;
-    p.sid[place] = a;
-  };
+  auto put = [&](int m0, const int (&k)[KEYS]) {
+    int place[KEYS];
 #pragma unroll
-  for (int i = 0; i < KEYS; ++i) put(i * 1024 + tid, keep[i]);
+    for (int i = 0; i < KEYS; ++i) place[i] = count(k[i]);
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      if (shared_by(k[i])) place[i] = __builtin_amdgcn_readfirstlane(place[i]) + __popcll(__ballot(k[i] >= 0) & lanemask_lt());
+      if (k[i] < 0) continue;
+      p.perm[place[i]] = m0 + i * 1024 + tid;
+      p.sid[place[i]] = k[i];
+    }
+  };
+  put(0, keep);
   for (int m = KEYS * 1024; m < p.M; m += KEYS * 1024) {
     int k[KEYS];
 #pragma unroll
     for (int i = 0; i < KEYS; ++i) k[i] = key(m + i * 1024 + tid);
-#pragma unroll
-    for (int i = 0; i < KEYS; ++i) put(m + i * 1024 + tid, k[i]);
+    put(m, k);
   }
 }
 
@@ -109,7 +109,7 @@ struct ShrinkParams {
   const uint16_t* x;
   const uint16_t* a;      // [L, R, K]
   const float* scales;    // [L]
-  const int32_t *perm, *sid, *ends;
+  const int32_t *perm, *sid;
   uint16_t* t;            // [M, 2R]
   float* tf;              // [M]
   float* part;            // [K ranges][M][R], with more than one
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   __shared__ float sum[RF * 16][ROWS + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, kq = (lane >> 4) * 8;
-  const int m0 = blockIdx.x * ROWS, last = min(m0 + ROWS, p.M);
+  const int m0 = blockIdx.x * ROWS;
   int id[FX];
   const uint16_t* xr[FX];
 #pragma unroll
@@ -176,11 +176,13 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   for (int i = 0; i < RF; ++i)
 #pragma unroll
     for (int j = 0; j < FX; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int pos = m0;
-  while (pos < last) {
-    const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
-    if (a >= p.L) break;
-    pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
+  uint64_t rows[FX];  // those whose adapter is still to come
+#pragma unroll
+  for (int j = 0; j < FX; ++j) rows[j] = __ballot(id[j] < p.L);
+  while (rows[0] | rows[FX - 1]) {
+    const int a = rows[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(rows[0])) : __builtin_amdgcn_readlane(id[FX - 1], __builtin_ctzll(rows[FX - 1]));
+#pragma unroll
+    for (int j = 0; j < FX; ++j) rows[j] &= ~__ballot(id[j] == a);
     f32x4 tmp[RF][FX];
     const uint16_t* ar[RF];
 #pragma unroll
@@ -320,20 +322,20 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
   u32x4 b[4][2];
   int held = -1;
   for (int x = 0; x < frags; ++x) {
-    const int r0 = (blockIdx.x * frags + x) * 16, end = min(r0 + 16, p.M);
+    const int r0 = (blockIdx.x * frags + x) * 16;
     if (r0 >= p.M) return;
     const int row = min(r0 + c, p.M - 1);
-    const int id = p.sid[row];
+    const int id = r0 + c < p.M ? p.sid[row] : p.L;
     const float f = p.tf[row];
+    const int64_t orow = p.perm[row];
     const uint16_t* t = p.t + (int64_t)row * 2 * p.R;
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int pos = r0;
-    while (pos < end) {
-      const int a = __builtin_amdgcn_readfirstlane(p.sid[pos]);
-      if (a >= p.L) break;
-      pos = max(pos + 1, __builtin_amdgcn_readfirstlane(p.ends[a]));
+    uint64_t rows = __ballot(id < p.L);
+    while (rows) {
+      const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rows));
+      rows &= ~__ballot(id == a);
       for (int c0 = 0; c0 < p.R; c0 += 64) {
         u32x4 hi[2], lo[2];
         const u32x4 zero = {0, 0, 0, 0};
@@ -371,7 +373,6 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
       }
     }
     if (r0 + c >= p.M) continue;
-    const int64_t orow = p.perm[row];
     uint16_t* out = (uint16_t*)p.out[0] + orow * p.ldo[0];
     const uint16_t* add = p.add ? (const uint16_t*)p.add + orow * p.ld_add : nullptr;
 #pragma unroll
