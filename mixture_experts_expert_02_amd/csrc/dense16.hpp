@@ -55,12 +55,19 @@ struct Params {
   int32_t vec;             // out and add take 16-byte accesses at multiples of 8 columns
   int32_t N8;              // N rounded down to a multiple of 8
   int32_t R, L;
-  const uint16_t* t;       // [M, 2R] upper and lower parts of the scaled x A^T, rows in sorted order
+  const uint16_t* t;       // upper and lower parts of the scaled x A^T, rows in sorted order (part_at)
   const float* tf;         // [M] their rows' powers of two
   const uint16_t* b;       // [L, N, R]
   const int32_t* perm;     // sorted row -> row
   const int32_t* sid;      // adapter of the sorted row, L where it has none
 };
+
+// Where value r < 2 R of sorted row m of t is (the upper parts of R ranks, then the lower ones): eight values of 32 rows
+// side by side, so that the MFMA's operand of 32 rows is 1 KB in one piece (rows of 2 R values cost the 256-row tiles
+// of 8192 x 2048 x 7168 with rank 64 37 us in place of 12: an instruction then asks for 32 lines).
+__host__ __device__ __forceinline__ int64_t part_at(int m, int r, int R) {
+  return (((int64_t)(m >> 5) * (R >> 2) + (r >> 3)) * 32 + (m & 31)) * 8 + (r & 7);
+}
 
 // ------------------------------------------------------------ activations
 __device__ __forceinline__ float sigm(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }

@@ -156,14 +156,12 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   }
 
   f32x16 acc[2][2][J];  // [N half][M half][32 rows]
+  auto clear = [&](int hm, int j) {
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+    for (int hn = 0; hn < 2; ++hn)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[a][b][j][r] = 0.f;
+      for (int r = 0; r < 16; ++r) acc[hn][hm][j][r] = 0.f;
+  };
 
   BigFrag<MM, HM> fm[J][4];   // 256 rows: an M half's [32 rows][K step]
   BigFrag<NM, 128> fn[3][4];  // and N halves' [set][K step]
@@ -199,25 +197,41 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   };
 
   // ---- adapters, a fragment of 32 sorted rows at a time, while the first stages load: both operands straight
-  // into registers (t and the factor's rows are as the MFMA wants them). A fragment that holds rows of several adapters gets each one's product in registers of its own
-  // and adds it to the rows it belongs to, so that what an adapter holds (an infinity, say) reaches no other
-  // adapter's rows.
+  // into registers (t and the factor's rows are as the MFMA wants them), t of all the wave's fragments at once, in the
+  // registers that their results take over. A fragment that holds rows of several adapters gets each one's product in
+  // registers of its own and adds it to the rows it belongs to, so that what an adapter holds (an infinity, say) reaches
+  // no other adapter's rows.
   auto adapters = [&]() {
     constexpr int F = 2 * J;
     int id[F];
     float f[F];
-    u32x4 hi[4], lo[4], b[2][4];
+    u32x4 hi[F][4], lo[F][4], b[2][4];
     const u32x4 zero = {0, 0, 0, 0};
     auto first_row = [&](int x) { return m0 + (x / J) * HM + wm * (HM / 2) + (x % J) * 32; };
+    // addresses as one for the wave and 32 bits for the lane
     auto load_t = [&](int x, int c0) {
-      const uint16_t* t = p.t + (int64_t)min(first_row(x) + lr, p.M - 1) * 2 * p.R;
+      const uint8_t* t = uniform(p.t + part_at(min(first_row(x), p.M - 1) & ~31, c0, p.R));
+      const uint8_t* l = t + p.R * 64;
+      const uint32_t at = lk * 512 + lr * 16;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const int k = c0 + 16 * ks + 8 * lk;
-        hi[ks] = lo[ks] = zero;
-        if (k < p.R) {
-          hi[ks] = *(const u32x4*)(t + k);
-          lo[ks] = *(const u32x4*)(t + p.R + k);
+        hi[x][ks] = lo[x][ks] = zero;
+        if (c0 + 16 * ks + 8 * lk < p.R) {
+          hi[x][ks] = *(const u32x4*)(t + (at + ks * 1024));
+          lo[x][ks] = *(const u32x4*)(l + (at + ks * 1024));
+        }
+      }
+    };
+    auto load_b = [&](int a, int c0) {
+#pragma unroll
+      for (int hn = 0; hn < 2; ++hn) {
+        const int col = n0 + wn * 64 + hn * 32;
+        const uint8_t* w = uniform(p.b + ((int64_t)a * p.N + col) * p.R + c0);
+        const uint32_t at = lr * (p.R * 2) + lk * 16;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          b[hn][ks] = zero;
+          if (c0 + 16 * ks + 8 * lk < p.R && col + lr < p.N) b[hn][ks] = *(const u32x4*)(w + (at + ks * 32));
         }
       }
     };
@@ -227,28 +241,20 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       id[x] = row < p.M ? p.sid[row] : p.L;
       f[x] = p.tf[min(row, p.M - 1)];
     }
+#pragma unroll
+    for (int x = 0; x < F; ++x) load_t(x, 0);
     int held = -1;  // whose factor b holds
 #pragma unroll
     for (int x = 0; x < F; ++x) {
-      load_t(x, 0);
+      clear(x / J, x % J);
       uint64_t rows = __ballot(id[x] < p.L);
       while (rows) {
         const int a = __builtin_amdgcn_readlane(id[x], __builtin_ctzll(rows));
         const bool mine = id[x] == a;
         rows &= ~__ballot(mine);
         for (int c0 = 0; c0 < p.R; c0 += 64) {
-          if (held != a || p.R > 64) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-              for (int hn = 0; hn < 2; ++hn) {
-                const int k = c0 + 16 * ks + 8 * lk, col = n0 + wn * 64 + hn * 32 + lr;
-                b[hn][ks] = zero;
-                if (k < p.R && col < p.N) b[hn][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
-              }
-            held = a;
-          }
-          if (p.R > 64) load_t(x, c0);
+          if (held != a || p.R > 64) load_b(a, c0);
+          held = a;
 #pragma unroll
           for (int hn = 0; hn < 2; ++hn) {
             f32x16 tmp;
@@ -257,18 +263,25 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               if (c0 + 16 * ks >= p.R) break;
-              tmp = mfma<DT>(b[hn][ks], hi[ks], tmp);
-              tmp = mfma<DT>(b[hn][ks], lo[ks], tmp);
+              tmp = mfma<DT>(b[hn][ks], hi[x][ks], tmp);
+              tmp = mfma<DT>(b[hn][ks], lo[x][ks], tmp);
             }
             if (mine) {
 #pragma unroll
               for (int r = 0; r < 16; ++r) acc[hn][x / J][x % J][r] += tmp[r] * f[x];
             }
           }
+          if (p.R > 64) load_t(x, c0 + 64 < p.R ? c0 + 64 : 0);
         }
       }
     }
   };
+  if (MODE != LORA || split != 0) {
+#pragma unroll
+    for (int hm = 0; hm < 2; ++hm)
+#pragma unroll
+      for (int j = 0; j < J; ++j) clear(hm, j);
+  }
 
   // ---- main loop
   // The two waves of a SIMD (wm = 0 and 1) work half a phase apart: while one multiplies, the other reads the operands

@@ -208,7 +208,7 @@ LoraLayout lora_layout(const moe_lora_problem& p, int rows) {
   l.sid = up256((size_t)rows * 4);
   l.tf = l.sid + up256((size_t)rows * 4);
   l.t = l.tf + up256((size_t)rows * 4);
-  l.part = l.t + up256((size_t)rows * 4 * p.R);
+  l.part = l.t + up256((size_t)cdiv(rows, 32) * 32 * 4 * p.R);
   // partial results of the first product, then of the second; the last part of a call may be its smallest, with the most ranges
   size_t part = 0;
   for (int64_t n : {(int64_t)rows, (int64_t)p.M % rows})

@@ -110,7 +110,7 @@ struct ShrinkParams {
   const uint16_t* a;      // [L, R, K]
   const float* scales;    // [L]
   const int32_t *perm, *sid;
-  uint16_t* t;            // [M, 2R]
+  uint16_t* t;            // see part_at
   float* tf;              // [M]
   float* part;            // [K ranges][M][R], with more than one
   int64_t ldx;
@@ -120,9 +120,9 @@ struct ShrinkParams {
 // A row's results over the power of two above their largest, in two parts of the
 // type, 16 significand bits or more together: what the second product loses by its 16-bit
 // operands is far below the output's own rounding, and float16 keeps results of any size.
-// v: this lane's ranks r0, r0 + LANES, ..; LANES lanes of the wave hold the row.
+// v: this lane's ranks r0, r0 + LANES, .. of row m; LANES lanes of the wave hold the row.
 template <int DT, int LANES, int N>
-__device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, uint16_t* t, float* tf) {
+__device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, int m, uint16_t* t, float* tf) {
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(v[i]));
@@ -132,20 +132,15 @@ __device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, uint16
   int e = most > 0.f && most < INFINITY ? ilogbf(most) + 1 : 0;
   e = min(max(e, -120), 120);
   const float inv = ldexpf(1.f, -e);
-  if (r0 == 0) *tf = ldexpf(1.f, e);
+  if (r0 == 0) tf[m] = ldexpf(1.f, e);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int r = r0 + i * LANES;
     if (r >= R) continue;
     const float w = v[i] * inv, h = round_to<DT>(w);
     const float l = fabsf(h) < INFINITY ? w - h : 0.f;
-    if constexpr (DT == T_BF16) {
-      ((__bf16*)t)[r] = (__bf16)h;
-      ((__bf16*)t)[R + r] = (__bf16)l;
-    } else {
-      ((_Float16*)t)[r] = (_Float16)h;
-      ((_Float16*)t)[R + r] = (_Float16)l;
-    }
+    store1<DT>(t, part_at(m, r, R), h);
+    store1<DT>(t, part_at(m, R + r, R), l);
   }
 }
 
@@ -259,7 +254,7 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   const float sc = a < p.L ? p.scales[a] : 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] *= sc;
-  store_parts<DT, LANES, N>(v, r0, p.R, p.t + (int64_t)(m0 + m) * 2 * p.R, p.tf + m0 + m);
+  store_parts<DT, LANES, N>(v, r0, p.R, m0 + m, p.t, p.tf);
 }
 
 // The K ranges' results joined in their order, a row to a wave, N ranks to a lane.
@@ -278,7 +273,7 @@ __global__ __launch_bounds__(256) void k_lora_finish(const ShrinkParams p, int r
     for (int k = 0; k < ranges; ++k) s += p.part[((size_t)k * p.M + m) * p.R + r];
     v[i] = a < p.L && lane + 64 * i < p.R ? s * sc : 0.f;
   }
-  store_parts<DT, 64, N>(v, lane, p.R, p.t + (int64_t)m * 2 * p.R, p.tf + m);
+  store_parts<DT, 64, N>(v, lane, p.R, m, p.t, p.tf);
 }
 
 // Few rows: row blockIdx.x's products with eight ranks of its adapter, two to a wave, in float32, scaled;
@@ -328,7 +323,6 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
     const int id = r0 + c < p.M ? p.sid[row] : p.L;
     const float f = p.tf[row];
     const int64_t orow = p.perm[row];
-    const uint16_t* t = p.t + (int64_t)row * 2 * p.R;
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -344,8 +338,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
           const int k = c0 + 32 * ks + 8 * g;
           hi[ks] = lo[ks] = zero;
           if (k < p.R) {
-            hi[ks] = *(const u32x4*)(t + k);
-            lo[ks] = *(const u32x4*)(t + p.R + k);
+            hi[ks] = *(const u32x4*)(p.t + part_at(row, k, p.R));
+            lo[ks] = *(const u32x4*)(p.t + part_at(row, p.R + k, p.R));
           }
           if (held != a || p.R > 64) {
 #pragma unroll
