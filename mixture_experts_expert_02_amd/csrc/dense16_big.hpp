@@ -42,6 +42,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // side by side, 64 (i / 32) + 32 h + i % 32, so that a wave's columns are 64 neighbours
   int m_row[LM], m_chunk[LM], n_row[2], n_chunk[2];
   uint32_t g_off[2][LM];  // LORA: rows of x are gathered
+  int g_row[2][LM];
 #pragma unroll
   for (int q = 0; q < LM; ++q) {
     const int i = LM * wave + q, r = i * 8 + (lane >> 3);
@@ -53,7 +54,11 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     if constexpr (MODE == LORA) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        g_off[h][q] = m0 + h * HM + r < p.M ? (uint32_t)p.perm[m0 + h * HM + r] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+      {
+        const bool in = m0 + h * HM + r < p.M;
+        g_row[h][q] = in ? p.perm[m0 + h * HM + r] : -1;
+        g_off[h][q] = in ? (uint32_t)g_row[h][q] * (uint32_t)(p.ldm[0] * 2) + m_chunk[q] * 16 : kNoLoad;
+      }
     }
   }
 #pragma unroll
@@ -128,6 +133,22 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     load(std::bool_constant<NM>{}, std::integral_constant<int, 2>{}, cn[h], n_row, n_chunk, nullptr,
          smem + N_AT + (buf * 2 + h) * HALF + wave * 2048);
   };
+
+  // LORA: the addend's lines of this tile are asked for a few stages before the end, by loads whose values nobody
+  // reads, so that the epilogue, in which all workgroups of a round meet, finds them nearer than memory.
+  __shared__ __attribute__((aligned(16))) uint8_t unread[MODE == LORA ? 256 : 16];
+  auto touch_addend = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < LM; ++q) {
+        const int c = n0 + (lane & 7) * 64;
+        if (g_row[h][q] >= 0 && (lane & 7) < 4 && c < p.N8)
+          __builtin_amdgcn_global_load_lds((const uint16_t*)p.add + (int64_t)g_row[h][q] * p.ld_add + c, (lds_void*)(lds_u8*)unread, 4, 0, 0);
+      }
+  };
+  const bool touch = MODE == LORA && p.add && p.vec && p.splits == 1;
+  const int touch_at = max(0, (nst - 8) & ~1);
 
   // ---- operand reads: bytes inside a half
   const int tr = (lane >> 2) & 3;
@@ -389,6 +410,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       barrier();
       if (wm) barrier();
       for (int s = 0; s < nst; s += 2) {
+        if (MODE == LORA && touch && s == touch_at) touch_addend();
         MOE_D16_STAGE(s, 0, 0, 1)
         if (s + 1 >= nst) break;
         MOE_D16_STAGE(s + 1, 1, 1, 0)
@@ -424,32 +446,44 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       v[r >> 2][r & 3] += p.bias[w][min(c, p.N - 1)];
     }
   };
+  int orow[2][J];
 #pragma unroll
-  for (int hm = 0; hm < 2; ++hm) {
-    uint2 old[J][2][4];  // LORA's addend, of both fragments before either is stored
-    int orow[J];
+  for (int hm = 0; hm < 2; ++hm)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int row = m0 + hm * HM + wm * (HM / 2) + j * 32 + lr;
-      orow[j] = MODE == LORA ? p.perm[min(row, p.M - 1)] : row;
-      if constexpr (MODE == LORA) {
-        if (p.add && p.vec && p.splits == 1 && row < p.M) {
-#pragma unroll
-          for (int hn = 0; hn < 2; ++hn)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int c = colw + hn * STEP + 8 * q + 4 * lk;
-              old[j][hn][q] = {0, 0};  // columns behind the last multiple of 8 get theirs where they are stored
-              if (c < p.N8) old[j][hn][q] = *(const uint2*)((const uint16_t*)p.add + orow[j] * p.ld_add + c);
-            }
-        }
-      }
+      orow[hm][j] = MODE == LORA ? p.perm[min(row, p.M - 1)] : row;
     }
+  // LORA's addend comes as whole lines, eight lanes to a row's 64 columns, all of it before the first result is stored,
+  // and takes its place beside the results through LDS (asked for in their order, 16 bytes of 32 rows an instruction,
+  // it cost the 256-row tiles of 8192 x 2048 x 7168 33 us).
+  constexpr int PITCH = 144;
+  uint8_t* strip = smem_arr + wave * 32 * PITCH;
+  u32x4 line[2][J][4];
+  const bool with_add = MODE == LORA && p.add && p.vec && p.splits == 1;
+  if constexpr (MODE == LORA) {
+    if (with_add) {
+      const int c = colw + (lane & 7) * 8;
+#pragma unroll
+      for (int hm = 0; hm < 2; ++hm)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 3), o = __shfl(orow[hm][j], r);
+            line[hm][j][i] = u32x4{0, 0, 0, 0};  // columns behind the last multiple of 8 get theirs where they are stored
+            if (m0 + hm * HM + wm * (HM / 2) + j * 32 + r < p.M && c < p.N8)
+              line[hm][j][i] = *(const u32x4*)((const uint16_t*)p.add + o * p.ld_add + c);
+          }
+    }
+  }
+#pragma unroll
+  for (int hm = 0; hm < 2; ++hm) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int row = m0 + hm * HM + wm * (HM / 2) + j * 32 + lr;
       const bool ok = row < p.M;
-      const int64_t o = orow[j];
+      const int64_t o = orow[hm][j];
       float v[2][4][4];
 #pragma unroll
       for (int hn = 0; hn < 2; ++hn)
@@ -503,15 +537,25 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
           else store_fragment<DT>((uint16_t*)p.out[z] + at, v[hn], lk, left, ok);
         }
       } else {
+        if (with_add) {
+          wave_sync();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *(u32x4*)(strip + (i * 8 + (lane >> 3)) * PITCH + (lane & 7) * 16) = line[hm][j][i];
+          wave_sync();
+        }
 #pragma unroll
         for (int hn = 0; hn < 2; ++hn) {
           const int col = colw + hn * STEP;
           uint16_t* out = (uint16_t*)p.out[0] + o * p.ldo[0] + col;
           if (p.bias[0]) add_bias(0, col, v[hn]);
           if (p.vec) {
-            if (p.add) {
+            if (with_add) {
 #pragma unroll
-              for (int r = 0; r < 16; ++r) v[hn][r >> 2][r & 3] += load1<DT>(&old[j][hn][r >> 2], r & 3);
+              for (int q = 0; q < 4; ++q) {
+                const uint2 x = *(const uint2*)(strip + lr * PITCH + (hn * 32 + 8 * q + 4 * lk) * 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
+              }
             }
             store_fragment<DT>(out, v[hn], lk, p.N8 - col, ok);
           }
