@@ -21,6 +21,7 @@
 
 #include <type_traits>
 
+#include "dense16_rule.hpp"
 #include "elem.hpp"
 
 namespace moe {
@@ -28,8 +29,6 @@ namespace d16 {
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) void lds_void;
-
-enum Mode { GATED, DX, DW, LORA };
 
 constexpr int BK = 64;                    // K values of a stage
 constexpr uint32_t kNoLoad = 0x80000000u; // buffer offset past any operand: reads 0

@@ -83,32 +83,6 @@ int with_type16(int32_t type, F f) {
 }
 
 // ------------------------------------------------------------ tiles
-struct Plan {
-  int bm, splits;
-  size_t part;  // bytes of partial results
-};
-// MODE's planes of results, columns of a tile, stages of all of K
-Plan plan_of(int mode, int64_t M, int64_t N, int64_t K) {
-  const int planes = mode == GATED || mode == DW ? 2 : 1, tn = mode == GATED ? 128 : 256;
-  const int64_t stages = cdiv(K, BK) * (mode == DX ? 2 : 1);
-  Plan best{256, 1, 0};
-  double least = 1e30;
-  for (int bm : {256, 128}) {
-    const int64_t tiles = cdiv(M, bm) * cdiv(N, tn) * (mode == DW ? 2 : 1);
-    for (int s = 1; s <= 16 && s * 4 <= std::max<int64_t>(stages, 4); ++s) {
-      const double rounds = (double)cdiv(tiles * s, 256);
-      const double part = s > 1 ? (double)s * planes * M * N * 4 : 0;
-      if (part > 256e6) break;
-      const double us = rounds * (cdiv(stages, s) * (bm == 256 ? 1.0 : 0.55) + (bm == 256 ? 8 : 6)) + (s > 1 ? 4 + part * 2 / 5e6 : 0);
-      if (us < least) {
-        least = us;
-        best = {bm, s, s > 1 ? up256((size_t)s * planes * M * ((N + 7) & ~7) * 4) : 0};
-      }
-    }
-  }
-  return best;
-}
-
 template <int DT, int MODE, int BM>
 int launch_big(Params& q, hipStream_t s) {
   q.mt = (int)cdiv(q.M, BM);
@@ -187,13 +161,6 @@ int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_
 // Rows of x are read by 32-bit offsets from its start, so a call of more goes in parts.
 int lora_rows(const moe_lora_problem& p, int64_t ldx) {
   return (int)std::min<int64_t>({(int64_t)p.M, (0x7fffffff - 2 * (int64_t)p.K) / (2 * ldx) / 256 * 256, (int64_t)1 << 20});
-}
-// The first product: 16-row fragments of a workgroup, and K ranges: at most one workgroup to a compute unit (us of the
-// kernel: 1000 rows of 4096, rank 24, 64 adapters 31, 17, 8.7, 12.5 and 17 with 1, 2, 4, 8 and 16 ranges; 256 of 7168,
-// rank 64, 34, 19, 11.6, 7.6 and 6.0; 8192 of 2048 18.6, 21 and 28 with 1, 2 and 4), at least 16 steps of 32 to a range.
-int shrink_frags(int64_t M, int R) { return R <= 64 && M > 2048 ? 2 : 1; }
-int shrink_ranges(int64_t M, int K, int R) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({256 / cdiv(M, 16 * shrink_frags(M, R)), cdiv(K, 32) / 16, 16}));
 }
 struct LoraLayout {
   size_t perm, sid, tf, t, part, bytes;

@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import mixture_experts_expert_02_amd as moe
+from dense16_cases import LORA, LORA_LARGE
 from oracle import dense16 as O
 
 pytestmark = pytest.mark.gpu
@@ -69,9 +70,7 @@ def check(got, c):
     assert r <= 1, r
 
 
-SHAPES = [(1, 64, 64, 8, 1), (1, 2048, 7168, 16, 8), (2, 8, 1, 8, 3), (3, 72, 33, 24, 2), (7, 1000, 200, 64, 5), (16, 264, 520, 128, 4),
-          (17, 128, 131, 256, 3), (33, 2880, 2895, 32, 32), (64, 512, 257, 16, 64), (65, 136, 72, 40, 70), (130, 776, 328, 64, 9),
-          (200, 64, 1000, 8, 1), (300, 1032, 515, 32, 16), (515, 520, 264, 16, 300), (1100, 264, 384, 64, 6)]
+SHAPES = LORA
 
 
 @pytest.mark.parametrize("M,K,N,R,L", SHAPES)
@@ -170,7 +169,7 @@ def test_rows_do_not_depend_on_their_batch():
         assert torch.equal(moe.lora_linear(**c), whole)
 
 
-@pytest.mark.parametrize("M,K,N,R,L", [(4099, 520, 2900, 24, 5), (4096, 72, 2057, 40, 90), (2300, 2056, 4112, 128, 3), (9000, 64, 1100, 8, 12)])
+@pytest.mark.parametrize("M,K,N,R,L", LORA_LARGE)
 @pytest.mark.parametrize("dt", T16)
 @pytest.mark.parametrize("ids", ["token", "run"])
 def test_many_rows(M, K, N, R, L, dt, ids):
