@@ -360,6 +360,30 @@ __device__ __forceinline__ void store_fragment_f32(float* base, const float (&v)
     if (row_ok && 8 * q + 4 * lk < left) *(f32x4*)(base + 8 * q + 4 * lk) = f32x4{v[q][0], v[q][1], v[q][2], v[q][3]};
 }
 
+// DW's 4 x 4 values of the lane at the output's row and the fragment's first column
+template <int DT>
+__device__ __forceinline__ void finish_dw(const Params& p, int z, int64_t row, int col, float (&v)[4][4], int lk, bool ok) {
+  const int64_t at = row * p.ldo[z] + col;
+  const int left = p.N - col;
+  if (p.accumulate) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!ok || 8 * q + 4 * lk >= left) continue;
+      if (p.f32_out) {
+        const f32x4 x = *(const f32x4*)((const float*)p.out[z] + at + 8 * q + 4 * lk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[q][i] += x[i];
+      } else {
+        const uint2 x = *(const uint2*)((const uint16_t*)p.out[z] + at + 8 * q + 4 * lk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[q][i] += load1<DT>(&x, i);
+      }
+    }
+  }
+  if (p.f32_out) store_fragment_f32((float*)p.out[z] + at, v, lk, left, ok);
+  else store_fragment<DT>((uint16_t*)p.out[z] + at, v, lk, left, ok);
+}
+
 // Partial results joined in the order of their K ranges, eight columns to a thread.
 template <int DT, int MODE>
 __global__ __launch_bounds__(256) void k_join(const Params p) {

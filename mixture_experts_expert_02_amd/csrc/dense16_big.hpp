@@ -515,27 +515,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
           store_fragment<DT>((uint16_t*)p.out[0] + o * p.ldo[0] + colw + hn * STEP, v[hn], lk, p.N - colw - hn * STEP, ok);
       } else if constexpr (MODE == DW) {
 #pragma unroll
-        for (int hn = 0; hn < 2; ++hn) {
-          const int64_t at = o * p.ldo[z] + colw + hn * STEP;
-          const int left = p.N - colw - hn * STEP;
-          if (p.accumulate) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (!ok || 8 * q + 4 * lk >= left) continue;
-              if (p.f32_out) {
-                const f32x4 x = *(const f32x4*)((const float*)p.out[z] + at + 8 * q + 4 * lk);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[hn][q][i] += x[i];
-              } else {
-                const uint2 x = *(const uint2*)((const uint16_t*)p.out[z] + at + 8 * q + 4 * lk);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
-              }
-            }
-          }
-          if (p.f32_out) store_fragment_f32((float*)p.out[z] + at, v[hn], lk, left, ok);
-          else store_fragment<DT>((uint16_t*)p.out[z] + at, v[hn], lk, left, ok);
-        }
+        for (int hn = 0; hn < 2; ++hn) finish_dw<DT>(p, z, o, colw + hn * STEP, v[hn], lk, ok);
       } else {
         if (with_add) {
           wave_sync();

@@ -10,6 +10,7 @@
 #include "../../include/moe_experts.h"
 #include "dense16.hpp"
 #include "dense16_big.hpp"
+#include "dense16_outer.hpp"
 #include "gated_grad.hpp"
 #include "lora.hpp"
 
@@ -92,6 +93,16 @@ int launch_big(Params& q, hipStream_t s) {
   hipLaunchKernelGGL((k_big<DT, MODE, BM>), dim3((unsigned)n), dim3(512), 0, s, q);
   if (q.splits > 1)
     hipLaunchKernelGGL((k_join<DT, MODE>), dim3((unsigned)cdiv((int64_t)q.M * ((q.N + 7) / 8), 256), MODE == DW ? 2 : 1), dim3(256), 0, s, q);
+  return launch_status();
+}
+
+template <int DT>
+int launch_outer(Params& q, hipStream_t s) {
+  q.mt = (int)cdiv(q.M, 128);
+  q.nt = (int)cdiv(q.N, 128);
+  const int64_t n = cdiv((int64_t)q.mt * q.nt * 2, 8) * 8;
+  if (n > kMaxGrid) return MOE_ENOTSUP;
+  hipLaunchKernelGGL((k_outer<DT>), dim3((unsigned)n), dim3(256), outer_lds(q.K), s, q);
   return launch_status();
 }
 
@@ -377,7 +388,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.K = f.M;
       d.f32_out = f32;
       d.accumulate = p->accumulate;
-      rc = launch<DT, DW>(d, ws + l.part, s);
+      rc = f.M <= kOuterRows ? launch_outer<DT>(d, s) : launch<DT, DW>(d, ws + l.part, s);
     }
     return rc;
   });
