@@ -48,6 +48,7 @@ struct Params {
   int64_t ld_keep[2];
   ActParams act;
   int32_t f32_out, accumulate;  // DW
+  int32_t fold;            // DX: rows m and m + fold are one row's upper and lower parts; DW: K rows k and k + fold; 0: none
   // LORA
   const void* add;
   int64_t ld_add;
@@ -384,12 +385,12 @@ __device__ __forceinline__ void finish_dw(const Params& p, int z, int64_t row, i
   else store_fragment<DT>((uint16_t*)p.out[z] + at, v, lk, left, ok);
 }
 
-// Partial results joined in the order of their K ranges, eight columns to a thread.
+// Partial results joined in the order of their K ranges, eight columns to a thread; DX: upper and lower parts of rows too.
 template <int DT, int MODE>
 __global__ __launch_bounds__(256) void k_join(const Params p) {
-  const int cpr = (p.N + 7) / 8, z = blockIdx.y;
+  const int cpr = (p.N + 7) / 8, z = blockIdx.y, rows = MODE == DX && p.fold ? p.fold : p.M;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)p.M * cpr) return;
+  if (i >= (int64_t)rows * cpr) return;
   const int row = (int)(i / cpr), col = (int)(i - (int64_t)row * cpr) * 8;
   float v[8], u[8];
 #pragma unroll
@@ -404,6 +405,13 @@ __global__ __launch_bounds__(256) void k_join(const Params p) {
       load8<T_FP32>(part_of<MODE>(p, s, 1, row, col), 0, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] += a[j];
+    }
+    if constexpr (MODE == DX) {
+      if (p.fold) {
+        load8<T_FP32>(part_of<MODE>(p, s, z, row + p.fold, col), 0, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += a[j];
+      }
     }
   }
   finish8<DT, MODE>(p, z, MODE == LORA ? p.perm[row] : row, col, v, u);

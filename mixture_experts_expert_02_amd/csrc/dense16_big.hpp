@@ -489,7 +489,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       for (int hn = 0; hn < 2; ++hn)
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[hn][r >> 2][r & 3] = acc[hn][hm][j][r];
-      if (p.splits > 1) {
+      if (p.splits > 1 || (MODE == DX && p.fold)) {
 #pragma unroll
         for (int hn = 0; hn < 2; ++hn) {
           const int col = MODE == GATED ? colw : colw + hn * STEP;

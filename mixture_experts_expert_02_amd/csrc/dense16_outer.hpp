@@ -26,14 +26,14 @@ __global__ __launch_bounds__(256, 4) void k_outer(const Params p) {
   const int ksteps = (p.K + 15) / 16;
   {
     const int64_t ldm = p.ldm[z], ldn = p.ldn[0];
-    const auto rm = rsrc(p.m[z] + m0, ((p.K - 1) * ldm + p.M - m0) * 2), rn = rsrc(p.n[0] + n0, ((p.K - 1) * ldn + p.N - n0) * 2);
+    const auto rm = rsrc(p.m[z] + m0, ((p.K - 1) * ldm + p.M - m0) * 2), rn = rsrc(p.n[0] + n0, ((p.fold ? p.fold - 1 : p.K - 1) * ldn + p.N - n0) * 2);
     for (int i = wave; i < ksteps * 4; i += 4) {  // 4 K rows of either operand
       int k, chunk;
       major_src<128>(i, lane, k, chunk);
       // rows past K read as zero: past the descriptor's end, or beyond it by offset
       const bool in = k < p.K;
       dma(rm, smem + i * 1024, in ? (uint32_t)(k * ldm * 2 + chunk * 16) : kNoLoad, 0);
-      dma(rn, smem + ksteps * 4096 + i * 1024, in ? (uint32_t)(k * ldn * 2 + chunk * 16) : kNoLoad, 0);
+      dma(rn, smem + ksteps * 4096 + i * 1024, in ? (uint32_t)((p.fold && k >= p.fold ? k - p.fold : k) * ldn * 2 + chunk * 16) : kNoLoad, 0);
     }
   }
   f32x16 acc[2][2];

@@ -91,8 +91,10 @@ int launch_big(Params& q, hipStream_t s) {
   const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : 1) * q.splits, 8) * 8;
   if (n > kMaxGrid / 2) return MOE_ENOTSUP;
   hipLaunchKernelGGL((k_big<DT, MODE, BM>), dim3((unsigned)n), dim3(512), 0, s, q);
-  if (q.splits > 1)
-    hipLaunchKernelGGL((k_join<DT, MODE>), dim3((unsigned)cdiv((int64_t)q.M * ((q.N + 7) / 8), 256), MODE == DW ? 2 : 1), dim3(256), 0, s, q);
+  const bool fold = MODE == DX && q.fold;
+  if (q.splits > 1 || fold)
+    hipLaunchKernelGGL((k_join<DT, MODE>), dim3((unsigned)cdiv((int64_t)(fold ? q.fold : q.M) * ((q.N + 7) / 8), 256), MODE == DW ? 2 : 1),
+                       dim3(256), 0, s, q);
   return launch_status();
 }
 
@@ -137,6 +139,10 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
+// Rows up to which dg and du go in two parts.
+constexpr int kPartRows = 64;
+static_assert(2 * kPartRows <= kOuterRows, "k_outer takes both parts");
+int grad_parts(int M) { return M <= kPartRows ? 2 : 1; }
 // Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
 int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
@@ -144,12 +150,16 @@ struct GradLayout {
 };
 GradLayout grad_layout(const moe_gated_problem& p) {
   GradLayout l;
-  const size_t mi = up256((size_t)p.M * p.I * 2);
+  const int M = p.M * grad_parts(p.M);
+  const size_t mi = up256((size_t)M * p.I * 2);
   l.dg = 0;
   l.du = mi;
   l.sums = 2 * mi;
   l.part = l.sums + up256((size_t)cdiv(p.M, grad_rows(p.M)) * 2 * p.I * 4);
-  l.bytes = l.part + std::max(plan_of(DX, p.M, p.H, p.I).part, plan_of(DW, p.I, p.H, p.M).part);
+  // two parts of a row always meet in the join
+  size_t dx = plan_of(DX, M, p.H, p.I).part;
+  if (M > p.M) dx = std::max(dx, up256((size_t)M * p.H * 4));
+  l.bytes = l.part + std::max(dx, p.M <= kOuterRows ? 0 : plan_of(DW, p.I, p.H, p.M).part);
   return l;
 }
 
@@ -342,6 +352,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.dbias[0] = dbias_gate;
   r.dbias[1] = dbias_up;
   r.accumulate = p->accumulate;
+  r.parts = grad_parts(f.M) == 2;
   r.ld_dout = g.ld_out;
   r.ld_gate = g.ld_gate;
   r.ld_up = g.ld_up;
@@ -355,6 +366,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   q.m[1] = (const uint16_t*)r.du;
   q.ldm[0] = q.ldm[1] = f.I;
   q.splits = 1;
+  q.fold = r.parts ? f.M : 0;
   return with_type16(f.type, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     hipLaunchKernelGGL((k_gated_grad<DT>), dim3((unsigned)blocks, (unsigned)cdiv(f.I, 64)), dim3(256), 0, s, r);
@@ -370,7 +382,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.ldn[1] = g.ld_wu;
       d.out[0] = dx;
       d.ldo[0] = ld_dx;
-      d.M = f.M;
+      d.M = r.parts ? 2 * f.M : f.M;
       d.N = f.H;
       d.K = f.I;
       rc = launch<DT, DX>(d, ws + l.part, s);
@@ -385,7 +397,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.ldo[1] = ld_dwu;
       d.M = f.I;
       d.N = f.H;
-      d.K = f.M;
+      d.K = r.parts ? 2 * f.M : f.M;
       d.f32_out = f32;
       d.accumulate = p->accumulate;
       rc = f.M <= kOuterRows ? launch_outer<DT>(d, s) : launch<DT, DW>(d, ws + l.part, s);

@@ -9,21 +9,40 @@ namespace d16 {
 
 // dg = dout f_g(g, u), du = dout f_u(g, u), rounded to the type: the matrix
 // instruction takes 16-bit operands, and each rounding is off by half a step of its own value, so a sum of
-// many carries an error of the size of its own last rounding. With sums != nullptr the columns'
+// many carries an error of the size of its own last rounding (together 1.41 times as much). A sum of few is
+// ruled by its largest terms (one row of 88 columns: 1.8 times as much), and where few rows make
+// the products wait for memory anyway a second part is nearly free: up to kPartRows rows the lower parts go along as
+// further rows, and the gradients are as exact as from unrounded values. With sums != nullptr the columns'
 // sums over this workgroup's rows as well, from the unrounded values: to their place where one workgroup
 // has all rows, else for k_column_sums.
 // Memory-bound: three reads and two writes of 16 bits a value. 64 columns to a workgroup, whole lines of 32 rows at a time.
 struct GradParams {
   const void *dout, *gate, *up;
-  void *dg, *du;      // [M, I] contiguous
+  void *dg, *du;      // [M or, in two parts, 2 M, I] contiguous
   float* sums;        // [row blocks][2][I] or nullptr
   float* dbias[2];    // [I]
   int64_t ld_dout, ld_gate, ld_up;
   int32_t M, I;
   int32_t rows;       // of a workgroup, a multiple of 32
   int32_t accumulate;
+  int32_t parts;      // lower parts too, M rows further on
   ActParams act;
 };
+
+// Stores v rounded to the type and leaves in v what that left of it; 0 of what it made an infinity, so that the products
+// stay infinite. The rest is taken from the bits that are stored, which the asm makes the compiler use: it would round
+// again, by an instruction that multiplies and rounds to 16 bits at once, and near a tie that is another value.
+template <int DT>
+__device__ __forceinline__ void store_upper(uint16_t* to, float (&v)[8]) {
+  u32x4 bits;
+  store8<DT>(&bits, 0, v);
+  asm("" : "+v"(bits));
+  *(u32x4*)to = bits;
+  float up[8];
+  load8<DT>(&bits, 0, up);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = fabsf(up[j]) < INFINITY ? v[j] - up[j] : 0.f;
+}
 
 template <int DT>
 __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
@@ -52,8 +71,12 @@ __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
           sg[j] += g[j];
           su[j] += u[j];
         }
-        store8<DT>(p.dg, (size_t)(row * p.I + col), g);
-        store8<DT>(p.du, (size_t)(row * p.I + col), u);
+        store_upper<DT>((uint16_t*)p.dg + row * p.I + col, g);
+        store_upper<DT>((uint16_t*)p.du + row * p.I + col, u);
+        if (p.parts) {
+          store8<DT>(p.dg, (size_t)((row + p.M) * p.I + col), g);
+          store8<DT>(p.du, (size_t)((row + p.M) * p.I + col), u);
+        }
       }
     });
   }

@@ -16,7 +16,7 @@ sigmoid by v_exp_f32 and v_rcp_f32 (1 ulp each) of an argument rounded to e |g| 
 ev = e (8 + 2 alpha |g|) |f| for silu and SwiGLU-OAI; SiTu's sigmoid the same with alpha 1. Then the rounding, u |f|.
 
 Backward, from the given gate and up: dg is evaluated within ev = e (16 + 2 alpha |g|) of the sum of its terms'
-magnitudes, then rounded: r = u |dg| + tiny. A product of it over K terms with b: sum (ev + r) |b| + acc(K, |dg||b|), and
+magnitudes, then rounded: r = u |dg| + tiny (u^2 |dg| + tiny where both parts are kept). A product of it over K terms with b: sum (ev + r) |b| + acc(K, |dg||b|), and
 the last rounding. Biases' sums: ev summed plus (M + 66) e sum |dg|."""
 import numpy as np
 import pytest
@@ -143,7 +143,7 @@ def test_strided_operands_and_outputs(M):
     assert (dxw[:, 136:] == 5).all() and (dwgw[:, 136:] == 5).all() and (dwuw[:, 136:] == 5).all()
 
 
-def grad_bounds(dout, x, wg, wu, gate, up, name, kw):
+def grad_bounds(dout, x, wg, wu, gate, up, name, kw, parts=1):
     dt, (M, I), H = x.dtype, dout.shape, x.shape[1]
     g, u, d = gate.double(), up.double(), dout.double()
     ref = O.gated_grads(dout, x, wg, wu, gate, up, name, **kw)
@@ -157,7 +157,7 @@ def grad_bounds(dout, x, wg, wu, gate, up, name, kw):
     sg = torch.sigmoid(a * g.clamp(max=kw.get("limit", float("inf"))))
     eg = E * (16 + 2 * a * g.abs()) * d.abs() * mag * sg * (2 + a * g.abs() * (1 - sg))
     eu = E * (16 + 2 * a * g.abs()) * d.abs() * ((g.abs() * sg) if name != "situ" else torch.full_like(u, kw["alpha"]) * sg)
-    h = half(dt)
+    h = half(dt) ** parts
     rg, ru = eg + h * dg.abs() + tiny(dt), eu + h * du.abs() + tiny(dt)
     ag, au, X = dg.abs() + rg, du.abs() + ru, x.double().abs()
     wga, wua = wg.double().abs(), wu.double().abs()
@@ -167,9 +167,9 @@ def grad_bounds(dout, x, wg, wu, gate, up, name, kw):
     return ref, bx, bg, bu, (eg.sum(0) + (M + 66) * E * dg.abs().sum(0)), (eu.sum(0) + (M + 66) * E * du.abs().sum(0))
 
 
-def check_grads(r, dout, x, wg, wu, gate, up, name, kw, old=(0, 0, 0, 0)):
+def check_grads(r, dout, x, wg, wu, gate, up, name, kw, old=(0, 0, 0, 0), parts=1):
     dt = x.dtype
-    ref, bx, bg, bu, bbg, bbu = grad_bounds(dout, x, wg, wu, gate, up, name, kw)
+    ref, bx, bg, bu, bbg, bbu = grad_bounds(dout, x, wg, wu, gate, up, name, kw, parts)
     rounded = lambda v, b, t: b * (1 + half(t)) + half(t) * v.abs() + tiny(t)  # noqa: E731
     if r.dx is not None:
         check(r.dx, ref[0], rounded(ref[0], bx, dt), "dx")
@@ -216,6 +216,19 @@ def test_backward_float32_weight_gradients_and_accumulation(name, dt):
                                   want_dx=False, **ACTS[name])
         torch.cuda.synchronize()
         check_grads(moe.GatedGrads(None, *dw, *db), *ops, name, ACTS[name], old)
+
+
+@pytest.mark.parametrize("M,H,I", [(1, 72, 88), (2, 264, 8), (17, 8200, 64), (63, 136, 72), (64, 2056, 520)])
+@pytest.mark.parametrize("dt", T16)
+def test_few_rows_gradients_are_rounded_once(M, H, I, dt):
+    """Up to 64 rows dg and du are two 16-bit values, the second of at most half a step of the first and itself off by half a step: in
+    the bound above r is the square of u."""
+    name = list(ACTS)[M % 3]
+    print(f"[grad] two parts {M}x{H}x{I} {dt} {name}", flush=True)
+    ops = grad_ops(M + H + I, M, H, I, dt)
+    r = moe.gated_linear_backward(*ops, act=name, **ACTS[name])
+    torch.cuda.synchronize()
+    check_grads(r, *ops, name, ACTS[name], parts=2)
 
 
 def test_backward_parts_alone_and_clamps():
@@ -326,3 +339,30 @@ def test_many_rows(M, H, I, dt):
     s = moe.gated_linear_backward(*args, act=name, want_dbias=True, **ACTS[name])
     torch.cuda.synchronize()
     check_grads(s, *args, name, ACTS[name])
+
+
+def test_rows_far_apart():
+    """Every operand's rows 2^21 elements apart, so that the last ones lie past 2^32: the bits of compact operands."""
+    print("[gated, grad] far", flush=True)
+    M, H, I, dt = 2057, 72, 2056, torch.bfloat16
+    base = torch.empty(2064, 1 << 21, dtype=dt, device=DEV)
+    at = iter(range(0, 1 << 21, 4096))
+
+    def far(t):
+        v = base[:t.shape[0]].narrow(1, next(at), t.shape[1])
+        return v.copy_(t)
+
+    d, x, wg, wu, _, _ = grad_ops(6, M, H, I, dt)
+    r = moe.gated_linear(x, wg, wu, save=True)
+    s = moe.gated_linear_backward(d, x, wg, wu, r.gate, r.up)
+    new = [far(torch.zeros_like(t)) for t in (r.out, r.gate, r.up, s.dx, s.dw_gate, s.dw_up)]
+    X, G, U, D = far(x), far(wg), far(wu), far(d)
+    for few in (3, M):
+        moe.gated_linear(X[:few], G, U, out=new[0][:few], gate=new[1][:few], up=new[2][:few])
+        ref = moe.gated_linear(x[:few], wg, wu, save=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[:few], b) for a, b in zip(new, ref))
+        moe.gated_linear_backward(D[:few], X[:few], G, U, new[1][:few], new[2][:few], dx=new[3][:few], dw_gate=new[4], dw_up=new[5])
+        ref = moe.gated_linear_backward(d[:few], x[:few], wg, wu, ref.gate, ref.up)
+        torch.cuda.synchronize()
+        assert torch.equal(new[3][:few], ref.dx) and torch.equal(new[4], ref.dw_gate) and torch.equal(new[5], ref.dw_up)
