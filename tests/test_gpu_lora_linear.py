@@ -178,3 +178,38 @@ def test_many_rows(M, K, N, R, L, dt, ids):
     out = moe.lora_linear(**c)
     torch.cuda.synchronize()
     check(out, c)
+
+
+@pytest.mark.parametrize("w", [True, False])
+def test_rows_far_apart(w):
+    """Rows 2^21 elements apart, so that the last ones lie past 2^32; x then goes in parts of fewer rows."""
+    print(f"[lora] far {w}", flush=True)
+    M, K, N, dt = 2057, 72, 2056, torch.bfloat16
+    base = torch.empty(2064, 1 << 21, dtype=dt, device=DEV)
+    at = iter(range(0, 1 << 21, 4096))
+    c = make(8, M, K, N, 16, 5, dt, w=w, add=True, bias=True)
+    far = {k: None if c[k] is None else base[:c[k].shape[0]].narrow(1, next(at), c[k].shape[1]).copy_(c[k]) for k in ("x", "w", "add")}
+    out = base[:M].narrow(1, next(at), N)
+    for m in (7, M):
+        part = {k: c[k][:m] for k in ("x", "add", "ids")}
+        moe.lora_linear(**{**c, **far, "x": far["x"][:m], "add": far["add"][:m], "ids": c["ids"][:m]}, out=out[:m])
+        torch.cuda.synchronize()
+        check(out[:m], {**c, **part})
+
+
+@pytest.mark.parametrize("M", [5, 70, 700])
+def test_adapters_far_apart(M):
+    """Factors of more than 2^32 bytes (of 2^31 values); adapters that no row names hold whatever the memory held."""
+    print(f"[lora] large factors {M}", flush=True)
+    L, R, K, N, dt = 600, 256, 16392, 14424, torch.float16
+    c = make(9, M, K, N, R, 3, dt)
+    a, b = [torch.empty(L, *c[k].shape[1:], dtype=dt, device=DEV) for k in ("lora_a", "lora_b")]
+    assert a.numel() > 1 << 31 and b.numel() > 1 << 31
+    use = torch.tensor([0, 311, L - 1, -1], device=DEV)
+    for i in range(3):
+        a[use[i]], b[use[i]] = c["lora_a"][i], c["lora_b"][i]
+    scales = torch.full((L,), float("nan"), device=DEV)
+    scales[use[:3]] = c["scales"]
+    got = moe.lora_linear(**{**c, "lora_a": a, "lora_b": b, "scales": scales, "ids": use[c["ids"].long()].to(torch.int32)})
+    torch.cuda.synchronize()
+    check(got, c)
