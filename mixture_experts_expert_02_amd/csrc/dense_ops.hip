@@ -139,10 +139,9 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
-// Rows up to which dg and du go in two parts.
-constexpr int kPartRows = 64;
-static_assert(2 * kPartRows <= kOuterRows, "k_outer takes both parts");
-int grad_parts(int M) { return M <= kPartRows ? 2 : 1; }
+// dg and du of so few values (see gated_grad.hpp) go in two parts, where k_outer takes both.
+constexpr int kPartValues = 16384;
+int grad_parts(const moe_gated_problem& p) { return 2 * p.M <= kOuterRows && (int64_t)p.M * p.I <= kPartValues ? 2 : 1; }
 // Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
 int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
@@ -150,7 +149,7 @@ struct GradLayout {
 };
 GradLayout grad_layout(const moe_gated_problem& p) {
   GradLayout l;
-  const int M = p.M * grad_parts(p.M);
+  const int M = p.M * grad_parts(p);
   const size_t mi = up256((size_t)M * p.I * 2);
   l.dg = 0;
   l.du = mi;
@@ -352,7 +351,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.dbias[0] = dbias_gate;
   r.dbias[1] = dbias_up;
   r.accumulate = p->accumulate;
-  r.parts = grad_parts(f.M) == 2;
+  r.parts = grad_parts(f) == 2;
   r.ld_dout = g.ld_out;
   r.ld_gate = g.ld_gate;
   r.ld_up = g.ld_up;

@@ -218,10 +218,10 @@ def test_backward_float32_weight_gradients_and_accumulation(name, dt):
         check_grads(moe.GatedGrads(None, *dw, *db), *ops, name, ACTS[name], old)
 
 
-@pytest.mark.parametrize("M,H,I", [(1, 72, 88), (2, 264, 8), (17, 8200, 64), (63, 136, 72), (64, 2056, 520)])
+@pytest.mark.parametrize("M,H,I", [(1, 72, 88), (1, 264, 16384), (2, 264, 8), (17, 8200, 960), (63, 136, 72), (64, 2056, 256)])
 @pytest.mark.parametrize("dt", T16)
-def test_few_rows_gradients_are_rounded_once(M, H, I, dt):
-    """Up to 64 rows dg and du are two 16-bit values, the second of at most half a step of the first and itself off by half a step: in
+def test_gradients_of_few_values_are_rounded_once(M, H, I, dt):
+    """Up to 16384 values (and 64 rows) dg and du are two 16-bit values, the second of at most half a step of the first and itself off by half a step: in
     the bound above r is the square of u."""
     name = list(ACTS)[M % 3]
     print(f"[grad] two parts {M}x{H}x{I} {dt} {name}", flush=True)
