@@ -225,32 +225,37 @@ template <int DT, int RF>
 void launch_shrink_of(const ShrinkParams& q, int ranges, hipStream_t s) {
   if constexpr (RF <= 4) {
     if (shrink_frags(q.M, q.R) == 2) {
-      hipLaunchKernelGGL((k_lora_shrink<DT, RF, 2>), dim3((unsigned)cdiv(q.M, 32), (unsigned)ranges), dim3(512), 0, s, q);
+      hipLaunchKernelGGL((k_lora_shrink<DT, RF, 2, false>), dim3((unsigned)cdiv(q.M, 32), (unsigned)ranges), dim3(512), 0, s, q);
       return;
     }
   }
-  hipLaunchKernelGGL((k_lora_shrink<DT, RF, 1>), dim3((unsigned)cdiv(q.M, 16), (unsigned)ranges), dim3(512), 0, s, q);
+  const dim3 g((unsigned)cdiv(q.M, 16), (unsigned)ranges);
+  if (q.M <= kSortRows) hipLaunchKernelGGL((k_lora_shrink<DT, RF, 1, true>), g, dim3(512), 0, s, q);
+  else hipLaunchKernelGGL((k_lora_shrink<DT, RF, 1, false>), g, dim3(512), 0, s, q);
 }
 
 template <int DT>
-void launch_shrink(const ShrinkParams& q, hipStream_t s) {
-  const int ranges = shrink_ranges(q.M, q.K, q.R);
+void launch_shrink(const ShrinkParams& q, int ranges, bool join, hipStream_t s) {
   if (q.R <= 16) launch_shrink_of<DT, 1>(q, ranges, s);
   else if (q.R <= 32) launch_shrink_of<DT, 2>(q, ranges, s);
   else if (q.R <= 64) launch_shrink_of<DT, 4>(q, ranges, s);
   else if (q.R <= 128) launch_shrink_of<DT, 8>(q, ranges, s);
   else launch_shrink_of<DT, 16>(q, ranges, s);
-  if (ranges == 1) return;
+  if (!join) return;
   const dim3 g((unsigned)cdiv(q.M, 4)), b(256);
   if (q.R <= 64) hipLaunchKernelGGL((k_lora_finish<DT, 1>), g, b, 0, s, q, ranges);
   else if (q.R <= 128) hipLaunchKernelGGL((k_lora_finish<DT, 2>), g, b, 0, s, q, ranges);
   else hipLaunchKernelGGL((k_lora_finish<DT, 4>), g, b, 0, s, q, ranges);
 }
 
+// 16-row fragments of a workgroup of k_lora_expand; with one it joins the first product's K ranges itself.
+int expand_frags(int M) { return M >= 2048 ? 4 : 1; }
 template <int DT>
-int launch_expand(const Params& q, hipStream_t s) {
-  const int frags = q.M >= 2048 ? 4 : 1;
-  hipLaunchKernelGGL((k_lora_expand<DT>), dim3((unsigned)cdiv(q.M, 16 * frags), (unsigned)cdiv(q.N, 256)), dim3(256), 0, s, q, frags);
+int launch_expand(const Params& q, const ShrinkParams& sh, int ranges, hipStream_t s) {
+  const int frags = expand_frags(q.M);
+  const dim3 g((unsigned)cdiv(q.M, 16 * frags), (unsigned)cdiv(q.N, 256));
+  if (ranges > 1) hipLaunchKernelGGL((k_lora_expand<DT, true>), g, dim3(256), 0, s, q, frags, sh, ranges);
+  else hipLaunchKernelGGL((k_lora_expand<DT, false>), g, dim3(256), 0, s, q, frags, sh, 1);
   return launch_status();
 }
 
@@ -454,7 +459,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
     q.sid = ids;
     return with_type16(p->type, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
-      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, ids, nullptr, (float*)ws, nullptr, ldx,
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, nullptr, ids, nullptr, (float*)ws, nullptr, ldx,
                             p->M, p->K, p->R, p->L};
       hipLaunchKernelGGL((k_lora_shrink_few<DT>), dim3((unsigned)p->M, (unsigned)p->R / 8), dim3(256), 0, s, sh);
       return launch_rows<DT, LORA>(q, s);
@@ -469,12 +474,14 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
       q.add = add ? (const uint16_t*)add + m * lda : nullptr;
       q.M = n;
       const SortParams sp{ids + m, (int32_t*)(ws + l.perm), (int32_t*)(ws + l.sid), n, p->L};
-      hipLaunchKernelGGL(k_lora_sort, dim3(1), dim3(1024), 0, s, sp);
-      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, q.perm, q.sid, (uint16_t*)(ws + l.t),
+      if (n > kSortRows) hipLaunchKernelGGL(k_lora_sort, dim3(1), dim3(1024), 0, s, sp);
+      const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, sp.perm, sp.sid, sp.ids, (uint16_t*)(ws + l.t),
                             (float*)(ws + l.tf), (float*)(ws + l.part), ldx, n, p->K, p->R, p->L};
-      launch_shrink<DT>(sh, s);
+      const int ranges = shrink_ranges(n, p->K, p->R);
+      const bool join = ranges > 1 && (w || expand_frags(n) > 1);
+      launch_shrink<DT>(sh, ranges, join, s);
       int rc = launch_status();
-      if (!rc) rc = w ? launch<DT, LORA>(q, ws + l.part, s) : launch_expand<DT>(q, s);
+      if (!rc) rc = w ? launch<DT, LORA>(q, ws + l.part, s) : launch_expand<DT>(q, sh, join ? 1 : ranges, s);
       if (rc) return rc;
     }
     return (int)MOE_OK;

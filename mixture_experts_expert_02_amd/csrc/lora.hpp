@@ -109,13 +109,26 @@ struct ShrinkParams {
   const uint16_t* x;
   const uint16_t* a;      // [L, R, K]
   const float* scales;    // [L]
-  const int32_t *perm, *sid;
+  int32_t *perm, *sid;    // of the sorted rows
+  const int32_t* ids;     // k_lora_shrink_few and SORT
   uint16_t* t;            // see part_at
   float* tf;              // [M]
   float* part;            // [K ranges][M][R], with more than one
   int64_t ldx;
   int32_t M, K, R, L;
 };
+
+// the power of two above |v|; float32's ends keep it and its inverse normal
+__device__ __forceinline__ int power_above(float most) {
+  const int e = most > 0.f && most < INFINITY ? ilogbf(most) + 1 : 0;
+  return min(max(e, -120), 120);
+}
+// w: a product with a power of two, so that however it is rounded the upper part is the same
+template <int DT>
+__device__ __forceinline__ void two_parts(float w, float& h, float& l) {
+  h = round_to<DT>(w);
+  l = fabsf(h) < INFINITY ? w - h : 0.f;
+}
 
 // A row's results over the power of two above their largest, in two parts of the
 // type, 16 significand bits or more together: what the second product loses by its 16-bit
@@ -128,25 +141,113 @@ __device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, int m,
   for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(v[i]));
 #pragma unroll
   for (int d = 1; d < LANES; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-  // float32's ends keep the power and its inverse normal
-  int e = most > 0.f && most < INFINITY ? ilogbf(most) + 1 : 0;
-  e = min(max(e, -120), 120);
+  const int e = power_above(most);
   const float inv = ldexpf(1.f, -e);
   if (r0 == 0) tf[m] = ldexpf(1.f, e);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int r = r0 + i * LANES;
     if (r >= R) continue;
-    const float w = v[i] * inv, h = round_to<DT>(w);
-    const float l = fabsf(h) < INFINITY ? w - h : 0.f;
+    float h, l;
+    two_parts<DT>(v[i] * inv, h, l);
     store1<DT>(t, part_at(m, r, R), h);
     store1<DT>(t, part_at(m, R + r, R), l);
   }
 }
 
+// Sorted rows m0 .. m0 + ROWS - 1 of at most kSortRows, found by a workgroup of 512 threads for itself: counts and
+// places of the adapters as in k_lora_sort, but rows of one adapter keep their order, so that all workgroups agree. A row's
+// place is its adapter's first one, the rows of it in the 64-row pieces before, and those in the lanes before.
+constexpr int kSortRows = 1024;
+template <int ROWS>
+__device__ __forceinline__ void sort_here(const ShrinkParams& p, int m0, int (&perm)[ROWS], int (&sid)[ROWS]) {
+  __shared__ int32_t at[kMaxAdapters + 1];
+  __shared__ int32_t wave_sum[8];
+  __shared__ __attribute__((aligned(16))) int32_t piece[ROWS][kSortRows / 64];  // rows of the adapter whose first place in the window this is
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int key[2] = {-1, -1};
+  {
+    const int m = min(tid, p.M - 1), m2 = min(tid + 512, p.M - 1);
+    const int a = p.ids[m], a2 = p.ids[m2];
+    if (tid < p.M) key[0] = a >= 0 && a < p.L ? a : p.L;
+    if (tid + 512 < p.M) key[1] = a2 >= 0 && a2 < p.L ? a2 : p.L;
+  }
+  for (int i = tid; i <= p.L; i += 512) at[i] = 0;
+  for (int i = tid; i < ROWS * (kSortRows / 64); i += 512) (&piece[0][0])[i] = 0;
+  __syncthreads();
+  if (key[0] >= 0) atomicAdd(&at[key[0]], 1);
+  if (key[1] >= 0) atomicAdd(&at[key[1]], 1);
+  __syncthreads();
+  const int per = p.L / 512 + 1;  // counters to a thread: at most 9
+  int sum = 0;
+#pragma unroll 1
+  for (int j = 0; j < per; ++j) {
+    const int i = tid * per + j;
+    if (i <= p.L) sum += at[i];
+  }
+  int run = sum;
+#pragma unroll 1
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(run, d);
+    if (lane >= d) run += o;
+  }
+  if (lane == 63) wave_sum[wave] = run;
+  __syncthreads();
+  int base = run - sum;
+#pragma unroll 1
+  for (int w = 0; w < wave; ++w) base += wave_sum[w];
+#pragma unroll 1
+  for (int j = 0; j < per; ++j) {
+    const int i = tid * per + j;
+    if (i > p.L) break;
+    const int n = at[i];
+    at[i] = base;
+    base += n;
+  }
+  __syncthreads();
+  // the adapters of the window in this wave's rows, one after the other
+  int place[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = key[i], first = k < 0 ? 0 : at[k], end = k < 0 ? 0 : k < p.L ? at[k + 1] : p.M;
+    const bool near = k >= 0 && first < m0 + ROWS && end > m0;
+    place[i] = near ? first : -1;
+    uint64_t left = __ballot(near);
+#pragma unroll 1
+    while (left) {
+      const int a = __builtin_amdgcn_readlane(k, __builtin_ctzll(left));
+      const uint64_t same = __ballot(k == a);
+      left &= ~same;
+      if (k == a) {
+        place[i] += __popcll(same & lanemask_lt());
+        piece[max(first - m0, 0)][i * 8 + wave] = __popcll(same);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (place[i] < 0) continue;
+    const int slot = max(at[key[i]] - m0, 0);
+    int before = 0;
+#pragma unroll
+    for (int q = 0; q < 16; q += 4) {
+      const int4 n = *(const int4*)&piece[slot][q];
+      const int here = i * 8 + wave - q;
+      before += (here > 0 ? n.x : 0) + (here > 1 ? n.y : 0) + (here > 2 ? n.z : 0) + (here > 3 ? n.w : 0);
+    }
+    const int at_row = place[i] + before - m0;
+    if (at_row >= 0 && at_row < ROWS) {
+      perm[at_row] = i * 512 + tid;
+      sid[at_row] = key[i];
+    }
+  }
+  __syncthreads();
+}
+
 // 16 FX sorted rows to a workgroup (and a K range: blockIdx.y); its eight waves split K and join in LDS in wave
-// order. RF: fragments of 16 ranks.
-template <int DT, int RF, int FX>
+// order. RF: fragments of 16 ranks. SORT: the rows are found here and their places stored for the kernels behind.
+template <int DT, int RF, int FX, bool SORT>
 __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   constexpr int ROWS = 16 * FX;
   constexpr int U = RF + FX <= 4 ? 6 : RF + FX <= 6 ? 4 : RF + FX <= 10 ? 2 : 1;  // K steps whose loads are issued together
@@ -158,11 +259,26 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   const int m0 = blockIdx.x * ROWS;
   int id[FX];
   const uint16_t* xr[FX];
+  __shared__ int32_t perm_of[ROWS], id_of[ROWS];
+  if constexpr (SORT) {
+    sort_here<ROWS>(p, m0, perm_of, id_of);
+    if (blockIdx.y == 0 && tid < ROWS && m0 + tid < p.M) {
+      p.perm[m0 + tid] = perm_of[tid];
+      p.sid[m0 + tid] = id_of[tid];
+    }
+  } else {
+    if (tid < ROWS) {
+      const int row = min(m0 + tid, p.M - 1);
+      perm_of[tid] = p.perm[row];
+      id_of[tid] = p.sid[row];
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int j = 0; j < FX; ++j) {
-    const int row = min(m0 + j * 16 + c, p.M - 1);
-    id[j] = m0 + j * 16 + c < p.M ? p.sid[row] : p.L;
-    xr[j] = p.x + (int64_t)p.perm[row] * p.ldx;
+    const int row = min(j * 16 + c, p.M - 1 - m0);
+    id[j] = m0 + j * 16 + c < p.M ? id_of[row] : p.L;
+    xr[j] = p.x + (int64_t)perm_of[row] * p.ldx;
   }
   const int steps = (p.K + 31) / 32, nw = 8 * gridDim.y, w = blockIdx.y * 8 + wave;
   const int lo = (int)((int64_t)w * steps / nw), hi = (int)((int64_t)(w + 1) * steps / nw);
@@ -241,7 +357,7 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   constexpr int LANES = 512 / ROWS, N = (RF * 16 + LANES - 1) / LANES;
   const int m = tid / LANES, r0 = tid % LANES;
   if (m0 + m >= p.M) return;
-  const int a = p.sid[m0 + m];
+  const int a = id_of[m];
   float v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = r0 + LANES * i < p.R && a < p.L ? sum[min(r0 + LANES * i, RF * 16 - 1)][m] : 0.f;
@@ -277,11 +393,11 @@ __global__ __launch_bounds__(256) void k_lora_finish(const ShrinkParams p, int r
 }
 
 // Few rows: row blockIdx.x's products with eight ranks of its adapter, two to a wave, in float32, scaled;
-// rows without an adapter are left out. p.sid: the ids, p.tf: [M, R].
+// rows without an adapter are left out. p.tf: [M, R].
 template <int DT>
 __global__ __launch_bounds__(256) void k_lora_shrink_few(const ShrinkParams p) {
   const int m = blockIdx.x, lane = threadIdx.x & 63, r = blockIdx.y * 8 + (threadIdx.x >> 6) * 2;
-  const int a = p.sid[m];
+  const int a = p.ids[m];
   if (a < 0 || a >= p.L) return;
   const uint16_t* x = p.x + (int64_t)m * p.ldx;
   const uint16_t* ar = p.a + ((int64_t)a * p.R + r) * p.K;
@@ -309,10 +425,49 @@ __global__ __launch_bounds__(256) void k_lora_shrink_few(const ShrinkParams p) {
 // The adapters' part alone (no projection): out = bias + add + f_m (t_m B_a^T). A workgroup owns 16 `frags` sorted rows
 // and 256 columns, 64 to a wave; both operands go straight into registers in the MFMA's layout, the factor's
 // rows once for all fragments of the same adapter. Bound by the factors' and outputs' bytes.
-template <int DT>
-__global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) {
+// JOIN (frags = 1): the first product's K ranges are joined here, every column tile's workgroup for itself, and the parts
+// stay in LDS.
+template <int DT, bool JOIN>
+__global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, const ShrinkParams sh, int ranges) {
+  constexpr int PITCH = 2 * kMaxRank + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t ts[JOIN ? 16 * PITCH : 8];
+  __shared__ float fs[16];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
+  if constexpr (JOIN) {
+    // sixteen lanes to a row, four neighbouring ranks of 64 to a lane
+    const int r = threadIdx.x >> 4, l4 = (threadIdx.x & 15) * 4, m = blockIdx.x * 16 + r;
+    const int a = m < p.M ? p.sid[m] : p.L;
+    const float sc = a < p.L ? sh.scales[a] : 0.f;
+    f32x4 v[kMaxRank / 64];
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxRank / 64; ++i) {
+      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (l4 + 64 * i >= p.R || m >= p.M) continue;
+      // rows without an adapter hold zeros
+#pragma unroll 8
+      for (int k = 0; k < ranges; ++k) v[i] += *(const f32x4*)(sh.part + ((size_t)k * p.M + m) * p.R + l4 + 64 * i);
+      v[i] *= sc;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) most = fmaxf(most, fabsf(v[i][q]));
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+    const int e = power_above(most);
+    const float inv = ldexpf(1.f, -e);
+    if (l4 == 0) fs[r] = ldexpf(1.f, e);
+#pragma unroll
+    for (int i = 0; i < kMaxRank / 64; ++i) {
+      if (l4 + 64 * i >= p.R) continue;
+      float h[4], l[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) two_parts<DT>(v[i][q] * inv, h[q], l[q]);
+      *(uint2*)(ts + r * PITCH + l4 + 64 * i) = pack4<DT>(h);
+      *(uint2*)(ts + r * PITCH + p.R + l4 + 64 * i) = pack4<DT>(l);
+    }
+    __syncthreads();
+  }
   if (col0 >= p.N) return;
   u32x4 b[4][2];
   int held = -1;
@@ -321,7 +476,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
     if (r0 >= p.M) return;
     const int row = min(r0 + c, p.M - 1);
     const int id = r0 + c < p.M ? p.sid[row] : p.L;
-    const float f = p.tf[row];
+    const float f = JOIN ? fs[c] : p.tf[row];
     const int64_t orow = p.perm[row];
     f32x4 acc[4];
 #pragma unroll
@@ -338,8 +493,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags) 
           const int k = c0 + 32 * ks + 8 * g;
           hi[ks] = lo[ks] = zero;
           if (k < p.R) {
-            hi[ks] = *(const u32x4*)(p.t + part_at(row, k, p.R));
-            lo[ks] = *(const u32x4*)(p.t + part_at(row, p.R + k, p.R));
+            hi[ks] = *(const u32x4*)(JOIN ? ts + c * PITCH + k : p.t + part_at(row, k, p.R));
+            lo[ks] = *(const u32x4*)(JOIN ? ts + c * PITCH + p.R + k : p.t + part_at(row, p.R + k, p.R));
           }
           if (held != a || p.R > 64) {
 #pragma unroll
