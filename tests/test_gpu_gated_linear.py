@@ -366,3 +366,27 @@ def test_rows_far_apart():
         ref = moe.gated_linear_backward(d[:few], x[:few], wg, wu, ref.gate, ref.up)
         torch.cuda.synchronize()
         assert torch.equal(new[3][:few], ref.dx) and torch.equal(new[4], ref.dw_gate) and torch.equal(new[5], ref.dw_up)
+
+
+@pytest.mark.parametrize("dt", T16)
+def test_derivatives_of_saturated_values(dt):
+    """SiTu's derivatives keep their relative precision where tanh nears 1. One row, so the biases' gradients are dg and
+    du themselves, in float32. With y = u / beta (division within 2 e), 4 q r^2, q = exp(-2 |y|) and r = 1 / (1 + q): the
+    exponent is off by at most 2 |y| (2 e + e), q by e (6 |y| + 1) of itself, r by 1.5 e, the products by e: e (6 |y| + 5). tanh is
+    within 2 e, a sigmoid e (3 |g| + 3), each further product e / 2: together less than e (6 |y| + 3 |g| + 16), and for
+    the sum of positive terms that g > 0 gives, e (6 |g| / alpha + 6 |g| + 24)."""
+    print(f"[grad] saturated {dt}", flush=True)
+    kw = ACTS["situ"]
+    I = 512
+    g = torch.linspace(0.05, 24, I, device=DEV).to(dt)[None]
+    u = (torch.linspace(0.1, 40, I, device=DEV).flip(0) * torch.tensor([1.0, -1.0], device=DEV).repeat(I // 2)).to(dt)[None]
+    d = torch.ones_like(g)
+    x, w = torch.ones(1, 8, dtype=dt, device=DEV), torch.ones(I, 8, dtype=dt, device=DEV)
+    r = moe.gated_linear_backward(d, x, w, w, g, u, act="situ", want_dx=False, want_dw=False, want_dbias=True, **kw)
+    torch.cuda.synchronize()
+    G, U, a, b = g.double()[0], u.double()[0], kw["alpha"], kw["beta"]
+    s, sech2 = torch.sigmoid(G), lambda v: 1 / torch.cosh(v).square()  # noqa: E731
+    fg = s * (sech2(G / a) + a * torch.tanh(G / a) * torch.sigmoid(-G)) * b * torch.tanh(U / b)
+    fu = a * torch.tanh(G / a) * s * sech2(U / b)
+    check(r.dbias_gate, fg, E * (6 * G / a + 6 * G + 24) * fg.abs())
+    check(r.dbias_up, fu, E * (6 * U.abs() / b + 3 * G + 16) * fu.abs())
