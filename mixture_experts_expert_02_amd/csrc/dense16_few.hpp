@@ -12,6 +12,8 @@
 namespace moe {
 namespace d16 {
 
+constexpr int kMaxRank = 256;
+
 template <int DT>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   if constexpr (DT == T_BF16)
@@ -20,8 +22,31 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// LORA here: p.tf holds the scaled x A^T in float32, [M, R] in the rows' own order, and p.sid the ids.
-template <int DT, int MODE, int S, int FN, int XI, int D>
+// Four neighbouring ranks' products of a row with its adapter's first factor, by one wave: sums of all lanes.
+template <int DT>
+__device__ __forceinline__ void first_products(const uint16_t* x, const uint16_t* a, int K, int lane, float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = 0.f;
+#pragma unroll 4
+  for (int k = lane * 8; k < K; k += 512) {
+    float xv[8], av[4][8];
+    load8<DT>(x, k, xv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load8<DT>(a, (size_t)i * K + k, av[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i] = fmaf(xv[j], av[i][j], s[i]);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += __shfl_xor(s[i], d);
+}
+
+// LORA here: p.sid holds the ids; the scaled x A^T, in float32, come from p.tf, [M, R] in the rows' own order, or (OWN) every
+// workgroup finds them for itself while its first units are on their way, which saves a launch where they are few.
+template <int DT, int MODE, int S, int FN, int XI, int D, bool OWN>
 __global__ __launch_bounds__(64 * S) void k_few(const Params p) {
   constexpr int FM = (XI + 1) / 2, NI = 2 * FN;  // 16-row fragments of x; load instructions of a unit's weights
   constexpr int UNIT = (NI + XI) * 1024;
@@ -89,6 +114,18 @@ __global__ __launch_bounds__(64 * S) void k_few(const Params p) {
   // (64 x 2880 x 2895 with rank 32 behind the main loop 13.5 us, here 12.9)
   constexpr int OUT = MODE == LORA ? (8 * XI * COLS + 64 * S - 1) / (64 * S) : 1;
   float lora[OUT], bias[OUT], add[OUT];
+  __shared__ float own[OWN ? 8 * XI * kMaxRank : 1];
+  if constexpr (OWN) {
+    const int per = p.R / 4;
+    for (int i = wave; i < min(p.M, 8 * XI) * per; i += S) {
+      const int m = i / per, r = (i - m * per) * 4, a = __builtin_amdgcn_readfirstlane(p.sid[m]);
+      if (a < 0 || a >= p.L) continue;
+      float s[4];
+      first_products<DT>(p.m[0] + m * p.ldm[0], p.a + ((int64_t)a * p.R + r) * p.K, p.K, lane, s);
+      if (lane < 4) own[m * p.R + r + lane] = (lane < 2 ? lane ? s[1] : s[0] : lane == 2 ? s[2] : s[3]) * p.scales[a];
+    }
+    __syncthreads();
+  }
   if constexpr (MODE == LORA) {
     int64_t b[OUT], t[OUT];
     bool has[OUT];
@@ -109,7 +146,7 @@ __global__ __launch_bounds__(64 * S) void k_few(const Params p) {
       for (int o = 0; o < OUT; ++o) {
         float bv[8], tv[8];
         load8<DT>(p.b, (size_t)(b[o] + r), bv);
-        load8<T_FP32>(p.tf, (size_t)(t[o] + r), tv);
+        load8<T_FP32>(OWN ? own : p.tf, (size_t)(t[o] + r), tv);
 #pragma unroll
         for (int q = 0; q < 8; ++q) lora[o] = fmaf(tv[q], bv[q], lora[o]);
       }

@@ -55,11 +55,12 @@ inline Plan plan_of(int mode, int64_t M, int64_t N, int64_t K) {
 // at least 16 steps of 32 to a range (us of the kernel: 1000 rows of 4096, rank 24, 64 adapters 31, 17, 8.7, 12.5 and 17
 // with 1, 2, 4, 8 and 16 ranges; 256 of 7168, rank 64, 34, 19, 11.6, 7.6 and 6.0; 8192 of 2048 18.6, 21 and 28 with 1, 2
 // and 4).
+constexpr int kMaxRanges = 16;
 inline int shrink_frags(int64_t M, int R) { return R <= 64 && M > 2048 ? 2 : 1; }
 inline int shrink_ranges(int64_t M, int K, int R) {
   const int64_t groups = (M + 16 * shrink_frags(M, R) - 1) / (16 * shrink_frags(M, R));
   const int64_t by_units = 256 / groups, by_k = (K + 31) / 32 / 16, r = by_units < by_k ? by_units : by_k;
-  return r < 1 ? 1 : r > 16 ? 16 : (int)r;
+  return r < 1 ? 1 : r > kMaxRanges ? kMaxRanges : (int)r;
 }
 
 }  // namespace d16

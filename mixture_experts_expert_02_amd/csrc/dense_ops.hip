@@ -121,21 +121,32 @@ int launch(Params& q, void* part, hipStream_t s) {
 constexpr int kFewRows = 64;  // of a projection with adapters
 constexpr int kFewGated = 32;
 
-template <int DT, int MODE, int S, int FN, int XI, int D>
+template <int DT, int MODE, int S, int FN, int XI, int D, bool OWN = false>
 int launch_few(Params& q, hipStream_t s) {
   q.mt = (int)cdiv(q.M, 8 * XI);
   q.nt = (int)cdiv(q.N, MODE == GATED ? 8 * FN : 16 * FN);
-  hipLaunchKernelGGL((k_few<DT, MODE, S, FN, XI, D>), dim3((unsigned)(q.mt * q.nt)), dim3(64 * S), 0, s, q);
+  hipLaunchKernelGGL((k_few<DT, MODE, S, FN, XI, D, OWN>), dim3((unsigned)(q.mt * q.nt)), dim3(64 * S), 0, s, q);
   return launch_status();
+}
+
+// Whether every workgroup finds the adapters' first products for itself: a wave has its four ranks' 2048 values on
+// their way at once, so these are the times it waits for memory.
+bool own_products(int M, int N, int K, int R) {
+  const int waves = cdiv(N, 16) <= 256 ? 8 : 4;
+  return M <= 8 && cdiv((int64_t)M * R / 4, waves) * cdiv(K, 2048) <= 2;
 }
 
 template <int DT, int MODE>
 int launch_rows(Params& q, hipStream_t s) {
   const bool few = cdiv(q.N, MODE == GATED ? 8 : 16) <= 256;
+  if constexpr (MODE == LORA) {
+    if (q.a) return few ? launch_few<DT, MODE, 8, 1, 1, 6, true>(q, s) : launch_few<DT, MODE, 4, 2, 1, 3, true>(q, s);
+  }
   if (q.M <= 8) return few ? launch_few<DT, MODE, 8, 1, 1, 6>(q, s) : launch_few<DT, MODE, 4, 2, 1, 3>(q, s);
   if (q.M <= 16) return few ? launch_few<DT, MODE, 8, 1, 2, 4>(q, s) : launch_few<DT, MODE, 4, 2, 2, 3>(q, s);
   if (q.M <= 32) return few ? launch_few<DT, MODE, 8, 1, 4, 3>(q, s) : launch_few<DT, MODE, 4, 2, 4, 2>(q, s);
-  return launch_few<DT, MODE, 4, 1, 8, 3>(q, s);
+  // two workgroups of 32 rows to the same weights, both on a compute unit (64 x 2880 x 2895 with 64 rows in one: 13.2 us, here 12.4)
+  return launch_few<DT, MODE, 4, 1, 4, 3>(q, s);
 }
 
 // ------------------------------------------------------------ backward workspace
@@ -461,7 +472,12 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
       constexpr int DT = decltype(dt)::value;
       const ShrinkParams sh{q.m[0], (const uint16_t*)lora_a, scales, nullptr, nullptr, ids, nullptr, (float*)ws, nullptr, ldx,
                             p->M, p->K, p->R, p->L};
-      hipLaunchKernelGGL((k_lora_shrink_few<DT>), dim3((unsigned)p->M, (unsigned)p->R / 8), dim3(256), 0, s, sh);
+      if (w && own_products(p->M, p->N, p->K, p->R)) {
+        q.a = sh.a;
+        q.scales = scales;
+      } else {
+        hipLaunchKernelGGL((k_lora_shrink_few<DT>), dim3((unsigned)p->M, (unsigned)p->R / 8), dim3(256), 0, s, sh);
+      }
       return launch_rows<DT, LORA>(q, s);
     });
   }

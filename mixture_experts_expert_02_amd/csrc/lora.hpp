@@ -9,7 +9,6 @@ namespace moe {
 namespace d16 {
 
 constexpr int kMaxAdapters = 4096;
-constexpr int kMaxRank = 256;
 
 struct SortParams {
   const int32_t* ids;  // [M]; outside [0, L): no adapter
@@ -373,7 +372,8 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
   store_parts<DT, LANES, N>(v, r0, p.R, m0 + m, p.t, p.tf);
 }
 
-// The K ranges' results joined in their order, a row to a wave, N ranks to a lane.
+// The K ranges' results joined in their order, a row to a wave, N ranks to a lane. All ranges' loads at once, whatever
+// their number, here and in k_lora_expand.
 template <int DT, int N>
 __global__ __launch_bounds__(256) void k_lora_finish(const ShrinkParams p, int ranges) {
   const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -384,9 +384,11 @@ __global__ __launch_bounds__(256) void k_lora_finish(const ShrinkParams p, int r
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int r = min(lane + 64 * i, p.R - 1);
-    float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < ranges; ++k) s += p.part[((size_t)k * p.M + m) * p.R + r];
+    float s = 0.f, x[kMaxRanges];
+#pragma unroll
+    for (int k = 0; k < kMaxRanges; ++k) x[k] = p.part[((size_t)min(k, ranges - 1) * p.M + m) * p.R + r];
+#pragma unroll
+    for (int k = 0; k < kMaxRanges; ++k) s = k < ranges ? s + x[k] : s;
     v[i] = a < p.L && lane + 64 * i < p.R ? s * sc : 0.f;
   }
   store_parts<DT, 64, N>(v, lane, p.R, m, p.t, p.tf);
@@ -434,7 +436,40 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
   __shared__ float fs[16];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
+  u32x4 b[4][2];  // the factor's rows of adapter `held`, ranks c0 .. c0 + 63
+  int held = -1;
+  auto load_b = [&](int a, int c0) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const int k = c0 + 32 * ks + 8 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = col0 + i * 16 + c;
+        b[i][ks] = u32x4{0, 0, 0, 0};
+        if (k < p.R && col < p.N) b[i][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
+      }
+    }
+    held = a;
+  };
+  // what a fragment needs besides its products: adapters and places of its rows, and the addend's values
+  int id = 0;
+  int64_t orow = 0;
+  uint2 old[4];
+  auto load_row = [&](int r0) {
+    const int row = min(r0 + c, p.M - 1);
+    id = r0 + c < p.M ? p.sid[row] : p.L;
+    orow = p.perm[row];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = col0 + i * 16 + 4 * g;
+      old[i] = uint2{0, 0};
+      if (p.add && p.vec && r0 + c < p.M && col + 4 <= p.N) old[i] = *(const uint2*)((const uint16_t*)p.add + orow * p.ld_add + col);
+    }
+  };
   if constexpr (JOIN) {
+    load_row(blockIdx.x * 16);
+    const uint64_t rows = __ballot(id < p.L);
+    if (rows) load_b(__builtin_amdgcn_readlane(id, __builtin_ctzll(rows)), 0);
     // sixteen lanes to a row, four neighbouring ranks of 64 to a lane
     const int r = threadIdx.x >> 4, l4 = (threadIdx.x & 15) * 4, m = blockIdx.x * 16 + r;
     const int a = m < p.M ? p.sid[m] : p.L;
@@ -446,8 +481,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
       v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (l4 + 64 * i >= p.R || m >= p.M) continue;
       // rows without an adapter hold zeros
-#pragma unroll 8
-      for (int k = 0; k < ranges; ++k) v[i] += *(const f32x4*)(sh.part + ((size_t)k * p.M + m) * p.R + l4 + 64 * i);
+      f32x4 x[kMaxRanges];
+#pragma unroll
+      for (int k = 0; k < kMaxRanges; ++k) x[k] = *(const f32x4*)(sh.part + ((size_t)min(k, ranges - 1) * p.M + m) * p.R + l4 + 64 * i);
+#pragma unroll
+      for (int k = 0; k < kMaxRanges; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[i][q] = k < ranges ? v[i][q] + x[k][q] : v[i][q];
       v[i] *= sc;
 #pragma unroll
       for (int q = 0; q < 4; ++q) most = fmaxf(most, fabsf(v[i][q]));
@@ -469,15 +509,12 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
     __syncthreads();
   }
   if (col0 >= p.N) return;
-  u32x4 b[4][2];
-  int held = -1;
   for (int x = 0; x < frags; ++x) {
     const int r0 = (blockIdx.x * frags + x) * 16;
     if (r0 >= p.M) return;
     const int row = min(r0 + c, p.M - 1);
-    const int id = r0 + c < p.M ? p.sid[row] : p.L;
+    if constexpr (!JOIN) load_row(r0);
     const float f = JOIN ? fs[c] : p.tf[row];
-    const int64_t orow = p.perm[row];
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -496,16 +533,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
             hi[ks] = *(const u32x4*)(JOIN ? ts + c * PITCH + k : p.t + part_at(row, k, p.R));
             lo[ks] = *(const u32x4*)(JOIN ? ts + c * PITCH + p.R + k : p.t + part_at(row, p.R + k, p.R));
           }
-          if (held != a || p.R > 64) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int col = col0 + i * 16 + c;
-              b[i][ks] = zero;
-              if (k < p.R && col < p.N) b[i][ks] = *(const u32x4*)(p.b + ((int64_t)a * p.N + col) * p.R + k);
-            }
-          }
         }
-        held = a;
+        if (held != a || p.R > 64) load_b(a, c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           f32x4 tmp = {0.f, 0.f, 0.f, 0.f};
@@ -528,14 +557,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
     for (int i = 0; i < 4; ++i) {
       const int col = col0 + i * 16 + 4 * g;  // four neighbours
       if (p.vec && col + 4 <= p.N) {
-        uint2 old = {0, 0}, res;
-        if (add) old = *(const uint2*)(add + col);
+        uint2 res;
         float v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = acc[i][q] + (p.bias[0] ? p.bias[0][col + q] : 0.f);
         if (add) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += load1<DT>(&old, q);
+          for (int q = 0; q < 4; ++q) v[q] += load1<DT>(&old[i], q);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) store1<DT>(&res, q, v[q]);
