@@ -130,7 +130,9 @@ int launch_few(Params& q, hipStream_t s) {
 }
 
 // Whether every workgroup finds the adapters' first products for itself: a wave has its four ranks' 2048 values on
-// their way at once, so these are the times it waits for memory.
+// their way at once, so these are the times it waits for memory. us in a graph with a launch of their own, and without (M x K x N,
+// rank): once 1 x 2048 x 7168, 16 11.1 and 9.9; twice 1 x 2048 x 7168, 32 11.5 and 11.7, 1 x 4096 x 4096, 32 13.8 and 13.9 (called
+// from Python the launch costs 2 more); four times 4 x 2048 x 7168, 16 11.5 and 14.6; eight 8 x 2048 x 7168, 16 11.6 and 20.6.
 bool own_products(int M, int N, int K, int R) {
   const int waves = cdiv(N, 16) <= 256 ? 8 : 4;
   return M <= 8 && cdiv((int64_t)M * R / 4, waves) * cdiv(K, 2048) <= 2;
