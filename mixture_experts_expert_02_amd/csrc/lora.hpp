@@ -280,7 +280,7 @@ __global__ __launch_bounds__(512) void k_lora_shrink(const ShrinkParams p) {
     xr[j] = p.x + (int64_t)perm_of[row] * p.ldx;
   }
   const int steps = (p.K + 31) / 32, nw = 8 * gridDim.y, w = blockIdx.y * 8 + wave;
-  const int lo = (int)((int64_t)w * steps / nw), hi = (int)((int64_t)(w + 1) * steps / nw);
+  const int lo = (int)((uint32_t)(w * steps) / (uint32_t)nw), hi = (int)((uint32_t)((w + 1) * steps) / (uint32_t)nw);  // below 2^23
   f32x4 acc[RF][FX];
 #pragma unroll
   for (int i = 0; i < RF; ++i)

@@ -213,3 +213,37 @@ def test_adapters_far_apart(M):
     got = moe.lora_linear(**{**c, "lora_a": a, "lora_b": b, "scales": scales, "ids": use[c["ids"].long()].to(torch.int32)})
     torch.cuda.synchronize()
     check(got, c)
+
+
+@pytest.mark.parametrize("M,K,N,R,L", [(1, 2048, 7168, 16, 8), (1, 2048, 7168, 32, 8), (2, 1024, 4500, 16, 3), (2, 2056, 4500, 16, 3),
+                                       (1, 4096, 4096, 32, 4), (8, 520, 129, 8, 5), (4, 1000, 200, 16, 2), (4, 8, 4100, 8, 64),
+                                       (8, 8, 4100, 8, 64), (1, 72, 5000, 24, 2), (1, 2048, 33, 64, 2), (1, 8, 1, 256, 1)])
+@pytest.mark.parametrize("dt", T16)
+def test_few_rows_with_their_own_first_products(M, K, N, R, L, dt):
+    """Both sides of the rule by which few rows' first products take no launch: rows without an adapter among them, an addend in
+    place, and a broken adapter that reaches its own rows alone."""
+    print(f"[lora] own {M}x{K}x{N} R={R} {dt}", flush=True)
+    c = make(M + K + N + R, M, K, N, R, L, dt, bias=True, add=True)
+    c["ids"] = (torch.arange(M, device=DEV, dtype=torch.int32) * 3) % L
+    out = moe.lora_linear(**c)
+    torch.cuda.synchronize()
+    check(out, c)
+    o = c["add"].clone()
+    moe.lora_linear(**{**c, "add": o}, out=o)
+    torch.cuda.synchronize()
+    assert torch.equal(o, out)
+    ids = c["ids"].clone()
+    ids[M // 2:] = torch.tensor([-1, L, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=DEV).repeat(2)[: M - M // 2]
+    some = {**c, "ids": ids}
+    got = moe.lora_linear(**some)
+    torch.cuda.synchronize()
+    check(got, some)
+    assert torch.equal(got[: M // 2], out[: M // 2])
+    if L > 1 and M > 1:
+        broken = {**c, "lora_a": c["lora_a"].clone(), "lora_b": c["lora_b"].clone(), "scales": c["scales"].clone()}
+        bad = int(c["ids"][0])
+        broken["lora_a"][bad], broken["lora_b"][bad], broken["scales"][bad] = float("nan"), float("inf"), float("inf")
+        got = moe.lora_linear(**broken)
+        torch.cuda.synchronize()
+        mine = c["ids"] == bad
+        assert torch.equal(got[~mine], out[~mine]) and got[mine].isnan().all()
