@@ -53,6 +53,7 @@ struct Params {
   const void* add;
   int64_t ld_add;
   int32_t vec;             // out and add take 16-byte accesses at multiples of 8 columns
+  int32_t pair;            // and else 4-byte ones at even columns
   int32_t N8;              // N rounded down to a multiple of 8
   int32_t R, L;
   const uint16_t* t;       // upper and lower parts of the scaled x A^T, rows in sorted order (part_at)
@@ -368,6 +369,55 @@ __device__ __forceinline__ void store_fragment_f32(float* base, const float (&v)
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (row_ok && 8 * q + 4 * lk < left) *(f32x4*)(base + 8 * q + 4 * lk) = f32x4{v[q][0], v[q][1], v[q][2], v[q][3]};
+}
+
+// Rows of 64 columns from out or add into a strip of LDS (LOAD), or back, where these rows begin anywhere: a row's
+// columns side by side over the lanes, two to a lane where rows begin at multiples of 4 bytes (pair). Lane r < ROWS holds in
+// `row` the place of the strip's row r; `rows` and `left`: how many rows and columns there are.
+constexpr int kStripPitch = 144;
+template <int ROWS, bool LOAD>
+__device__ __forceinline__ void move_rows(uint8_t* strip, uint16_t* base, int64_t ld, int row, int rows, int left, bool pair, int lane) {
+  constexpr int U = 8;  // accesses at a time
+  const int per = pair ? 2 : 1, c = pair ? 2 * (lane & 31) : lane, n = ROWS / per;
+  const int r1 = pair ? lane >> 5 : 0;
+  const bool two = pair && c + 1 < left;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += U) {
+    uint32_t x[U];
+    uint16_t* at[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int r = (i0 + i) * per + r1;
+      at[i] = base + (int64_t)__shfl(row, r) * ld + c;
+      x[i] = 0;
+      if constexpr (!LOAD) x[i] = pair ? *(const uint32_t*)(strip + r * kStripPitch + 2 * c) : *(const uint16_t*)(strip + r * kStripPitch + 2 * c);
+    }
+    if (c < left) {
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if ((i0 + i) * per + r1 < rows) {
+            if constexpr (LOAD) x[i] = *(const uint32_t*)at[i];
+            else *(uint32_t*)at[i] = x[i];
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if ((i0 + i) * per + r1 < rows) {
+            if constexpr (LOAD) x[i] = *at[i];
+            else *at[i] = (uint16_t)x[i];
+          }
+      }
+    }
+    if constexpr (LOAD) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        uint8_t* to = strip + ((i0 + i) * per + r1) * kStripPitch + 2 * c;
+        if (pair) *(uint32_t*)to = x[i];
+        else *(uint16_t*)to = (uint16_t)x[i];
+      }
+    }
+  }
 }
 
 // DW's 4 x 4 values of the lane at the output's row and the fragment's first column

@@ -457,8 +457,52 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   // LORA's addend comes as whole lines, eight lanes to a row's 64 columns, all of it before the first result is stored,
   // and takes its place beside the results through LDS (asked for in their order, 16 bytes of 32 rows an instruction,
   // it cost the 256-row tiles of 8192 x 2048 x 7168 33 us).
-  constexpr int PITCH = 144;
+  constexpr int PITCH = kStripPitch;
   uint8_t* strip = smem_arr + wave * 32 * PITCH;
+  if constexpr (MODE == LORA) {
+    if (!p.vec && p.splits == 1) {
+#pragma unroll
+      for (int hm = 0; hm < 2; ++hm)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          float v[2][4][4];
+#pragma unroll
+          for (int hn = 0; hn < 2; ++hn)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[hn][r >> 2][r & 3] = acc[hn][hm][j][r];
+          // rows that begin anywhere go through the strip both ways (a lane's values on their own, 2 bytes of 64 places an
+          // instruction, cost 3330 x 264 x 8940 132 us, here 71 us)
+          const int left = p.N - colw, rows = p.M - (m0 + hm * HM + wm * (HM / 2) + j * 32);
+          if (left > 0 && rows > 0) {
+            if (p.add) {
+              wave_sync();
+              move_rows<32, true>(strip, (uint16_t*)p.add + colw, p.ld_add, orow[hm][j], rows, left, p.pair, lane);
+              wave_sync();
+            }
+#pragma unroll
+            for (int hn = 0; hn < 2; ++hn) {
+              if (p.bias[0]) add_bias(0, colw + hn * STEP, v[hn]);
+              if (p.add) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint2 x = *(const uint2*)(strip + lr * PITCH + (hn * 32 + 8 * q + 4 * lk) * 2);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
+                }
+              }
+            }
+            wave_sync();
+#pragma unroll
+            for (int hn = 0; hn < 2; ++hn)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) *(uint2*)(strip + lr * PITCH + (hn * 32 + 8 * q + 4 * lk) * 2) = pack4<DT>(v[hn][q]);
+            wave_sync();
+            move_rows<32, false>(strip, (uint16_t*)p.out[0] + colw, p.ldo[0], orow[hm][j], rows, left, p.pair, lane);
+          }
+        }
+      return;
+    }
+  }
   u32x4 line[2][J][4];
   const bool with_add = MODE == LORA && p.add && p.vec && p.splits == 1;
   if constexpr (MODE == LORA) {
@@ -528,24 +572,22 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
           const int col = colw + hn * STEP;
           uint16_t* out = (uint16_t*)p.out[0] + o * p.ldo[0] + col;
           if (p.bias[0]) add_bias(0, col, v[hn]);
-          if (p.vec) {
-            if (with_add) {
+          if (with_add) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint2 x = *(const uint2*)(strip + lr * PITCH + (hn * 32 + 8 * q + 4 * lk) * 2);
+            for (int q = 0; q < 4; ++q) {
+              const uint2 x = *(const uint2*)(strip + lr * PITCH + (hn * 32 + 8 * q + 4 * lk) * 2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
-              }
+              for (int i = 0; i < 4; ++i) v[hn][q][i] += load1<DT>(&x, i);
             }
-            store_fragment<DT>(out, v[hn], lk, p.N8 - col, ok);
           }
-          // what no 16-byte store takes: everything, or the columns behind the last multiple of 8
-          if (ok && (!p.vec || col + 32 > p.N8)) {
+          store_fragment<DT>(out, v[hn], lk, p.N8 - col, ok);
+          // the columns behind the last multiple of 8
+          if (ok && col + 32 > p.N8) {
             const uint16_t* add = p.add ? (const uint16_t*)p.add + o * p.ld_add + col : nullptr;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const int c = 8 * (r >> 2) + 4 * lk + (r & 3);
-              if (col + c < p.N && (!p.vec || col + c >= p.N8)) store1<DT>(out, c, v[hn][r >> 2][r & 3] + (add ? load1<DT>(add, c) : 0.f));
+              if (col + c < p.N && col + c >= p.N8) store1<DT>(out, c, v[hn][r >> 2][r & 3] + (add ? load1<DT>(add, c) : 0.f));
             }
           }
         }

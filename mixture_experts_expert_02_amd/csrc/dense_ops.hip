@@ -455,6 +455,7 @@ int moe_lora_linear(const moe_lora_problem* p, const void* x, const void* w, con
   q.bias[0] = bias;
   q.ld_add = lda;
   q.vec = aligned(out, 16) && ldo % 8 == 0 && (!add || (aligned(add, 16) && lda % 8 == 0));
+  q.pair = aligned(out, 4) && ldo % 2 == 0 && (!add || (aligned(add, 4) && lda % 2 == 0));
   q.N8 = p->N / 8 * 8;
   q.R = p->R;
   q.L = p->L;

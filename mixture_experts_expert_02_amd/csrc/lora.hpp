@@ -434,6 +434,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
   constexpr int PITCH = 2 * kMaxRank + 8;
   __shared__ __attribute__((aligned(16))) uint16_t ts[JOIN ? 16 * PITCH : 8];
   __shared__ float fs[16];
+  __shared__ __attribute__((aligned(16))) uint8_t strips[4][16 * kStripPitch];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
   u32x4 b[4][2];  // the factor's rows of adapter `held`, ranks c0 .. c0 + 63
@@ -550,13 +551,41 @@ __global__ __launch_bounds__(256) void k_lora_expand(const Params p, int frags, 
         }
       }
     }
+    if (!p.vec) {  // rows that begin anywhere: see move_rows
+      uint8_t* strip = strips[threadIdx.x >> 6];
+      const int left = p.N - col0, rows = p.M - r0;
+      if (p.add) {
+        wave_sync();
+        move_rows<16, true>(strip, (uint16_t*)p.add + col0, p.ld_add, (int)orow, rows, left, p.pair, lane);
+        wave_sync();
+      }
+      uint2 res[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+        const uint2 x = *(const uint2*)(strip + c * kStripPitch + (i * 16 + 4 * g) * 2);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = col0 + i * 16 + 4 * g + q;
+          v[q] = acc[i][q] + (p.bias[0] ? p.bias[0][min(col, p.N - 1)] : 0.f);
+          if (p.add) v[q] += load1<DT>(&x, q);
+        }
+        res[i] = pack4<DT>(v);
+      }
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *(uint2*)(strip + c * kStripPitch + (i * 16 + 4 * g) * 2) = res[i];
+      wave_sync();
+      move_rows<16, false>(strip, (uint16_t*)p.out[0] + col0, p.ldo[0], (int)orow, rows, left, p.pair, lane);
+      continue;
+    }
     if (r0 + c >= p.M) continue;
     uint16_t* out = (uint16_t*)p.out[0] + orow * p.ldo[0];
     const uint16_t* add = p.add ? (const uint16_t*)p.add + orow * p.ld_add : nullptr;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int col = col0 + i * 16 + 4 * g;  // four neighbours
-      if (p.vec && col + 4 <= p.N) {
+      if (col + 4 <= p.N) {
         uint2 res;
         float v[4];
 #pragma unroll

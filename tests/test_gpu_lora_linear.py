@@ -247,3 +247,23 @@ def test_few_rows_with_their_own_first_products(M, K, N, R, L, dt):
         torch.cuda.synchronize()
         mine = c["ids"] == bad
         assert torch.equal(got[~mine], out[~mine]) and got[mine].isnan().all()
+
+
+@pytest.mark.parametrize("M", [70, 700, 2100])
+@pytest.mark.parametrize("N", [201, 330, 515])
+@pytest.mark.parametrize("w", [True, False])
+def test_rows_that_begin_anywhere(M, N, w):
+    """Outputs and addends whose rows begin at multiples of 2, 4 and 16 bytes give the same bits, in place too, and what lies
+    between the rows stays."""
+    print(f"[lora] rows {M}x{N} w={w}", flush=True)
+    c = make(M + N, M, 136, N, 24, 5, torch.bfloat16, w=w, bias=True, add=True)
+    out = moe.lora_linear(**c)
+    torch.cuda.synchronize()
+    check(out, c)
+    for ld, at in ((N + 8 - N % 8, 0), (N + 2 - N % 2, 0), (N + 4 - N % 2, 2), (N + 5 - N % 2, 1)):
+        whole = torch.full((M, ld), float("nan"), dtype=torch.bfloat16, device=DEV)
+        o = whole[:, at: at + N]
+        o.copy_(c["add"])
+        moe.lora_linear(**{**c, "add": o}, out=o)
+        torch.cuda.synchronize()
+        assert torch.equal(o, out) and whole[:, :at].isnan().all() and whole[:, at + N:].isnan().all()
