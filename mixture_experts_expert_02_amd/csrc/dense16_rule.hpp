@@ -63,5 +63,8 @@ inline int shrink_ranges(int64_t M, int K, int R) {
   return r < 1 ? 1 : r > kMaxRanges ? kMaxRanges : (int)r;
 }
 
+// 16-row fragments of a workgroup of k_lora_expand; with one it joins the first product's K ranges itself.
+inline int expand_frags(int64_t M) { return M >= 2048 ? 4 : 1; }
+
 }  // namespace d16
 }  // namespace moe

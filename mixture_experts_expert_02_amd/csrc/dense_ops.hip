@@ -261,8 +261,6 @@ void launch_shrink(const ShrinkParams& q, int ranges, bool join, hipStream_t s) 
   else hipLaunchKernelGGL((k_lora_finish<DT, 4>), g, b, 0, s, q, ranges);
 }
 
-// 16-row fragments of a workgroup of k_lora_expand; with one it joins the first product's K ranges itself.
-int expand_frags(int M) { return M >= 2048 ? 4 : 1; }
 template <int DT>
 int launch_expand(const Params& q, const ShrinkParams& sh, int ranges, hipStream_t s) {
   const int frags = expand_frags(q.M);
