@@ -645,7 +645,8 @@ size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p
  *   dg = dout df/dg, du = dout df/du   (f's clamps pass gradients on their limits and none beyond)
  *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dbias_gate = sum_m dg, dbias_up = sum_m du
  * dg and du are rounded to the type for the products (to half a step of each value; the biases' sums take them
- * unrounded), so dx, dw_gate and dw_up carry that beside their own rounding, with dw_type MOE_T_FP32 too.
+ * unrounded), so dx, dw_gate and dw_up carry that beside their own rounding, with dw_type MOE_T_FP32 too. Where
+ * M * I <= 16384 they are two values of the type each, the second one what rounding left of the first.
  *   dout             (device) [M, I]
  *   dx               (device) [M, H], overwritten, or NULL
  *   dw_gate, dw_up   (device) [I, H] of dw_type, both or neither (NULL)

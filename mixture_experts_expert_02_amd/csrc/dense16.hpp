@@ -49,6 +49,7 @@ struct Params {
   ActParams act;
   int32_t f32_out, accumulate;  // DW
   int32_t fold;            // DX: rows m and m + fold are one row's upper and lower parts; DW: K rows k and k + fold; 0: none
+  int64_t lower;           // k_big's PARTS: elements from dg's and du's upper parts to their lower ones
   // LORA
   const void* add;
   int64_t ld_add;

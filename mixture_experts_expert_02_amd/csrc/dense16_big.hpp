@@ -18,9 +18,13 @@
 namespace moe {
 namespace d16 {
 
-template <int DT, int MODE, int BM>
+// PARTS (DX and DW): dg and du are two parts each, and every part is a product of its own over the same K values, its upper
+// part's before its lower one's.
+template <int DT, int MODE, int BM, bool PARTS>
 __global__ __launch_bounds__(512) void k_big(const Params p) {
   constexpr bool MM = MODE == DW, NM = MODE == DX || MODE == DW;  // K-major operands
+  static_assert(NM || !PARTS, "gradients only");
+  constexpr int SEGS = (MODE == DX ? 2 : 1) * (PARTS ? 2 : 1);  // products added, one after the other
   constexpr int HM = BM / 2, J = BM / 128, NB = BM == 256 ? 2 : 3;  // rows of an M half, a wave's 32-row fragments of it, buffers
   constexpr int TN = MODE == GATED ? 128 : 256, HALF = 16384, HALF_M = HM * 128;
   constexpr int N_AT = NB * 2 * HALF_M;  // M halves [stage buffer][half], then N halves
@@ -34,7 +38,7 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
   const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lk = lane >> 5;
   const int m0 = it.mt * BM, n0 = it.nt * TN;
   const int z = MODE == DW ? it.z & 1 : 0, split = MODE == DW ? it.z >> 1 : it.z;
-  const int kt = (p.K + BK - 1) / BK, all = MODE == DX ? 2 * kt : kt;
+  const int kt = (p.K + BK - 1) / BK, all = SEGS * kt;
   const int s_lo = (int)((int64_t)split * all / p.splits), nst = (int)((int64_t)(split + 1) * all / p.splits) - s_lo;
 
   // ---- loads: instructions 2 wave and 2 wave + 1 of the 16 of a half (BM = 128: instruction `wave` of the 8 of an M half)
@@ -70,8 +74,8 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
       n_chunk[q] = c;
     }
   }
-  // Where each half's next stage begins, at the operand's row k (K-major) or at its first row; DX's operands change once,
-  // from the gate's product to the up one. All of it in scalar registers and in 32 bits where they suffice, for a
+  // Where each half's next stage begins, at the operand's row k (K-major) or at its first row; the operands change from
+  // product to product (DX: the gate's, then the up one). All of it in scalar registers and in 32 bits where they suffice, for a
   // wave's turn beside the other's 256 cycles of MFMAs is short (among the MFMAs the same instructions cost more:
   // a stage 1.30 us in place of 1.10 for DX, 0.97 in place of 0.91 for GATED).
   struct Cursor {
@@ -80,20 +84,21 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     uint32_t ld2;   // bytes between rows
     int bytes;      // K-contiguous: of the half; K-major: of a row from its first column on
   };
-  const int seg0 = MODE == DX && s_lo >= kt ? 1 : 0;
-  const int second = MODE == DX && !seg0 ? kt - s_lo : 0x7fffffff;  // the first stage of DX's second product
+  const int seg0 = SEGS > 2 ? s_lo / kt : SEGS > 1 && s_lo >= kt ? 1 : 0;
+  const int second = SEGS == 2 && !seg0 ? kt - s_lo : 0x7fffffff;  // the first stage of the second of two products
   auto first_k = [&](int seg) { return seg == seg0 ? (s_lo - seg * kt) * BK : 0; };
   auto end_k = [&](int seg) { return __builtin_amdgcn_readfirstlane(min(p.K, (s_lo + nst - seg * kt) * BK)); };
   auto m_cursor = [&](int h, int seg) {
-    const int i = MODE == DX ? seg : z, k = first_k(seg);
-    const int64_t ld = p.ldm[i], at = MODE == LORA ? 0 : MM ? k * ld + m0 + h * HM : (m0 + h * HM) * ld;
+    const int i = MODE == DX ? PARTS ? seg >> 1 : seg : z, k = first_k(seg);
+    const int64_t ld = p.ldm[i], part = PARTS ? (seg & 1) * p.lower : 0;
+    const int64_t at = MODE == LORA ? 0 : (MM ? k * ld + m0 + h * HM : (m0 + h * HM) * ld) + part;
     const int rows = min(HM, p.M - m0 - h * HM);
     const int bytes = MM ? (p.M - m0 - h * HM) * 2 : MODE == LORA ? 0x7fffffff : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
     return Cursor{uniform(p.m[i] + at), k, end_k(seg), (uint32_t)__builtin_amdgcn_readfirstlane((int)ld * 2),
                   __builtin_amdgcn_readfirstlane(bytes)};
   };
   auto n_cursor = [&](int h, int seg) {
-    const int i = MODE == GATED ? h : seg, k = first_k(seg);
+    const int i = MODE == GATED ? h : MODE == DX ? PARTS ? seg >> 1 : seg : 0, k = first_k(seg);
     const int64_t ld = p.ldn[i], at = NM ? k * ld + n0 + h * 128 : (n0 + (MODE == GATED ? 0 : h * 32)) * ld;
     const int rows = min(MODE == GATED ? 128 : 224, p.N - n0 - (MODE == GATED ? 0 : h * 32));
     const int bytes = NM ? (p.N - n0 - h * 128) * 2 : rows > 0 ? (rows - 1) * (int)ld * 2 + p.K * 2 : 0;
@@ -123,13 +128,24 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     }
     c.k += BK;
   };
+  // with more than two products: which one a half is in, and the stage at which its next one begins (none behind the last)
+  int in_m[2] = {seg0, seg0}, in_n[2] = {seg0, seg0};
+  auto next_of = [&](int seg) { return seg + 1 < SEGS ? (seg + 1) * kt - s_lo : 0x7fffffff; };
   auto load_m = [&](int h, int st, int buf) {
-    if (MODE == DX && st == second) cm[h] = m_cursor(h, 1);
+    if constexpr (SEGS == 2) {
+      if (st == second) cm[h] = m_cursor(h, 1);
+    } else if constexpr (SEGS > 2) {
+      if (st == next_of(in_m[h])) cm[h] = m_cursor(h, ++in_m[h]);
+    }
     load(std::bool_constant<MM>{}, std::integral_constant<int, LM>{}, cm[h], m_row, m_chunk, MODE == LORA ? g_off[h] : nullptr,
          smem + (buf * 2 + h) * HALF_M + wave * LM * 1024);
   };
   auto load_n = [&](int h, int st, int buf) {
-    if (MODE == DX && st == second) cn[h] = n_cursor(h, 1);
+    if constexpr (SEGS == 2) {
+      if (st == second) cn[h] = n_cursor(h, 1);
+    } else if constexpr (SEGS > 2) {
+      if (st == next_of(in_n[h])) cn[h] = n_cursor(h, ++in_n[h]);
+    }
     load(std::bool_constant<NM>{}, std::integral_constant<int, 2>{}, cn[h], n_row, n_chunk, nullptr,
          smem + N_AT + (buf * 2 + h) * HALF + wave * 2048);
   };

@@ -51,6 +51,9 @@ inline Plan plan_of(int mode, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// K of a product whose dg or du is two parts: whole stages of each.
+inline int64_t parts_k(int64_t K) { return (K + 63) / 64 * 64 * 2; }
+
 // The first product of adapters: 16-row fragments of a workgroup, and K ranges: at most one workgroup to a compute unit,
 // at least 16 steps of 32 to a range (us of the kernel: 1000 rows of 4096, rank 24, 64 adapters 31, 17, 8.7, 12.5 and 17
 // with 1, 2, 4, 8 and 16 ranges; 256 of 7168, rank 64, 34, 19, 11.6, 7.6 and 6.0; 8192 of 2048 18.6, 21 and 28 with 1, 2

@@ -84,13 +84,13 @@ int with_type16(int32_t type, F f) {
 }
 
 // ------------------------------------------------------------ tiles
-template <int DT, int MODE, int BM>
+template <int DT, int MODE, int BM, bool PARTS>
 int launch_big(Params& q, hipStream_t s) {
   q.mt = (int)cdiv(q.M, BM);
   q.nt = (int)cdiv(q.N, MODE == GATED ? 128 : 256);
   const int64_t n = cdiv((int64_t)q.mt * q.nt * (MODE == DW ? 2 : 1) * q.splits, 8) * 8;
   if (n > kMaxGrid / 2) return MOE_ENOTSUP;
-  hipLaunchKernelGGL((k_big<DT, MODE, BM>), dim3((unsigned)n), dim3(512), 0, s, q);
+  hipLaunchKernelGGL((k_big<DT, MODE, BM, PARTS>), dim3((unsigned)n), dim3(512), 0, s, q);
   const bool fold = MODE == DX && q.fold;
   if (q.splits > 1 || fold)
     hipLaunchKernelGGL((k_join<DT, MODE>), dim3((unsigned)cdiv((int64_t)(fold ? q.fold : q.M) * ((q.N + 7) / 8), 256), MODE == DW ? 2 : 1),
@@ -108,13 +108,13 @@ int launch_outer(Params& q, hipStream_t s) {
   return launch_status();
 }
 
-// q.K: of one product; part: room for plan_of's partial results
-template <int DT, int MODE>
+// q.K: of one product; PARTS: dg and du in two parts (k_big); part: room for plan_of's partial results
+template <int DT, int MODE, bool PARTS = false>
 int launch(Params& q, void* part, hipStream_t s) {
-  const Plan plan = plan_of(MODE, q.M, q.N, q.K);
+  const Plan plan = plan_of(MODE, q.M, q.N, PARTS ? parts_k(q.K) : q.K);
   q.splits = plan.splits;
   q.part = (float*)part;
-  return plan.bm == 256 ? launch_big<DT, MODE, 256>(q, s) : launch_big<DT, MODE, 128>(q, s);
+  return plan.bm == 256 ? launch_big<DT, MODE, 256, PARTS>(q, s) : launch_big<DT, MODE, 128, PARTS>(q, s);
 }
 
 // ------------------------------------------------------------ few rows
@@ -152,9 +152,13 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
-// dg and du of so few values (see gated_grad.hpp) go in two parts, where k_outer takes both.
+// dg and du of so few values (see gated_grad.hpp) go in two parts.
 constexpr int kPartValues = 16384;
-int grad_parts(const moe_gated_problem& p) { return 2 * p.M <= kOuterRows && (int64_t)p.M * p.I <= kPartValues ? 2 : 1; }
+int grad_parts(const moe_gated_problem& p) { return (int64_t)p.M * p.I <= kPartValues ? 2 : 1; }
+// The two parts of so few rows are further rows of dx's product, which a tile of 128 has room for, and further K rows of the weights',
+// which k_outer holds; beyond, they are products of their own in k_big (us of a backward pass in one part and two: 100 x 2048 x 160
+// 18.8 and 27.8, 200 x 264 x 72 24.3 and 36.3, 2048 x 4096 x 8 27.9 and 36.8).
+bool parts_as_rows(const moe_gated_problem& p) { return grad_parts(p) == 2 && 2 * p.M <= kOuterRows; }
 // Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
 int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
@@ -162,16 +166,18 @@ struct GradLayout {
 };
 GradLayout grad_layout(const moe_gated_problem& p) {
   GradLayout l;
-  const int M = p.M * grad_parts(p);
-  const size_t mi = up256((size_t)M * p.I * 2);
+  const int parts = grad_parts(p), M = parts_as_rows(p) ? 2 * p.M : p.M;
+  const bool apart = parts == 2 && M == p.M;
+  const size_t mi = up256((size_t)parts * p.M * p.I * 2);
   l.dg = 0;
   l.du = mi;
   l.sums = 2 * mi;
   l.part = l.sums + up256((size_t)cdiv(p.M, grad_rows(p.M)) * 2 * p.I * 4);
   // two parts of a row always meet in the join
-  size_t dx = plan_of(DX, M, p.H, p.I).part;
+  size_t dx = plan_of(DX, M, p.H, apart ? parts_k(p.I) : p.I).part;
   if (M > p.M) dx = std::max(dx, up256((size_t)M * p.H * 4));
-  l.bytes = l.part + std::max(dx, p.M <= kOuterRows ? 0 : plan_of(DW, p.I, p.H, p.M).part);
+  const bool outer = !apart && p.M <= kOuterRows;
+  l.bytes = l.part + std::max(dx, outer ? 0 : plan_of(DW, p.I, p.H, apart ? parts_k(p.M) : p.M).part);
   return l;
 }
 
@@ -376,12 +382,14 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.rows = grad_rows(f.M);
   r.act = act_of(f);
   const int blocks = (int)cdiv(f.M, r.rows);
+  const bool as_rows = parts_as_rows(f), apart = r.parts && !as_rows;
   Params q{};
   q.m[0] = (const uint16_t*)r.dg;
   q.m[1] = (const uint16_t*)r.du;
   q.ldm[0] = q.ldm[1] = f.I;
   q.splits = 1;
-  q.fold = r.parts ? f.M : 0;
+  q.fold = as_rows ? f.M : 0;
+  q.lower = (int64_t)f.M * f.I;
   return with_type16(f.type, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     hipLaunchKernelGGL((k_gated_grad<DT>), dim3((unsigned)blocks, (unsigned)cdiv(f.I, 64)), dim3(256), 0, s, r);
@@ -397,10 +405,10 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.ldn[1] = g.ld_wu;
       d.out[0] = dx;
       d.ldo[0] = ld_dx;
-      d.M = r.parts ? 2 * f.M : f.M;
+      d.M = as_rows ? 2 * f.M : f.M;
       d.N = f.H;
       d.K = f.I;
-      rc = launch<DT, DX>(d, ws + l.part, s);
+      rc = apart ? launch<DT, DX, true>(d, ws + l.part, s) : launch<DT, DX>(d, ws + l.part, s);
     }
     if (!rc && dw_gate) {
       Params d = q;
@@ -412,10 +420,11 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
       d.ldo[1] = ld_dwu;
       d.M = f.I;
       d.N = f.H;
-      d.K = r.parts ? 2 * f.M : f.M;
+      d.K = as_rows ? 2 * f.M : f.M;
       d.f32_out = f32;
       d.accumulate = p->accumulate;
-      rc = f.M <= kOuterRows ? launch_outer<DT>(d, s) : launch<DT, DW>(d, ws + l.part, s);
+      rc = apart ? launch<DT, DW, true>(d, ws + l.part, s)
+                 : f.M <= kOuterRows ? launch_outer<DT>(d, s) : launch<DT, DW>(d, ws + l.part, s);
     }
     return rc;
   });

@@ -11,7 +11,7 @@ namespace d16 {
 // instruction takes 16-bit operands, and each rounding is off by half a step of its own value, so a sum of
 // many carries an error of the size of its own last rounding (together 1.41 times as much, 1.48 at most seen from
 // 4096 values on). A few values are ruled by the largest (one row of 88 columns: 1.8 times, of 256: 1.7), so up to
-// kPartValues their lower parts go along as further rows, and the gradients are as exact as from unrounded
+// kPartValues, in however many rows, their lower parts go along, and the gradients are as exact as from unrounded
 // values. (For all calls of up to 64 rows that costs 64 x 7168 x 2048 44 -> 54 us, 64 x 4096 x 14336 143 -> 176.) With sums != nullptr the columns'
 // sums over this workgroup's rows as well, from the unrounded values: to their place where one workgroup
 // has all rows, else for k_column_sums.
