@@ -637,6 +637,7 @@ typedef struct {
   int32_t accumulate;     /* 1: the weights' and biases' gradients are added to what dw_gate, dw_up, dbias_gate and
                              dbias_up hold; 0: these are overwritten */
   int64_t ld_dx, ld_dwg, ld_dwu; /* elements between rows; ld_dwg, ld_dwu with float32 at most 2^40, multiples of 4 */
+  int32_t two_parts;      /* 1: dg and du take part in the products as two values of the type each; 0: see below */
 } moe_gated_grad_problem;
 
 size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p);
@@ -644,9 +645,13 @@ size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p
 /* Gradients of moe_gated_linear from dout, the gradient of out, and the gate and up it kept:
  *   dg = dout df/dg, du = dout df/du   (f's clamps pass gradients on their limits and none beyond)
  *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dbias_gate = sum_m dg, dbias_up = sum_m du
- * dg and du are rounded to the type for the products (to half a step of each value; the biases' sums take them
- * unrounded), so dx, dw_gate and dw_up carry that beside their own rounding, with dw_type MOE_T_FP32 too. Where
- * M * I <= 16384 they are two values of the type each, the second one what rounding left of the first.
+ * With two_parts 0 and M * I > 16384 dg and du are rounded to the type for the products (to half a step of each value; the
+ * biases' sums take them unrounded), so dx, dw_gate and dw_up carry that beside their own rounding (1.4 times the
+ * error of that one alone), with dw_type MOE_T_FP32 too. With two_parts 1, or up to 16384 values, they are two values of the type each,
+ * the second one what rounding left of the first (16 significand bits and more), and no sum is off by more than float32
+ * sums are and 2^-16 (MOE_T_FP16: 2^-22) of its terms; the products then take twice the time.
+ * MOE_T_FP16: dg and du have that type's range, in two parts too. What lies beyond 65504 becomes infinite, and below 2^-14 digits are
+ * lost (a step is 2^-24), so the loss is to be scaled as it is for any float16 gradient.
  *   dout             (device) [M, I]
  *   dx               (device) [M, H], overwritten, or NULL
  *   dw_gate, dw_up   (device) [I, H] of dw_type, both or neither (NULL)

@@ -99,7 +99,7 @@ class MoeGatedProblem(ctypes.Structure):
 
 class MoeGatedGradProblem(ctypes.Structure):
     _fields_ = [("fwd", MoeGatedProblem), ("dw_type", ctypes.c_int32), ("accumulate", ctypes.c_int32),
-                ("ld_dx", ctypes.c_int64), ("ld_dwg", ctypes.c_int64), ("ld_dwu", ctypes.c_int64)]
+                ("ld_dx", ctypes.c_int64), ("ld_dwg", ctypes.c_int64), ("ld_dwu", ctypes.c_int64), ("two_parts", ctypes.c_int32)]
 
 
 class MoeLoraProblem(ctypes.Structure):
@@ -900,10 +900,12 @@ def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: f
 def gated_linear_backward(dout, x, w_gate, w_up, gate, up, act: str = "silu", alpha: float = 1.0, beta: float = 0.0,
                           limit: float = math.inf, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = False,
                           accumulate: bool = False, dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None,
-                          workspace=None) -> GatedGrads:
+                          workspace=None, two_parts: bool = False) -> GatedGrads:
     """Gradients of gated_linear from dout [M, I] and the gate and up [M, I] it kept: dx [M, H], dw_gate and
     dw_up [I, H] (given tensors may be float32), float32 dbias_gate and dbias_up [I]. accumulate: the
-    weights' and biases' gradients are added to the given tensors. See moe_gated_linear_backward."""
+    weights' and biases' gradients are added to the given tensors. The gradients of the two projections are rounded to
+    the type before their products with the weights and with x; two_parts keeps what that rounding leaves off as well, in
+    twice the time. See moe_gated_linear_backward."""
     where = "gated_linear_backward"
     M, I, dev, ldo = _rows16(dout, where, "dout")
     _, H, _ = _matrix(x, where, "x")
@@ -936,7 +938,7 @@ def gated_linear_backward(dout, x, w_gate, w_up, gate, up, act: str = "silu", al
             _refuse(where, "accumulate needs dbias_gate and dbias_up")
         dbias_gate, dbias_up = (dout.new_empty(I, dtype=torch.float32) for _ in range(2))
     f = MoeGatedProblem(M, H, I, _TYPE[dout.dtype], _act(act, where), alpha, beta, limit, ldx, ld_wg, ld_wu, ldo, ld_g, ld_u)
-    p = MoeGatedGradProblem(f, _TYPE[dw_type], 1 if accumulate else 0, ld_dx, ld_dwg, ld_dwu)
+    p = MoeGatedGradProblem(f, _TYPE[dw_type], 1 if accumulate else 0, ld_dx, ld_dwg, ld_dwu, 1 if two_parts else 0)
     ref = ctypes.byref(p)
     ws, size, keep = _workspace(workspace, lib().moe_gated_linear_backward_workspace_bytes(ref), dout, dev, where)
     at = [None if t is None else t.data_ptr() for t in (dx, dw_gate, dw_up, dbias_gate, dbias_up)]

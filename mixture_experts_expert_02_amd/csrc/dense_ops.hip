@@ -152,21 +152,22 @@ int launch_rows(Params& q, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ backward workspace
-// dg and du of so few values (see gated_grad.hpp) go in two parts.
+// dg and du of so few values (see gated_grad.hpp) go in two parts, others where the caller asks for it.
 constexpr int kPartValues = 16384;
-int grad_parts(const moe_gated_problem& p) { return (int64_t)p.M * p.I <= kPartValues ? 2 : 1; }
+int grad_parts(const moe_gated_grad_problem& p) { return p.two_parts || (int64_t)p.fwd.M * p.fwd.I <= kPartValues ? 2 : 1; }
 // The two parts of so few rows are further rows of dx's product, which a tile of 128 has room for, and further K rows of the weights',
 // which k_outer holds; beyond, they are products of their own in k_big (us of a backward pass in one part and two: 100 x 2048 x 160
 // 18.8 and 27.8, 200 x 264 x 72 24.3 and 36.3, 2048 x 4096 x 8 27.9 and 36.8).
-bool parts_as_rows(const moe_gated_problem& p) { return grad_parts(p) == 2 && 2 * p.M <= kOuterRows; }
+bool parts_as_rows(const moe_gated_grad_problem& p) { return grad_parts(p) == 2 && 2 * p.fwd.M <= kOuterRows; }
 // Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
 int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
   size_t dg, du, sums, part, bytes;
 };
-GradLayout grad_layout(const moe_gated_problem& p) {
+GradLayout grad_layout(const moe_gated_grad_problem& g) {
   GradLayout l;
-  const int parts = grad_parts(p), M = parts_as_rows(p) ? 2 * p.M : p.M;
+  const moe_gated_problem& p = g.fwd;
+  const int parts = grad_parts(g), M = parts_as_rows(g) ? 2 * p.M : p.M;
   const bool apart = parts == 2 && M == p.M;
   const size_t mi = up256((size_t)parts * p.M * p.I * 2);
   l.dg = 0;
@@ -185,7 +186,7 @@ int grad_sizes(const moe_gated_grad_problem* p, Gated& g, int64_t& ld_dx, int64_
   if (!p) return MOE_EINVAL;
   int rc = gated_sizes(&p->fwd, g);
   if (rc) return rc;
-  if (p->accumulate != 0 && p->accumulate != 1) return MOE_EINVAL;
+  if ((p->accumulate != 0 && p->accumulate != 1) || (p->two_parts != 0 && p->two_parts != 1)) return MOE_EINVAL;
   const bool f32 = p->dw_type == MOE_T_FP32;
   if (!f32 && p->dw_type != p->fwd.type) return p->dw_type == MOE_T_BF16 || p->dw_type == MOE_T_FP16 ? MOE_ENOTSUP : MOE_EINVAL;
   const int H = p->fwd.H;
@@ -330,7 +331,7 @@ size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p
   Gated g;
   int64_t a, b, c;
   if (grad_sizes(p, g, a, b, c) || p->fwd.M == 0) return 0;
-  return grad_layout(p->fwd).bytes;
+  return grad_layout(*p).bytes;
 }
 
 int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout, const void* x, const void* w_gate,
@@ -360,7 +361,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
     return launch_status();
   }
   if (!given16({dout, gate, up, workspace}) || (dw_gate && !given16({x})) || (dx && !given16({w_gate, w_up}))) return MOE_EINVAL;
-  const GradLayout l = grad_layout(f);
+  const GradLayout l = grad_layout(*p);
   if (workspace_bytes < l.bytes) return MOE_ENOSPC;
   uint8_t* ws = (uint8_t*)workspace;
   GradParams r{};
@@ -373,7 +374,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.dbias[0] = dbias_gate;
   r.dbias[1] = dbias_up;
   r.accumulate = p->accumulate;
-  r.parts = grad_parts(f) == 2;
+  r.parts = grad_parts(*p) == 2;
   r.ld_dout = g.ld_out;
   r.ld_gate = g.ld_gate;
   r.ld_up = g.ld_up;
@@ -382,7 +383,7 @@ int moe_gated_linear_backward(const moe_gated_grad_problem* p, const void* dout,
   r.rows = grad_rows(f.M);
   r.act = act_of(f);
   const int blocks = (int)cdiv(f.M, r.rows);
-  const bool as_rows = parts_as_rows(f), apart = r.parts && !as_rows;
+  const bool as_rows = parts_as_rows(*p), apart = r.parts && !as_rows;
   Params q{};
   q.m[0] = (const uint16_t*)r.dg;
   q.m[1] = (const uint16_t*)r.du;
