@@ -108,7 +108,9 @@ __device__ __forceinline__ void act_df(const ActParams& a, float g, float u, flo
     const float gc = g > a.limit ? a.limit : g;
     const float uc = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
     const float s = sigm(a.alpha * gc);
-    fg = g > a.limit ? 0.f : (uc + a.beta) * s * (1.f + a.alpha * gc * sigm(-a.alpha * gc));
+    // beyond 128 the sigmoid or its complement is 0 in float32, which an infinite product would make NaN
+    const float t = __builtin_amdgcn_fmed3f(a.alpha * gc, -128.f, 128.f);
+    fg = g > a.limit ? 0.f : (uc + a.beta) * s * (1.f + t * sigm(-t));
     fu = u > a.limit || u < -a.limit ? 0.f : gc * s;
   }
 }
