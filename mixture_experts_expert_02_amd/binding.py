@@ -10,6 +10,7 @@ import ctypes
 import math
 import operator
 import os
+import warnings
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -847,6 +848,16 @@ def _act(act, where: str) -> int:
     return a
 
 
+def _no_graph(where: str, *tensors) -> None:
+    """Says so where autograd would have recorded a step on these tensors: the library's calls record none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and getattr(t, "requires_grad", False):
+                warnings.warn(f"{where} records no autograd graph, and gradients do not pass through it: call it under "
+                              "torch.no_grad(), and gated_linear_backward for gated_linear's gradients", stacklevel=3)
+                return
+
+
 def _workspace(workspace, need: int, like, dev: int, where: str):
     """(address, bytes) of the given workspace, or of a new one; the tensor to keep alive."""
     if workspace is None:
@@ -864,8 +875,10 @@ def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: f
                  workspace=None) -> GatedOut:
     """f(x w_gate^T + bias_gate, x w_up^T + bias_up) for x [M, H] and weights [I, H] of one type (bf16 or
     float16; rows may be strided), float32 biases [I]. save (or gate and up given): the two
-    projections [M, I] as well, for gated_linear_backward. See moe_gated_linear."""
+    projections [M, I] as well, for gated_linear_backward. No autograd graph is recorded (a warning says so where
+    tensors ask for one). See moe_gated_linear."""
     where = "gated_linear"
+    _no_graph(where, x, w_gate, w_up, bias_gate, bias_up)
     M, H, dev, ldx = _rows16(x, where, "x")
     I, _, _ = _matrix(w_gate, where, "w_gate")
     same = (x.dtype,)
@@ -951,8 +964,9 @@ def lora_linear(x, w, lora_a, lora_b, ids, scales, bias=None, add=None, out=None
     """x w^T + bias + add + scales[a] (x lora_a[a]^T) lora_b[a]^T with a = ids[m] for row m of x [M, K]; a row whose
     id is outside [0, L) has no adapter. w [N, K] or None, lora_a [L, R, K], lora_b [L, N, R], all of x's type (bf16 or
     float16); ids int32 [M], scales float32 [L], bias float32 [N]; add and out [M, N] (out may be add).
-    See moe_lora_linear."""
+    For serving: no autograd graph is recorded (a warning says so where tensors ask for one). See moe_lora_linear."""
     where = "lora_linear"
+    _no_graph(where, x, w, lora_a, lora_b, scales, bias, add)
     M, K, dev, ldx = _rows16(x, where, "x")
     same = (x.dtype,)
     for t, name in ((lora_a, "lora_a"), (lora_b, "lora_b")):
