@@ -143,12 +143,12 @@ int launch_rows(Params& q, hipStream_t s) {
   const bool few = cdiv(q.N, MODE == GATED ? 8 : 16) <= 256;
   if constexpr (MODE == LORA) {
     if (q.a) return few ? launch_few<DT, MODE, 8, 1, 1, 6, true>(q, s) : launch_few<DT, MODE, 4, 2, 1, 3, true>(q, s);
+    // two workgroups of 32 rows to the same weights, both on a compute unit (64 x 2880 x 2895 with 64 rows in one: 13.2 us, here 12.4)
+    if (q.M > 32) return launch_few<DT, MODE, 4, 1, 4, 3>(q, s);
   }
   if (q.M <= 8) return few ? launch_few<DT, MODE, 8, 1, 1, 6>(q, s) : launch_few<DT, MODE, 4, 2, 1, 3>(q, s);
   if (q.M <= 16) return few ? launch_few<DT, MODE, 8, 1, 2, 4>(q, s) : launch_few<DT, MODE, 4, 2, 2, 3>(q, s);
-  if (q.M <= 32) return few ? launch_few<DT, MODE, 8, 1, 4, 3>(q, s) : launch_few<DT, MODE, 4, 2, 4, 2>(q, s);
-  // two workgroups of 32 rows to the same weights, both on a compute unit (64 x 2880 x 2895 with 64 rows in one: 13.2 us, here 12.4)
-  return launch_few<DT, MODE, 4, 1, 4, 3>(q, s);
+  return few ? launch_few<DT, MODE, 8, 1, 4, 3>(q, s) : launch_few<DT, MODE, 4, 2, 4, 2>(q, s);
 }
 
 // ------------------------------------------------------------ backward workspace
