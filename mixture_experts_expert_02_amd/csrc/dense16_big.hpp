@@ -1,16 +1,15 @@
-// The largest tiles of the dense 16-bit products: 256 x 256 outputs by eight waves
-// (GATED: 128 gate and the same 128 up columns).
+// Tiles of 256 x 256 or 128 x 256 outputs by eight waves (GATED: 128 gate and the same 128 up columns).
 //
-// A stage of 64 K values is four half operands of 16 KB: M0, M1 (rows 0-127 and
-// 128-255) and N0, N1. Wave (wm, wn) of 2 x 4 owns 64 rows of each M half and 32
-// columns of each N half, so a stage is four phases of 64 x 32 x 64 products, eight
-// MFMAs a wave: M0 N0, M0 N1, M1 N1, M1 N0. While a phase multiplies, the wave reads
-// the operands of the next one from LDS (N1, M1, the next stage's M0, its N0: four or eight
-// fragments, each into registers that the last phases have used up) and loads the half
-// whose buffer the phase before has read for the last time, for the stage after the
-// next. So every half has six phases (3000 cycles at the MFMA rate) to arrive, 96 of the 128 KB of
-// buffers are in flight at any time, and a phase ends with one barrier, its reads done and the half
-// that the next one reads landed (all but the twelve youngest loads).
+// A stage of 64 K values is four half operands: M0, M1 (the two halves of the rows, 16 KB each, or 8 with 128 rows) and N0, N1 (16 KB). Wave
+// (wm, wn) of 2 x 4 owns a half of each M half's rows and 32 columns of each N half, and the two waves of a SIMD (wm = 0 and 1)
+// work half a phase apart: while one multiplies, the other reads the operands of its own next products from LDS and starts loads;
+// a barrier ends each turn, two a phase.
+//   256 rows: a stage is four phases of 64 x 32 x 64 products, eight MFMAs a wave: M0 N0, M0 N1, M1 N1, M1 N0, each behind the reads of
+//   the half that is new to it (four or eight fragments; the next stage's N0 in the last one). Two buffers of 64 KB: a phase loads the half whose
+//   buffer the phase before has read for the last time, for the stage after the next, so every half has six phases to arrive
+//   (3000 cycles at the MFMA rate), and a wave waits for all loads but its twelve youngest.
+//   128 rows: a stage is two phases, all four blocks of two K steps each; three buffers of 48 KB, each loaded anew in the two phases behind its
+//   last read.
 #pragma once
 
 #include "dense16.hpp"
@@ -351,8 +350,8 @@ __global__ __launch_bounds__(512) void k_big(const Params p) {
     MOE_D16_PHASE(1, 1, 2, MOE_D16_ALL_M(1, B), load_n(1, (st) + 2, B), tie_m())                   \
     MOE_D16_PHASE(0, 1, X, MOE_D16_ALL_N(Y, 0, 1 - B), load_m(1, (st) + 2, B), tie_n(Y))           \
   }
-  // 128 rows: a phase is all four blocks of two K steps, and a buffer is loaded anew, for the stage after the next
-  // but one, in the two phases behind its last read.
+  // 128 rows: a phase is all four blocks of two K steps, and the buffer read last is loaded anew, for the stage after the next,
+  // in the two phases behind its last read.
 #define MOE_D16_READ_P(B, p_)                                                                          \
   _Pragma("unroll") for (int x = 0; x < 2; ++x) {                                                      \
     if constexpr (MM) {                                                                                \

@@ -57,7 +57,9 @@ inline int64_t parts_k(int64_t K) { return (K + 63) / 64 * 64 * 2; }
 // The first product of adapters: 16-row fragments of a workgroup, and K ranges: at most one workgroup to a compute unit,
 // at least 16 steps of 32 to a range (us of the kernel: 1000 rows of 4096, rank 24, 64 adapters 31, 17, 8.7, 12.5 and 17
 // with 1, 2, 4, 8 and 16 ranges; 256 of 7168, rank 64, 34, 19, 11.6, 7.6 and 6.0; 8192 of 2048 18.6, 21 and 28 with 1, 2
-// and 4).
+// and 4). Two fragments share the factor's loads (us of a call without a projection, 512 columns, rank 64, one fragment second: 2049 of
+// 4096 45.3 and 61.3, 8192 of 2048 54.6 and 60.4; rank 16 39.8 and 39.5). Both limits are on the cautious side: 1100 to 2048 rows of 4096 would
+// gain 4, and rank 128 with two 2100 of 4096 101 -> 71, 8192 of 2048 95 -> 82.
 constexpr int kMaxRanges = 16;
 inline int shrink_frags(int64_t M, int R) { return R <= 64 && M > 2048 ? 2 : 1; }
 inline int shrink_ranges(int64_t M, int K, int R) {
@@ -66,7 +68,9 @@ inline int shrink_ranges(int64_t M, int K, int R) {
   return r < 1 ? 1 : r > kMaxRanges ? kMaxRanges : (int)r;
 }
 
-// 16-row fragments of a workgroup of k_lora_expand; with one it joins the first product's K ranges itself.
+// 16-row fragments of a workgroup of k_lora_expand; with one it joins the first product's K ranges itself. us of a call, rank 64, this
+// and the other number: one 512 x 2048 x 7168 31.8 and 31.9, 1000 x 4096 x 2048 29.5 and 36.8, but 2040 x 2048 x 7168 75.6 and 61.7; four 2048 x 2048 x
+// 7168 61.6 and 75.5, 8192 x 2048 x 7168 173 and 197, 2100 x 4096 x 2048 50.2 and 46.8.
 inline int expand_frags(int64_t M) { return M >= 2048 ? 4 : 1; }
 
 }  // namespace d16

@@ -118,6 +118,11 @@ int launch(Params& q, void* part, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ few rows
+// Rows up to which the weights are streamed (k_few), by what the present kernels gain on either side (us in a graph, rank 32):
+//   adapters, 64: 33 x 2048 x 7168 (rows, in, out) 20.7 (tiles 37.2), 64 x 2880 x 2895 16.8 (35.3). The limit is a low one: 65 to 128 rows would
+//   take 28 to 34 and 22 to 24 in place of tiles' 33 to 37 and 36 to 38.
+//   gated, 32: 17 x 7168 x 2048 12.0 (tiles 21.1), 32 x 2880 x 2880 9.0 (16.2). Low, too: 33 to 64 rows in two workgroups of 32
+//   would take 18 to 20 and 13 to 13.5 in place of 22 to 23 and 17 to 18.
 constexpr int kFewRows = 64;  // of a projection with adapters
 constexpr int kFewGated = 32;
 
@@ -138,6 +143,9 @@ bool own_products(int M, int N, int K, int R) {
   return M <= 8 && cdiv((int64_t)M * R / 4, waves) * cdiv(K, 2048) <= 2;
 }
 
+// One weight fragment to eight waves where that makes at most a workgroup for every compute unit, else two fragments to four waves (us, the
+// other form second; gated: 16 x 7168 x 2048 11.6 and 11.8, 32 12.8 and 14.5, 16 x 2880 x 2880 7.9 and 10.3; adapters: 16 x 4096 x 4096 11.6 and 12.7,
+// 16 x 2048 x 7168 10.5 and 13.7).
 template <int DT, int MODE>
 int launch_rows(Params& q, hipStream_t s) {
   const bool few = cdiv(q.N, MODE == GATED ? 8 : 16) <= 256;
@@ -159,7 +167,9 @@ int grad_parts(const moe_gated_grad_problem& p) { return p.two_parts || (int64_t
 // which k_outer holds; beyond, they are products of their own in k_big (us of a backward pass in one part and two: 100 x 2048 x 160
 // 18.8 and 27.8, 200 x 264 x 72 24.3 and 36.3, 2048 x 4096 x 8 27.9 and 36.8).
 bool parts_as_rows(const moe_gated_grad_problem& p) { return grad_parts(p) == 2 && 2 * p.fwd.M <= kOuterRows; }
-// Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel.
+// Rows of k_gated_grad's workgroups: all of them up to 256, so that the columns' sums need no second kernel, which pays where there are
+// biases and columns enough (us of this step and the sums, 64 rows second: 128 x 2048 5.0 and 5.9, 256 x 14336 9.3 and 10.6; but 256 x 512 7.0 and
+// 6.1). Without biases' gradients 64 rows would be the faster ones (with the weights' products 256 x 2048 15.5 and 12.5).
 int grad_rows(int M) { return M <= 256 ? (M + 31) / 32 * 32 : 64; }
 struct GradLayout {
   size_t dg, du, sums, part, bytes;

@@ -156,7 +156,8 @@ __device__ __forceinline__ void store_parts(float (&v)[N], int r0, int R, int m,
 
 // Sorted rows m0 .. m0 + ROWS - 1 of at most kSortRows, found by a workgroup of 512 threads for itself: counts and
 // places of the adapters as in k_lora_sort, but rows of one adapter keep their order, so that all workgroups agree. A row's
-// place is its adapter's first one, the rows of it in the 64-row pieces before, and those in the lanes before.
+// place is its adapter's first one, the rows of it in the 64-row pieces before, and those in the lanes before. Two keys to a thread are
+// the most. us of a call without a projection, rank 64, with k_lora_sort in place of this: 513 x 4096 x 2048 24.4 and 27.5, 1024 x 7168 x 2048 38.2 and 41.0.
 constexpr int kSortRows = 1024;
 template <int ROWS>
 __device__ __forceinline__ void sort_here(const ShrinkParams& p, int m0, int (&perm)[ROWS], int (&sid)[ROWS]) {
