@@ -848,14 +848,13 @@ def _act(act, where: str) -> int:
     return a
 
 
-def _no_graph(where: str, *tensors) -> None:
-    """Says so where autograd would have recorded a step on these tensors: the library's calls record none."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and getattr(t, "requires_grad", False):
-                warnings.warn(f"{where} records no autograd graph, and gradients do not pass through it: call it under "
-                              "torch.no_grad(), and gated_linear_backward for gated_linear's gradients", stacklevel=3)
-                return
+# Whether autograd would record a step on tensors that require gradients.
+_grad_enabled = torch.is_grad_enabled
+
+
+def _no_graph(where: str) -> None:
+    warnings.warn(f"{where} records no autograd graph, and gradients do not pass through it: call it under "
+                  "torch.no_grad(), and gated_linear_backward for gated_linear's gradients", stacklevel=3)
 
 
 def _workspace(workspace, need: int, like, dev: int, where: str):
@@ -878,7 +877,6 @@ def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: f
     projections [M, I] as well, for gated_linear_backward. No autograd graph is recorded (a warning says so where
     tensors ask for one). See moe_gated_linear."""
     where = "gated_linear"
-    _no_graph(where, x, w_gate, w_up, bias_gate, bias_up)
     M, H, dev, ldx = _rows16(x, where, "x")
     I, _, _ = _matrix(w_gate, where, "w_gate")
     same = (x.dtype,)
@@ -888,6 +886,9 @@ def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: f
     if _both(bias_gate, bias_up, where, "bias_gate and bias_up"):
         bg = _vector(bias_gate, I, _F32, dev, where, "bias_gate")
         bu = _vector(bias_up, I, _F32, dev, where, "bias_up")
+    if _grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad or
+                            (bg is not None and (bias_gate.requires_grad or bias_up.requires_grad))):
+        _no_graph(where)
     shape = (M, I)
     ldo = ld_g = ld_u = 0
     g_ptr = u_ptr = None
@@ -904,8 +905,9 @@ def gated_linear(x, w_gate, w_up, act: str = "silu", alpha: float = 1.0, beta: f
         ldo = _ld(out, shape, same, dev, where, "out")
     p = MoeGatedProblem(M, H, I, _TYPE[x.dtype], _act(act, where), alpha, beta, limit, ldx, ld_wg, ld_wu, ldo, ld_g, ld_u)
     ref = ctypes.byref(p)
-    ws, size, keep = _workspace(workspace, lib().moe_gated_linear_workspace_bytes(ref), x, dev, where)
-    _run(lib().moe_gated_linear, "moe_gated_linear", dev, ref, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), bg, bu,
+    so = lib()
+    ws, size, keep = _workspace(workspace, so.moe_gated_linear_workspace_bytes(ref), x, dev, where)
+    _run(so.moe_gated_linear, "moe_gated_linear", dev, ref, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), bg, bu,
          out.data_ptr(), g_ptr, u_ptr, ws, size)
     return GatedOut(out, gate, up)
 
@@ -966,7 +968,6 @@ def lora_linear(x, w, lora_a, lora_b, ids, scales, bias=None, add=None, out=None
     float16); ids int32 [M], scales float32 [L], bias float32 [N]; add and out [M, N] (out may be add).
     For serving: no autograd graph is recorded (a warning says so where tensors ask for one). See moe_lora_linear."""
     where = "lora_linear"
-    _no_graph(where, x, w, lora_a, lora_b, scales, bias, add)
     M, K, dev, ldx = _rows16(x, where, "x")
     same = (x.dtype,)
     for t, name in ((lora_a, "lora_a"), (lora_b, "lora_b")):
@@ -976,9 +977,9 @@ def lora_linear(x, w, lora_a, lora_b, ids, scales, bias=None, add=None, out=None
             _refuse(where, f"{name} has type {t.dtype}")
         if t.get_device() != dev:
             _refuse(where, f"{name} must be on the GPU of the other tensors")
-    L, R, _ = lora_a.shape
-    N = lora_b.shape[1]
-    if lora_a.shape[2] != K or lora_b.shape[0] != L or lora_b.shape[2] != R:
+    L, R, K_a = lora_a.shape
+    L_b, N, R_b = lora_b.shape
+    if K_a != K or L_b != L or R_b != R:
         _refuse(where, f"lora_a {tuple(lora_a.shape)} and lora_b {tuple(lora_b.shape)} do not fit rows of {K}")
     _size(max(N, L, R), where)
     ldw = 0 if w is None else _ld(w, (N, K), same, dev, where, "w")
@@ -992,10 +993,15 @@ def lora_linear(x, w, lora_a, lora_b, ids, scales, bias=None, add=None, out=None
         ldo = _ld(out, (M, N), same, dev, where, "out")
     if add is not None:
         ld_add = _ld(add, (M, N), same, dev, where, "add")
+    if _grad_enabled() and (x.requires_grad or lora_a.requires_grad or lora_b.requires_grad or scales.requires_grad or
+                            (w is not None and w.requires_grad) or (bias is not None and bias.requires_grad) or
+                            (add is not None and add.requires_grad)):
+        _no_graph(where)
     p = MoeLoraProblem(M, N, K, R, L, _TYPE[x.dtype], ldx, ldw, ldo, ld_add)
     ref = ctypes.byref(p)
-    ws, size, keep = _workspace(workspace, lib().moe_lora_linear_workspace_bytes(ref), x, dev, where)
-    _run(lib().moe_lora_linear, "moe_lora_linear", dev, ref, x.data_ptr(), None if w is None else w.data_ptr(),
+    so = lib()
+    ws, size, keep = _workspace(workspace, so.moe_lora_linear_workspace_bytes(ref), x, dev, where)
+    _run(so.moe_lora_linear, "moe_lora_linear", dev, ref, x.data_ptr(), None if w is None else w.data_ptr(),
          lora_a.data_ptr(), lora_b.data_ptr(), i_ptr, s_ptr, b_ptr, None if add is None else add.data_ptr(),
          out.data_ptr(), ws, size)
     return out
