@@ -647,7 +647,7 @@ size_t moe_gated_linear_backward_workspace_bytes(const moe_gated_grad_problem* p
  *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, dbias_gate = sum_m dg, dbias_up = sum_m du
  * With two_parts 0 and M * I > 16384 dg and du are rounded to the type for the products (to half a step of each value; the
  * biases' sums take them unrounded), so dx, dw_gate and dw_up carry that beside their own rounding (1.4 times the
- * error of that one alone), with dw_type MOE_T_FP32 too. With two_parts 1, or up to 16384 values, they are two values of the type each,
+ * error of that one alone, up to 1.9 times where few large values make up the sums), with dw_type MOE_T_FP32 too. With two_parts 1, or up to 16384 values, they are two values of the type each,
  * the second one what rounding left of the first (16 significand bits and more), and no sum is off by more than float32
  * sums are and 2^-16 (MOE_T_FP16: 2^-22) of its terms; the products then take twice the time.
  * MOE_T_FP16: dg and du have that type's range, in two parts too. What lies beyond 65504 becomes infinite, and below 2^-14 digits are

@@ -2,7 +2,7 @@
 //
 // 128 x 128 of the output to a workgroup of four waves, all of K in LDS at once (rows of 256 bytes of either
 // operand, read transposed), no pipeline: several workgroups share a compute unit, one's loads and products under
-// another's stores. 128 rows take the 64 KB that a launch gets without more ado, two workgroups to a unit. us of the weights' gradients
+// another's stores. 128 rows take 64 KB, which leaves two workgroups to a unit. us of the weights' gradients
 // with k_gated_grad before them, k_big second: 65 x 7168 x 2048 25.3 and 27.3, 96 x 2880 x 2880 19.7 and 26.5, 128 x 7168 x 2048 28.5 and 29.4.
 #pragma once
 

@@ -9,9 +9,9 @@ namespace d16 {
 
 // dg = dout f_g(g, u), du = dout f_u(g, u), rounded to the type: the matrix
 // instruction takes 16-bit operands, and each rounding is off by half a step of its own value, so a sum of
-// many carries an error of the size of its own last rounding (together 1.41 times as much, 1.48 at most seen from
-// 4096 values on). A few values are ruled by the largest (one row of 88 columns: 1.8 times, of 256: 1.7), so up to
-// kPartValues, in however many rows, their lower parts go along, and the gradients are as exact as from unrounded
+// many carries an error of the size of its own last rounding (together 1.41 times as much; of 1500 sizes beyond kPartValues 1.52 in
+// one output of a hundred, 1.86 at most, where heavy rows or columns rule the sums). A few values always are ruled by the largest (one row of
+// 88 columns: 1.8 times, of 256: 1.7), so up to kPartValues, in however many rows, their lower parts go along, and the gradients are as exact as from unrounded
 // values. Others get them on request (64 x 7168 x 2048 44 -> 54 us, 77 x 2880 x 2880 40 -> 58, 1023 x 7168 x 2048 145 -> 242,
 // 4096 x 4096 x 14336 1554 -> 3006; root mean square errors of bf16 results 0.00234 and 0.00166). With sums != nullptr the columns'
 // sums over this workgroup's rows as well, from the unrounded values: to their place where one workgroup
